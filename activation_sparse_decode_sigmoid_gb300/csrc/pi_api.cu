@@ -14,8 +14,10 @@
 #include <vector>
 
 #include "pi.h"
+#include "pi_host.h"
 #include "pi_kernels.h"
 
+using pi::DeviceGuard;
 using pi::LayerDev;
 using pi::StepParams;
 
@@ -33,20 +35,6 @@ struct LayerSlot {
 };
 
 int round_up(int v, int a) { return (v + a - 1) / a * a; }
-
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) cudaSetDevice(dev);
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 } // namespace
 
@@ -285,6 +273,26 @@ pi_status check_batch(pi_ctx *c, int B)
 }
 
 } // namespace
+
+namespace pi {
+
+CtxView ctx_view(pi_ctx *c)
+{
+    return {c->device, c->stream, c->G, c->smem_optin, c->ctl + 2, c->ctl + 3, c->wait_ns};
+}
+
+pi_status ctx_fail(pi_ctx *c, pi_status code, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    c->err = buf;
+    return code;
+}
+
+} // namespace pi
 
 extern "C" {
 

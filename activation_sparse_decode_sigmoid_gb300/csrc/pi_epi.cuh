@@ -1,0 +1,220 @@
+// Device side of the products' epilogues: activations, their derivatives, and
+// 8 consecutive outputs of a row at a time.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "pi_block.h"
+
+namespace pi {
+namespace {
+
+template <typename T> struct C16;
+template <> struct C16<__half> {
+    static __device__ __forceinline__ float one(uint16_t u) { return __half2float(__ushort_as_half(u)); }
+    static __device__ __forceinline__ uint16_t round(float f) { return __half_as_ushort(__float2half_rn(f)); }
+    static __device__ __forceinline__ uint32_t round2(float a, float b)
+    {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+template <> struct C16<__nv_bfloat16> {
+    static __device__ __forceinline__ float one(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+    static __device__ __forceinline__ uint16_t round(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+    static __device__ __forceinline__ uint32_t round2(float a, float b)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+// Clamp that keeps NaN (fminf and fmaxf would drop it): beyond +-lim the
+// smooth functions below equal their limits in fp32, and inf * 0 is avoided.
+__device__ __forceinline__ float clampn(float z, float lim) { return z < -lim ? -lim : (z > lim ? lim : z); }
+
+// fn(z).  __expf's error is a few units in the last place for the arguments
+// that matter, far below the 16-bit rounding that follows every use.
+__device__ __forceinline__ float act_f(int fn, float z)
+{
+    switch (fn) {
+    case PI_FN_RELU: return z < 0.f ? 0.f : z;
+    case PI_FN_SQRELU: return z < 0.f ? 0.f : z * z;
+    case PI_FN_SIGMOID: return __fdividef(1.f, 1.f + __expf(-z)); // (0 below -87)
+    case PI_FN_SILU: return z < -80.f ? -0.f : __fdividef(z, 1.f + __expf(-z));
+    case PI_FN_GELU: return z < -30.f ? -0.f : 0.5f * z * (1.f + erff(z * 0.70710678f));
+    case PI_FN_GELU_TANH: {
+        // z (1 + tanh t) / 2 = z / (1 + exp(-2 t))
+        const float c = clampn(z, 30.f);
+        const float t = 0.79788456f * (c + 0.044715f * c * c * c);
+        return z < -30.f ? -0.f : __fdividef(z, 1.f + __expf(-2.f * clampn(t, 40.f)));
+    }
+    default: return z;
+    }
+}
+
+__device__ __forceinline__ float act_df(int fn, float z)
+{
+    switch (fn) {
+    case PI_FN_RELU: return z > 0.f ? 1.f : 0.f;
+    case PI_FN_SQRELU: return z < 0.f ? 0.f : 2.f * z;
+    case PI_FN_SIGMOID: {
+        const float p = __fdividef(1.f, 1.f + __expf(-clampn(z, 80.f)));
+        return p * (1.f - p);
+    }
+    case PI_FN_SILU: {
+        const float c = clampn(z, 80.f);
+        const float p = __fdividef(1.f, 1.f + __expf(-c));
+        return p * (1.f + c * (1.f - p));
+    }
+    case PI_FN_GELU: {
+        const float c = clampn(z, 30.f);
+        return 0.5f * (1.f + erff(c * 0.70710678f)) + 0.39894228f * c * __expf(-0.5f * c * c);
+    }
+    case PI_FN_GELU_TANH: {
+        const float c = clampn(z, 10.f);
+        const float t = 0.79788456f * (c + 0.044715f * c * c * c);
+        const float p = __fdividef(1.f, 1.f + __expf(-2.f * clampn(t, 40.f))); // (1 + tanh t) / 2
+        return p + 2.f * c * p * (1.f - p) * 0.79788456f * (1.f + 0.134145f * c * c);
+    }
+    default: return 1.f;
+    }
+}
+
+// ---------------------------------------------------------------- 8 elements
+template <typename T> __device__ __forceinline__ void unpack8(const uint4 &q, float (&v)[8])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = C16<T>::one((uint16_t)(w[i] & 0xffffu));
+        v[2 * i + 1] = C16<T>::one((uint16_t)(w[i] >> 16));
+    }
+}
+
+template <typename T> __device__ __forceinline__ uint4 pack8(const float (&v)[8])
+{
+    return make_uint4(C16<T>::round2(v[0], v[1]), C16<T>::round2(v[2], v[3]), C16<T>::round2(v[4], v[5]),
+                      C16<T>::round2(v[6], v[7]));
+}
+
+// 8 16-bit elements at p (n of them exist; the rest read as 0)
+template <typename T> __device__ __forceinline__ void load8(const uint16_t *p, int n, bool vec, float (&v)[8])
+{
+    if (vec && n >= 8) {
+        unpack8<T>(*reinterpret_cast<const uint4 *>(p), v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? C16<T>::one(p[i]) : 0.f;
+}
+
+template <typename T> __device__ __forceinline__ void store8(uint16_t *p, int n, bool vec, const float (&v)[8])
+{
+    if (vec && n >= 8) {
+        *reinterpret_cast<uint4 *>(p) = pack8<T>(v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = C16<T>::round(v[i]);
+}
+
+__device__ __forceinline__ void load8f(const float *p, int n, bool vec, float (&v)[8])
+{
+    if (vec && n >= 8) {
+        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.f;
+}
+
+__device__ __forceinline__ void store8f(float *p, int n, bool vec, const float (&v)[8])
+{
+    if (vec && n >= 8) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = v[i];
+}
+
+// The epilogue of row `row`, columns [col, col + 8) (col a multiple of 8;
+// the caller checks row < M and col < N): v the accumulators, v2 the second
+// product's (EPI_GATED).
+template <typename T, int MODE>
+__device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int col, float (&v)[8], float (&v2)[8])
+{
+    const int n = N - col;
+    if (MODE == EPI_LINEAR) {
+        if (e.bias) {
+            float b[8];
+            load8<T>(e.bias + col, n, e.vec & V_BIAS, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += b[i];
+        }
+        if (e.out2) store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
+        if (e.fn != PI_FN_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_f(e.fn, v[i]);
+        }
+        if (e.scale != 1.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= e.scale;
+        }
+        if (e.res) {
+            float r[8];
+            if (e.out32) load8f(static_cast<const float *>(e.res) + row * e.ldr + col, n, e.vec & V_RES, r);
+            else load8<T>(static_cast<const uint16_t *>(e.res) + row * e.ldr + col, n, e.vec & V_RES, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+        if (e.out32) store8f(static_cast<float *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);
+        else store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);
+    } else if (MODE == EPI_GATED) {
+        if (e.bias) {
+            float b[8];
+            load8<T>(e.bias + col, n, e.vec & V_BIAS, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += b[i];
+        }
+        if (e.bias2) {
+            float b[8];
+            load8<T>(e.bias2 + col, n, e.vec & V_BIAS2, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v2[i] += b[i];
+        }
+        if (e.out2) store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
+        if (e.out3) store8<T>(e.out3 + row * e.ld3 + col, n, e.vec & V_OUT3, v2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_f(e.fn, v[i]) * v2[i];
+        store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);
+    } else {
+        float g[8];
+        load8<T>(e.in1 + row * e.ldi1 + col, n, e.vec & V_IN1, g);
+        if (e.in2) {
+            float u[8];
+            load8<T>(e.in2 + row * e.ldi2 + col, n, e.vec & V_IN2, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                u[i] *= v[i] * act_df(e.fn, g[i]);
+                v[i] *= act_f(e.fn, g[i]);
+            }
+            store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, u);
+            store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= e.scale * act_df(e.fn, g[i]);
+            store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);
+        }
+    }
+}
+
+} // namespace
+} // namespace pi

@@ -23,7 +23,9 @@ PI_OK = 0
 PI_ERR_ARG, PI_ERR_SHAPE, PI_ERR_CUDA, PI_ERR_OOM = -1, -2, -3, -4
 PI_ERR_NOT_LOADED, PI_ERR_TIMEOUT, PI_ERR_DEVICE_FLAG, PI_ERR_UNSUPPORTED = -5, -6, -7, -8
 PI_RELU, PI_REGLU, PI_SQRELU = 0, 1, 2
-PI_F16, PI_BF16, PI_Q4_0 = 0, 1, 2
+PI_F16, PI_BF16, PI_Q4_0, PI_F32 = 0, 1, 2, 3
+PI_FN_NONE, PI_FN_RELU, PI_FN_SQRELU, PI_FN_SIGMOID, PI_FN_SILU, PI_FN_GELU, PI_FN_GELU_TANH = range(7)
+PI_NORM_NONE, PI_NORM_RMS, PI_NORM_LAYER = 0, 1, 2
 
 # every symbol include/pi.h declares
 EXPORTS = ("pi_create", "pi_destroy", "pi_set_stream", "pi_load_layer", "pi_layer_counts",
@@ -34,7 +36,9 @@ EXPORTS = ("pi_create", "pi_destroy", "pi_set_stream", "pi_load_layer", "pi_laye
            "pi_debug_set_tuning", "pi_debug_copy_hidden", "pi_debug_set_mma_min_batch",
            "pi_sparse_ffn_noalloc", "pi_set_hot_prefix", "pi_hot_prefix_crossover", "pi_choose_hot_prefix",
            "pi_layerwise_min_batch", "pi_load_layer_shard", "pi_layer_shard", "pi_layer_partial",
-           "pi_residual_add")
+           "pi_residual_add", "pi_linear_workspace", "pi_linear", "pi_linear_bwd", "pi_gated_ffn_workspace",
+           "pi_gated_ffn", "pi_gated_ffn_bwd", "pi_norm_residual", "pi_norm_residual_bwd_workspace",
+           "pi_norm_residual_bwd")
 
 
 class PiError(RuntimeError):
@@ -59,6 +63,30 @@ class pi_layer_weights(ctypes.Structure):
                 ("w_down", ctypes.c_void_p), ("b_down", ctypes.c_void_p), ("p_w1", ctypes.c_void_p),
                 ("p_b1", ctypes.c_void_p), ("p_w2", ctypes.c_void_p), ("p_b2", ctypes.c_void_p),
                 ("on_device", ctypes.c_int32)]
+
+
+def _struct(name, i32=(), f32=(), i64=(), ptr=()):
+    """A ctypes struct of 32-bit integers, floats, 64-bit integers and
+    pointers; f32 maps the names among i32 that are floats."""
+    fields = [(n, ctypes.c_float if n in f32 else ctypes.c_int32) for n in i32]
+    fields += [(n, ctypes.c_int64) for n in i64] + [(n, ctypes.c_void_p) for n in ptr]
+    return type(name, (ctypes.Structure,), {"_fields_": fields})
+
+
+pi_linear_desc = _struct("pi_linear_desc", ("T", "K", "N", "dtype", "out_dtype", "grad_dtype", "fn", "scale", "unaligned"),
+                         ("scale",), ("ldx", "ldw", "ldz", "ldr", "ldy", "lddx", "lddw"))
+pi_gated_ffn_desc = _struct("pi_gated_ffn_desc", ("T", "d", "n", "dtype", "grad_dtype", "fn", "gated", "unaligned"), (),
+                            ("ldx", "ldy", "ld_gate", "ld_up", "ld_down", "ldg", "ldu", "lda"))
+pi_gated_ffn_weights = _struct("pi_gated_ffn_weights", ptr=("w_gate", "w_up", "w_down", "b_gate", "b_up", "b_down"))
+pi_gated_ffn_save = _struct("pi_gated_ffn_save", ptr=("g", "u", "a"))
+pi_gated_ffn_grads = _struct("pi_gated_ffn_grads", ptr=("w_gate", "w_up", "w_down", "b_gate", "b_up", "b_down"))
+pi_norm_residual_desc = _struct("pi_norm_residual_desc",
+                                ("T", "d", "x_dtype", "dtype", "grad_dtype", "pre", "post", "gate_rows", "res_scale",
+                                 "branch_scale", "eps"), ("res_scale", "branch_scale", "eps"),
+                                ("ldx", "ldxo", "ldy", "ldh", "ldgate"))
+pi_norm_residual_params = _struct("pi_norm_residual_params", ptr=("w_pre", "b_pre", "w_post", "b_post"))
+pi_norm_residual_grads = _struct("pi_norm_residual_grads",
+                                 ptr=("dx", "dy", "dgate", "dw_pre", "db_pre", "dw_post", "db_post"))
 
 
 _lib = None
@@ -106,6 +134,15 @@ def load_library(path: str = LIB_PATH):
         "pi_layer_shard": (st, [P, I32, P, P]),
         "pi_layer_partial": (st, [P, I32, P, I32, P]),
         "pi_residual_add": (st, [P, P, P, I32]),
+        "pi_linear_workspace": (st, [P, P, I32, P]),
+        "pi_linear": (st, [P] * 9 + [ctypes.c_size_t]),
+        "pi_linear_bwd": (st, [P] * 9 + [I32, P, ctypes.c_size_t]),
+        "pi_gated_ffn_workspace": (st, [P, P, I32, P]),
+        "pi_gated_ffn": (st, [P] * 7 + [ctypes.c_size_t]),
+        "pi_gated_ffn_bwd": (st, [P] * 8 + [I32, P, ctypes.c_size_t]),
+        "pi_norm_residual": (st, [P] * 8),
+        "pi_norm_residual_bwd_workspace": (st, [P, P, P]),
+        "pi_norm_residual_bwd": (st, [P] * 9 + [I32, P, ctypes.c_size_t]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -302,6 +339,67 @@ def pi_debug_barrier_extra(ctx: int, extra: int) -> None:
     _check(ctx, load_library().pi_debug_barrier_extra(ctx, extra), "pi_debug_barrier_extra")
 
 
+def _ref(struct) -> int | None:
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def pi_linear_workspace(ctx: int, desc, backward: bool) -> int:
+    n = ctypes.c_size_t()
+    _check(ctx, load_library().pi_linear_workspace(ctx, _ref(desc), int(backward), ctypes.addressof(n)),
+           "pi_linear_workspace")
+    return n.value
+
+
+def pi_linear(ctx: int, desc, x, w, b, residual, z, y, ws, ws_bytes: int) -> None:
+    rc = load_library().pi_linear(ctx, _ref(desc), _ptr(x), _ptr(w), _ptr(b), _ptr(residual), _ptr(z), _ptr(y), _ptr(ws),
+                                  ws_bytes)
+    _check(ctx, rc, "pi_linear")
+
+
+def pi_linear_bwd(ctx: int, desc, dy, x, w, z, dx, dw, db, accumulate: bool, ws, ws_bytes: int) -> None:
+    rc = load_library().pi_linear_bwd(ctx, _ref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(z), _ptr(dx), _ptr(dw), _ptr(db),
+                                      int(accumulate), _ptr(ws), ws_bytes)
+    _check(ctx, rc, "pi_linear_bwd")
+
+
+def pi_gated_ffn_workspace(ctx: int, desc, backward: bool) -> int:
+    n = ctypes.c_size_t()
+    _check(ctx, load_library().pi_gated_ffn_workspace(ctx, _ref(desc), int(backward), ctypes.addressof(n)),
+           "pi_gated_ffn_workspace")
+    return n.value
+
+
+def pi_gated_ffn(ctx: int, desc, weights, x, save, y, ws, ws_bytes: int) -> None:
+    rc = load_library().pi_gated_ffn(ctx, _ref(desc), _ref(weights), _ptr(x), _ref(save), _ptr(y), _ptr(ws), ws_bytes)
+    _check(ctx, rc, "pi_gated_ffn")
+
+
+def pi_gated_ffn_bwd(ctx: int, desc, weights, x, dy, save, dx, grads, accumulate: bool, ws, ws_bytes: int) -> None:
+    rc = load_library().pi_gated_ffn_bwd(ctx, _ref(desc), _ref(weights), _ptr(x), _ptr(dy), _ref(save), _ptr(dx),
+                                         _ref(grads), int(accumulate), _ptr(ws), ws_bytes)
+    _check(ctx, rc, "pi_gated_ffn_bwd")
+
+
+def pi_norm_residual(ctx: int, desc, params, x, y, gate, x_out, h) -> None:
+    rc = load_library().pi_norm_residual(ctx, _ref(desc), _ref(params), _ptr(x), _ptr(y), _ptr(gate), _ptr(x_out),
+                                         _ptr(h))
+    _check(ctx, rc, "pi_norm_residual")
+
+
+def pi_norm_residual_bwd_workspace(ctx: int, desc) -> int:
+    n = ctypes.c_size_t()
+    _check(ctx, load_library().pi_norm_residual_bwd_workspace(ctx, _ref(desc), ctypes.addressof(n)),
+           "pi_norm_residual_bwd_workspace")
+    return n.value
+
+
+def pi_norm_residual_bwd(ctx: int, desc, params, dx_out, dh, x_out, y, gate, grads, accumulate: bool, ws,
+                         ws_bytes: int) -> None:
+    rc = load_library().pi_norm_residual_bwd(ctx, _ref(desc), _ref(params), _ptr(dx_out), _ptr(dh), _ptr(x_out), _ptr(y),
+                                             _ptr(gate), _ref(grads), int(accumulate), _ptr(ws), ws_bytes)
+    _check(ctx, rc, "pi_norm_residual_bwd")
+
+
 # ---------------------------------------------------------------- convenience wrapper
 class Context:
     """Owns a pi_ctx; every call runs on torch's current stream of `device`."""
@@ -456,6 +554,262 @@ class Context:
     def dense_step(self, x) -> None:
         self._s()
         pi_dense_step(self.handle, x, x.shape[0])
+
+    # -- block operators: long prompts and training (tensors of torch's float16, bfloat16 and float32)
+    def _args(self, dtype, **tensors):
+        """Checks the tensors of a call: on the context's device, of `dtype`
+        (or, for names ending in an underscore, also float32), rows of
+        consecutive elements.  True if a base is not 16-byte aligned."""
+        import torch
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise PiError(PI_ERR_ARG, f"dtype {dtype} is not float16 or bfloat16")
+        odd = False
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if t.device != self.torch_device:
+                raise PiError(PI_ERR_ARG, f"{name.rstrip('_')} is on {t.device}, the context on {self.torch_device}")
+            if t.dtype != dtype and not (name[-1] == "_" and t.dtype == torch.float32):
+                raise PiError(PI_ERR_ARG, f"{name.rstrip('_')} is {t.dtype}, expected {dtype}")
+            if t.dim() not in (1, 2):
+                raise PiError(PI_ERR_SHAPE, f"{name.rstrip('_')} has {t.dim()} dimensions")
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise PiError(PI_ERR_ARG, f"{name.rstrip('_')}: a row's elements are not consecutive")
+            if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+                raise PiError(PI_ERR_SHAPE, f"{name.rstrip('_')}: rows overlap (stride {t.stride(0)})")
+            odd |= t.data_ptr() % 16 != 0
+        return odd
+
+    @staticmethod
+    def _shape(name, t, *shape):
+        if t is not None and tuple(t.shape) != shape:
+            raise PiError(PI_ERR_SHAPE, f"{name} is {list(t.shape)}, expected {list(shape)}")
+
+    @staticmethod
+    def _packed(name, t):
+        if t is not None and not t.is_contiguous():
+            raise PiError(PI_ERR_ARG, f"{name} is not packed")
+
+    @staticmethod
+    def _ld(t) -> int:
+        """Row stride of a matrix (a single row's own stride says nothing)."""
+        return 0 if t is None or t.shape[0] <= 1 else t.stride(0)
+
+    @staticmethod
+    def _code(dtype) -> int:
+        import torch
+        return {torch.float16: PI_F16, torch.bfloat16: PI_BF16, torch.float32: PI_F32}[dtype]
+
+    def _ws(self, n: int):
+        import torch
+        return torch.empty(n, dtype=torch.uint8, device=self.torch_device) if n else None
+
+    def linear(self, x, w, b=None, *, fn=PI_FN_NONE, scale=1.0, residual=None, z=None, y=None):
+        """y = residual + scale * fn(x W^T + b).  y is x's type, or the
+        residual's (float32 residual stream); z, if given, receives
+        x W^T + b for the backward pass."""
+        import torch
+        (T, K), N = x.shape, w.shape[0]
+        if y is None:
+            y = torch.empty((T, N), dtype=x.dtype if residual is None else residual.dtype, device=self.torch_device)
+        odd = self._args(x.dtype, x=x, w=w, b=b, z=z, residual_=residual, y_=y)
+        self._shape("w", w, N, K), self._shape("b", b, N), self._shape("z", z, T, N)
+        self._shape("residual", residual, T, N), self._shape("y", y, T, N)
+        if residual is not None and residual.dtype != y.dtype:
+            raise PiError(PI_ERR_ARG, f"residual is {residual.dtype}, y {y.dtype}")
+        code = self._code(x.dtype)
+        desc = pi_linear_desc(T, K, N, code, self._code(y.dtype), code, fn, scale, odd, self._ld(x), self._ld(w),
+                              self._ld(z), self._ld(residual), self._ld(y), 0, 0)
+        self._s()
+        n = pi_linear_workspace(self.handle, desc, False)
+        pi_linear(self.handle, desc, x, w, b, residual, z, y, self._ws(n), n)
+        return y
+
+    def linear_bwd(self, dy, x, w, z=None, *, fn=PI_FN_NONE, scale=1.0, need=(True, True, True), dx=None, dw=None,
+                   db=None, accumulate=False):
+        """(dx, dw, db) of ``linear`` for the gradient dy of y (the residual's
+        is dy itself).  need: which of them; buffers may be given, dw and db
+        in x's type or float32, and are added to with `accumulate`."""
+        import torch
+        (T, K), N = x.shape, w.shape[0]
+        new = lambda shape: torch.empty(shape, dtype=x.dtype, device=self.torch_device)
+        if accumulate and any(n and g is None for n, g in zip(need[1:], (dw, db))):
+            raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
+        dx = (new((T, K)) if dx is None else dx) if need[0] else None
+        dw = (new((N, K)) if dw is None else dw) if need[1] else None
+        db = (torch.empty(N, dtype=x.dtype if dw is None else dw.dtype, device=self.torch_device) if db is None
+              else db) if need[2] else None
+        odd = self._args(x.dtype, dy_=dy, x=x, w=w, z=z, dx=dx, dw_=dw, db_=db)
+        self._shape("dy", dy, T, N), self._shape("w", w, N, K), self._shape("z", z, T, N), self._shape("dx", dx, T, K)
+        self._shape("dw", dw, N, K), self._shape("db", db, N)
+        if dw is not None and db is not None and dw.dtype != db.dtype:
+            raise PiError(PI_ERR_ARG, f"dw is {dw.dtype}, db {db.dtype}")
+        grad = dw if dw is not None else db
+        code = self._code(x.dtype)
+        desc = pi_linear_desc(T, K, N, code, self._code(dy.dtype), code if grad is None else self._code(grad.dtype), fn,
+                              scale, odd, self._ld(x), self._ld(w), self._ld(z), 0, self._ld(dy), self._ld(dx),
+                              self._ld(dw))
+        self._s()
+        n = pi_linear_workspace(self.handle, desc, True)
+        pi_linear_bwd(self.handle, desc, dy, x, w, z, dx, dw, db, accumulate, self._ws(n), n)
+        return dx, dw, db
+
+    def gated_ffn_save(self, x, w_gate, w_up):
+        """Buffers (g, u, a) for ``gated_ffn`` to leave for its backward pass,
+        [T][n] with rows that start on 128-byte boundaries (g None if not gated)."""
+        import torch
+        T, n = x.shape[0], w_up.shape[0]
+        new = lambda: torch.empty((T, (n + 63) // 64 * 64), dtype=x.dtype, device=self.torch_device)[:, :n]
+        return (new() if w_gate is not None else None), new(), new()
+
+    def _ffn_desc(self, x, w_gate, w_up, w_down, g, u, a, y, fn, grad_code, odd):
+        T, d = x.shape
+        n = w_up.shape[0]
+        for name, t, shape in (("w_gate", w_gate, (n, d)), ("w_up", w_up, (n, d)), ("w_down", w_down, (d, n)),
+                               ("g", g, (T, n)), ("u", u, (T, n)), ("a", a, (T, n)), ("y", y, (T, d))):
+            self._shape(name, t, *shape)
+        return pi_gated_ffn_desc(T, d, n, self._code(x.dtype), grad_code, fn, w_gate is not None, odd, self._ld(x),
+                                 self._ld(y), self._ld(w_gate), self._ld(w_up), self._ld(w_down), self._ld(g),
+                                 self._ld(u), self._ld(a))
+
+    def gated_ffn(self, x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, *, fn=PI_FN_RELU, save=None,
+                  y=None):
+        """y = (fn(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd, weights in the
+        model's layout; w_gate None: y = fn(x Wu^T + bu) Wd^T + bd.  save
+        (``gated_ffn_save``) keeps g, u and a for the backward pass."""
+        import torch
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=self.torch_device)
+        g, u, a = save if save is not None else (None, None, None)
+        odd = self._args(x.dtype, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, b_gate=b_gate, b_up=b_up, b_down=b_down,
+                         g=g, u=u, a=a, y=y)
+        desc = self._ffn_desc(x, w_gate, w_up, w_down, g, u, a, y, fn, self._code(x.dtype), odd)
+        self._shape("b_gate", b_gate, desc.n), self._shape("b_up", b_up, desc.n), self._shape("b_down", b_down, desc.d)
+        self._s()
+        n = pi_gated_ffn_workspace(self.handle, desc, False)
+        ws = pi_gated_ffn_weights(*map(_ptr, (w_gate, w_up, w_down, b_gate, b_up, b_down)))
+        pi_gated_ffn(self.handle, desc, ws, x, pi_gated_ffn_save(*map(_ptr, (g, u, a))), y, self._ws(n), n)
+        return y
+
+    def gated_ffn_bwd(self, dy, x, w_gate, w_up, w_down, save, *, fn=PI_FN_RELU, need_dx=True, weight_grads=True,
+                      bias_grads=True, grads=None, accumulate=False):
+        """Gradients of ``gated_ffn`` for the gradient dy of y, as a dict with
+        keys dx, w_gate, w_up, w_down, b_gate, b_up, b_down (None: not
+        wanted).  grads: the parameter gradients' buffers by the same keys,
+        packed, in x's type or float32 (all alike), used instead of new ones
+        and added to with `accumulate`; then only the given ones are computed."""
+        import torch
+        g, u, a = save
+        T, d = x.shape
+        n, gated = w_up.shape[0], w_gate is not None
+        shapes = {"w_gate": (n, d), "w_up": (n, d), "w_down": (d, n), "b_gate": (n,), "b_up": (n,), "b_down": (d,)}
+        if grads is None:
+            if accumulate:
+                raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
+            want = {k: weight_grads if k[0] == "w" else bias_grads for k in shapes}
+            grads = {k: torch.empty(s, dtype=x.dtype, device=self.torch_device) for k, s in shapes.items()
+                     if want[k] and (gated or k[2:] != "gate")}
+        out = {k: grads.get(k) for k in shapes}
+        dx = torch.empty((T, d), dtype=x.dtype, device=self.torch_device) if need_dx else None
+        odd = self._args(x.dtype, dy=dy, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, g=g, u=u, a=a,
+                         **{k + "_": v for k, v in out.items()})
+        for k, v in out.items():
+            self._shape(k, v, *shapes[k]), self._packed(k, v)
+        types = {v.dtype for v in out.values() if v is not None}
+        if len(types) > 1:
+            raise PiError(PI_ERR_ARG, f"gradient buffers of several types: {types}")
+        if x.stride(0) != d and T > 1 and dx is not None:  # (x and dx share their stride)
+            dx = torch.empty((T, x.stride(0)), dtype=x.dtype, device=self.torch_device)[:, :d]
+        desc = self._ffn_desc(x, w_gate, w_up, w_down, g, u, a, dy, fn, self._code(types.pop() if types else x.dtype), odd)
+        self._s()
+        nb = pi_gated_ffn_workspace(self.handle, desc, True)
+        ws = pi_gated_ffn_weights(*map(_ptr, (w_gate, w_up, w_down)), None, None, None)
+        pi_gated_ffn_bwd(self.handle, desc, ws, x, dy, pi_gated_ffn_save(*map(_ptr, (g, u, a))), dx,
+                         pi_gated_ffn_grads(*(_ptr(out[k]) for k in shapes)), accumulate, self._ws(nb), nb)
+        return {"dx": dx, **out}
+
+    def _norm_desc(self, x, dtype, gate, pre, post, gate_rows, res_scale, branch_scale, eps, grad_code, lds):
+        T, d = x.shape
+        rows = 1 if gate_rows == 0 else -(-T // max(gate_rows, 1))
+        self._shape("gate", gate, rows, d)
+        return pi_norm_residual_desc(T, d, self._code(x.dtype), self._code(dtype), grad_code, pre, post, gate_rows,
+                                     res_scale, branch_scale, eps, *lds)
+
+    def norm_residual(self, x, y=None, gate=None, *, pre=PI_NORM_RMS, post=PI_NORM_NONE, w_pre=None, b_pre=None,
+                      w_post=None, b_post=None, res_scale=1.0, branch_scale=1.0, gate_rows=0, eps=1e-5, dtype=None,
+                      x_out=None, h=None):
+        """(x', h): x' = res_scale * x + branch_scale * gate * norm_post(y),
+        h = norm_pre(x') in y's type (`dtype` without a y).  gate [rows][d]:
+        token t uses row t // gate_rows, 0 = one row for all.  x_out may be x."""
+        import torch
+        dtype = y.dtype if y is not None else dtype or (x.dtype if x.dtype != torch.float32 else torch.bfloat16)
+        T, d = x.shape
+        if x_out is None:
+            x_out = torch.empty((T, d), dtype=x.dtype, device=self.torch_device)
+        if h is None and pre != PI_NORM_NONE:
+            h = torch.empty((T, d), dtype=dtype, device=self.torch_device)
+        self._args(dtype, x_=x, y=y, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post, b_post=b_post, x_out_=x_out, h=h)
+        if x_out.dtype != x.dtype:
+            raise PiError(PI_ERR_ARG, f"x_out is {x_out.dtype}, x {x.dtype}")
+        for name, t in (("y", y), ("x_out", x_out), ("h", h)):
+            self._shape(name, t, T, d)
+        for name, t in (("w_pre", w_pre), ("b_pre", b_pre), ("w_post", w_post), ("b_post", b_post)):
+            self._shape(name, t, d)
+        desc = self._norm_desc(x, dtype, gate, pre, post, gate_rows, res_scale, branch_scale, eps, self._code(dtype),
+                               (self._ld(x), self._ld(x_out), self._ld(y), self._ld(h), self._ld(gate)))
+        self._s()
+        pi_norm_residual(self.handle, desc, pi_norm_residual_params(*map(_ptr, (w_pre, b_pre, w_post, b_post))), x, y,
+                         gate, x_out, h)
+        return x_out, h
+
+    def norm_residual_bwd(self, dx_out, dh, x_out, y=None, gate=None, *, pre=PI_NORM_RMS, post=PI_NORM_NONE, w_pre=None,
+                          b_pre=None, w_post=None, b_post=None, res_scale=1.0, branch_scale=1.0, gate_rows=0, eps=1e-5,
+                          grads=None, accumulate=False):
+        """Gradients of ``norm_residual`` for the gradients dx_out of x' (None:
+        0) and dh of h, as a dict with keys dx, dy, gate, w_pre, b_pre,
+        w_post, b_post; a parameter that was not given has none.  grads:
+        buffers for gate and the parameters, packed, in h's type or float32
+        (all alike), used instead of new ones and added to with `accumulate`."""
+        import torch
+        dtype = next((t.dtype for t in (dh, y) if t is not None), None)
+        if dtype is None:
+            raise PiError(PI_ERR_ARG, "neither dh nor y given")
+        T, d = x_out.shape
+        given = {"gate": gate, "w_pre": w_pre, "b_pre": b_pre, "w_post": w_post, "b_post": b_post}
+        if grads is None:
+            if accumulate:
+                raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
+            grads = {k: torch.empty(v.shape, dtype=dtype, device=self.torch_device) for k, v in given.items()
+                     if v is not None}
+        out = {k: grads.get(k) for k in given}
+        dx = torch.empty((T, d), dtype=x_out.dtype, device=self.torch_device)
+        # (y and dy share their stride)
+        dy = None if y is None else torch.empty((T, max(d, self._ld(y))), dtype=dtype, device=self.torch_device)[:, :d]
+        self._args(dtype, dx_out_=dx_out, dh=dh, x_out_=x_out, y=y, **given, **{"d" + k + "_": v for k, v in out.items()})
+        for name, t in (("dx_out", dx_out), ("dh", dh), ("y", y)):
+            self._shape(name, t, T, d)
+        for k, v in out.items():
+            self._shape("gradient of " + k, v, *(given[k].shape if given[k] is not None else (d,)))
+            self._packed("gradient of " + k, v)
+            if k != "gate":
+                self._shape(k, given[k], d)
+        if dx_out is not None and dx_out.dtype != x_out.dtype:
+            raise PiError(PI_ERR_ARG, f"dx_out is {dx_out.dtype}, x_out {x_out.dtype}")
+        if dx_out is not None and self._ld(dx_out) != self._ld(x_out):
+            raise PiError(PI_ERR_ARG, "dx_out and x_out differ in their row stride")
+        types = {v.dtype for v in out.values() if v is not None}
+        if len(types) > 1:
+            raise PiError(PI_ERR_ARG, f"gradient buffers of several types: {types}")
+        desc = self._norm_desc(x_out, dtype, gate, pre, post, gate_rows, res_scale, branch_scale, eps,
+                               self._code(types.pop() if types else dtype),
+                               (0, self._ld(x_out), self._ld(y), self._ld(dh), self._ld(gate)))
+        self._s()
+        n = pi_norm_residual_bwd_workspace(self.handle, desc)
+        pi_norm_residual_bwd(self.handle, desc, pi_norm_residual_params(*map(_ptr, (w_pre, b_pre, w_post, b_post))),
+                             dx_out, dh, x_out, y, gate, pi_norm_residual_grads(_ptr(dx), _ptr(dy),
+                                                                               *(_ptr(out[k]) for k in given)),
+                             accumulate, self._ws(n), n)
+        return {"dx": dx, "dy": dy, **out}
 
     def set_trace(self, x_trace=None, xhat_trace=None, idx_trace=None, count_trace=None) -> None:
         pi_set_trace(self.handle, x_trace, xhat_trace, idx_trace, count_trace)

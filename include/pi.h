@@ -69,7 +69,8 @@ typedef int32_t pi_status;
  *   PI_SQRELU  a_i = max(W_up[i].x_hat + b_i, 0)^2
  * A neuron is active (its activation nonzero) exactly when its ReLU is. */
 typedef enum { PI_RELU = 0, PI_REGLU = 1, PI_SQRELU = 2 } pi_act;
-typedef enum { PI_F16 = 0, PI_BF16 = 1, PI_Q4_0 = 2 } pi_dtype;
+typedef enum { PI_F16 = 0, PI_BF16 = 1, PI_Q4_0 = 2, PI_F32 = 3 } pi_dtype;
+/* (PI_F32: the residual stream and gradients of the block operators below; no layer type) */
 
 /* Shape and types of one FFN layer and its predictor.
  *   d_model in [8, 8192], multiple of 8 (of 32 for Q4_0 weights)
@@ -385,6 +386,189 @@ pi_status pi_debug_set_mma_min_batch(pi_ctx *ctx, int32_t min_batch);
  * layer's rows could not be mapped for the tensor cores).  A decode step
  * takes the path of layer 0 for the whole stack. */
 pi_status pi_layerwise_min_batch(pi_ctx *ctx, int32_t layer, int32_t *min_batch);
+
+/* ---------------------------------------------------------------- block operators
+ * The FFN block outside the sparse decode path: long prompts, and training
+ * the models that the sparse path then serves (the pages' ReLU models are
+ * dense models trained further with ReLU; de.news.hada.io summary,
+ * "Einschränkungen und FAQ").  They take the weights in the model's own
+ * layout, from the caller's buffers, without a loaded layer.
+ *
+ * Common rules
+ *   - All pointers are device pointers; 16-bit data is `dtype` (PI_F16 or
+ *     PI_BF16).  Row strides (ld*) count elements; 0 means packed rows.
+ *     Rows may start anywhere and have any stride of at least their length;
+ *     buffers whose base and stride are multiples of 16 bytes are read in
+ *     place, others are first copied (by a kernel) into the workspace.
+ *   - T counts tokens and may be 0: forward calls then do nothing, backward
+ *     calls leave zero parameter gradients (or the old ones, accumulating).
+ *   - Outputs do not overlap inputs, except where a call says so.
+ *   - ws is device memory of at least the bytes that the call's
+ *     *_workspace function gives for the same desc, 16-byte aligned (NULL if
+ *     0 bytes).  With `unaligned` set in the desc those bytes have room for
+ *     copies of every operand, else only of those whose stride is not a
+ *     multiple of 16 bytes.  It holds nothing between calls; calls that may run at the
+ *     same time (two streams, two captured graphs) need their own.
+ *   - The calls launch kernels on the context's stream only and can be
+ *     captured into a CUDA graph.
+ *   - Products are accumulated in fp32; bias, activation, residual and
+ *     normalisation are computed in fp32 and rounded once.  What a backward
+ *     pass multiplies by a weight or an input (dz, dg, du) is first rounded
+ *     to `dtype`: a 16-bit tensor-core product takes both operands in it.
+ *   - Sums run in a fixed order: the same call on the same data gives the
+ *     same bits.
+ */
+typedef enum {
+    PI_FN_NONE = 0,     /* z */
+    PI_FN_RELU = 1,     /* max(z, 0); derivative 0 at 0 */
+    PI_FN_SQRELU = 2,   /* max(z, 0)^2 */
+    PI_FN_SIGMOID = 3,  /* 1 / (1 + exp(-z)) */
+    PI_FN_SILU = 4,     /* z sigmoid(z) */
+    PI_FN_GELU = 5,     /* z Phi(z), Phi the normal distribution function */
+    PI_FN_GELU_TANH = 6 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} pi_fn;
+
+/* A linear layer with bias, activation and residual:
+ *     z = x W^T + b,   y = r + scale * fn(z)
+ * x [T][K], W [N][K], b [N], z / r / y [T][N].  T in [0, 2^22], K and N in
+ * [1, 2^20]. */
+typedef struct {
+    int32_t T, K, N;
+    int32_t dtype;      /* of x, W, b, z, dx: PI_F16 or PI_BF16 */
+    int32_t out_dtype;  /* of y, r and dy: dtype or PI_F32 */
+    int32_t grad_dtype; /* of dw and db: dtype or PI_F32 */
+    int32_t fn;         /* pi_fn */
+    float scale;        /* finite */
+    int32_t unaligned;  /* 1: a buffer's base may not be a multiple of 16 bytes */
+    int64_t ldx, ldw, ldz, ldr, ldy; /* row strides; ldy also dy's */
+    int64_t lddx, lddw;
+} pi_linear_desc;
+
+/* *bytes = the workspace of pi_linear (backward = 0) or pi_linear_bwd (1). */
+pi_status pi_linear_workspace(pi_ctx *ctx, const pi_linear_desc *desc, int32_t backward, size_t *bytes);
+
+/* b, residual and z may be NULL; z, if given, receives x W^T + b rounded to
+ * dtype (what the backward pass needs unless fn is PI_FN_NONE).  y may be the
+ * residual itself (same type, same stride). */
+pi_status pi_linear(pi_ctx *ctx, const pi_linear_desc *desc, const void *x, const void *w, const void *b,
+                    const void *residual, void *z, void *y, void *ws, size_t ws_bytes);
+
+/* Gradients of pi_linear for the gradient dy of y (the residual's gradient is
+ * dy itself):
+ *     dz = scale * dy * fn'(z),  dx = dz W,  dw = dz^T x,  db = sum over tokens of dz
+ * Each of dx, dw, db may be NULL (not wanted); x is needed for dw, w for dx,
+ * z unless fn is PI_FN_NONE.  accumulate != 0: dw and db are added to what
+ * their buffers hold. */
+pi_status pi_linear_bwd(pi_ctx *ctx, const pi_linear_desc *desc, const void *dy, const void *x, const void *w,
+                        const void *z, void *dx, void *dw, void *db, int32_t accumulate, void *ws, size_t ws_bytes);
+
+/* A feed-forward block, gated or not:
+ *     gated:  g = x Wg^T + bg,  u = x Wu^T + bu,  a = fn(g) * u
+ *     else:   u = x Wu^T + bu,                    a = fn(u)
+ *     y = a Wd^T + bd
+ * x and y [T][d], Wg and Wu [n][d], Wd [d][n] (the model's layout), biases
+ * NULL = 0.  ReGLU, SwiGLU, GeGLU ... are gated with PI_FN_RELU, PI_FN_SILU,
+ * PI_FN_GELU.  T in [0, 2^22], d and n in [1, 2^20]. */
+typedef struct {
+    int32_t T, d, n;
+    int32_t dtype;      /* PI_F16 or PI_BF16 */
+    int32_t grad_dtype; /* of the parameter gradients: dtype or PI_F32 */
+    int32_t fn;         /* pi_fn */
+    int32_t gated;      /* 0 or 1 */
+    int32_t unaligned;  /* 1: a buffer's base may not be a multiple of 16 bytes */
+    int64_t ldx, ldy;             /* x and dx; y and dy */
+    int64_t ld_gate, ld_up, ld_down; /* weight rows */
+    int64_t ldg, ldu, lda;        /* rows of the saved g, u, a */
+} pi_gated_ffn_desc;
+
+typedef struct {
+    const void *w_gate, *w_up, *w_down; /* w_gate NULL if not gated */
+    const void *b_gate, *b_up, *b_down; /* NULL = 0 */
+} pi_gated_ffn_weights;
+
+/* g, u and a as the forward pass leaves them for the backward pass, [T][n]
+ * each in dtype (g NULL if not gated).  Forward: all may be NULL (nothing
+ * saved), or all wanted ones given. */
+typedef struct {
+    void *g, *u, *a;
+} pi_gated_ffn_save;
+
+/* Parameter gradients, packed, in grad_dtype; NULL = not wanted. */
+typedef struct {
+    void *w_gate, *w_up, *w_down;
+    void *b_gate, *b_up, *b_down;
+} pi_gated_ffn_grads;
+
+pi_status pi_gated_ffn_workspace(pi_ctx *ctx, const pi_gated_ffn_desc *desc, int32_t backward, size_t *bytes);
+
+/* save may be NULL. */
+pi_status pi_gated_ffn(pi_ctx *ctx, const pi_gated_ffn_desc *desc, const pi_gated_ffn_weights *w, const void *x,
+                       const pi_gated_ffn_save *save, void *y, void *ws, size_t ws_bytes);
+
+/* Gradients for the gradient dy of y:
+ *     da = dy Wd;  gated: dg = da * u * fn'(g), du = da * fn(g);  else du = da * fn'(u)
+ *     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T a,
+ *     dbg, dbu, dbd = the sums of dg, du, dy over the tokens
+ * dx and grads may be NULL.  save->a is needed for w_down's gradient only.
+ * accumulate != 0: parameter gradients are added to what the buffers hold. */
+pi_status pi_gated_ffn_bwd(pi_ctx *ctx, const pi_gated_ffn_desc *desc, const pi_gated_ffn_weights *w, const void *x,
+                           const void *dy, const pi_gated_ffn_save *save, void *dx, const pi_gated_ffn_grads *grads,
+                           int32_t accumulate, void *ws, size_t ws_bytes);
+
+/* The norms around a block, with its gate and residual scale:
+ *     v  = y, or norm_post(y)
+ *     x' = res_scale * x + branch_scale * gate * v
+ *     h  = norm_pre(x')                       (the next block's input)
+ *     RMS:    norm(v) = v / sqrt(mean(v^2) + eps) * w + b
+ *     LAYER:  norm(v) = (v - mean v) / sqrt(mean((v - mean v)^2) + eps) * w + b
+ * x, x' [T][d] in x_dtype (the residual stream), y, h [T][d] and every
+ * parameter in dtype; w NULL = 1, b NULL = 0.  h is computed from x' before
+ * its rounding to x_dtype.  gate NULL = 1, else [ceil(T / gate_rows)][d]:
+ * token t uses row t / gate_rows; gate_rows 0 = one row for every token.
+ * Without a block before it (y NULL; gate and post then unused) x' =
+ * res_scale * x and x_out may be NULL; with pre PI_NORM_NONE h must be NULL.
+ * T in [0, 2^22], d in [1, 16384]. */
+typedef enum { PI_NORM_NONE = 0, PI_NORM_RMS = 1, PI_NORM_LAYER = 2 } pi_norm;
+
+typedef struct {
+    int32_t T, d;
+    int32_t x_dtype;    /* dtype or PI_F32 */
+    int32_t dtype;      /* PI_F16 or PI_BF16 */
+    int32_t grad_dtype; /* of the parameter gradients and the gate's: dtype or PI_F32 */
+    int32_t pre, post;  /* pi_norm */
+    int32_t gate_rows;
+    float res_scale, branch_scale, eps; /* finite, eps >= 0 */
+    int64_t ldx, ldxo, ldy, ldh, ldgate; /* backward: ldx dx's, ldxo x_out's and dx_out's, ldy y's and dy's, ldh dh's */
+} pi_norm_residual_desc;
+
+typedef struct {
+    const void *w_pre, *b_pre, *w_post, *b_post;
+} pi_norm_residual_params;
+
+/* dx, dy: gradients of x (x_dtype) and y (dtype); the rest in grad_dtype,
+ * packed.  NULL = not wanted. */
+typedef struct {
+    void *dx, *dy, *dgate;
+    void *dw_pre, *db_pre, *dw_post, *db_post;
+} pi_norm_residual_grads;
+
+/* x_out may be x itself (same stride). */
+pi_status pi_norm_residual(pi_ctx *ctx, const pi_norm_residual_desc *desc, const pi_norm_residual_params *p,
+                           const void *x, const void *y, const void *gate, void *x_out, void *h);
+
+pi_status pi_norm_residual_bwd_workspace(pi_ctx *ctx, const pi_norm_residual_desc *desc, size_t *bytes);
+
+/* Gradients for the gradients dx_out of x' (NULL = 0) and dh of h; x_out is
+ * x' as the forward pass stored it (without a block before it, y NULL, it is
+ * res_scale * x), y and gate the forward pass's.  With D = dx_out + the
+ * gradient through norm_pre:
+ *     dx = res_scale * D,  dy = the gradient of branch_scale * gate * D through norm_post,
+ *     dgate = branch_scale * sum over the row's tokens of D * v
+ * accumulate != 0: the parameter gradients and dgate are added to what their
+ * buffers hold. */
+pi_status pi_norm_residual_bwd(pi_ctx *ctx, const pi_norm_residual_desc *desc, const pi_norm_residual_params *p,
+                               const void *dx_out, const void *dh, const void *x_out, const void *y, const void *gate,
+                               const pi_norm_residual_grads *grads, int32_t accumulate, void *ws, size_t ws_bytes);
 
 #ifdef __cplusplus
 }
