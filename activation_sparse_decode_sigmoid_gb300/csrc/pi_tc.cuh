@@ -37,7 +37,8 @@ __device__ __forceinline__ uint64_t gtimer()
     return t;
 }
 
-__device__ __forceinline__ void fail(const MmaParams &p, int code)
+// (P: any parameter block with status, abort_flag and wait_ns)
+template <typename P> __device__ __forceinline__ void fail(const P &p, int code)
 {
     atomicCAS(p.status, 0, code);
     atomicExch(p.abort_flag, 1);
@@ -66,7 +67,8 @@ __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity)
 // wait has to spin, the clock is read after every try_wait (each may suspend
 // the thread for a while, so the limit holds however short it is) and the
 // abort flag, an L2 read, after every 16th.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t *b, uint32_t parity, const MmaParams &p)
+template <typename P>
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t *b, uint32_t parity, const P &p)
 {
     if (mbar_try(b, parity)) return true;
     const uint64_t t0 = gtimer();
@@ -99,7 +101,8 @@ __device__ __forceinline__ bool mbar_drain(uint64_t *b, uint32_t parity, unsigne
 // whatever happened before): ignores the abort flag, so tensor memory is
 // never read or freed while an MMA runs; a timeout past the MMA lane's own
 // bounded waits is reported.
-__device__ __forceinline__ bool mbar_settle(uint64_t *b, uint32_t parity, const MmaParams &p)
+template <typename P>
+__device__ __forceinline__ bool mbar_settle(uint64_t *b, uint32_t parity, const P &p)
 {
     if (mbar_drain(b, parity, p.wait_ns + kDrainNs)) return true;
     fail(p, PI_DEV_TIMEOUT);
