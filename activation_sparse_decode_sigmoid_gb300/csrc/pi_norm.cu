@@ -22,6 +22,7 @@
 #include "pi_block.h"
 #include "pi_epi.cuh"
 #include "pi_kernels.h"
+#include "pi_tc.cuh"
 
 namespace pi {
 namespace {
@@ -53,7 +54,7 @@ struct NormP {
     int g32, acc;
 };
 
-enum : unsigned { NV_X = 1, NV_XO = 2, NV_Y = 4, NV_H = 8, NV_GATE = 16, NV_PAR = 32, NV_DX = 64, NV_DY = 128, NV_DXO = 256 };
+enum : unsigned { NV_X = 1, NV_XO = 2, NV_Y = 4, NV_H = 8, NV_GATE = 16, NV_PAR = 32, NV_DX = 64, NV_DY = 128, NV_DXO = 256, NV_DGATE = 512 };
 
 template <typename T> __device__ __forceinline__ void loadx8(const void *p, int x32, int64_t at, int n, bool vec, float (&v)[8])
 {
@@ -319,11 +320,11 @@ template <typename T> __global__ void __launch_bounds__(512) norm_bwd_rows(const
                     o[j] = p.bs * D[j] * fmaf(yh[j], p.w_post ? w[j] : 1.f, p.b_post ? b[j] : 0.f);
                 if (p.acc) {
                     float old[8];
-                    loadx8<T>(p.dgate, p.g32, at, n, false, old);
+                    loadx8<T>(p.dgate, p.g32, at, n, p.vec & NV_DGATE, old);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[j] += old[j];
                 }
-                storex8<T>(p.dgate, p.g32, at, n, false, o);
+                storex8<T>(p.dgate, p.g32, at, n, p.vec & NV_DGATE, o);
             }
             if (p.dy) {
                 float o[8];
@@ -434,19 +435,650 @@ template <typename T> __global__ void norm_bwd_sum(const __grid_constant__ NormP
     put<T>(p, p.db_post, c, db);
 }
 
+// ------------------------------------------------------------------ pipelined rows
+constexpr int kPipeThreads = 512, kPipeMaxD = 8192;
+
+struct PipeP {
+    int slots, slotB;                     // ring
+    int off_dxo, off_dh, off_y, off_gate; // regions of a slot (x at 0); off_gate -1: one gate row for many tokens
+    int off_hold;                         // after the ring: the current gate row
+    uint32_t row_bytes;                   // bytes of a row's copies in all
+    int *status, *abort_flag;
+    unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ void bulk(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// Starts the copies of token t's rows into slot s (one thread).
+__device__ __forceinline__ void issue_row(const NormP &p, const PipeP &q, uint8_t *ring, uint64_t *full, int s, int64_t t)
+{
+    const uint32_t dst = smem_addr(ring) + (uint32_t)(s * q.slotB), xB = (uint32_t)p.d * (p.x32 ? 4 : 2), hB = (uint32_t)p.d * 2;
+    const int xe = p.x32 ? 4 : 2;
+    uint64_t *b = full + s;
+    mbar_expect(b, q.row_bytes);
+    if (p.x) bulk(dst, (const uint8_t *)p.x + t * p.ldx * xe, xB, b);
+    if (p.dxo) bulk(dst + q.off_dxo, (const uint8_t *)p.dxo + t * p.ldxo * xe, xB, b);
+    if (p.dh) bulk(dst + q.off_dh, p.dh + t * p.ldh, hB, b);
+    if (p.y) bulk(dst + q.off_y, p.y + t * p.ldy, hB, b);
+    if (q.off_gate >= 0) bulk(dst + q.off_gate, p.gate + t * p.ldgate, hB, b);
+}
+
+template <typename T, bool X32> __device__ __forceinline__ void ring8x(const uint8_t *row, int c, float (&v)[8])
+{
+    if (X32) load8f(reinterpret_cast<const float *>(row) + c, 8, true, v);
+    else load8<T>(reinterpret_cast<const uint16_t *>(row) + c, 8, true, v);
+}
+
+// a parameter's 8 elements, packed; 1 or 0 where there is none
+template <typename T> __device__ __forceinline__ uint4 param8(const uint16_t *w, int c, int d, float none)
+{
+    if (w && c < d) return *reinterpret_cast<const uint4 *>(w + c);
+    const uint32_t v = C16<T>::round2(none, none);
+    return make_uint4(v, v, v, v);
+}
+
+template <typename T> __device__ __forceinline__ void ring8(const uint8_t *row, int c, float (&v)[8])
+{
+    unpack8<T>(*reinterpret_cast<const uint4 *>(row + 2 * c), v);
+}
+
+// The columns past the row, and rows that are not there, are zeros that no
+// copy ever overwrites: the kernels compute on whole chunks without a test.
+__device__ __forceinline__ void clear_ring(uint8_t *ring, int bytes)
+{
+    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) *reinterpret_cast<uint4 *>(ring + i) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // before the copies write there
+}
+
+// The gate row of the tokens to come (ones without a gate), each thread its own columns.
+template <typename T, int V> __device__ __forceinline__ void hold_gate(const NormP &p, uint8_t *hold, int group)
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        if (c < p.d)
+            *reinterpret_cast<uint4 *>(hold + 2 * c) = param8<T>(p.gate ? p.gate + (int64_t)group * p.ldgate : nullptr, c, p.d, 1.f);
+    }
+}
+
+__device__ __forceinline__ float warp_add(float a)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+}
+
+// sum over 16 lanes (both halves hold the same values)
+__device__ __forceinline__ float half_add(float a)
+{
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+}
+
+// Row statistics without a second pass over the CTA: each warp publishes the
+// sum s of its n elements and the squares m about its own mean; the whole
+// row's squares about its mean are sum (m_w + n_w (mean_w - mean)^2).
+struct WarpStat {
+    float s, m, n;
+};
+
+// mean and 1 / sqrt(... + eps) from this lane's warp's share (lanes l and l + 16 alike, 0 past the warps)
+__device__ __forceinline__ void join_stats(int kind, const WarpStat &w, int d, float eps, float &mean, float &r)
+{
+    mean = 0.f;
+    float m = w.m;
+    if (kind == PI_NORM_LAYER) {
+        mean = half_add(w.s) / (float)d;
+        const float e = w.n > 0.f ? w.s / w.n - mean : 0.f;
+        m = fmaf(w.n * e, e, m);
+    }
+    r = 1.f / sqrtf(half_add(m) / (float)d + eps);
+}
+
+__device__ __forceinline__ int row_of(int64_t Tn, int c, int G) { return (int)(Tn * c / G); }
+
+// the CTA of G whose range holds token t
+__device__ __forceinline__ int cta_of(const NormP &p, int64_t t, int G) { return (int)(((t + 1) * G + p.Tn - 1) / p.Tn - 1); }
+
+// Elements of this warp within the row (its chunks start every blockDim * 8 columns).
+template <int V> __device__ __forceinline__ float warp_elems(int d)
+{
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) n += max(0, min(256, d - (int)((threadIdx.x >> 5) * 256 + i * blockDim.x * 8)));
+    return (float)n;
+}
+
+// End of a pipelined kernel that gave up: copies in flight land before it leaves.
+__device__ __forceinline__ void pipe_settle()
+{
+    const uint64_t t0 = gtimer();
+    while (gtimer() - t0 < 5000000ull) {
+    }
+}
+
+template <typename T, bool X32, int V>
+__global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[8];
+    __shared__ WarpStat red[2][2][16];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5, S = q.slots, d = p.d;
+    const int r0 = row_of(p.Tn, blockIdx.x, gridDim.x), r1 = row_of(p.Tn, blockIdx.x + 1, gridDim.x);
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) mbar_init1(full + s);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    uint8_t *hold = ring + q.off_hold;
+    clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
+    __syncthreads();
+    pdl_enter();
+    int issued = r0;
+    if (tid == 0)
+        for (; issued < min(r1, r0 + S); ++issued) issue_row(p, q, ring, full, issued - r0, issued);
+    uint4 wp[V], bp[V], wq[V], bq[V];
+    int c[V];
+    bool on[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        c[i] = (tid + i * blockDim.x) * 8;
+        on[i] = c[i] < d;
+        wp[i] = param8<T>(p.w_pre, c[i], d, 1.f), bp[i] = param8<T>(p.b_pre, c[i], d, 0.f);
+        wq[i] = param8<T>(p.w_post, c[i], d, 1.f), bq[i] = param8<T>(p.b_post, c[i], d, 0.f);
+    }
+    const bool post = p.y && p.post != PI_NORM_NONE;
+    const float nel = warp_elems<V>(d);
+    int group = -1, slot = 0, flip = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    for (int t = r0; t < r1; ++t) {
+        ok = mbar_wait_bounded(full + slot, par, q);
+        if (!__syncthreads_and(ok)) break; // also: every thread is done with the previous row's slot
+        if (tid == 0 && t > r0 && issued < r1) issue_row(p, q, ring, full, slot ? slot - 1 : S - 1, issued), ++issued;
+        const uint8_t *row = ring + slot * q.slotB, *gate = q.off_gate >= 0 ? row + q.off_gate : hold;
+        if (q.off_gate < 0 && t / p.gate_rows != group) {
+            group = t / p.gate_rows;
+            hold_gate<T, V>(p, hold, group);
+        }
+        float x[V][8], y[V][8];
+#pragma unroll
+        for (int i = 0; i < V; ++i) ring8<T>(row + q.off_y, c[i], y[i]);
+        if (post) {
+            WarpStat w = {0.f, 0.f, nel};
+            float mean = 0.f, r;
+            if (p.post == PI_NORM_LAYER) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w.s += y[i][j];
+                w.s = warp_add(w.s);
+                mean = nel > 0.f ? w.s / nel : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float m = on[i] ? mean : 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w.m = fmaf(y[i][j] - m, y[i][j] - m, w.m);
+            }
+            w.m = warp_add(w.m);
+            if (lane == 0) red[0][flip][warp] = w;
+            __syncthreads();
+            WarpStat z = {0.f, 0.f, 0.f};
+            if ((lane & 15) < nw) z = red[0][flip][lane & 15];
+            join_stats(p.post, z, d, p.eps, mean, r);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float w8[8], b8[8];
+                unpack8<T>(wq[i], w8), unpack8<T>(bq[i], b8);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[i][j] = fmaf((y[i][j] - mean) * r, w8[j], b8[j]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float g[8];
+            ring8x<T, X32>(row, c[i], x[i]);
+            ring8<T>(gate, c[i], g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i][j] = fmaf(p.bs * g[j], y[i][j], p.rs * x[i][j]);
+            if (p.xo && on[i]) storex8<T>(p.xo, X32, (int64_t)t * p.ldxo + c[i], 8, true, x[i]);
+        }
+        if (p.h) {
+            WarpStat w = {0.f, 0.f, nel};
+            float mean = 0.f, r;
+            if (p.pre == PI_NORM_LAYER) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) w.s += x[i][j];
+                w.s = warp_add(w.s);
+                mean = nel > 0.f ? w.s / nel : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float m = on[i] ? mean : 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w.m = fmaf(x[i][j] - m, x[i][j] - m, w.m);
+            }
+            w.m = warp_add(w.m);
+            if (lane == 0) red[1][flip][warp] = w;
+            __syncthreads();
+            WarpStat z = {0.f, 0.f, 0.f};
+            if ((lane & 15) < nw) z = red[1][flip][lane & 15];
+            join_stats(p.pre, z, d, p.eps, mean, r);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float w8[8], b8[8];
+                unpack8<T>(wp[i], w8), unpack8<T>(bp[i], b8);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[i][j] = fmaf((x[i][j] - mean) * r, w8[j], b8[j]);
+                if (on[i]) store8<T>(p.h + (int64_t)t * p.ldh + c[i], 8, true, x[i]);
+            }
+        }
+        flip ^= 1;
+        if (++slot == S) slot = 0, par ^= 1u;
+    }
+    if (!ok || *(volatile int *)q.abort_flag) pipe_settle();
+}
+
+// What a warp publishes of a row in the backward pass.
+struct BwdStat {
+    float sx, mx, sq, sqx, sy, my;
+};
+
+// FULL: layer norms, and the plain sums P0 and S0 (biases); else RMS norms
+// without them.  Per row two barriers: each warp publishes its share of the
+// statistics about its own mean, then of the sums for y's gradient.
+template <typename T, bool X32, int V, bool FULL>
+__global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[8];
+    __shared__ BwdStat red[2][16];
+    __shared__ float2 red2[2][16];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5, S = q.slots, d = p.d;
+    const int r0 = row_of(p.Tn, blockIdx.x, gridDim.x), r1 = row_of(p.Tn, blockIdx.x + 1, gridDim.x);
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) mbar_init1(full + s);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    uint8_t *hold = ring + q.off_hold;
+    clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
+    __syncthreads();
+    pdl_enter();
+    int issued = r0;
+    if (tid == 0)
+        for (; issued < min(r1, r0 + S); ++issued) issue_row(p, q, ring, full, issued - r0, issued);
+    const bool row_gate = q.off_gate >= 0, pre = p.dh != nullptr, post = p.y && p.post != PI_NORM_NONE;
+    const bool lpre = FULL && p.pre == PI_NORM_LAYER, lpost = FULL && p.post == PI_NORM_LAYER;
+    uint4 wp[V], wq[V];
+    int c[V];
+    bool on[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        c[i] = (tid + i * blockDim.x) * 8;
+        on[i] = c[i] < d;
+        wp[i] = param8<T>(p.w_pre, c[i], d, 1.f), wq[i] = param8<T>(p.w_post, c[i], d, 1.f);
+    }
+    float P1[V][8] = {}, P0[V][8] = {}, S1[V][8] = {}, S0[V][8] = {};
+    const float nel = warp_elems<V>(d), inv_d = 1.f / (float)d;
+    // elements of warp (lane mod 16), whose share this lane joins
+    float nz = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) nz += (float)max(0, min(256, d - (int)((lane & 15) * 256 + i * blockDim.x * 8)));
+    if ((lane & 15) >= nw) nz = 0.f;
+    const float inv_nz = nz > 0.f ? 1.f / nz : 0.f;
+    int group = -1, slot = 0, flip = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    // S1 and S0 of the rows of one gate row so far -> their partial slot
+    auto flush = [&]() {
+        float *o = p.part + (2 * (int64_t)gridDim.x + 2 * ((int64_t)blockIdx.x + (p.per_token ? 0 : group))) * d;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (on[i]) store8f(o + c[i], 8, true, S1[i]);
+            if (FULL && on[i]) store8f(o + d + c[i], 8, true, S0[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) S1[i][j] = S0[i][j] = 0.f;
+        }
+    };
+    for (int t = r0; t < r1; ++t) {
+        ok = mbar_wait_bounded(full + slot, par, q);
+        if (!__syncthreads_and(ok)) break; // also: every thread is done with the previous row's slot
+        if (tid == 0 && t > r0 && issued < r1) issue_row(p, q, ring, full, slot ? slot - 1 : S - 1, issued), ++issued;
+        const uint8_t *row = ring + slot * q.slotB, *gate = row_gate ? row + q.off_gate : hold;
+        if (!row_gate && t / p.gate_rows != group) {
+            if (group >= 0 && p.part) flush();
+            group = t / p.gate_rows;
+            hold_gate<T, V>(p, hold, group);
+        }
+        // statistics of x' and y, and the sums of dh w and dh w xh, about the warp's means
+        BwdStat st = {};
+        float wmx = 0.f, wmy = 0.f;
+        if (FULL) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float v[8], u[8];
+                ring8x<T, X32>(row, c[i], v);
+                ring8<T>(row + q.off_y, c[i], u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) st.sx += v[j], st.sy += u[j];
+            }
+            st.sx = warp_add(st.sx), st.sy = warp_add(st.sy);
+            if (lpre && nel > 0.f) wmx = st.sx / nel;
+            if (lpost && nel > 0.f) wmy = st.sy / nel;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float v[8], h[8], u[8], w[8];
+            ring8x<T, X32>(row, c[i], v);
+            ring8<T>(row + q.off_dh, c[i], h);
+            ring8<T>(row + q.off_y, c[i], u);
+            unpack8<T>(wp[i], w);
+            const float mx = on[i] ? wmx : 0.f, my = on[i] ? wmy : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e = FULL ? v[j] - mx : v[j], f = FULL ? u[j] - my : u[j], k = h[j] * w[j];
+                st.mx = fmaf(e, e, st.mx);
+                if (FULL) st.sq += k;
+                st.sqx = fmaf(k, e, st.sqx);
+                st.my = fmaf(f, f, st.my);
+            }
+        }
+        st.mx = warp_add(st.mx), st.sqx = warp_add(st.sqx), st.my = warp_add(st.my);
+        if (FULL) st.sq = warp_add(st.sq);
+        if (lane == 0) red[flip][warp] = st;
+        __syncthreads();
+        float mx = 0.f, rx, c1 = 0.f, c2, my = 0.f, ry;
+        {
+            BwdStat z = {};
+            if ((lane & 15) < nw) z = red[flip][lane & 15];
+            if (lpre) {
+                mx = half_add(z.sx) * inv_d, c1 = half_add(z.sq) * inv_d;
+                const float e = z.sx * inv_nz - mx;
+                z.mx = fmaf(nz * e, e, z.mx), z.sqx = fmaf(e, z.sq, z.sqx);
+            }
+            if (lpost) {
+                my = half_add(z.sy) * inv_d;
+                const float e = z.sy * inv_nz - my;
+                z.my = fmaf(nz * e, e, z.my);
+            }
+            rx = pre ? 1.f / sqrtf(half_add(z.mx) * inv_d + p.eps) : 0.f;
+            ry = post ? 1.f / sqrtf(half_add(z.my) * inv_d + p.eps) : 1.f;
+            c2 = half_add(z.sqx) * rx * inv_d;
+        }
+        // D, dx, the column sums, and the sums for y's gradient
+        float D[V][8];
+        float s1 = 0.f, s2 = 0.f;
+        const float k0 = -rx * c1, kx = -rx * c2;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float v[8], h[8], w[8];
+            ring8x<T, X32>(row + q.off_dxo, c[i], D[i]);
+            ring8x<T, X32>(row, c[i], v);
+            ring8<T>(row + q.off_dh, c[i], h);
+            unpack8<T>(wp[i], w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float xh = FULL ? (v[j] - mx) * rx : v[j] * rx;
+                float e = fmaf(rx * h[j], w[j], D[i][j]);
+                if (FULL) e += k0;
+                D[i][j] = fmaf(kx, xh, e);
+                P1[i][j] = fmaf(h[j], xh, P1[i][j]);
+                if (FULL) P0[i][j] += h[j];
+                v[j] = p.rs * D[i][j];
+            }
+            if (p.dx && on[i]) storex8<T>(p.dx, X32, (int64_t)t * p.lddx + c[i], 8, true, v);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float y[8], w[8], g[8];
+            ring8<T>(row + q.off_y, c[i], y);
+            ring8<T>(gate, c[i], g);
+            unpack8<T>(wq[i], w);
+            if (row_gate && p.dgate && on[i]) {
+                float b[8], o[8];
+                unpack8<T>(param8<T>(p.b_post, c[i], d, 0.f), b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = p.bs * D[i][j] * fmaf((y[j] - my) * ry, w[j], b[j]);
+                const int64_t at = (int64_t)t * d + c[i];
+                if (p.acc) {
+                    float old[8];
+                    loadx8<T>(p.dgate, p.g32, at, 8, true, old);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] += old[j];
+                }
+                storex8<T>(p.dgate, p.g32, at, 8, true, o);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float yh = FULL ? (y[j] - my) * ry : y[j] * ry;
+                const float k = row_gate ? g[j] * D[i][j] : D[i][j]; // (what S1 and S0 sum)
+                D[i][j] *= p.bs * g[j];                            // dv from here on
+                const float e = D[i][j] * w[j];
+                if (FULL) s1 += e;
+                s2 = fmaf(e, yh, s2);
+                S1[i][j] = fmaf(k, yh, S1[i][j]);
+                if (FULL) S0[i][j] += k;
+            }
+        }
+        if (p.dy) {
+            float k1 = 0.f, k2 = 0.f;
+            if (post) {
+                s2 = warp_add(s2);
+                if (FULL) s1 = warp_add(s1);
+                if (lane == 0) red2[flip][warp] = make_float2(s1, s2);
+                __syncthreads();
+                float2 z = make_float2(0.f, 0.f);
+                if ((lane & 15) < nw) z = red2[flip][lane & 15];
+                if (lpost) k1 = half_add(z.x) * inv_d;
+                k2 = half_add(z.y) * inv_d;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float y[8], w[8];
+                ring8<T>(row + q.off_y, c[i], y);
+                unpack8<T>(wq[i], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float yh = FULL ? (y[j] - my) * ry : y[j] * ry;
+                    float e = D[i][j] * w[j];
+                    if (FULL) e -= k1;
+                    y[j] = ry * fmaf(-k2, yh, e);
+                }
+                if (on[i]) store8<T>(p.dy + (int64_t)t * p.ldy + c[i], 8, true, y);
+            }
+        }
+        flip ^= 1;
+        if (++slot == S) slot = 0, par ^= 1u;
+    }
+    if (!ok || *(volatile int *)q.abort_flag) {
+        pipe_settle();
+        return;
+    }
+    if (!p.part) return;
+    flush();
+    float *o = p.part + 2 * (int64_t)blockIdx.x * d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (on[i]) store8f(o + c[i], 8, true, P1[i]);
+        if (FULL && on[i]) store8f(o + d + c[i], 8, true, P0[i]);
+    }
+}
+
+// The CTAs' partials in order: 32 columns a CTA, 8 lanes that share the parts.
+// Tokens of gate row g lie in CTAs c0 .. c1 of the row kernel; partial slot c + g.
+template <typename T> __global__ void __launch_bounds__(256) norm_bwd_join(const __grid_constant__ NormP p, int G, int groups, int sums)
+{
+    __shared__ float red[8][6][32];
+    pdl_enter();
+    const int l = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + l, d = p.d;
+    const bool in = c < d;
+    const float w = in && p.w_post ? C16<T>::one(p.w_post[c]) : 1.f, b = in && p.b_post ? C16<T>::one(p.b_post[c]) : 0.f;
+    const float *S = p.part + (int64_t)G * 2 * d;
+    float v[6] = {}; // P1, P0, gate S1, gate S0, S1, S0
+    if (in)
+        for (int i = k; i < G; i += 8) {
+            v[0] += p.part[(int64_t)i * 2 * d + c];
+            if (sums) v[1] += p.part[((int64_t)i * 2 + 1) * d + c];
+            if (!p.y) continue;
+            const int r0 = row_of(p.Tn, i, G), r1 = row_of(p.Tn, i + 1, G);
+            const int g0 = p.per_token ? 0 : r0 / p.gate_rows, g1 = p.per_token ? 0 : (r1 - 1) / p.gate_rows;
+            for (int g = g0; g <= g1; ++g) {
+                const float gate = p.gate && !p.per_token ? C16<T>::one(p.gate[(int64_t)g * p.ldgate + c]) : 1.f;
+                const float a = S[(int64_t)(i + g) * 2 * d + c], z = sums ? S[((int64_t)(i + g) * 2 + 1) * d + c] : 0.f;
+                v[2] = fmaf(gate, a, v[2]);
+                v[3] = fmaf(gate, z, v[3]);
+                v[4] += a;
+                v[5] += z;
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) red[k][i][l] = v[i];
+    __syncthreads();
+    if (in && k == 0) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            for (int j = 1; j < 8; ++j) v[i] += red[j][i][l];
+        put<T>(p, p.dw_pre, c, v[0]);
+        put<T>(p, p.db_pre, c, v[1]);
+        put<T>(p, p.dw_post, c, p.bs * v[2]);
+        put<T>(p, p.db_post, c, p.bs * v[3]);
+        if (p.dgate && groups == 1 && !p.per_token) put<T>(p, p.dgate, c, p.bs * fmaf(w, v[4], b * v[5]));
+    }
+    if (!p.dgate || p.per_token || groups == 1) return;
+    // few, long gate rows: the lanes share a row's parts; many short ones: a lane each
+    if (groups < 32) {
+        for (int g = 0; g < groups; ++g) {
+            const int c0 = cta_of(p, g * (int64_t)p.gate_rows, G), c1 = cta_of(p, min((int64_t)p.Tn, (g + 1) * (int64_t)p.gate_rows) - 1, G);
+            float a = 0.f, z = 0.f;
+            if (in)
+                for (int i = c0 + k; i <= c1; i += 8) {
+                    a += S[(int64_t)(i + g) * 2 * d + c];
+                    if (sums) z += S[((int64_t)(i + g) * 2 + 1) * d + c];
+                }
+            __syncthreads();
+            red[k][0][l] = a, red[k][1][l] = z;
+            __syncthreads();
+            if (in && k == 0) {
+                for (int j = 1; j < 8; ++j) a += red[j][0][l], z += red[j][1][l];
+                put<T>(p, p.dgate, (int64_t)g * d + c, p.bs * fmaf(w, a, b * z));
+            }
+        }
+        return;
+    }
+    if (!in) return;
+    for (int g = k; g < groups; g += 8) {
+        const int c0 = cta_of(p, g * (int64_t)p.gate_rows, G), c1 = cta_of(p, min((int64_t)p.Tn, (g + 1) * (int64_t)p.gate_rows) - 1, G);
+        float a = 0.f, z = 0.f;
+        for (int i = c0; i <= c1; ++i) {
+            a += S[(int64_t)(i + g) * 2 * d + c];
+            if (sums) z += S[((int64_t)(i + g) * 2 + 1) * d + c];
+        }
+        put<T>(p, p.dgate, (int64_t)g * d + c, p.bs * fmaf(w, a, b * z));
+    }
+}
+
 template <typename T, int V> cudaError_t launch_fwd(const NormP &p, cudaStream_t s)
 {
     const int nt = ((p.d + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
     return launch_pdl(norm_fwd<T, V>, dim3(p.Tn), dim3(nt), 0, s, p);
 }
 
-template <typename T> cudaError_t fwd(const NormP &p, cudaStream_t s)
+// The ring of a pipelined launch: rows of up to kPipeMaxD elements, all 16-byte
+// aligned; false if they are not.  CTAs per SM: as many as 512 threads and
+// about 200 KB of ring allow, with two to four slots each.
+struct Pipe {
+    PipeP q;
+    int threads, v, grid, smem;
+};
+
+bool plan_pipe(const NormP &p, bool backward, bool row_gate, const CtxView &c, Pipe &o)
 {
-    return p.d <= 8192 ? launch_fwd<T, 1>(p, s) : launch_fwd<T, 2>(p, s);
+    if (p.d % 8 || p.d > kPipeMaxD) return false;
+    const unsigned need = NV_PAR | (p.x ? NV_X : 0) | (p.y ? NV_Y : 0) | (p.gate ? NV_GATE : 0) |
+                          (backward ? (p.dxo ? NV_DXO : 0) | (p.dh ? NV_H : 0) | (p.dx ? NV_DX : 0) | (p.dy ? NV_DY : 0) |
+                                          (p.dgate ? NV_DGATE : 0)
+                                    : (p.xo ? NV_XO : 0) | (p.h ? NV_H : 0));
+    if ((p.vec & need) != need) return false;
+    o.v = p.d > 4096 ? 2 : 1;
+    o.threads = (p.d / 8 + 32 * o.v - 1) / (32 * o.v) * 32;
+    // regions of whole chunks: a row's own bytes, then zeros
+    const int wide = o.threads * 8 * o.v, xB = wide * (p.x32 ? 4 : 2), hB = wide * 2, xe = p.x32 ? 4 : 2;
+    PipeP &q = o.q;
+    int at = xB;
+    auto take = [&](int bytes) { const int r = at; at += bytes; return r; };
+    q.off_dxo = backward ? take(xB) : 0;
+    q.off_dh = backward ? take(hB) : 0;
+    q.off_y = take(hB);
+    q.off_gate = row_gate ? take(hB) : -1;
+    q.slotB = at;
+    q.row_bytes = (uint32_t)p.d * ((p.x ? xe : 0) + (backward && p.dxo ? xe : 0) + (backward && p.dh ? 2 : 0) + (p.y ? 2 : 0) +
+                                   (row_gate ? 2 : 0));
+    const int budget = c.smem_optin - 2048 - hB;
+    int per_sm = std::min(8, kPipeThreads / o.threads);
+    while (per_sm > 1 && per_sm * (2 * q.slotB + hB + 4096) > budget) --per_sm;
+    q.slots = std::min(4, (budget / per_sm - (per_sm > 1 ? hB + 4096 : 0)) / q.slotB);
+    if (q.slots < 2) return false;
+    q.off_hold = q.slots * q.slotB;
+    o.smem = q.off_hold + hB;
+    o.grid = std::min(p.Tn, c.sms * per_sm);
+    q.status = c.status, q.abort_flag = c.abort_flag, q.wait_ns = c.wait_ns;
+    return true;
 }
 
-template <typename T> cudaError_t bwd(const NormP &p, bool cols, cudaStream_t s)
+template <typename K> cudaError_t run_pipe(K kern, const NormP &p, const Pipe &o, cudaStream_t s)
 {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, o.smem);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(o.grid), dim3(o.threads), o.smem, s, p, o.q);
+}
+
+// Tokens from which the pipelined forward kernel runs: below two per SM
+// nothing is left to overlap, and one CTA per token with the whole row in
+// flight at once answers sooner.
+constexpr int kPipeRows = 2;
+
+template <typename T> cudaError_t fwd(const NormP &p, const CtxView &c)
+{
+    Pipe o;
+    const bool row_gate = p.gate && p.gate_rows == 1;
+    if (p.Tn >= kPipeRows * c.sms && plan_pipe(p, false, row_gate, c, o)) {
+        if (p.x32)
+            return o.v == 1 ? run_pipe(norm_fwd_pipe<T, true, 1>, p, o, c.stream)
+                            : run_pipe(norm_fwd_pipe<T, true, 2>, p, o, c.stream);
+        return o.v == 1 ? run_pipe(norm_fwd_pipe<T, false, 1>, p, o, c.stream)
+                        : run_pipe(norm_fwd_pipe<T, false, 2>, p, o, c.stream);
+    }
+    return p.d <= 8192 ? launch_fwd<T, 1>(p, c.stream) : launch_fwd<T, 2>(p, c.stream);
+}
+
+template <typename T, bool FULL> cudaError_t bwd_pipe(const NormP &p, const Pipe &o, cudaStream_t s)
+{
+    if (p.x32)
+        return o.v == 1 ? run_pipe(norm_bwd_pipe<T, true, 1, FULL>, p, o, s)
+                        : run_pipe(norm_bwd_pipe<T, true, 2, FULL>, p, o, s);
+    return o.v == 1 ? run_pipe(norm_bwd_pipe<T, false, 1, FULL>, p, o, s)
+                    : run_pipe(norm_bwd_pipe<T, false, 2, FULL>, p, o, s);
+}
+
+template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &c)
+{
+    Pipe o;
+    const cudaStream_t s = c.stream;
+    if (plan_pipe(p, true, p.per_token != 0, c, o)) {
+        const bool sums = p.db_pre || p.db_post || (p.dgate && p.b_post);
+        const bool full = sums || p.pre == PI_NORM_LAYER || p.post == PI_NORM_LAYER;
+        const cudaError_t e = full ? bwd_pipe<T, true>(p, o, s) : bwd_pipe<T, false>(p, o, s);
+        if (e != cudaSuccess || !cols) return e;
+        const int groups = p.per_token ? 1 : (int)((p.Tn + (int64_t)p.gate_rows - 1) / p.gate_rows);
+        return launch_pdl(norm_bwd_join<T>, dim3((p.d + 31) / 32), dim3(256), 0, s, p, o.grid, groups, (int)full);
+    }
     const int nt = std::min(512, ((p.d + 7) / 8 + 31) / 32 * 32);
     cudaError_t e = launch_pdl(norm_bwd_rows<T>, dim3(p.Tn), dim3(nt), 0, s, p);
     if (e != cudaSuccess || !cols) return e;
@@ -512,7 +1144,7 @@ struct Units {
     size_t stats, part;
 };
 
-Units plan_units(const pi_norm_residual_desc &d, bool gate)
+Units plan_units(const pi_norm_residual_desc &d, bool gate, int sms)
 {
     Units u;
     const int gr = gate && d.gate_rows ? d.gate_rows : std::max(1, d.T);
@@ -523,6 +1155,9 @@ Units plan_units(const pi_norm_residual_desc &d, bool gate)
     u.units = (int)(groups * u.per_group);
     u.stats = ((size_t)d.T * 8 * 4 + 255) / 256 * 256;
     u.part = (size_t)u.units * 4 * d.d * 4;
+    // the pipelined kernel: [CTAs][2][d], then [CTAs + gate rows][2][d]
+    const size_t ctas = std::min<size_t>(d.T, (size_t)8 * sms);
+    u.part = std::max(u.part, (2 * ctas + (size_t)groups) * 2 * d.d * 4);
     return u;
 }
 
@@ -557,7 +1192,7 @@ pi_status pi_norm_residual(pi_ctx *c, const pi_norm_residual_desc *desc, const p
     p.vec |= vb(x, p.ldx, xe, NV_X) | vb(x_out, p.ldxo, xe, NV_XO) | vb(y, p.ldy, 2, NV_Y) | vb(h, p.ldh, 2, NV_H) |
              vb(gate, p.ldgate, 2, NV_GATE);
     DeviceGuard g(v.device);
-    CUN(d.dtype == PI_BF16 ? fwd<__nv_bfloat16>(p, v.stream) : fwd<__half>(p, v.stream));
+    CUN(d.dtype == PI_BF16 ? fwd<__nv_bfloat16>(p, v) : fwd<__half>(p, v));
     return PI_OK;
 }
 
@@ -567,7 +1202,8 @@ pi_status pi_norm_residual_bwd_workspace(pi_ctx *c, const pi_norm_residual_desc 
     if (!bytes) return ctx_fail(c, PI_ERR_ARG, "bytes is NULL");
     pi_norm_residual_desc d;
     if (pi_status st = check(c, desc, d)) return st;
-    const Units a = plan_units(d, true), b = plan_units(d, false);
+    const int sms = ctx_view(c).sms;
+    const Units a = plan_units(d, true, sms), b = plan_units(d, false, sms);
     *bytes = d.T ? a.stats + std::max(a.part, b.part) : 0;
     return PI_OK;
 }
@@ -604,7 +1240,7 @@ pi_status pi_norm_residual_bwd(pi_ctx *c, const pi_norm_residual_desc *desc, con
     p.dxo = dx_out, p.dh = (const uint16_t *)dh, p.dx = gr->dx, p.dy = (uint16_t *)gr->dy;
     p.dgate = gr->dgate, p.dw_pre = gr->dw_pre, p.db_pre = gr->db_pre, p.dw_post = gr->dw_post, p.db_post = gr->db_post;
     p.g32 = d.grad_dtype == PI_F32, p.acc = accumulate != 0;
-    const Units u = plan_units(d, p.gate != nullptr);
+    const Units u = plan_units(d, p.gate != nullptr, v.sms);
     p.units = u.units, p.per_group = u.per_group, p.per_token = u.per_token;
     if (!p.gate) p.gate_rows = d.T;
     if (want) {
@@ -616,11 +1252,13 @@ pi_status pi_norm_residual_bwd(pi_ctx *c, const pi_norm_residual_desc *desc, con
         p.part = (float *)((uint8_t *)ws + u.stats);
     }
     p.lddx = d.ldx, p.ldx = d.ldxo;
+    if (p.pre == PI_NORM_NONE) p.x = nullptr; // (not needed)
     const int xe = p.x32 ? 4 : 2;
     p.vec |= vb(x_out, p.ldx, xe, NV_X) | vb(y, p.ldy, 2, NV_Y) | vb(dh, p.ldh, 2, NV_H) | vb(gate, p.ldgate, 2, NV_GATE) |
-             vb(gr->dx, p.lddx, xe, NV_DX) | vb(gr->dy, p.ldy, 2, NV_DY) | vb(dx_out, p.ldxo, xe, NV_DXO);
+             vb(gr->dx, p.lddx, xe, NV_DX) | vb(gr->dy, p.ldy, 2, NV_DY) | vb(dx_out, p.ldxo, xe, NV_DXO) |
+             vb(gr->dgate, d.d, p.g32 ? 4 : 2, NV_DGATE);
     DeviceGuard g(v.device);
-    CUN(d.dtype == PI_BF16 ? bwd<__nv_bfloat16>(p, want, v.stream) : bwd<__half>(p, want, v.stream));
+    CUN(d.dtype == PI_BF16 ? bwd<__nv_bfloat16>(p, want, v) : bwd<__half>(p, want, v));
     return PI_OK;
 }
 
