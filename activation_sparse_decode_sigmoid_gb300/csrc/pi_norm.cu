@@ -437,6 +437,7 @@ template <typename T> __global__ void norm_bwd_sum(const __grid_constant__ NormP
 
 // ------------------------------------------------------------------ pipelined rows
 constexpr int kPipeThreads = 512, kPipeMaxD = 8192;
+constexpr int kBwdThreads = 256; // backward: more columns a thread instead (see norm_bwd_pipe)
 
 struct PipeP {
     int slots, slotB;                     // ring
@@ -696,7 +697,7 @@ struct BwdStat {
 // without them.  Per row two barriers: each warp publishes its share of the
 // statistics about its own mean, then of the sums for y's gradient.
 template <typename T, bool X32, int V, bool FULL>
-__global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
+__global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[8];
@@ -1007,7 +1008,9 @@ bool plan_pipe(const NormP &p, bool backward, bool row_gate, const CtxView &c, P
                                           (p.dgate ? NV_DGATE : 0)
                                     : (p.xo ? NV_XO : 0) | (p.h ? NV_H : 0));
     if ((p.vec & need) != need) return false;
-    o.v = p.d > 4096 ? 2 : 1;
+    const int most = backward ? kBwdThreads : kPipeThreads;
+    o.v = 1;
+    while (o.v * 8 * most < p.d) o.v *= 2;
     o.threads = (p.d / 8 + 32 * o.v - 1) / (32 * o.v) * 32;
     // regions of whole chunks: a row's own bytes, then zeros
     const int wide = o.threads * 8 * o.v, xB = wide * (p.x32 ? 4 : 2), hB = wide * 2, xe = p.x32 ? 4 : 2;
@@ -1022,7 +1025,7 @@ bool plan_pipe(const NormP &p, bool backward, bool row_gate, const CtxView &c, P
     q.row_bytes = (uint32_t)p.d * ((p.x ? xe : 0) + (backward && p.dxo ? xe : 0) + (backward && p.dh ? 2 : 0) + (p.y ? 2 : 0) +
                                    (row_gate ? 2 : 0));
     const int budget = c.smem_optin - 2048 - hB;
-    int per_sm = std::min(8, kPipeThreads / o.threads);
+    int per_sm = std::min(8, most / o.threads);
     while (per_sm > 1 && per_sm * (2 * q.slotB + hB + 4096) > budget) --per_sm;
     q.slots = std::min(4, (budget / per_sm - (per_sm > 1 ? hB + 4096 : 0)) / q.slotB);
     if (q.slots < 2) return false;
@@ -1058,13 +1061,11 @@ template <typename T> cudaError_t fwd(const NormP &p, const CtxView &c)
     return p.d <= 8192 ? launch_fwd<T, 1>(p, c.stream) : launch_fwd<T, 2>(p, c.stream);
 }
 
-template <typename T, bool FULL> cudaError_t bwd_pipe(const NormP &p, const Pipe &o, cudaStream_t s)
+template <typename T, bool X32, bool FULL> cudaError_t bwd_pipe(const NormP &p, const Pipe &o, cudaStream_t s)
 {
-    if (p.x32)
-        return o.v == 1 ? run_pipe(norm_bwd_pipe<T, true, 1, FULL>, p, o, s)
-                        : run_pipe(norm_bwd_pipe<T, true, 2, FULL>, p, o, s);
-    return o.v == 1 ? run_pipe(norm_bwd_pipe<T, false, 1, FULL>, p, o, s)
-                    : run_pipe(norm_bwd_pipe<T, false, 2, FULL>, p, o, s);
+    return o.v == 1   ? run_pipe(norm_bwd_pipe<T, X32, 1, FULL>, p, o, s)
+           : o.v == 2 ? run_pipe(norm_bwd_pipe<T, X32, 2, FULL>, p, o, s)
+                      : run_pipe(norm_bwd_pipe<T, X32, 4, FULL>, p, o, s);
 }
 
 template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &c)
@@ -1074,7 +1075,8 @@ template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &
     if (plan_pipe(p, true, p.per_token != 0, c, o)) {
         const bool sums = p.db_pre || p.db_post || (p.dgate && p.b_post);
         const bool full = sums || p.pre == PI_NORM_LAYER || p.post == PI_NORM_LAYER;
-        const cudaError_t e = full ? bwd_pipe<T, true>(p, o, s) : bwd_pipe<T, false>(p, o, s);
+        const cudaError_t e = p.x32 ? (full ? bwd_pipe<T, true, true>(p, o, s) : bwd_pipe<T, true, false>(p, o, s))
+                                    : (full ? bwd_pipe<T, false, true>(p, o, s) : bwd_pipe<T, false, false>(p, o, s));
         if (e != cudaSuccess || !cols) return e;
         const int groups = p.per_token ? 1 : (int)((p.Tn + (int64_t)p.gate_rows - 1) / p.gate_rows);
         return launch_pdl(norm_bwd_join<T>, dim3((p.d + 31) / 32), dim3(256), 0, s, p, o.grid, groups, (int)full);
