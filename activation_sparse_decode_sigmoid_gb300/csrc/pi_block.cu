@@ -21,19 +21,28 @@ namespace {
 constexpr int kMaxT = 1 << 22, kMaxDim = 1 << 20;
 
 // ------------------------------------------------------------------ kernels
-__global__ void pack_rows(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd, int rows, int cols)
+// 256 columns a CTA by 8 rows at a time: lanes along a row.
+__global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd, int rows, int cols)
 {
     pdl_enter();
-    const int64_t total = (int64_t)rows * cols;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = i / cols, c = i % cols;
-        dst[r * ldd + c] = src[r * lds + c];
-    }
+    const int ncb = (cols + 255) / 256;
+    const int c = (int)(blockIdx.x % ncb) * 256 + threadIdx.x;
+    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * 32;
+    if (c >= cols) return;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i)
+        if (r0 + i < rows) dst[(r0 + i) * ldd + c] = src[(r0 + i) * lds + c];
 }
 
-// Column sums in two launches: a CTA sums kSumRows rows of 256 columns (8 per
+// Column sums in two launches: a CTA sums some rows of 256 columns (8 per
 // thread, 8 row lanes), then the row blocks' partials are added in order.
-constexpr int kSumRows = 256;
+// Rows per CTA: enough CTAs for four on every SM (152), at least 8 rows; a
+// 4096 x 1024 dz took 52 us with 256 rows each (64 CTAs).
+int sum_rows(int T, int N)
+{
+    const int64_t ncb = (N + 255) / 256, want = (T * ncb + 607) / 608;
+    return (int)std::min<int64_t>(256, std::max<int64_t>(8, (want + 7) / 8 * 8));
+}
 
 // dz = scale * dy * fn'(z), rounded into dz unless that is NULL, and the
 // column sums of the unrounded values over the CTA's rows into part [row
@@ -41,7 +50,7 @@ constexpr int kSumRows = 256;
 template <typename T>
 __global__ void __launch_bounds__(256) dact_rows(const void *dy, int dy32, int64_t ldy, const uint16_t *z, int64_t ldz,
                                                  int fn, float scale, uint16_t *dz, int64_t lddz, int Trows, int N,
-                                                 float *part, int vec)
+                                                 float *part, int vec, int rpb)
 {
     __shared__ float red[8][256];
     pdl_enter();
@@ -49,10 +58,10 @@ __global__ void __launch_bounds__(256) dact_rows(const void *dy, int dy32, int64
     const int rb = (int)(blockIdx.x / nb), cb = (int)(blockIdx.x % nb);
     const int lane = threadIdx.x & 31, wr = threadIdx.x >> 5;
     const int c = cb * 256 + lane * 8, n = N - c;
-    const int r1 = min(Trows, (rb + 1) * kSumRows);
+    const int r1 = (int)min((int64_t)Trows, (rb + 1) * (int64_t)rpb);
     float sum[8] = {};
     if (n > 0) {
-        for (int r = rb * kSumRows + wr; r < r1; r += 8) {
+        for (int r = rb * rpb + wr; r < r1; r += 8) {
             float v[8];
             if (dy32) load8f(static_cast<const float *>(dy) + (int64_t)r * ldy + c, n, vec & 1, v);
             else load8<T>(static_cast<const uint16_t *>(dy) + (int64_t)r * ldy + c, n, vec & 1, v);
@@ -80,14 +89,22 @@ __global__ void __launch_bounds__(256) dact_rows(const void *dy, int dy32, int64
     if (cc < N) part[(int64_t)rb * N + cc] = s;
 }
 
+// 32 columns a CTA, 8 lanes that share the parts.
 template <typename T>
-__global__ void sum_parts(const float *part, int nparts, int N, void *out, int out32, int accumulate)
+__global__ void __launch_bounds__(256) sum_parts(const float *part, int nparts, int N, void *out, int out32, int accumulate)
 {
+    __shared__ float red[8][32];
     pdl_enter();
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= N) return;
+    const int l = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
     float s = 0.f;
-    for (int i = 0; i < nparts; ++i) s += part[(int64_t)i * N + c];
+    if (c < N) {
+#pragma unroll 4
+        for (int i = k; i < nparts; i += 8) s += part[(int64_t)i * N + c];
+    }
+    red[k][l] = s;
+    __syncthreads();
+    if (k || c >= N) return;
+    for (int j = 1; j < 8; ++j) s += red[j][l];
     if (out32) {
         float *o = static_cast<float *>(out);
         o[c] = accumulate ? o[c] + s : s;
@@ -103,7 +120,7 @@ template <typename T>
 cudaError_t dact_t(const void *dy, int dy32, int64_t ldy, const void *z, int64_t ldz, int fn, float scale, void *dz,
                    int64_t lddz, int Trows, int N, void *db, int db32, int accumulate, float *part, cudaStream_t s)
 {
-    const int nrb = (Trows + kSumRows - 1) / kSumRows;
+    const int rpb = sum_rows(Trows, N), nrb = (Trows + rpb - 1) / rpb;
     const int64_t blocks = (int64_t)nrb * ((N + 255) / 256);
     const int vec = (aligned16(dy, ldy, dy32 ? 4 : 2) ? 1 : 0) | (z && aligned16(z, ldz, 2) ? 2 : 0) |
                     (dz && aligned16(dz, lddz, 2) ? 4 : 0);
@@ -111,10 +128,10 @@ cudaError_t dact_t(const void *dy, int dy32, int64_t ldy, const void *z, int64_t
     cudaError_t e = cudaSuccess;
     if (blocks > 0) {
         e = launch_pdl(dact_rows<T>, dim3((unsigned)blocks), dim3(256), 0, s, dy, dy32, ldy, (const uint16_t *)z, ldz, fn,
-                       scale, (uint16_t *)dz, lddz, Trows, N, pt, vec);
+                       scale, (uint16_t *)dz, lddz, Trows, N, pt, vec, rpb);
     }
     if (e != cudaSuccess || !db) return e;
-    return launch_pdl(sum_parts<T>, dim3((N + 127) / 128), dim3(128), 0, s, (const float *)part, nrb, N, db, db32,
+    return launch_pdl(sum_parts<T>, dim3((N + 31) / 32), dim3(256), 0, s, (const float *)part, nrb, N, db, db32,
                       accumulate);
 }
 
@@ -450,7 +467,7 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
     }
     if (gr.w_up || gr.w_gate) f.x = stage(ar, x, d.ldx, d.T, d.d, 1);
     if (gr.w_down) f.a = stage(ar, s.a, d.lda, d.T, d.n, 1);
-    f.part = gr.b_up || gr.b_gate || gr.b_down ? ar.take(colsum_bytes(d.T, std::max(d.n, d.d))) : nullptr;
+    f.part = gr.b_up || gr.b_gate || gr.b_down ? ar.take(std::max(colsum_bytes(d.T, d.n), colsum_bytes(d.T, d.d))) : nullptr;
     const int g32 = d.grad_dtype == PI_F32;
     if (want_d) {
         f.i_da = f.p.n;
@@ -506,14 +523,17 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
 
 cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
 {
-    const int64_t total = (int64_t)rows * cols;
-    if (total == 0) return cudaSuccess;
-    const unsigned blocks = (unsigned)std::min<int64_t>((total + 1023) / 1024, 4096);
-    return launch_pdl(pack_rows, dim3(blocks), dim3(256), 0, s, (const uint16_t *)src, lds, (uint16_t *)dst, ldd, rows,
+    const int64_t blocks = (int64_t)((rows + 31) / 32) * ((cols + 255) / 256);
+    if (!blocks) return cudaSuccess;
+    return launch_pdl(pack_rows, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t *)src, lds, (uint16_t *)dst, ldd, rows,
                       cols);
 }
 
-size_t colsum_bytes(int T, int N) { return (size_t)((T + kSumRows - 1) / kSumRows) * N * sizeof(float); }
+size_t colsum_bytes(int T, int N)
+{
+    const int rpb = sum_rows(T, N);
+    return (size_t)((T + rpb - 1) / rpb) * N * sizeof(float);
+}
 
 cudaError_t launch_dact(const void *dy, int dy32, int64_t ldy, const void *z, int64_t ldz, int fn, float scale,
                         void *dz, int64_t lddz, int T, int N, void *db, int db32, int accumulate, bool bf16,

@@ -25,6 +25,13 @@
 // MN-major forms, 128-byte swizzle), so the backward products read dz, W and
 // x as they lie.
 //
+// The epilogue moves its tiles of outputs (and of the inputs it needs: the
+// residual, or g and u) through shared memory in boxes of 32 x 32 per warp,
+// by TMA where rows are 16-byte aligned, else element by element with the
+// lanes along a row.  (A thread holds one row of the accumulator; writing it
+// straight to memory, 16 bytes in each of 32 rows at a time, took 8 us a tile
+// against 4 us for the products of 1024 values of k.)
+//
 // Every wait is bounded; after one that ran out a pair stops issuing, waits
 // for what it has in flight, frees its tensor memory and returns.
 #include <cuda_bf16.h>
@@ -33,6 +40,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pi_block.h"
 #include "pi_epi.cuh"
@@ -49,9 +57,12 @@ constexpr uint32_t kOpBytes = 16384;            // one operand of one CTA's stag
 constexpr uint32_t kStageBytes = 2 * kOpBytes;
 constexpr uint32_t kAtom = 8192;                // MN-major: 64 rows x 64 k
 constexpr int kTile = 256;
+constexpr uint32_t kBox = 2048;                 // 32 rows x 32 columns of an epilogue warp
+constexpr uint32_t kBoxes = kEpiWarps * 2 * kBox;
 
 struct TcParams {
     CUtensorMap ma[2], mb[2];
+    CUtensorMap mout, mout2, mout3, min1, min2; // boxes of 32 x 32 (out; in1 also the residual)
     int M, N, tm, tn;     // tiles along M and N
     int kt0, KT;          // k steps of the first segment, and of all
     int a_mn, b_mn;
@@ -184,6 +195,93 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// ------------------------------------------------------------------ boxes of the epilogue
+// A warp's box: row r (lane) at 64 r, 16-byte chunk j at j ^ ((r >> 1) & 3)
+// (the 64-byte TMA swizzle; 8 lanes' chunks fall into different banks).
+__device__ __forceinline__ uint32_t box_at(uint32_t box, int r, int j) { return box + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
+
+__device__ __forceinline__ void box_wait_read(int lane, bool all)
+{
+    if (lane == 0) {
+        if (all) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    }
+    __syncwarp();
+}
+
+template <typename T> __device__ __forceinline__ void box_put(uint32_t box, int lane, int j, const float *v)
+{
+    const uint32_t a = C16<T>::round2(v[0], v[1]), b = C16<T>::round2(v[2], v[3]), c = C16<T>::round2(v[4], v[5]),
+                   d = C16<T>::round2(v[6], v[7]);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_at(box, lane, j)), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+template <typename T> __device__ __forceinline__ void box_get(uint32_t box, int lane, int j, float (&v)[8])
+{
+    uint4 q;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(box_at(box, lane, j)));
+    unpack8<T>(q, v);
+}
+
+// The box as rows [row, row + 32), columns [col, col + 32) of an output; what
+// lies outside is left out.  (A TMA store cuts a row at 16 bytes, not at an
+// element: a row's end inside a 16-byte chunk takes the other way.)
+__device__ __forceinline__ void box_send(uint32_t box, int lane, const CUtensorMap *tm, bool tma, uint16_t *out, int64_t ld,
+                                         int row, int col, int M, int N)
+{
+    if (tma && (col + 32 <= N || N % 8 == 0)) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tm),
+                         "r"(box), "r"(col), "r"(row)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    } else {
+        __syncwarp();
+        if (col + lane < N) {
+            uint16_t *o = out + (int64_t)row * ld + col + lane;
+            const int rows = min(32, M - row);
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r, o += ld) {
+                uint16_t v;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box_at(box, r, lane >> 3) + (lane & 7) * 2));
+                *o = v;
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// The reverse: starts a copy of an input into the box (arriving on bar), or makes it element by element.
+__device__ __forceinline__ void box_fetch(uint32_t box, int lane, const CUtensorMap *tm, bool tma, const uint16_t *in,
+                                          int64_t ld, int row, int col, int M, int N, uint64_t *bar)
+{
+    if (tma) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // (after this warp's accesses to the box)
+        __syncwarp();
+        if (lane == 0) {
+            mbar_expect(bar, kBox);
+            asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                             box),
+                         "l"(tm), "r"(smem_addr(bar)), "r"(col), "r"(row)
+                         : "memory");
+        }
+    } else {
+        const bool in_n = col + lane < N;
+        const uint16_t *p = in + (int64_t)row * ld + col + lane;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            const uint16_t v = in_n && row + r < M ? p[r * ld] : (uint16_t)0;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(box_at(box, r, lane >> 3) + (lane & 7) * 2), "h"(v) : "memory");
+        }
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+        __syncwarp();
+    }
+}
+
 // After a failure: copies and MMAs in flight finish within microseconds; the
 // CTA stays for a bounded time that covers them.
 __device__ __forceinline__ void linger()
@@ -202,14 +300,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile; // output columns of a tile
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes); // used in the first CTA
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kBoxes); // used in the first CTA
     uint64_t *empty = full + kStages;
     uint64_t *acc_full = empty + kStages;  // [2]
     uint64_t *acc_empty = acc_full + 2;    // [2], used in the first CTA
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *in_full = acc_empty + 2;     // [8][2], one per box
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(in_full + 2 * kEpiWarps);
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init1(full + s), mbar_init1(empty + s);
         for (int s = 0; s < 2; ++s) mbar_init1(acc_full + s), mbar_init(acc_empty + s, 2 * kEpiWarps);
+        for (int s = 0; s < 2 * kEpiWarps; ++s) mbar_init1(in_full + s);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -305,59 +405,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         // epilogue: warp w reads TMEM lanes 32 (w mod 4) .., the first or second half of the columns
         const int q = warp & 3, half = warp >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+        const uint32_t box0 = base + kStages * kStageBytes + (uint32_t)warp * 2 * kBox, box1 = box0 + kBox;
+        uint64_t *bar0 = in_full + 2 * warp, *bar1 = bar0 + 1;
+        uint32_t fetched = 0; // fetches into each box so far
+        const Epi &e = p.e;
+        const bool aux = e.out2 || e.out3, has_in = MODE == EPI_DACT || (MODE == EPI_LINEAR && e.res && !e.out32), two = MODE == EPI_DACT && e.in2;
+        const uint16_t *in1 = MODE == EPI_DACT ? e.in1 : static_cast<const uint16_t *>(e.res);
+        const int64_t ldi1 = MODE == EPI_DACT ? e.ldi1 : e.ldr;
+        const bool t_in1 = (e.vec & (MODE == EPI_DACT ? V_IN1 : V_RES)) != 0;
+        constexpr int kCols = kOutN / 2; // of this warp
         for (uint32_t it = 0; ok && walk.next(w); ++it) {
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
+            int mi, ni;
+            tile_at(w.tile, p.tm, p.tn, mi, ni);
+            const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * kOutN + half * kCols;
+            const bool whole = w.slot < 0;
+            auto fetch = [&](int col) {
+                box_wait_read(lane, true); // (what was sent from the boxes has been read)
+                box_fetch(box0, lane, &p.min1, t_in1, in1, ldi1, row0, col, p.M, p.N, bar0);
+                if (two) box_fetch(box1, lane, &p.min2, e.vec & V_IN2, e.in2, e.ldi2, row0, col, p.M, p.N, bar1);
+                ++fetched;
+            };
+            const bool early = whole && has_in && row0 < p.M && col0 < p.N;
+            if (early) fetch(col0); // in flight while the products finish
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + buf, ph, p));
             if (!ok) break;
             tc_after();
-            int mi, ni;
-            tile_at(w.tile, p.tm, p.tn, mi, ni);
-            const int r = (int)rank * 128 + q * 32 + lane; // row within the tile
-            const int row = mi * kTile + r;
             const uint32_t ta = lane_addr + buf * 256u;
-            if (w.slot >= 0) {
+            if (!whole) {
+                const int r = (int)rank * 128 + q * 32 + lane; // row within the tile
                 float *dst = p.part + ((size_t)w.slot * kTile + r) * kTile;
 #pragma unroll 1
                 for (int c = half * 128; c < half * 128 + 128; c += 32) {
                     float v[32];
                     tmem_ld32(ta + c, v);
-                    if (row < p.M) {
+                    if (row0 + lane < p.M) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
-            } else if (MODE == EPI_GATED) {
+            } else if (row0 < p.M) {
 #pragma unroll 1
-                for (int c = half * 64; c < half * 64 + 64; c += 16) {
-                    float g[16], u[16];
-                    tmem_ld16(ta + c, g);
-                    tmem_ld16(ta + 128 + c, u);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int col = ni * kOutN + c + 8 * i;
-                        if (row < p.M && col < p.N)
-                            epilogue8<T, MODE>(p.e, p.N, row, col, *reinterpret_cast<float(*)[8]>(g + 8 * i),
-                                               *reinterpret_cast<float(*)[8]>(u + 8 * i));
+                for (int c = 0; c < kCols; c += 32) {
+                    const int col = col0 + c;
+                    if (col >= p.N) break;
+                    float v[32], u[MODE == EPI_GATED ? 32 : 1];
+                    tmem_ld32(ta + half * kCols + c, v);
+                    if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
+                    if (c + 32 >= kCols || col + 32 >= p.N) {
+                        // the accumulator is in registers: the next tile's products may begin
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
                     }
-                }
-            } else {
-#pragma unroll 1
-                for (int c = half * 128; c < half * 128 + 128; c += 32) {
-                    float v[32];
-                    tmem_ld32(ta + c, v);
+                    if (MODE == EPI_LINEAR && e.out32) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int col = ni * kOutN + c + 8 * i;
-                        float(&v8)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * i);
-                        if (row < p.M && col < p.N) epilogue8<T, MODE>(p.e, p.N, row, col, v8, v8);
+                        for (int j = 0; j < 4; ++j)
+                            if (row0 + lane < p.M && col + 8 * j < p.N)
+                                epilogue8<T, MODE>(e, p.N, row0 + lane, col + 8 * j, *reinterpret_cast<float(*)[8]>(v + 8 * j),
+                                                   *reinterpret_cast<float(*)[8]>(v + 8 * j));
+                        continue;
                     }
+                    if (has_in) {
+                        if (c) fetch(col);
+                        ok = mbar_wait_bounded(bar0, (fetched - 1) & 1, p) && (!two || mbar_wait_bounded(bar1, (fetched - 1) & 1, p));
+                        ok = __all_sync(0xffffffffu, ok);
+                    }
+                    const uint32_t box = has_in || aux || !((c >> 5) & 1) ? box0 : box1;
+                    if (!has_in) box_wait_read(lane, aux);
+                    if (MODE == EPI_LINEAR || MODE == EPI_GATED) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float b[8];
+                            if (e.bias) {
+                                load8<T>(e.bias + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS, b);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
+                            }
+                            if (MODE == EPI_GATED && e.bias2) {
+                                load8<T>(e.bias2 + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS2, b);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) u[(8 * j + i) % (MODE == EPI_GATED ? 32 : 1)] += b[i];
+                            }
+                            if (e.out2) box_put<T>(box1, lane, j, v + 8 * j);
+                        }
+                        if (e.out2) box_send(box1, lane, &p.mout2, e.vec & V_OUT2, e.out2, e.ld2, row0, col, p.M, p.N);
+                    }
+                    if (MODE == EPI_GATED && e.out3) {
+                        if (e.out2) box_wait_read(lane, true);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) box_put<T>(box1, lane, j, u + (8 * j) % (MODE == EPI_GATED ? 32 : 1));
+                        box_send(box1, lane, &p.mout3, e.vec & V_OUT3, e.out3, e.ld3, row0, col, p.M, p.N);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float *x = v + 8 * j;
+                        if (MODE == EPI_LINEAR) {
+                            if (e.fn != PI_FN_NONE) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] = act_f(e.fn, x[i]);
+                            }
+                            if (e.scale != 1.f) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] *= e.scale;
+                            }
+                            if (has_in) {
+                                float r[8];
+                                box_get<T>(box0, lane, j, r);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] += r[i];
+                            }
+                        } else if (MODE == EPI_GATED) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = act_f(e.fn, x[i]) * u[(8 * j + i) % (MODE == EPI_GATED ? 32 : 1)];
+                        } else {
+                            float g[8];
+                            box_get<T>(box0, lane, j, g);
+                            if (two) {
+                                float s[8];
+                                box_get<T>(box1, lane, j, s);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    s[i] *= x[i] * act_df(e.fn, g[i]);
+                                    x[i] *= act_f(e.fn, g[i]);
+                                }
+                                box_put<T>(box1, lane, j, x); // du
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] = s[i];
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] *= e.scale * act_df(e.fn, g[i]);
+                            }
+                        }
+                        box_put<T>(box, lane, j, x);
+                    }
+                    if (two) box_send(box1, lane, &p.mout2, e.vec & V_OUT2, e.out2, e.ld2, row0, col, p.M, p.N);
+                    box_send(box, lane, &p.mout, e.vec & V_OUT, static_cast<uint16_t *>(e.out), e.ldo, row0, col, p.M, p.N);
                 }
+                if (col0 < p.N) continue; // (released above)
             }
             tc_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // everything sent is written
     }
     __syncwarp();
     if (*(volatile int *)p.abort_flag) linger();
@@ -442,9 +634,15 @@ cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K)
 
 template <typename T, int MODE> cudaError_t run(const TcParams &p, int pairs, cudaStream_t s)
 {
-    constexpr int smem = kStages * kStageBytes + (2 * kStages + 4) * 8 + 16;
+    constexpr int smem = kStages * kStageBytes + kBoxes + (2 * kStages + 4 + 2 * kEpiWarps) * 8 + 16;
     auto kern = gemm_tc<T, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0}; // devices whose limit has been raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
+    }
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(2 * pairs), dim3(kGemmThreads), smem, s, p);
     if (e != cudaSuccess || !p.nsplit) return e;
     constexpr int kCols = (MODE == EPI_GATED ? 128 : kTile) / 8;
@@ -477,6 +675,19 @@ cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws)
     const int nb = g.mode == EPI_GATED ? 2 : g.segs;
     for (int i = 0; i < nb && e == cudaSuccess; ++i)
         e = map_of(&p.mb[i], g.b[i], g.N, g.K[g.mode == EPI_GATED ? 0 : i]);
+    // the epilogue's boxes
+    auto boxes = [&](CUtensorMap *m, const void *base, int64_t ld, unsigned bit) {
+        if (e == cudaSuccess && base && (g.e.vec & bit))
+            e = encode_map(m, base, (uint64_t)g.N, (uint64_t)g.M, (uint64_t)ld * 2, 32, 32);
+    };
+    if (!g.e.out32) {
+        boxes(&p.mout, g.e.out, g.e.ldo, V_OUT);
+        boxes(&p.min1, g.e.res, g.e.ldr, V_RES);
+    }
+    boxes(&p.mout2, g.e.out2, g.e.ld2, V_OUT2);
+    boxes(&p.mout3, g.e.out3, g.e.ld3, V_OUT3);
+    boxes(&p.min1, g.e.in1, g.e.ldi1, V_IN1);
+    boxes(&p.min2, g.e.in2, g.e.ldi2, V_IN2);
     if (e != cudaSuccess) return e;
     const int pairs = std::min(v.sms / 2, std::max(std::min(p.nfull, v.sms / 2), p.parts));
     return bf16 ? run_mode<__nv_bfloat16>(g, p, pairs, v.stream) : run_mode<__half>(g, p, pairs, v.stream);

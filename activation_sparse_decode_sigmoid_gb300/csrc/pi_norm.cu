@@ -913,24 +913,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_pipe(const __grid_con
     }
 }
 
-// The CTAs' partials in order: 32 columns a CTA, 8 lanes that share the parts.
-// Tokens of gate row g lie in CTAs c0 .. c1 of the row kernel; partial slot c + g.
-template <typename T> __global__ void __launch_bounds__(256) norm_bwd_join(const __grid_constant__ NormP p, int G, int groups, int sums)
+// The CTAs' partials in order: 32 columns a CTA, 16 lanes that share the parts.
+// Tokens of gate row g lie in CTAs c0 .. c1 of the row kernel; partial slot
+// c + g.  blockIdx.y 0: the parameters' gradients; y > 0: gate rows y - 1,
+// y - 1 + (gridDim.y - 1), ...
+constexpr int kJoinLanes = 16;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_constant__ NormP p, int G, int groups, int sums)
 {
-    __shared__ float red[8][6][32];
+    __shared__ float red[kJoinLanes][6][32];
     pdl_enter();
     const int l = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + l, d = p.d;
     const bool in = c < d;
-    const float w = in && p.w_post ? C16<T>::one(p.w_post[c]) : 1.f, b = in && p.b_post ? C16<T>::one(p.b_post[c]) : 0.f;
     const float *S = p.part + (int64_t)G * 2 * d;
+    const float w = in && p.w_post ? C16<T>::one(p.w_post[c]) : 1.f, b = in && p.b_post ? C16<T>::one(p.b_post[c]) : 0.f;
+    if (blockIdx.y > 0) {
+        for (int g = (int)blockIdx.y - 1; g < groups; g += (int)gridDim.y - 1) {
+            const int c0 = cta_of(p, g * (int64_t)p.gate_rows, G);
+            const int c1 = cta_of(p, min((int64_t)p.Tn, (g + 1) * (int64_t)p.gate_rows) - 1, G);
+            float a = 0.f, z = 0.f;
+            if (in) {
+#pragma unroll 4
+                for (int i = c0 + k; i <= c1; i += kJoinLanes) {
+                    a += S[(int64_t)(i + g) * 2 * d + c];
+                    if (sums) z += S[((int64_t)(i + g) * 2 + 1) * d + c];
+                }
+            }
+            red[k][0][l] = a, red[k][1][l] = z;
+            __syncthreads();
+            if (in && k == 0) {
+                for (int j = 1; j < kJoinLanes; ++j) a += red[j][0][l], z += red[j][1][l];
+                put<T>(p, p.dgate, (int64_t)g * d + c, p.bs * fmaf(w, a, b * z));
+            }
+            __syncthreads();
+        }
+        return;
+    }
     float v[6] = {}; // P1, P0, gate S1, gate S0, S1, S0
-    if (in)
-        for (int i = k; i < G; i += 8) {
+    if (in) {
+#pragma unroll 2
+        for (int i = k; i < G; i += kJoinLanes) {
             v[0] += p.part[(int64_t)i * 2 * d + c];
             if (sums) v[1] += p.part[((int64_t)i * 2 + 1) * d + c];
             if (!p.y) continue;
             const int r0 = row_of(p.Tn, i, G), r1 = row_of(p.Tn, i + 1, G);
             const int g0 = p.per_token ? 0 : r0 / p.gate_rows, g1 = p.per_token ? 0 : (r1 - 1) / p.gate_rows;
+#pragma unroll 4
             for (int g = g0; g <= g1; ++g) {
                 const float gate = p.gate && !p.per_token ? C16<T>::one(p.gate[(int64_t)g * p.ldgate + c]) : 1.f;
                 const float a = S[(int64_t)(i + g) * 2 * d + c], z = sums ? S[((int64_t)(i + g) * 2 + 1) * d + c] : 0.f;
@@ -940,50 +969,19 @@ template <typename T> __global__ void __launch_bounds__(256) norm_bwd_join(const
                 v[5] += z;
             }
         }
+    }
 #pragma unroll
     for (int i = 0; i < 6; ++i) red[k][i][l] = v[i];
     __syncthreads();
-    if (in && k == 0) {
+    if (!in || k) return;
 #pragma unroll
-        for (int i = 0; i < 6; ++i)
-            for (int j = 1; j < 8; ++j) v[i] += red[j][i][l];
-        put<T>(p, p.dw_pre, c, v[0]);
-        put<T>(p, p.db_pre, c, v[1]);
-        put<T>(p, p.dw_post, c, p.bs * v[2]);
-        put<T>(p, p.db_post, c, p.bs * v[3]);
-        if (p.dgate && groups == 1 && !p.per_token) put<T>(p, p.dgate, c, p.bs * fmaf(w, v[4], b * v[5]));
-    }
-    if (!p.dgate || p.per_token || groups == 1) return;
-    // few, long gate rows: the lanes share a row's parts; many short ones: a lane each
-    if (groups < 32) {
-        for (int g = 0; g < groups; ++g) {
-            const int c0 = cta_of(p, g * (int64_t)p.gate_rows, G), c1 = cta_of(p, min((int64_t)p.Tn, (g + 1) * (int64_t)p.gate_rows) - 1, G);
-            float a = 0.f, z = 0.f;
-            if (in)
-                for (int i = c0 + k; i <= c1; i += 8) {
-                    a += S[(int64_t)(i + g) * 2 * d + c];
-                    if (sums) z += S[((int64_t)(i + g) * 2 + 1) * d + c];
-                }
-            __syncthreads();
-            red[k][0][l] = a, red[k][1][l] = z;
-            __syncthreads();
-            if (in && k == 0) {
-                for (int j = 1; j < 8; ++j) a += red[j][0][l], z += red[j][1][l];
-                put<T>(p, p.dgate, (int64_t)g * d + c, p.bs * fmaf(w, a, b * z));
-            }
-        }
-        return;
-    }
-    if (!in) return;
-    for (int g = k; g < groups; g += 8) {
-        const int c0 = cta_of(p, g * (int64_t)p.gate_rows, G), c1 = cta_of(p, min((int64_t)p.Tn, (g + 1) * (int64_t)p.gate_rows) - 1, G);
-        float a = 0.f, z = 0.f;
-        for (int i = c0; i <= c1; ++i) {
-            a += S[(int64_t)(i + g) * 2 * d + c];
-            if (sums) z += S[((int64_t)(i + g) * 2 + 1) * d + c];
-        }
-        put<T>(p, p.dgate, (int64_t)g * d + c, p.bs * fmaf(w, a, b * z));
-    }
+    for (int i = 0; i < 6; ++i)
+        for (int j = 1; j < kJoinLanes; ++j) v[i] += red[j][i][l];
+    put<T>(p, p.dw_pre, c, v[0]);
+    put<T>(p, p.db_pre, c, v[1]);
+    put<T>(p, p.dw_post, c, p.bs * v[2]);
+    put<T>(p, p.db_post, c, p.bs * v[3]);
+    if (p.dgate && groups == 1 && !p.per_token) put<T>(p, p.dgate, c, p.bs * fmaf(w, v[4], b * v[5]));
 }
 
 template <typename T, int V> cudaError_t launch_fwd(const NormP &p, cudaStream_t s)
@@ -1079,7 +1077,9 @@ template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &
                                     : (full ? bwd_pipe<T, false, true>(p, o, s) : bwd_pipe<T, false, false>(p, o, s));
         if (e != cudaSuccess || !cols) return e;
         const int groups = p.per_token ? 1 : (int)((p.Tn + (int64_t)p.gate_rows - 1) / p.gate_rows);
-        return launch_pdl(norm_bwd_join<T>, dim3((p.d + 31) / 32), dim3(256), 0, s, p, o.grid, groups, (int)full);
+        const int gy = p.dgate && !p.per_token && groups > 1 ? std::min(groups, 64) : 0;
+        return launch_pdl(norm_bwd_join<T>, dim3((p.d + 31) / 32, 1 + gy), dim3(32 * kJoinLanes), 0, s, p, o.grid, groups,
+                          (int)full);
     }
     const int nt = std::min(512, ((p.d + 7) / 8 + 31) / 32 * 32);
     cudaError_t e = launch_pdl(norm_bwd_rows<T>, dim3(p.Tn), dim3(nt), 0, s, p);

@@ -160,9 +160,28 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream_ptr(device) -> int:
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    """The handle of torch's current stream on `device`."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(device.index)
+
+
+_CODES: dict = {}
+
+
+def _codes() -> dict:
+    """pi_dtype by torch type."""
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float16: PI_F16, torch.bfloat16: PI_BF16, torch.float32: PI_F32})
+    return _CODES
 
 
 # ---------------------------------------------------------------- same-named calls
@@ -556,73 +575,113 @@ class Context:
         pi_dense_step(self.handle, x, x.shape[0])
 
     # -- block operators: long prompts and training (tensors of torch's float16, bfloat16 and float32)
-    def _args(self, dtype, **tensors):
-        """Checks the tensors of a call: on the context's device, of `dtype`
-        (or, for names ending in an underscore, also float32), rows of
-        consecutive elements.  True if a base is not 16-byte aligned."""
-        import torch
-        if dtype not in (torch.float16, torch.bfloat16):
-            raise PiError(PI_ERR_ARG, f"dtype {dtype} is not float16 or bfloat16")
-        odd = False
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if t.device != self.torch_device:
-                raise PiError(PI_ERR_ARG, f"{name.rstrip('_')} is on {t.device}, the context on {self.torch_device}")
-            if t.dtype != dtype and not (name[-1] == "_" and t.dtype == torch.float32):
-                raise PiError(PI_ERR_ARG, f"{name.rstrip('_')} is {t.dtype}, expected {dtype}")
-            if t.dim() not in (1, 2):
-                raise PiError(PI_ERR_SHAPE, f"{name.rstrip('_')} has {t.dim()} dimensions")
-            if t.shape[-1] > 1 and t.stride(-1) != 1:
-                raise PiError(PI_ERR_ARG, f"{name.rstrip('_')}: a row's elements are not consecutive")
-            if t.dim() == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-                raise PiError(PI_ERR_SHAPE, f"{name.rstrip('_')}: rows overlap (stride {t.stride(0)})")
-            odd |= t.data_ptr() % 16 != 0
-        return odd
+    # Calls of few tokens take less time on the GPU than here, so the checks
+    # are written for the good case: _at() compares what a tensor is with what
+    # is expected and leaves the reason for a refusal to _refuse(); a call's
+    # desc and workspace size are kept by its sizes, types and strides.
+    def _at(self, name, t, shape, dtype):
+        """(address, row stride) of a matrix or vector; (0, 0) of None.  The
+        stride of a single row says nothing and counts as packed."""
+        if t is None:
+            return 0, 0
+        if t.dtype != dtype or t.shape != shape or t.device != self.torch_device:
+            self._refuse(name, t, shape, dtype)
+        st = t.stride()
+        if st[-1] != 1 and shape[-1] > 1:
+            self._refuse(name, t, shape, dtype)
+        if len(shape) == 1 or shape[0] <= 1:
+            return t.data_ptr(), 0
+        if st[0] < shape[1]:
+            self._refuse(name, t, shape, dtype)
+        return t.data_ptr(), st[0]
 
-    @staticmethod
-    def _shape(name, t, *shape):
-        if t is not None and tuple(t.shape) != shape:
+    def _refuse(self, name, t, shape, dtype):
+        if t.device != self.torch_device:
+            raise PiError(PI_ERR_ARG, f"{name} is on {t.device}, the context on {self.torch_device}")
+        if t.dtype != dtype:
+            raise PiError(PI_ERR_ARG, f"{name} is {t.dtype}, expected {dtype}")
+        if tuple(t.shape) != tuple(shape):
             raise PiError(PI_ERR_SHAPE, f"{name} is {list(t.shape)}, expected {list(shape)}")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise PiError(PI_ERR_ARG, f"{name}: a row's elements are not consecutive")
+        raise PiError(PI_ERR_SHAPE, f"{name}: rows overlap (stride {t.stride(0)})")
 
     @staticmethod
-    def _packed(name, t):
-        if t is not None and not t.is_contiguous():
-            raise PiError(PI_ERR_ARG, f"{name} is not packed")
-
-    @staticmethod
-    def _ld(t) -> int:
-        """Row stride of a matrix (a single row's own stride says nothing)."""
-        return 0 if t is None or t.shape[0] <= 1 else t.stride(0)
+    def _dims(name, t):
+        if t.dim() != 2:
+            raise PiError(PI_ERR_SHAPE, f"{name} has {t.dim()} dimensions, expected 2")
+        return t.shape
 
     @staticmethod
     def _code(dtype) -> int:
-        import torch
-        return {torch.float16: PI_F16, torch.bfloat16: PI_BF16, torch.float32: PI_F32}[dtype]
+        code = _codes().get(dtype)
+        if code is None:
+            raise PiError(PI_ERR_ARG, f"type {dtype} is not float16, bfloat16 or float32")
+        return code
+
+    def _code16(self, dtype) -> int:
+        code = self._code(dtype)
+        if code == PI_F32:
+            raise PiError(PI_ERR_ARG, f"dtype {dtype} is not float16 or bfloat16")
+        return code
+
+    def _plan(self, kind, fields, query, *more):
+        """(desc, workspace bytes) of a call, by the desc's fields."""
+        plans = self.__dict__.setdefault("_plans", {})
+        key = (kind, fields, query, more)
+        got = plans.get(key)
+        if got is None:
+            desc = kind(*fields)
+            got = plans[key] = desc, (query(self.handle, desc, *more) if query else 0)
+            if len(plans) > 4096:  # (a program of ever new lengths)
+                plans.clear()
+        return got
 
     def _ws(self, n: int):
         import torch
         return torch.empty(n, dtype=torch.uint8, device=self.torch_device) if n else None
 
+    def _grad_buffers(self, given: dict, accumulate: bool, shapes: dict, dtype):
+        """Checks gradient buffers: packed, one type; returns that type."""
+        kind = None
+        for k, t in given.items():
+            if t is None:
+                continue
+            if kind is None:
+                kind = t.dtype
+                if kind != dtype and self._code(kind) != PI_F32:
+                    raise PiError(PI_ERR_ARG, f"gradient of {k} is {kind}, expected {dtype} or float32")
+            elif t.dtype != kind:
+                raise PiError(PI_ERR_ARG, f"gradient of {k} is {t.dtype}, another's {kind}")
+            self._at("gradient of " + k, t, shapes[k], kind)
+            if not t.is_contiguous():
+                raise PiError(PI_ERR_ARG, f"gradient of {k} is not packed")
+        return kind or dtype
+
     def linear(self, x, w, b=None, *, fn=PI_FN_NONE, scale=1.0, residual=None, z=None, y=None):
         """y = residual + scale * fn(x W^T + b).  y is x's type, or the
         residual's (float32 residual stream); z, if given, receives
         x W^T + b for the backward pass."""
-        import torch
-        (T, K), N = x.shape, w.shape[0]
+        dt = x.dtype
+        code = self._code16(dt)
+        T, K = self._dims("x", x)
+        N = self._dims("w", w)[0]
         if y is None:
-            y = torch.empty((T, N), dtype=x.dtype if residual is None else residual.dtype, device=self.torch_device)
-        odd = self._args(x.dtype, x=x, w=w, b=b, z=z, residual_=residual, y_=y)
-        self._shape("w", w, N, K), self._shape("b", b, N), self._shape("z", z, T, N)
-        self._shape("residual", residual, T, N), self._shape("y", y, T, N)
-        if residual is not None and residual.dtype != y.dtype:
-            raise PiError(PI_ERR_ARG, f"residual is {residual.dtype}, y {y.dtype}")
-        code = self._code(x.dtype)
-        desc = pi_linear_desc(T, K, N, code, self._code(y.dtype), code, fn, scale, odd, self._ld(x), self._ld(w),
-                              self._ld(z), self._ld(residual), self._ld(y), 0, 0)
+            y = x.new_empty((T, N), dtype=dt if residual is None else residual.dtype)
+        out = self._code(y.dtype)
+        px, ldx = self._at("x", x, (T, K), dt)
+        pw, ldw = self._at("w", w, (N, K), dt)
+        pb, _ = self._at("b", b, (N,), dt)
+        pr, ldr = self._at("residual", residual, (T, N), y.dtype)
+        pz, ldz = self._at("z", z, (T, N), dt)
+        py, ldy = self._at("y", y, (T, N), y.dtype)
+        desc, n = self._plan(pi_linear_desc, (T, K, N, code, out, code, fn, scale, (px | pw) & 15 != 0, ldx, ldw, ldz, ldr,
+                                              ldy, 0, 0), pi_linear_workspace, False)
+        ws = self._ws(n)
         self._s()
-        n = pi_linear_workspace(self.handle, desc, False)
-        pi_linear(self.handle, desc, x, w, b, residual, z, y, self._ws(n), n)
+        rc = load_library().pi_linear(self.handle, ctypes.addressof(desc), px, pw, pb, pr, pz, py, _ptr(ws), n)
+        if rc:
+            _check(self.handle, rc, "pi_linear")
         return y
 
     def linear_bwd(self, dy, x, w, z=None, *, fn=PI_FN_NONE, scale=1.0, need=(True, True, True), dx=None, dw=None,
@@ -630,65 +689,79 @@ class Context:
         """(dx, dw, db) of ``linear`` for the gradient dy of y (the residual's
         is dy itself).  need: which of them; buffers may be given, dw and db
         in x's type or float32, and are added to with `accumulate`."""
-        import torch
-        (T, K), N = x.shape, w.shape[0]
-        new = lambda shape: torch.empty(shape, dtype=x.dtype, device=self.torch_device)
+        dt = x.dtype
+        code = self._code16(dt)
+        T, K = self._dims("x", x)
+        N = self._dims("w", w)[0]
         if accumulate and any(n and g is None for n, g in zip(need[1:], (dw, db))):
             raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
-        dx = (new((T, K)) if dx is None else dx) if need[0] else None
-        dw = (new((N, K)) if dw is None else dw) if need[1] else None
-        db = (torch.empty(N, dtype=x.dtype if dw is None else dw.dtype, device=self.torch_device) if db is None
-              else db) if need[2] else None
-        odd = self._args(x.dtype, dy_=dy, x=x, w=w, z=z, dx=dx, dw_=dw, db_=db)
-        self._shape("dy", dy, T, N), self._shape("w", w, N, K), self._shape("z", z, T, N), self._shape("dx", dx, T, K)
-        self._shape("dw", dw, N, K), self._shape("db", db, N)
-        if dw is not None and db is not None and dw.dtype != db.dtype:
-            raise PiError(PI_ERR_ARG, f"dw is {dw.dtype}, db {db.dtype}")
-        grad = dw if dw is not None else db
-        code = self._code(x.dtype)
-        desc = pi_linear_desc(T, K, N, code, self._code(dy.dtype), code if grad is None else self._code(grad.dtype), fn,
-                              scale, odd, self._ld(x), self._ld(w), self._ld(z), 0, self._ld(dy), self._ld(dx),
-                              self._ld(dw))
+        gdt = dt if not (need[1] or need[2]) else next((t.dtype for t in (dw, db) if t is not None), dt)
+        grad = self._code(gdt)
+        dx = (x.new_empty((T, K)) if dx is None else dx) if need[0] else None
+        dw = (x.new_empty((N, K), dtype=gdt) if dw is None else dw) if need[1] else None
+        db = (x.new_empty(N, dtype=gdt) if db is None else db) if need[2] else None
+        pdy, ldy = self._at("dy", dy, (T, N), dy.dtype)
+        px, ldx = self._at("x", x, (T, K), dt)
+        pw, ldw = self._at("w", w, (N, K), dt)
+        pz, ldz = self._at("z", z, (T, N), dt)
+        pdx, lddx = self._at("dx", dx, (T, K), dt)
+        pdw, lddw = self._at("dw", dw, (N, K), gdt)
+        pdb, _ = self._at("db", db, (N,), gdt)
+        desc, n = self._plan(pi_linear_desc, (T, K, N, code, self._code(dy.dtype), grad, fn, scale,
+                                              (pdy | px | pw) & 15 != 0, ldx, ldw, ldz, 0, ldy, lddx, lddw),
+                             pi_linear_workspace, True)
+        ws = self._ws(n)
         self._s()
-        n = pi_linear_workspace(self.handle, desc, True)
-        pi_linear_bwd(self.handle, desc, dy, x, w, z, dx, dw, db, accumulate, self._ws(n), n)
+        rc = load_library().pi_linear_bwd(self.handle, ctypes.addressof(desc), pdy, px, pw, pz, pdx, pdw, pdb,
+                                          int(accumulate), _ptr(ws), n)
+        if rc:
+            _check(self.handle, rc, "pi_linear_bwd")
         return dx, dw, db
 
     def gated_ffn_save(self, x, w_gate, w_up):
         """Buffers (g, u, a) for ``gated_ffn`` to leave for its backward pass,
         [T][n] with rows that start on 128-byte boundaries (g None if not gated)."""
-        import torch
         T, n = x.shape[0], w_up.shape[0]
-        new = lambda: torch.empty((T, (n + 63) // 64 * 64), dtype=x.dtype, device=self.torch_device)[:, :n]
-        return (new() if w_gate is not None else None), new(), new()
+        wide = (n + 63) // 64 * 64
 
-    def _ffn_desc(self, x, w_gate, w_up, w_down, g, u, a, y, fn, grad_code, odd):
-        T, d = x.shape
-        n = w_up.shape[0]
-        for name, t, shape in (("w_gate", w_gate, (n, d)), ("w_up", w_up, (n, d)), ("w_down", w_down, (d, n)),
-                               ("g", g, (T, n)), ("u", u, (T, n)), ("a", a, (T, n)), ("y", y, (T, d))):
-            self._shape(name, t, *shape)
-        return pi_gated_ffn_desc(T, d, n, self._code(x.dtype), grad_code, fn, w_gate is not None, odd, self._ld(x),
-                                 self._ld(y), self._ld(w_gate), self._ld(w_up), self._ld(w_down), self._ld(g),
-                                 self._ld(u), self._ld(a))
+        def new():
+            t = x.new_empty((T, wide))
+            return t if wide == n else t[:, :n]
+
+        return (new() if w_gate is not None else None), new(), new()
 
     def gated_ffn(self, x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, *, fn=PI_FN_RELU, save=None,
                   y=None):
         """y = (fn(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd, weights in the
         model's layout; w_gate None: y = fn(x Wu^T + bu) Wd^T + bd.  save
         (``gated_ffn_save``) keeps g, u and a for the backward pass."""
-        import torch
+        dt = x.dtype
+        code = self._code16(dt)
+        T, d = self._dims("x", x)
+        n = self._dims("w_up", w_up)[0]
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=self.torch_device)
+            y = x.new_empty((T, d))
         g, u, a = save if save is not None else (None, None, None)
-        odd = self._args(x.dtype, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, b_gate=b_gate, b_up=b_up, b_down=b_down,
-                         g=g, u=u, a=a, y=y)
-        desc = self._ffn_desc(x, w_gate, w_up, w_down, g, u, a, y, fn, self._code(x.dtype), odd)
-        self._shape("b_gate", b_gate, desc.n), self._shape("b_up", b_up, desc.n), self._shape("b_down", b_down, desc.d)
+        px, ldx = self._at("x", x, (T, d), dt)
+        pwg, ldwg = self._at("w_gate", w_gate, (n, d), dt)
+        pwu, ldwu = self._at("w_up", w_up, (n, d), dt)
+        pwd, ldwd = self._at("w_down", w_down, (d, n), dt)
+        pg, ldg = self._at("g", g, (T, n), dt)
+        pu, ldu = self._at("u", u, (T, n), dt)
+        pa, lda = self._at("a", a, (T, n), dt)
+        py, ldy = self._at("y", y, (T, d), dt)
+        pbg, pbu = self._at("b_gate", b_gate, (n,), dt)[0], self._at("b_up", b_up, (n,), dt)[0]
+        pbd = self._at("b_down", b_down, (d,), dt)[0]
+        desc, nb = self._plan(pi_gated_ffn_desc, (T, d, n, code, code, fn, w_gate is not None,
+                                                  (px | pwg | pwu | pwd | pa) & 15 != 0, ldx, ldy, ldwg, ldwu, ldwd, ldg,
+                                                  ldu, lda), pi_gated_ffn_workspace, False)
+        wts, sv = pi_gated_ffn_weights(pwg, pwu, pwd, pbg, pbu, pbd), pi_gated_ffn_save(pg, pu, pa)
+        ws = self._ws(nb)
         self._s()
-        n = pi_gated_ffn_workspace(self.handle, desc, False)
-        ws = pi_gated_ffn_weights(*map(_ptr, (w_gate, w_up, w_down, b_gate, b_up, b_down)))
-        pi_gated_ffn(self.handle, desc, ws, x, pi_gated_ffn_save(*map(_ptr, (g, u, a))), y, self._ws(n), n)
+        rc = load_library().pi_gated_ffn(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px,
+                                         ctypes.addressof(sv), py, _ptr(ws), nb)
+        if rc:
+            _check(self.handle, rc, "pi_gated_ffn")
         return y
 
     def gated_ffn_bwd(self, dy, x, w_gate, w_up, w_down, save, *, fn=PI_FN_RELU, need_dx=True, weight_grads=True,
@@ -698,42 +771,45 @@ class Context:
         wanted).  grads: the parameter gradients' buffers by the same keys,
         packed, in x's type or float32 (all alike), used instead of new ones
         and added to with `accumulate`; then only the given ones are computed."""
-        import torch
+        dt = x.dtype
+        code = self._code16(dt)
         g, u, a = save
-        T, d = x.shape
-        n, gated = w_up.shape[0], w_gate is not None
+        T, d = self._dims("x", x)
+        n, gated = self._dims("w_up", w_up)[0], w_gate is not None
         shapes = {"w_gate": (n, d), "w_up": (n, d), "w_down": (d, n), "b_gate": (n,), "b_up": (n,), "b_down": (d,)}
         if grads is None:
             if accumulate:
                 raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
-            want = {k: weight_grads if k[0] == "w" else bias_grads for k in shapes}
-            grads = {k: torch.empty(s, dtype=x.dtype, device=self.torch_device) for k, s in shapes.items()
-                     if want[k] and (gated or k[2:] != "gate")}
-        out = {k: grads.get(k) for k in shapes}
-        dx = torch.empty((T, d), dtype=x.dtype, device=self.torch_device) if need_dx else None
-        odd = self._args(x.dtype, dy=dy, x=x, w_gate=w_gate, w_up=w_up, w_down=w_down, g=g, u=u, a=a,
-                         **{k + "_": v for k, v in out.items()})
-        for k, v in out.items():
-            self._shape(k, v, *shapes[k]), self._packed(k, v)
-        types = {v.dtype for v in out.values() if v is not None}
-        if len(types) > 1:
-            raise PiError(PI_ERR_ARG, f"gradient buffers of several types: {types}")
-        if x.stride(0) != d and T > 1 and dx is not None:  # (x and dx share their stride)
-            dx = torch.empty((T, x.stride(0)), dtype=x.dtype, device=self.torch_device)[:, :d]
-        desc = self._ffn_desc(x, w_gate, w_up, w_down, g, u, a, dy, fn, self._code(types.pop() if types else x.dtype), odd)
+            out = {k: x.new_empty(s) if (weight_grads if k[0] == "w" else bias_grads) and (gated or k[2:] != "gate")
+                   else None for k, s in shapes.items()}
+            gdt = dt
+        else:
+            out = {k: grads.get(k) for k in shapes}
+            gdt = self._grad_buffers(out, accumulate, shapes, dt)
+        pdy, ldy = self._at("dy", dy, (T, d), dt)
+        px, ldx = self._at("x", x, (T, d), dt)
+        dx = None
+        if need_dx:  # (x and dx share their stride)
+            dx = x.new_empty((T, d)) if ldx in (0, d) else x.new_empty((T, ldx))[:, :d]
+        pwg, ldwg = self._at("w_gate", w_gate, (n, d), dt)
+        pwu, ldwu = self._at("w_up", w_up, (n, d), dt)
+        pwd, ldwd = self._at("w_down", w_down, (d, n), dt)
+        pg, ldg = self._at("g", g, (T, n), dt)
+        pu, ldu = self._at("u", u, (T, n), dt)
+        pa, lda = self._at("a", a, (T, n), dt)
+        desc, nb = self._plan(pi_gated_ffn_desc, (T, d, n, code, self._code(gdt), fn, gated,
+                                                  (pdy | px | pwg | pwu | pwd | pa) & 15 != 0, ldx, ldy, ldwg, ldwu, ldwd,
+                                                  ldg, ldu, lda), pi_gated_ffn_workspace, True)
+        wts, sv = pi_gated_ffn_weights(pwg, pwu, pwd, 0, 0, 0), pi_gated_ffn_save(pg, pu, pa)
+        gr = pi_gated_ffn_grads(*(_ptr(v) for v in out.values()))
+        ws = self._ws(nb)
         self._s()
-        nb = pi_gated_ffn_workspace(self.handle, desc, True)
-        ws = pi_gated_ffn_weights(*map(_ptr, (w_gate, w_up, w_down)), None, None, None)
-        pi_gated_ffn_bwd(self.handle, desc, ws, x, dy, pi_gated_ffn_save(*map(_ptr, (g, u, a))), dx,
-                         pi_gated_ffn_grads(*(_ptr(out[k]) for k in shapes)), accumulate, self._ws(nb), nb)
+        rc = load_library().pi_gated_ffn_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px, pdy,
+                                             ctypes.addressof(sv), _ptr(dx), ctypes.addressof(gr), int(accumulate),
+                                             _ptr(ws), nb)
+        if rc:
+            _check(self.handle, rc, "pi_gated_ffn_bwd")
         return {"dx": dx, **out}
-
-    def _norm_desc(self, x, dtype, gate, pre, post, gate_rows, res_scale, branch_scale, eps, grad_code, lds):
-        T, d = x.shape
-        rows = 1 if gate_rows == 0 else -(-T // max(gate_rows, 1))
-        self._shape("gate", gate, rows, d)
-        return pi_norm_residual_desc(T, d, self._code(x.dtype), self._code(dtype), grad_code, pre, post, gate_rows,
-                                     res_scale, branch_scale, eps, *lds)
 
     def norm_residual(self, x, y=None, gate=None, *, pre=PI_NORM_RMS, post=PI_NORM_NONE, w_pre=None, b_pre=None,
                       w_post=None, b_post=None, res_scale=1.0, branch_scale=1.0, gate_rows=0, eps=1e-5, dtype=None,
@@ -741,25 +817,32 @@ class Context:
         """(x', h): x' = res_scale * x + branch_scale * gate * norm_post(y),
         h = norm_pre(x') in y's type (`dtype` without a y).  gate [rows][d]:
         token t uses row t // gate_rows, 0 = one row for all.  x_out may be x."""
-        import torch
-        dtype = y.dtype if y is not None else dtype or (x.dtype if x.dtype != torch.float32 else torch.bfloat16)
-        T, d = x.shape
+        xdt = x.dtype
+        xcode = self._code(xdt)
+        if y is not None:
+            dtype = y.dtype
+        elif dtype is None:
+            import torch
+            dtype = torch.bfloat16 if xcode == PI_F32 else xdt
+        code = self._code16(dtype)
+        T, d = self._dims("x", x)
         if x_out is None:
-            x_out = torch.empty((T, d), dtype=x.dtype, device=self.torch_device)
+            x_out = x.new_empty((T, d))
         if h is None and pre != PI_NORM_NONE:
-            h = torch.empty((T, d), dtype=dtype, device=self.torch_device)
-        self._args(dtype, x_=x, y=y, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post, b_post=b_post, x_out_=x_out, h=h)
-        if x_out.dtype != x.dtype:
-            raise PiError(PI_ERR_ARG, f"x_out is {x_out.dtype}, x {x.dtype}")
-        for name, t in (("y", y), ("x_out", x_out), ("h", h)):
-            self._shape(name, t, T, d)
-        for name, t in (("w_pre", w_pre), ("b_pre", b_pre), ("w_post", w_post), ("b_post", b_post)):
-            self._shape(name, t, d)
-        desc = self._norm_desc(x, dtype, gate, pre, post, gate_rows, res_scale, branch_scale, eps, self._code(dtype),
-                               (self._ld(x), self._ld(x_out), self._ld(y), self._ld(h), self._ld(gate)))
+            h = x.new_empty((T, d), dtype=dtype)
+        px, ldx = self._at("x", x, (T, d), dtype if xcode != PI_F32 else xdt)
+        py, ldy = self._at("y", y, (T, d), dtype)
+        pg, ldg = self._at("gate", gate, (1 if gate_rows == 0 else -(-T // max(gate_rows, 1)), d), dtype)
+        po, ldo = self._at("x_out", x_out, (T, d), xdt)
+        ph, ldh = self._at("h", h, (T, d), dtype)
+        par = pi_norm_residual_params(self._at("w_pre", w_pre, (d,), dtype)[0], self._at("b_pre", b_pre, (d,), dtype)[0],
+                                      self._at("w_post", w_post, (d,), dtype)[0], self._at("b_post", b_post, (d,), dtype)[0])
+        desc, _ = self._plan(pi_norm_residual_desc, (T, d, xcode, code, code, pre, post, gate_rows, res_scale, branch_scale,
+                                                     eps, ldx, ldo, ldy, ldh, ldg), None)
         self._s()
-        pi_norm_residual(self.handle, desc, pi_norm_residual_params(*map(_ptr, (w_pre, b_pre, w_post, b_post))), x, y,
-                         gate, x_out, h)
+        rc = load_library().pi_norm_residual(self.handle, ctypes.addressof(desc), ctypes.addressof(par), px, py, pg, po, ph)
+        if rc:
+            _check(self.handle, rc, "pi_norm_residual")
         return x_out, h
 
     def norm_residual_bwd(self, dx_out, dh, x_out, y=None, gate=None, *, pre=PI_NORM_RMS, post=PI_NORM_NONE, w_pre=None,
@@ -770,45 +853,47 @@ class Context:
         w_post, b_post; a parameter that was not given has none.  grads:
         buffers for gate and the parameters, packed, in h's type or float32
         (all alike), used instead of new ones and added to with `accumulate`."""
-        import torch
-        dtype = next((t.dtype for t in (dh, y) if t is not None), None)
-        if dtype is None:
+        xdt = x_out.dtype
+        xcode = self._code(xdt)
+        if dh is None and y is None:
             raise PiError(PI_ERR_ARG, "neither dh nor y given")
-        T, d = x_out.shape
+        dtype = (dh if dh is not None else y).dtype
+        code = self._code16(dtype)
+        T, d = self._dims("x_out", x_out)
+        rows = 1 if gate_rows == 0 else -(-T // max(gate_rows, 1))
         given = {"gate": gate, "w_pre": w_pre, "b_pre": b_pre, "w_post": w_post, "b_post": b_post}
         if grads is None:
             if accumulate:
                 raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
-            grads = {k: torch.empty(v.shape, dtype=dtype, device=self.torch_device) for k, v in given.items()
-                     if v is not None}
-        out = {k: grads.get(k) for k in given}
-        dx = torch.empty((T, d), dtype=x_out.dtype, device=self.torch_device)
-        # (y and dy share their stride)
-        dy = None if y is None else torch.empty((T, max(d, self._ld(y))), dtype=dtype, device=self.torch_device)[:, :d]
-        self._args(dtype, dx_out_=dx_out, dh=dh, x_out_=x_out, y=y, **given, **{"d" + k + "_": v for k, v in out.items()})
-        for name, t in (("dx_out", dx_out), ("dh", dh), ("y", y)):
-            self._shape(name, t, T, d)
-        for k, v in out.items():
-            self._shape("gradient of " + k, v, *(given[k].shape if given[k] is not None else (d,)))
-            self._packed("gradient of " + k, v)
-            if k != "gate":
-                self._shape(k, given[k], d)
-        if dx_out is not None and dx_out.dtype != x_out.dtype:
-            raise PiError(PI_ERR_ARG, f"dx_out is {dx_out.dtype}, x_out {x_out.dtype}")
-        if dx_out is not None and self._ld(dx_out) != self._ld(x_out):
+            out = {k: None if v is None else v.new_empty(v.shape) for k, v in given.items()}
+            gdt = dtype
+        else:
+            out = {k: grads.get(k) for k in given}
+            gdt = self._grad_buffers(out, accumulate, {k: (rows, d) if k == "gate" else (d,) for k in given}, dtype)
+        if xcode != PI_F32 and xdt != dtype:
+            raise PiError(PI_ERR_ARG, f"x_out is {xdt}, expected {dtype} or float32")
+        px, ldxo = self._at("x_out", x_out, (T, d), xdt)
+        pdxo, lddxo = self._at("dx_out", dx_out, (T, d), xdt)
+        if dx_out is not None and lddxo != ldxo:
             raise PiError(PI_ERR_ARG, "dx_out and x_out differ in their row stride")
-        types = {v.dtype for v in out.values() if v is not None}
-        if len(types) > 1:
-            raise PiError(PI_ERR_ARG, f"gradient buffers of several types: {types}")
-        desc = self._norm_desc(x_out, dtype, gate, pre, post, gate_rows, res_scale, branch_scale, eps,
-                               self._code(types.pop() if types else dtype),
-                               (0, self._ld(x_out), self._ld(y), self._ld(dh), self._ld(gate)))
+        pdh, ldh = self._at("dh", dh, (T, d), dtype)
+        py, ldy = self._at("y", y, (T, d), dtype)
+        pg, ldg = self._at("gate", gate, (rows, d), dtype)
+        par = pi_norm_residual_params(self._at("w_pre", w_pre, (d,), dtype)[0], self._at("b_pre", b_pre, (d,), dtype)[0],
+                                      self._at("w_post", w_post, (d,), dtype)[0], self._at("b_post", b_post, (d,), dtype)[0])
+        dx = x_out.new_empty((T, d))
+        # (y and dy share their stride)
+        dy = None if y is None else y.new_empty((T, d)) if ldy in (0, d) else y.new_empty((T, ldy))[:, :d]
+        desc, n = self._plan(pi_norm_residual_desc, (T, d, xcode, code, self._code(gdt), pre, post, gate_rows, res_scale,
+                                                     branch_scale, eps, 0, ldxo, ldy, ldh, ldg),
+                             pi_norm_residual_bwd_workspace)
+        gr = pi_norm_residual_grads(dx.data_ptr(), _ptr(dy), *(_ptr(v) for v in out.values()))
+        ws = self._ws(n)
         self._s()
-        n = pi_norm_residual_bwd_workspace(self.handle, desc)
-        pi_norm_residual_bwd(self.handle, desc, pi_norm_residual_params(*map(_ptr, (w_pre, b_pre, w_post, b_post))),
-                             dx_out, dh, x_out, y, gate, pi_norm_residual_grads(_ptr(dx), _ptr(dy),
-                                                                               *(_ptr(out[k]) for k in given)),
-                             accumulate, self._ws(n), n)
+        rc = load_library().pi_norm_residual_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(par), pdxo, pdh, px,
+                                                 py, pg, ctypes.addressof(gr), int(accumulate), _ptr(ws), n)
+        if rc:
+            _check(self.handle, rc, "pi_norm_residual_bwd")
         return {"dx": dx, "dy": dy, **out}
 
     def set_trace(self, x_trace=None, xhat_trace=None, idx_trace=None, count_trace=None) -> None:

@@ -142,6 +142,44 @@ def test_linear_bwd(c, T, K, N, pad, off, dt):
     R.check(only[2], (want["db"][0], want["db"][1] + R.rnd(want["db"][0], dt)), "db alone")
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 63, 9), (20, 1001, 515), (70, 130, 261), (300, 75, 1029)])
+def test_what_lies_beside_the_rows_does_not_matter(c, T, K, N):
+    """Rows that end inside a 16-byte chunk, with NaN behind them: none of it
+    is read into a result, and none of it is written."""
+    m = Maker(15)
+
+    def beside_nan(rows, cols, std=1.0):
+        buf = torch.full((rows + 1, (cols + 15) // 8 * 8), float("nan"), dtype=F16, device="cuda")
+        buf[:rows, :cols] = m(rows, cols, std=std)
+        return buf, buf[:rows, :cols]
+
+    (xb, x), (wb, w), (rb, r) = beside_nan(T, K), beside_nan(N, K, K ** -0.5), beside_nan(T, N)
+    (yb, y), (zb, z), (dyb, dy), (dxb, dx) = beside_nan(T, N), beside_nan(T, N), beside_nan(T, N), beside_nan(T, K)
+    want = R.linear(x, w, None, "gelu", 1.0, r, F16)
+    c.linear(x, w, fn=pi.PI_FN_GELU, residual=r, z=z, y=y)
+    R.check(y, want["y"], "y")
+    R.check(z, want["z"], "z")
+    want = R.linear_bwd(dy, x, w, z, "gelu", 1.0, F16)
+    got = c.linear_bwd(dy, x, w, z, fn=pi.PI_FN_GELU, dx=dx)
+    for k, v in zip(("dx", "dw", "db"), got):
+        R.check(v, want[k], k)
+    for buf, cols in ((xb, K), (wb, K), (rb, N), (yb, N), (zb, N), (dyb, N), (dxb, K)):
+        assert bool(buf[-1].isnan().all()) and bool(buf[:, cols:].isnan().all())
+    (ub, u), (ab, a) = beside_nan(T, N), beside_nan(T, N)
+    wd = m(K, N, std=N ** -0.5)
+    y = c.gated_ffn(x, None, w, wd, fn=pi.PI_FN_SILU, save=(None, u, a))
+    want = R.ffn(x, None, w, wd, None, None, None, "silu")
+    R.check(y, want["y"], "ffn y")
+    R.check(a, want["a"], "a")
+    dy = m(T, K)
+    want = R.ffn_bwd(dy, x, None, w, wd, None, u, a, "silu", F16)
+    got = c.gated_ffn_bwd(dy, x, None, w, wd, (None, u, a), fn=pi.PI_FN_SILU)
+    for k in want:
+        R.check(got[k], want[k], k)
+    for buf in (ub, ab):
+        assert bool(buf[-1].isnan().all()) and bool(buf[:, N:].isnan().all())
+
+
 def test_linear_bwd_without_activation_takes_dy_itself(c):
     m = Maker(8)
     for T, K, N in ((1, 40, 24), (70, 264, 33)):
