@@ -59,6 +59,13 @@ struct Gemm {
 size_t gemm_workspace(const Gemm &g, const CtxView &v);
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
+// Products of up to this many rows of A go to skinny_tc (pi_skinny.cu) where
+// both operands lie along k.
+constexpr int kSkinnyRows = 64;
+bool skinny_takes(const Gemm &g);
+size_t skinny_workspace(const Gemm &g, const CtxView &v);
+cudaError_t launch_skinny(const Gemm &g, bool bf16, const CtxView &v, void *ws);
+
 // dst [rows][cols] (row stride ldd) = src (row stride lds), 16-bit elements
 cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s);
 

@@ -658,10 +658,14 @@ template <typename T> cudaError_t run_mode(const Gemm &g, const TcParams &p, int
 
 } // namespace
 
-size_t gemm_workspace(const Gemm &g, const CtxView &v) { return plan_split(g, v.sms).bytes; }
+size_t gemm_workspace(const Gemm &g, const CtxView &v)
+{
+    return skinny_takes(g) ? skinny_workspace(g, v) : plan_split(g, v.sms).bytes;
+}
 
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws)
 {
+    if (skinny_takes(g)) return launch_skinny(g, bf16, v, ws);
     const Split s = plan_split(g, v.sms);
     TcParams p = {};
     p.M = g.M, p.N = g.N, p.tm = s.tm, p.tn = s.tn, p.kt0 = s.kt0, p.KT = s.KT;

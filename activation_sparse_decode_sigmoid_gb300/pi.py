@@ -423,11 +423,14 @@ def pi_norm_residual_bwd(ctx: int, desc, params, dx_out, dh, x_out, y, gate, gra
 class Context:
     """Owns a pi_ctx; every call runs on torch's current stream of `device`."""
 
+    _plans: dict = {}  # (see _plan; a context's own is set when it is created)
+
     def __init__(self, device: int = 0, max_layers: int = 1, max_batch: int = 1):
         import torch
         self.device = device
         self.torch_device = torch.device("cuda", device)
         self.max_layers, self.max_batch = max_layers, max_batch
+        self._plans = {}
         self.handle = pi_create(device, _stream_ptr(self.torch_device), max_layers, max_batch)
         self.descs: dict[int, pi_layer_desc] = {}
         self.hot: dict[int, int] = {}  # each layer's always-active prefix
@@ -444,7 +447,9 @@ class Context:
             pass
 
     def _s(self):
-        pi_set_stream(self.handle, _stream_ptr(self.torch_device))
+        rc = _lib.pi_set_stream(self.handle, _stream_ptr(self.torch_device))
+        if rc:
+            _check(self.handle, rc, "pi_set_stream")
 
     @property
     def grid(self) -> int:
@@ -580,20 +585,18 @@ class Context:
     # is expected and leaves the reason for a refusal to _refuse(); a call's
     # desc and workspace size are kept by its sizes, types and strides.
     def _at(self, name, t, shape, dtype):
-        """(address, row stride) of a matrix or vector; (0, 0) of None.  The
-        stride of a single row says nothing and counts as packed."""
+        """(address, row stride) of a matrix or vector, 0 for packed rows (the
+        stride of a single row says nothing); (0, 0) of None."""
         if t is None:
             return 0, 0
         if t.dtype != dtype or t.shape != shape or t.device != self.torch_device:
             self._refuse(name, t, shape, dtype)
-        st = t.stride()
-        if st[-1] != 1 and shape[-1] > 1:
-            self._refuse(name, t, shape, dtype)
-        if len(shape) == 1 or shape[0] <= 1:
+        if t.is_contiguous():
             return t.data_ptr(), 0
-        if st[0] < shape[1]:
+        st = t.stride()
+        if (st[-1] != 1 and shape[-1] > 1) or (len(shape) == 2 and shape[0] > 1 and st[0] < shape[1]):
             self._refuse(name, t, shape, dtype)
-        return t.data_ptr(), st[0]
+        return t.data_ptr(), st[0] if len(shape) == 2 and shape[0] > 1 else 0
 
     def _refuse(self, name, t, shape, dtype):
         if t.device != self.torch_device:
@@ -614,20 +617,21 @@ class Context:
 
     @staticmethod
     def _code(dtype) -> int:
-        code = _codes().get(dtype)
+        code = (_CODES or _codes()).get(dtype)
         if code is None:
             raise PiError(PI_ERR_ARG, f"type {dtype} is not float16, bfloat16 or float32")
         return code
 
-    def _code16(self, dtype) -> int:
-        code = self._code(dtype)
-        if code == PI_F32:
+    @staticmethod
+    def _code16(dtype) -> int:
+        code = (_CODES or _codes()).get(dtype)
+        if code is None or code == PI_F32:
             raise PiError(PI_ERR_ARG, f"dtype {dtype} is not float16 or bfloat16")
         return code
 
     def _plan(self, kind, fields, query, *more):
         """(desc, workspace bytes) of a call, by the desc's fields."""
-        plans = self.__dict__.setdefault("_plans", {})
+        plans = self._plans
         key = (kind, fields, query, more)
         got = plans.get(key)
         if got is None:
@@ -679,7 +683,7 @@ class Context:
                                               ldy, 0, 0), pi_linear_workspace, False)
         ws = self._ws(n)
         self._s()
-        rc = load_library().pi_linear(self.handle, ctypes.addressof(desc), px, pw, pb, pr, pz, py, _ptr(ws), n)
+        rc = _lib.pi_linear(self.handle, ctypes.addressof(desc), px, pw, pb, pr, pz, py, _ptr(ws), n)
         if rc:
             _check(self.handle, rc, "pi_linear")
         return y
@@ -712,7 +716,7 @@ class Context:
                              pi_linear_workspace, True)
         ws = self._ws(n)
         self._s()
-        rc = load_library().pi_linear_bwd(self.handle, ctypes.addressof(desc), pdy, px, pw, pz, pdx, pdw, pdb,
+        rc = _lib.pi_linear_bwd(self.handle, ctypes.addressof(desc), pdy, px, pw, pz, pdx, pdw, pdb,
                                           int(accumulate), _ptr(ws), n)
         if rc:
             _check(self.handle, rc, "pi_linear_bwd")
@@ -758,7 +762,7 @@ class Context:
         wts, sv = pi_gated_ffn_weights(pwg, pwu, pwd, pbg, pbu, pbd), pi_gated_ffn_save(pg, pu, pa)
         ws = self._ws(nb)
         self._s()
-        rc = load_library().pi_gated_ffn(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px,
+        rc = _lib.pi_gated_ffn(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px,
                                          ctypes.addressof(sv), py, _ptr(ws), nb)
         if rc:
             _check(self.handle, rc, "pi_gated_ffn")
@@ -804,7 +808,7 @@ class Context:
         gr = pi_gated_ffn_grads(*(_ptr(v) for v in out.values()))
         ws = self._ws(nb)
         self._s()
-        rc = load_library().pi_gated_ffn_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px, pdy,
+        rc = _lib.pi_gated_ffn_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px, pdy,
                                              ctypes.addressof(sv), _ptr(dx), ctypes.addressof(gr), int(accumulate),
                                              _ptr(ws), nb)
         if rc:
@@ -840,7 +844,7 @@ class Context:
         desc, _ = self._plan(pi_norm_residual_desc, (T, d, xcode, code, code, pre, post, gate_rows, res_scale, branch_scale,
                                                      eps, ldx, ldo, ldy, ldh, ldg), None)
         self._s()
-        rc = load_library().pi_norm_residual(self.handle, ctypes.addressof(desc), ctypes.addressof(par), px, py, pg, po, ph)
+        rc = _lib.pi_norm_residual(self.handle, ctypes.addressof(desc), ctypes.addressof(par), px, py, pg, po, ph)
         if rc:
             _check(self.handle, rc, "pi_norm_residual")
         return x_out, h
@@ -890,7 +894,7 @@ class Context:
         gr = pi_norm_residual_grads(dx.data_ptr(), _ptr(dy), *(_ptr(v) for v in out.values()))
         ws = self._ws(n)
         self._s()
-        rc = load_library().pi_norm_residual_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(par), pdxo, pdh, px,
+        rc = _lib.pi_norm_residual_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(par), pdxo, pdh, px,
                                                  py, pg, ctypes.addressof(gr), int(accumulate), _ptr(ws), n)
         if rc:
             _check(self.handle, rc, "pi_norm_residual_bwd")
