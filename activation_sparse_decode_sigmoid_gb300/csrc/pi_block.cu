@@ -429,6 +429,7 @@ FfnFwd plan_ffn(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated_ffn
     h.mode = EPI_LINEAR;
     h.M = d.T, h.N = d.d, h.K[0] = d.n;
     h.a[0] = f.a.m, h.b[0] = f.wd.m;
+    h.early = 1;
     h.e.bias = (const uint16_t *)w.b_down;
     h.e.out = y, h.e.ldo = d.ldy;
     set_vec(h.e);

@@ -52,6 +52,10 @@ struct Gemm {
     int segs;
     int K[2];
     Mat a[2], b[2];
+    // B is complete before the launch in front of this one starts: it may be
+    // read before that launch has finished (launches wait for their
+    // predecessor before they let their successor start)
+    int early;
     Epi e;
 };
 

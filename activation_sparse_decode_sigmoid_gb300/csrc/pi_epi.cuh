@@ -216,5 +216,28 @@ __device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int 
     }
 }
 
+// The epilogue of one element (EPI_LINEAR, EPI_GATED).
+template <typename T, int MODE>
+__device__ __forceinline__ void epilogue1(const Epi &e, int64_t row, int col, float v, float v2)
+{
+    if (e.bias) v += C16<T>::one(e.bias[col]);
+    if (MODE == EPI_GATED && e.bias2) v2 += C16<T>::one(e.bias2[col]);
+    if (e.out2) e.out2[row * e.ld2 + col] = C16<T>::round(v);
+    if (MODE == EPI_GATED && e.out3) e.out3[row * e.ld3 + col] = C16<T>::round(v2);
+    v = act_f(e.fn, v);
+    if (MODE == EPI_GATED) v *= v2;
+    else {
+        v *= e.scale;
+        if (e.res)
+            v += e.out32 ? static_cast<const float *>(e.res)[row * e.ldr + col]
+                         : C16<T>::one(static_cast<const uint16_t *>(e.res)[row * e.ldr + col]);
+        if (e.out32) {
+            static_cast<float *>(e.out)[row * e.ldo + col] = v;
+            return;
+        }
+    }
+    static_cast<uint16_t *>(e.out)[row * e.ldo + col] = C16<T>::round(v);
+}
+
 } // namespace
 } // namespace pi

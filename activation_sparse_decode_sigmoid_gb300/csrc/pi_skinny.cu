@@ -11,6 +11,9 @@
 // its one to three tiles, [tokens][128], and skinny_join adds the parts of a
 // tile in the order of k and runs the epilogue - bias, activation, gate,
 // residual - on 8 features at a time.
+//
+// One token, and up to four of a smaller matrix (gemv_takes), take one launch
+// of gemv_rows instead: dot products on the CUDA cores, no workspace.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -37,6 +40,7 @@ struct SkParams {
     int tn, tiles, KT;    // tiles of one matrix, of all; k steps
     int parts, smax;
     int slots;            // ring
+    int early;            // the weights are older than the launch before this one: load them ahead of its results
     uint32_t slotB;
     float *part;          // [tiles][smax][T][128]
     int *status, *abort_flag;
@@ -66,7 +70,7 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const uint32_t tmem = tmem_alloc(tslot, 128); // two accumulators of up to 64 columns
-    pdl_enter();
+    if (!(p.early && warp == 4)) pdl_enter();
     const int64_t units = (int64_t)p.tiles * p.KT;
     int64_t u = sk_range(units, (int)blockIdx.x, p.parts);
     const int64_t u1 = sk_range(units, (int)blockIdx.x + 1, p.parts);
@@ -78,16 +82,33 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
             uint32_t round = 0;
             const uint32_t bytes = kWTile + (uint32_t)p.Tp * 128u;
             int tile = (int)(u / p.KT), k = (int)(u - (int64_t)tile * p.KT);
+            auto load_w = [&](uint32_t s) {
+                const int m = tile >= p.tn ? 1 : 0;
+                mbar_expect(full + s, bytes);
+                tile_load(base + s * p.slotB, &p.mw[m], k * kBK, (tile - m * p.tn) * 128, full + s);
+            };
+            if (p.early) {
+                // fill the ring's weights while the launch before finishes, then their tokens
+                const int k0 = k;
+                for (; u < u1 && round < S; ++u, ++round) {
+                    load_w(round);
+                    if (++k == p.KT) k = 0, ++tile;
+                }
+                pdl_enter();
+                int kx = k0;
+                for (uint32_t s = 0; s < round; ++s) {
+                    tile_load(base + s * p.slotB + kWTile, &p.mx, kx * kBK, 0, full + s);
+                    if (++kx == p.KT) kx = 0;
+                }
+                cur = Cur(round, S);
+            }
             for (; u < u1; ++u) {
                 if (round >= S && !mbar_wait_bounded(empty + cur.s, cur.ph ^ 1u, p)) {
                     ok = false;
                     break;
                 }
-                const int m = tile >= p.tn ? 1 : 0;
-                const uint32_t dst = base + cur.s * p.slotB;
-                mbar_expect(full + cur.s, bytes);
-                tile_load(dst, &p.mw[m], k * kBK, (tile - m * p.tn) * 128, full + cur.s);
-                tile_load(dst + kWTile, &p.mx, k * kBK, 0, full + cur.s);
+                load_w(cur.s);
+                tile_load(base + cur.s * p.slotB + kWTile, &p.mx, k * kBK, 0, full + cur.s);
                 cur.next(S);
                 ++round;
                 if (++k == p.KT) k = 0, ++tile;
@@ -179,6 +200,132 @@ template <typename T, int MODE> __global__ void __launch_bounds__(128) skinny_jo
     epilogue8<T, MODE>(p.e, p.N, t, f, v[0], v[1]);
 }
 
+// ------------------------------------------------------------------ one token, or few and a smaller matrix
+// A group of `wpr` warps of a CTA computes R features (gated: their g and u)
+// for all tokens: lanes take chunks of 8 elements of the rows, 4 loads or
+// more in flight each, and the warps' sums are added in order.  With 2 to 4
+// tokens two rows share each chunk of x read (four rows, with half the loads
+// in flight, took 95 us instead of 85 for 8192 x 28672 at 4 tokens).
+constexpr int kGvWarps = 8, kGvTokens = 4;
+
+struct GvParams {
+    int T, N, K, wpr;
+    const uint16_t *x, *w[2];
+    int64_t ldx, ldw[2];
+    Epi e;
+};
+
+template <typename T, int MODE, int TT, int R>
+__global__ void __launch_bounds__(32 * kGvWarps) gemv_rows(const __grid_constant__ GvParams p)
+{
+    constexpr int NM = MODE == EPI_GATED ? 2 : 1, NR = NM * R, U = NR > 2 ? 2 : 4;
+    __shared__ float red[kGvWarps][NR][TT];
+    pdl_enter();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = warp % p.wpr, f0 = ((int)blockIdx.x * (kGvWarps / p.wpr) + warp / p.wpr) * R;
+    float acc[NR][TT] = {};
+    if (f0 < p.N) {
+        const uint4 *w[NR], *x = reinterpret_cast<const uint4 *>(p.x);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) // (past the last feature: the last again, not kept)
+            w[i] = reinterpret_cast<const uint4 *>(p.w[i / R] + (int64_t)min(f0 + i % R, p.N - 1) * p.ldw[i / R]);
+        const int nch = p.K >> 3, step = 32 * p.wpr;
+        const int64_t ldx = p.ldx >> 3;
+        int c = part * 32 + lane;
+        for (; c + (U - 1) * step < nch; c += U * step) {
+            uint4 q[NR][U];
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int j = 0; j < U; ++j) q[i][j] = __ldg(w[i] + c + j * step);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const uint4 v = x[t * ldx + c + j * step];
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) acc[i][t] = fma8<T>(q[i][j], v, acc[i][t]);
+                }
+        }
+        for (; c < nch; c += step)
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const uint4 q = __ldg(w[i] + c);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) acc[i][t] = fma8<T>(q, x[t * ldx + c], acc[i][t]);
+            }
+        const int k = nch * 8 + lane; // the last K mod 8 elements
+        if (part == 0 && k < p.K)
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    acc[i][t] = fmaf(C16<T>::one(reinterpret_cast<const uint16_t *>(w[i])[k]), C16<T>::one(p.x[t * p.ldx + k]), acc[i][t]);
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) acc[i][t] += __shfl_xor_sync(0xffffffffu, acc[i][t], o);
+            if (lane == 0) red[warp][i][t] = acc[i][t];
+        }
+    if (p.wpr > 1) __syncthreads();
+    else __syncwarp();
+    const int t = lane % TT, r = lane / TT;
+    if (part || r >= R || f0 + r >= p.N) return;
+    float v[2] = {};
+    for (int w = 0; w < p.wpr; ++w)
+#pragma unroll
+        for (int m = 0; m < NM; ++m) v[m] += red[warp + w][m * R + r][t];
+    epilogue1<T, MODE>(p.e, t, f0 + r, v[0], v[1]);
+}
+
+template <typename T, int MODE, int TT, int R> cudaError_t run_gemv(const GvParams &p, cudaStream_t s)
+{
+    const int per = kGvWarps / p.wpr * R;
+    return launch_pdl(gemv_rows<T, MODE, TT, R>, dim3((p.N + per - 1) / per), dim3(32 * kGvWarps), 0, s, p);
+}
+
+template <typename T, int MODE> cudaError_t pick_gemv(const GvParams &p, cudaStream_t s)
+{
+    constexpr int NM = MODE == EPI_GATED ? 2 : 1;
+    return p.T == 1   ? run_gemv<T, MODE, 1, 1>(p, s)
+           : p.T == 2 ? run_gemv<T, MODE, 2, 2 / NM>(p, s)
+           : p.T == 3 ? run_gemv<T, MODE, 3, 2 / NM>(p, s)
+                      : run_gemv<T, MODE, 4, 2 / NM>(p, s);
+}
+
+template <typename T> cudaError_t gemv(const Gemm &g, const CtxView &v)
+{
+    GvParams p = {};
+    p.T = g.M, p.N = g.N, p.K = g.K[0];
+    p.x = static_cast<const uint16_t *>(g.a[0].p), p.ldx = g.a[0].ld;
+    const int nm = g.mode == EPI_GATED ? 2 : 1;
+    for (int m = 0; m < nm; ++m) p.w[m] = static_cast<const uint16_t *>(g.b[m].p), p.ldw[m] = g.b[m].ld;
+    // warps to a group of rows: one, unless there are too few rows for about
+    // 54 warps' work per SM (8192 x K at one token: 1, 2, 4 and 8 warps
+    // 70, 70, 69, 70 us at K = 28672; 2048 rows 32, 23, 20, 21 us; 28672 rows of 1024 13, 18, 26, 41 us)
+    const int rows = p.T == 1 ? nm : 2; // rows of a group
+    const int64_t groups = (int64_t)p.N * nm / rows;
+    p.wpr = 1;
+    while (p.wpr < kGvWarps && groups * p.wpr < 54 * (int64_t)v.sms && p.K >= 2048 * p.wpr) p.wpr *= 2;
+    p.e = g.e;
+    return g.mode == EPI_GATED ? pick_gemv<T, EPI_GATED>(p, v.stream) : pick_gemv<T, EPI_LINEAR>(p, v.stream);
+}
+
+// One token: always (8192 x 28672: 70 us, 6.7 TB/s; skinny_tc 80 us).  Two to
+// four: matrices of up to this many bytes; beyond, the reads of x through L1
+// cost more than skinny_tc's second launch (4 tokens, 8.4, 34, 134 and 268 MB:
+// 4.4, 9, 27 and 52 us, skinny_tc 8, 13, 29 and 49 us).
+constexpr int64_t kGemvBytes = 128 << 20;
+
+bool gemv_takes(const Gemm &g)
+{
+    const int64_t bytes = (int64_t)g.N * g.K[0] * 2 * (g.mode == EPI_GATED ? 2 : 1);
+    return g.M == 1 || (g.M <= kGvTokens && bytes <= kGemvBytes);
+}
+
 SkParams plan(const Gemm &g, const CtxView &v)
 {
     SkParams p = {};
@@ -192,6 +339,7 @@ SkParams plan(const Gemm &g, const CtxView &v)
     p.slotB = kWTile + (uint32_t)p.Tp * 128u;
     p.slots = std::min(kMaxRing, (v.smem_optin - 1024) / (int)p.slotB);
     p.status = v.status, p.abort_flag = v.abort_flag, p.wait_ns = v.wait_ns;
+    p.early = g.early;
     p.e = g.e;
     return p;
 }
@@ -228,12 +376,14 @@ bool skinny_takes(const Gemm &g)
 
 size_t skinny_workspace(const Gemm &g, const CtxView &v)
 {
+    if (gemv_takes(g)) return 0;
     const SkParams p = plan(g, v);
     return (size_t)p.tiles * p.smax * p.T * 128 * sizeof(float);
 }
 
 cudaError_t launch_skinny(const Gemm &g, bool bf16, const CtxView &v, void *ws)
 {
+    if (gemv_takes(g)) return bf16 ? gemv<__nv_bfloat16>(g, v) : gemv<__half>(g, v);
     SkParams p = plan(g, v);
     p.part = static_cast<float *>(ws);
     const int nm = g.mode == EPI_GATED ? 2 : 1;

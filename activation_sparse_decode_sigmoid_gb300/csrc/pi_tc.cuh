@@ -219,6 +219,32 @@ __device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t ncols)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
 }
 
+// c + the eight products of a 16-bit chunk pair, in element order (the
+// mixed-precision fma multiplies the exactly widened operands, rounds once)
+template <typename T> __device__ __forceinline__ float fma8(const uint4 &w, const uint4 &x, float c);
+template <> __device__ __forceinline__ float fma8<__half>(const uint4 &w, const uint4 &x, float c)
+{
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{ .reg .b16 al, ah, bl, bh; mov.b32 {al, ah}, %1; mov.b32 {bl, bh}, %2;"
+            " fma.rn.f32.f16 %0, al, bl, %0; fma.rn.f32.f16 %0, ah, bh, %0; }"
+            : "+f"(c)
+            : "r"(a[i]), "r"(b[i]));
+    return c;
+}
+template <> __device__ __forceinline__ float fma8<__nv_bfloat16>(const uint4 &w, const uint4 &x, float c)
+{
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{ .reg .b16 al, ah, bl, bh; mov.b32 {al, ah}, %1; mov.b32 {bl, bh}, %2;"
+            " fma.rn.f32.bf16 %0, al, bl, %0; fma.rn.f32.bf16 %0, ah, bh, %0; }"
+            : "+f"(c)
+            : "r"(a[i]), "r"(b[i]));
+    return c;
+}
+
 __device__ __forceinline__ int slice_at(int m, int c, int G) { return (int)(((long long)m * c) / G); }
 
 __device__ __forceinline__ int list_len(const MmaParams &p, int n)
