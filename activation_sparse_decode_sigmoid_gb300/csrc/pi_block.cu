@@ -68,10 +68,11 @@ __global__ void __launch_bounds__(256) dact_rows(const void *dy, int dy32, int64
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= scale;
             if (fn != PI_FN_NONE) {
-                float zz[8];
+                float zz[8], f[8], df[8];
                 load8<T>(z + (int64_t)r * ldz + c, n, vec & 2, zz);
+                both8(fn, zz, f, df);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= act_df(fn, zz[i]);
+                for (int i = 0; i < 8; ++i) v[i] *= df[i];
             }
             if (dz) store8<T>(dz + (int64_t)r * lddz + c, n, vec & 4, v);
 #pragma unroll

@@ -35,51 +35,99 @@ template <> struct C16<__nv_bfloat16> {
 // smooth functions below equal their limits in fp32, and inf * 0 is avoided.
 __device__ __forceinline__ float clampn(float z, float lim) { return z < -lim ? -lim : (z > lim ? lim : z); }
 
-// fn(z).  __expf's error is a few units in the last place for the arguments
-// that matter, far below the 16-bit rounding that follows every use.
-__device__ __forceinline__ float act_f(int fn, float z)
+// fn(z), and with both also fn'(z), which shares its exponential.  __expf's
+// error is a few units in the last place for the arguments that matter, far
+// below the 16-bit rounding that follows every use.
+template <int FN> __device__ __forceinline__ float act_one(float z)
 {
-    switch (fn) {
-    case PI_FN_RELU: return z < 0.f ? 0.f : z;
-    case PI_FN_SQRELU: return z < 0.f ? 0.f : z * z;
-    case PI_FN_SIGMOID: return __fdividef(1.f, 1.f + __expf(-z)); // (0 below -87)
-    case PI_FN_SILU: return z < -80.f ? -0.f : __fdividef(z, 1.f + __expf(-z));
-    case PI_FN_GELU: return z < -30.f ? -0.f : 0.5f * z * (1.f + erff(z * 0.70710678f));
-    case PI_FN_GELU_TANH: {
-        // z (1 + tanh t) / 2 = z / (1 + exp(-2 t))
+    if (FN == PI_FN_RELU) return z < 0.f ? 0.f : z;
+    if (FN == PI_FN_SQRELU) return z < 0.f ? 0.f : z * z;
+    if (FN == PI_FN_SIGMOID) return __fdividef(1.f, 1.f + __expf(-z)); // (0 below -87)
+    if (FN == PI_FN_SILU) return z < -80.f ? -0.f : __fdividef(z, 1.f + __expf(-z));
+    if (FN == PI_FN_GELU) return z < -30.f ? -0.f : 0.5f * z * (1.f + erff(z * 0.70710678f));
+    if (FN == PI_FN_GELU_TANH) { // z (1 + tanh t) / 2 = z / (1 + exp(-2 t))
         const float c = clampn(z, 30.f);
         const float t = 0.79788456f * (c + 0.044715f * c * c * c);
         return z < -30.f ? -0.f : __fdividef(z, 1.f + __expf(-2.f * clampn(t, 40.f)));
     }
-    default: return z;
-    }
+    return z;
 }
 
-__device__ __forceinline__ float act_df(int fn, float z)
+template <int FN> __device__ __forceinline__ void act_both(float z, float &f, float &df)
 {
-    switch (fn) {
-    case PI_FN_RELU: return z > 0.f ? 1.f : 0.f;
-    case PI_FN_SQRELU: return z < 0.f ? 0.f : 2.f * z;
-    case PI_FN_SIGMOID: {
-        const float p = __fdividef(1.f, 1.f + __expf(-clampn(z, 80.f)));
-        return p * (1.f - p);
-    }
-    case PI_FN_SILU: {
+    if (FN == PI_FN_RELU) f = z < 0.f ? 0.f : z, df = z > 0.f ? 1.f : 0.f;
+    else if (FN == PI_FN_SQRELU) f = z < 0.f ? 0.f : z * z, df = z < 0.f ? 0.f : 2.f * z;
+    else if (FN == PI_FN_SIGMOID || FN == PI_FN_SILU) {
         const float c = clampn(z, 80.f);
         const float p = __fdividef(1.f, 1.f + __expf(-c));
-        return p * (1.f + c * (1.f - p));
-    }
-    case PI_FN_GELU: {
+        if (FN == PI_FN_SIGMOID) f = p, df = p * (1.f - p);
+        else f = z < -80.f ? -0.f : z * p, df = p * (1.f + c * (1.f - p));
+    } else if (FN == PI_FN_GELU) {
         const float c = clampn(z, 30.f);
-        return 0.5f * (1.f + erff(c * 0.70710678f)) + 0.39894228f * c * __expf(-0.5f * c * c);
-    }
-    case PI_FN_GELU_TANH: {
+        const float p = 0.5f * (1.f + erff(c * 0.70710678f));
+        f = z < -30.f ? -0.f : z * p;
+        df = p + 0.39894228f * c * __expf(-0.5f * c * c);
+    } else if (FN == PI_FN_GELU_TANH) {
         const float c = clampn(z, 10.f);
         const float t = 0.79788456f * (c + 0.044715f * c * c * c);
         const float p = __fdividef(1.f, 1.f + __expf(-2.f * clampn(t, 40.f))); // (1 + tanh t) / 2
-        return p + 2.f * c * p * (1.f - p) * 0.79788456f * (1.f + 0.134145f * c * c);
+        f = z < -10.f ? -0.f : z * p;
+        df = p + 2.f * c * p * (1.f - p) * 0.79788456f * (1.f + 0.134145f * c * c);
+    } else
+        f = z, df = 1.f;
+}
+
+template <int FN> __device__ __forceinline__ void act8_of(float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_one<FN>(v[i]);
+}
+
+template <int FN> __device__ __forceinline__ void both8_of(const float (&z)[8], float (&f)[8], float (&df)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) act_both<FN>(z[i], f[i], df[i]);
+}
+
+// (The choice of function stays outside the 8 elements: inside an unrolled
+// loop it filled the instruction cache, and a 2048 x 28672 x 8192 product
+// with EPI_DACT took 1055 us.)
+__device__ __forceinline__ void act8(int fn, float (&v)[8])
+{
+    switch (fn) {
+    case PI_FN_RELU: act8_of<PI_FN_RELU>(v); break;
+    case PI_FN_SQRELU: act8_of<PI_FN_SQRELU>(v); break;
+    case PI_FN_SIGMOID: act8_of<PI_FN_SIGMOID>(v); break;
+    case PI_FN_SILU: act8_of<PI_FN_SILU>(v); break;
+    case PI_FN_GELU: act8_of<PI_FN_GELU>(v); break;
+    case PI_FN_GELU_TANH: act8_of<PI_FN_GELU_TANH>(v); break;
+    default: break;
     }
-    default: return 1.f;
+}
+
+__device__ __forceinline__ void both8(int fn, const float (&z)[8], float (&f)[8], float (&df)[8])
+{
+    switch (fn) {
+    case PI_FN_RELU: both8_of<PI_FN_RELU>(z, f, df); break;
+    case PI_FN_SQRELU: both8_of<PI_FN_SQRELU>(z, f, df); break;
+    case PI_FN_SIGMOID: both8_of<PI_FN_SIGMOID>(z, f, df); break;
+    case PI_FN_SILU: both8_of<PI_FN_SILU>(z, f, df); break;
+    case PI_FN_GELU: both8_of<PI_FN_GELU>(z, f, df); break;
+    case PI_FN_GELU_TANH: both8_of<PI_FN_GELU_TANH>(z, f, df); break;
+    default: both8_of<PI_FN_NONE>(z, f, df); break;
+    }
+}
+
+__device__ __forceinline__ float act1(int fn, float z)
+{
+    switch (fn) {
+    case PI_FN_RELU: return act_one<PI_FN_RELU>(z);
+    case PI_FN_SQRELU: return act_one<PI_FN_SQRELU>(z);
+    case PI_FN_SIGMOID: return act_one<PI_FN_SIGMOID>(z);
+    case PI_FN_SILU: return act_one<PI_FN_SILU>(z);
+    case PI_FN_GELU: return act_one<PI_FN_GELU>(z);
+    case PI_FN_GELU_TANH: return act_one<PI_FN_GELU_TANH>(z);
+    default: return z;
     }
 }
 
@@ -160,10 +208,7 @@ __device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int 
             for (int i = 0; i < 8; ++i) v[i] += b[i];
         }
         if (e.out2) store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
-        if (e.fn != PI_FN_NONE) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = act_f(e.fn, v[i]);
-        }
+        act8(e.fn, v);
         if (e.scale != 1.f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= e.scale;
@@ -192,25 +237,27 @@ __device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int 
         }
         if (e.out2) store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
         if (e.out3) store8<T>(e.out3 + row * e.ld3 + col, n, e.vec & V_OUT3, v2);
+        act8(e.fn, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_f(e.fn, v[i]) * v2[i];
+        for (int i = 0; i < 8; ++i) v[i] *= v2[i];
         store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);
     } else {
-        float g[8];
+        float g[8], f[8], df[8];
         load8<T>(e.in1 + row * e.ldi1 + col, n, e.vec & V_IN1, g);
+        both8(e.fn, g, f, df);
         if (e.in2) {
             float u[8];
             load8<T>(e.in2 + row * e.ldi2 + col, n, e.vec & V_IN2, u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                u[i] *= v[i] * act_df(e.fn, g[i]);
-                v[i] *= act_f(e.fn, g[i]);
+                u[i] *= v[i] * df[i];
+                v[i] *= f[i];
             }
             store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, u);
             store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= e.scale * act_df(e.fn, g[i]);
+            for (int i = 0; i < 8; ++i) v[i] *= e.scale * df[i];
             store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);
         }
     }
@@ -224,7 +271,7 @@ __device__ __forceinline__ void epilogue1(const Epi &e, int64_t row, int col, fl
     if (MODE == EPI_GATED && e.bias2) v2 += C16<T>::one(e.bias2[col]);
     if (e.out2) e.out2[row * e.ld2 + col] = C16<T>::round(v);
     if (MODE == EPI_GATED && e.out3) e.out3[row * e.ld3 + col] = C16<T>::round(v2);
-    v = act_f(e.fn, v);
+    v = act1(e.fn, v);
     if (MODE == EPI_GATED) v *= v2;
     else {
         v *= e.scale;

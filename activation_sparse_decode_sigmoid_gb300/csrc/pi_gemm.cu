@@ -195,6 +195,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 8 consecutive columns of this thread's lane (tmem_wait before their use)
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void to_float(const uint32_t (&r)[8], float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// After a failure: copies and MMAs in flight finish within microseconds; the
+// CTA stays for a bounded time that covers them.
+__device__ __forceinline__ void linger()
+{
+    const uint64_t t0 = gtimer();
+    while (gtimer() - t0 < 5000000ull) {
+    }
+}
+
 // ------------------------------------------------------------------ boxes of the epilogue
 // A warp's box: row r (lane) at 64 r, 16-byte chunk j at j ^ ((r >> 1) & 3)
 // (the 64-byte TMA swizzle; 8 lanes' chunks fall into different banks).
@@ -279,15 +302,6 @@ __device__ __forceinline__ void box_fetch(uint32_t box, int lane, const CUtensor
         }
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
         __syncwarp();
-    }
-}
-
-// After a failure: copies and MMAs in flight finish within microseconds; the
-// CTA stays for a bounded time that covers them.
-__device__ __forceinline__ void linger()
-{
-    const uint64_t t0 = gtimer();
-    while (gtimer() - t0 < 5000000ull) {
     }
 }
 
@@ -409,6 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         uint64_t *bar0 = in_full + 2 * warp, *bar1 = bar0 + 1;
         uint32_t fetched = 0; // fetches into each box so far
         const Epi &e = p.e;
+        Epi e_out = e; // (fp32 outputs: z has been kept by its own pass)
+        e_out.out2 = nullptr;
         const bool aux = e.out2 || e.out3, has_in = MODE == EPI_DACT || (MODE == EPI_LINEAR && e.res && !e.out32), two = MODE == EPI_DACT && e.in2;
         const uint16_t *in1 = MODE == EPI_DACT ? e.in1 : static_cast<const uint16_t *>(e.res);
         const int64_t ldi1 = MODE == EPI_DACT ? e.ldi1 : e.ldr;
@@ -450,23 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 for (int c = 0; c < kCols; c += 32) {
                     const int col = col0 + c;
                     if (col >= p.N) break;
-                    float v[32], u[MODE == EPI_GATED ? 32 : 1];
-                    tmem_ld32(ta + half * kCols + c, v);
-                    if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
-                    if (c + 32 >= kCols || col + 32 >= p.N) {
-                        // the accumulator is in registers: the next tile's products may begin
-                        tc_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
-                    }
-                    if (MODE == EPI_LINEAR && e.out32) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (row0 + lane < p.M && col + 8 * j < p.N)
-                                epilogue8<T, MODE>(e, p.N, row0 + lane, col + 8 * j, *reinterpret_cast<float(*)[8]>(v + 8 * j),
-                                                   *reinterpret_cast<float(*)[8]>(v + 8 * j));
-                        continue;
-                    }
+                    const bool last = c + 32 >= kCols || col + 32 >= p.N;
                     if (has_in) {
                         if (c) fetch(col);
                         ok = mbar_wait_bounded(bar0, (fetched - 1) & 1, p) && (!two || mbar_wait_bounded(bar1, (fetched - 1) & 1, p));
@@ -474,72 +474,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     }
                     const uint32_t box = has_in || aux || !((c >> 5) & 1) ? box0 : box1;
                     if (!has_in) box_wait_read(lane, aux);
-                    if (MODE == EPI_LINEAR || MODE == EPI_GATED) {
-#pragma unroll
+                    // passes over the chunk: the pre-activation g or z, u (only if they are kept), then the output
+                    const int pass0 = e.out2 && MODE != EPI_DACT ? 0 : e.out3 ? 1 : 2;
+#pragma unroll 1
+                    for (int pass = pass0; pass < 3; ++pass) {
+                        if (pass == 1 && !e.out3) continue;
+                        if (pass == 1 && pass0 == 0) box_wait_read(lane, true);
+#pragma unroll 1
                         for (int j = 0; j < 4; ++j) {
-                            float b[8];
-                            if (e.bias) {
-                                load8<T>(e.bias + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS, b);
+                            uint32_t rv[8], ru[8];
+                            float v[8], u[8];
+                            tmem_ld8(ta + half * kCols + c + 8 * j, rv);
+                            if (MODE == EPI_GATED) tmem_ld8(ta + 128 + half * kCols + c + 8 * j, ru);
+                            tmem_wait();
+                            to_float(rv, v);
+                            if (MODE == EPI_GATED) to_float(ru, u);
+                            if (last && j == 3 && pass == 2) {
+                                // the accumulator has been read: the next tile's products may begin
+                                tc_before();
+                                __syncwarp();
+                                if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
+                            }
+                            const int cj = col + 8 * j;
+                            if (MODE == EPI_LINEAR && e.out32 && pass == 2) {
+                                if (row0 + lane < p.M && cj < p.N) epilogue8<T, MODE>(e_out, p.N, row0 + lane, cj, v, v);
+                                continue;
+                            }
+                            if (MODE != EPI_DACT && e.bias) {
+                                float b[8];
+                                load8<T>(e.bias + cj, p.N - cj, e.vec & V_BIAS, b);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
+                                for (int i = 0; i < 8; ++i) v[i] += b[i];
                             }
                             if (MODE == EPI_GATED && e.bias2) {
-                                load8<T>(e.bias2 + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS2, b);
+                                float b[8];
+                                load8<T>(e.bias2 + cj, p.N - cj, e.vec & V_BIAS2, b);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) u[(8 * j + i) % (MODE == EPI_GATED ? 32 : 1)] += b[i];
+                                for (int i = 0; i < 8; ++i) u[i] += b[i];
                             }
-                            if (e.out2) box_put<T>(box1, lane, j, v + 8 * j);
-                        }
-                        if (e.out2) box_send(box1, lane, &p.mout2, e.vec & V_OUT2, e.out2, e.ld2, row0, col, p.M, p.N);
-                    }
-                    if (MODE == EPI_GATED && e.out3) {
-                        if (e.out2) box_wait_read(lane, true);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) box_put<T>(box1, lane, j, u + (8 * j) % (MODE == EPI_GATED ? 32 : 1));
-                        box_send(box1, lane, &p.mout3, e.vec & V_OUT3, e.out3, e.ld3, row0, col, p.M, p.N);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float *x = v + 8 * j;
-                        if (MODE == EPI_LINEAR) {
-                            if (e.fn != PI_FN_NONE) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] = act_f(e.fn, x[i]);
+                            if (pass == 0) {
+                                box_put<T>(box1, lane, j, v);
+                                continue;
                             }
-                            if (e.scale != 1.f) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] *= e.scale;
+                            if (MODE == EPI_GATED && pass == 1) {
+                                box_put<T>(box1, lane, j, u);
+                                continue;
                             }
-                            if (has_in) {
-                                float r[8];
-                                box_get<T>(box0, lane, j, r);
+                            if (MODE == EPI_LINEAR) {
+                                act8(e.fn, v);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] += r[i];
-                            }
-                        } else if (MODE == EPI_GATED) {
+                                for (int i = 0; i < 8; ++i) v[i] *= e.scale;
+                                if (has_in) {
+                                    float r[8];
+                                    box_get<T>(box0, lane, j, r);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = act_f(e.fn, x[i]) * u[(8 * j + i) % (MODE == EPI_GATED ? 32 : 1)];
-                        } else {
-                            float g[8];
-                            box_get<T>(box0, lane, j, g);
-                            if (two) {
-                                float s[8];
-                                box_get<T>(box1, lane, j, s);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    s[i] *= x[i] * act_df(e.fn, g[i]);
-                                    x[i] *= act_f(e.fn, g[i]);
+                                    for (int i = 0; i < 8; ++i) v[i] += r[i];
                                 }
-                                box_put<T>(box1, lane, j, x); // du
+                            } else if (MODE == EPI_GATED) {
+                                act8(e.fn, v);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] = s[i];
+                                for (int i = 0; i < 8; ++i) v[i] *= u[i];
                             } else {
+                                float g[8], f[8], df[8];
+                                box_get<T>(box0, lane, j, g);
+                                both8(e.fn, g, f, df);
+                                if (two) {
+                                    box_get<T>(box1, lane, j, u);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] *= e.scale * act_df(e.fn, g[i]);
+                                    for (int i = 0; i < 8; ++i) f[i] *= v[i], v[i] *= u[i] * df[i];
+                                    box_put<T>(box1, lane, j, f); // du
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) v[i] *= e.scale * df[i];
+                                }
                             }
+                            box_put<T>(box, lane, j, v);
                         }
-                        box_put<T>(box, lane, j, x);
+                        if (pass == 0) box_send(box1, lane, &p.mout2, e.vec & V_OUT2, e.out2, e.ld2, row0, col, p.M, p.N);
+                        if (pass == 1) box_send(box1, lane, &p.mout3, e.vec & V_OUT3, e.out3, e.ld3, row0, col, p.M, p.N);
                     }
+                    if (MODE == EPI_LINEAR && e.out32) continue;
                     if (two) box_send(box1, lane, &p.mout2, e.vec & V_OUT2, e.out2, e.ld2, row0, col, p.M, p.N);
                     box_send(box, lane, &p.mout, e.vec & V_OUT, static_cast<uint16_t *>(e.out), e.ldo, row0, col, p.M, p.N);
                 }
