@@ -77,10 +77,10 @@ template <int FN> __device__ __forceinline__ void act_both(float z, float &f, fl
         f = z, df = 1.f;
 }
 
-template <int FN> __device__ __forceinline__ void act8_of(float (&v)[8])
+template <int FN, int W> __device__ __forceinline__ void act_of(float (&v)[W])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_one<FN>(v[i]);
+    for (int i = 0; i < W; ++i) v[i] = act_one<FN>(v[i]);
 }
 
 template <int FN> __device__ __forceinline__ void both8_of(const float (&z)[8], float (&f)[8], float (&df)[8])
@@ -89,18 +89,18 @@ template <int FN> __device__ __forceinline__ void both8_of(const float (&z)[8], 
     for (int i = 0; i < 8; ++i) act_both<FN>(z[i], f[i], df[i]);
 }
 
-// (The choice of function stays outside the 8 elements: inside an unrolled
+// (The choice of function stays outside the elements: inside an unrolled
 // loop it filled the instruction cache, and a 2048 x 28672 x 8192 product
 // with EPI_DACT took 1055 us.)
-__device__ __forceinline__ void act8(int fn, float (&v)[8])
+template <int W> __device__ __forceinline__ void acts(int fn, float (&v)[W])
 {
     switch (fn) {
-    case PI_FN_RELU: act8_of<PI_FN_RELU>(v); break;
-    case PI_FN_SQRELU: act8_of<PI_FN_SQRELU>(v); break;
-    case PI_FN_SIGMOID: act8_of<PI_FN_SIGMOID>(v); break;
-    case PI_FN_SILU: act8_of<PI_FN_SILU>(v); break;
-    case PI_FN_GELU: act8_of<PI_FN_GELU>(v); break;
-    case PI_FN_GELU_TANH: act8_of<PI_FN_GELU_TANH>(v); break;
+    case PI_FN_RELU: act_of<PI_FN_RELU>(v); break;
+    case PI_FN_SQRELU: act_of<PI_FN_SQRELU>(v); break;
+    case PI_FN_SIGMOID: act_of<PI_FN_SIGMOID>(v); break;
+    case PI_FN_SILU: act_of<PI_FN_SILU>(v); break;
+    case PI_FN_GELU: act_of<PI_FN_GELU>(v); break;
+    case PI_FN_GELU_TANH: act_of<PI_FN_GELU_TANH>(v); break;
     default: break;
     }
 }
@@ -208,7 +208,7 @@ __device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int 
             for (int i = 0; i < 8; ++i) v[i] += b[i];
         }
         if (e.out2) store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
-        act8(e.fn, v);
+        acts(e.fn, v);
         if (e.scale != 1.f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= e.scale;
@@ -237,7 +237,7 @@ __device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int 
         }
         if (e.out2) store8<T>(e.out2 + row * e.ld2 + col, n, e.vec & V_OUT2, v);
         if (e.out3) store8<T>(e.out3 + row * e.ld3 + col, n, e.vec & V_OUT3, v2);
-        act8(e.fn, v);
+        acts(e.fn, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= v2[i];
         store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);

@@ -25,12 +25,12 @@
 // MN-major forms, 128-byte swizzle), so the backward products read dz, W and
 // x as they lie.
 //
-// The epilogue moves its tiles of outputs (and of the inputs it needs: the
-// residual, or g and u) through shared memory in boxes of 32 x 32 per warp,
-// by TMA where rows are 16-byte aligned, else element by element with the
-// lanes along a row.  (A thread holds one row of the accumulator; writing it
-// straight to memory, 16 bytes in each of 32 rows at a time, took 8 us a tile
-// against 4 us for the products of 1024 values of k.)
+// A thread of the epilogue holds one row of the accumulator; outputs, and the
+// inputs that the epilogue needs (the residual, or g and u), pass through
+// shared memory in boxes of 32 x 32 per warp, so that memory sees 64
+// consecutive bytes per row.  (Straight from the registers, 16 bytes in each
+// of 32 rows at a time, or by TMA stores of such boxes, a 256 x 256 tile took
+// 6.5 us or more; its products take 4.3 us at 1024 values of k.)
 //
 // Every wait is bounded; after one that ran out a pair stops issuing, waits
 // for what it has in flight, frees its tensor memory and returns.
@@ -62,7 +62,6 @@ constexpr uint32_t kBoxes = kEpiWarps * 2 * kBox;
 
 struct TcParams {
     CUtensorMap ma[2], mb[2];
-    CUtensorMap mout, mout2, mout3, min1, min2; // boxes of 32 x 32 (out; in1 also the residual)
     int M, N, tm, tn;     // tiles along M and N
     int kt0, KT;          // k steps of the first segment, and of all
     int a_mn, b_mn;
@@ -195,20 +194,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 8 consecutive columns of this thread's lane (tmem_wait before their use)
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void to_float(const uint32_t (&r)[8], float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // After a failure: copies and MMAs in flight finish within microseconds; the
 // CTA stays for a bounded time that covers them.
 __device__ __forceinline__ void linger()
@@ -219,90 +204,95 @@ __device__ __forceinline__ void linger()
 }
 
 // ------------------------------------------------------------------ boxes of the epilogue
-// A warp's box: row r (lane) at 64 r, 16-byte chunk j at j ^ ((r >> 1) & 3)
-// (the 64-byte TMA swizzle; 8 lanes' chunks fall into different banks).
+// A warp's box: row r at 64 r, 16-byte chunk j at j ^ ((r >> 1) & 3): 8 lanes'
+// chunks fall into different banks, by rows and by chunks of a row.
 __device__ __forceinline__ uint32_t box_at(uint32_t box, int r, int j) { return box + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
 
-__device__ __forceinline__ void box_wait_read(int lane, bool all)
+__device__ __forceinline__ void sts16(uint32_t at, const uint4 &q)
 {
-    if (lane == 0) {
-        if (all) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    }
-    __syncwarp();
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
 }
-
-template <typename T> __device__ __forceinline__ void box_put(uint32_t box, int lane, int j, const float *v)
-{
-    const uint32_t a = C16<T>::round2(v[0], v[1]), b = C16<T>::round2(v[2], v[3]), c = C16<T>::round2(v[4], v[5]),
-                   d = C16<T>::round2(v[6], v[7]);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_at(box, lane, j)), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
-}
-
-template <typename T> __device__ __forceinline__ void box_get(uint32_t box, int lane, int j, float (&v)[8])
+__device__ __forceinline__ uint4 lds16(uint32_t at)
 {
     uint4 q;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(box_at(box, lane, j)));
-    unpack8<T>(q, v);
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+    return q;
 }
 
-// The box as rows [row, row + 32), columns [col, col + 32) of an output; what
-// lies outside is left out.  (A TMA store cuts a row at 16 bytes, not at an
-// element: a row's end inside a 16-byte chunk takes the other way.)
-__device__ __forceinline__ void box_send(uint32_t box, int lane, const CUtensorMap *tm, bool tma, uint16_t *out, int64_t ld,
-                                         int row, int col, int M, int N)
+// 32 columns of this thread's row into the box
+template <typename T> __device__ __forceinline__ void box_put(uint32_t box, int lane, const float (&v)[32])
 {
-    if (tma && (col + 32 <= N || N % 8 == 0)) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tm),
-                         "r"(box), "r"(col), "r"(row)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sts16(box_at(box, lane, j), pack8<T>(*reinterpret_cast<const float(*)[8]>(v + 8 * j)));
+}
+
+// A matrix that the epilogue reads or writes, seen from a warp: lane l moves
+// chunk l mod 4 of rows l / 4, l / 4 + 8, ...; rows that are not 16-byte
+// aligned, and the last columns of others, element by element.
+struct Strip {
+    uint16_t *p;
+    int64_t ld;
+    bool vec;
+};
+
+// 32 x 32 values at (row, col) on their way into the box: loads now, box later
+__device__ __forceinline__ void strip_load(const Strip &s, int lane, int row, int col, int M, int N, uint4 (&q)[4])
+{
+    const int c = col + (lane & 3) * 8, n = N - c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = row + i * 8 + (lane >> 2);
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (r >= M || n <= 0) continue;
+        const uint16_t *p = s.p + r * s.ld + c;
+        if (s.vec && n >= 8) q[i] = *reinterpret_cast<const uint4 *>(p);
+        else {
+            uint32_t w[4] = {};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < n) w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+            q[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-    } else {
-        __syncwarp();
-        if (col + lane < N) {
-            uint16_t *o = out + (int64_t)row * ld + col + lane;
-            const int rows = min(32, M - row);
-#pragma unroll 8
-            for (int r = 0; r < rows; ++r, o += ld) {
-                uint16_t v;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box_at(box, r, lane >> 3) + (lane & 7) * 2));
-                *o = v;
+    }
+}
+
+__device__ __forceinline__ void strip_to_box(uint32_t box, int lane, const uint4 (&q)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sts16(box_at(box, i * 8 + (lane >> 2), lane & 3), q[i]);
+}
+
+// The box into rows [row, row + 32), columns [col, col + 32); what lies outside is left out.
+__device__ __forceinline__ void box_send(uint32_t box, const Strip &s, int lane, int row, int col, int M, int N)
+{
+    __syncwarp();
+    const int c = col + (lane & 3) * 8, n = N - c;
+    if (s.vec) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = row + i * 8 + (lane >> 2);
+            if (r >= M || n <= 0) continue;
+            const uint4 q = lds16(box_at(box, i * 8 + (lane >> 2), lane & 3));
+            uint16_t *p = s.p + r * s.ld + c;
+            if (n >= 8) *reinterpret_cast<uint4 *>(p) = q;
+            else {
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
             }
         }
-        __syncwarp();
-    }
-}
-
-// The reverse: starts a copy of an input into the box (arriving on bar), or makes it element by element.
-__device__ __forceinline__ void box_fetch(uint32_t box, int lane, const CUtensorMap *tm, bool tma, const uint16_t *in,
-                                          int64_t ld, int row, int col, int M, int N, uint64_t *bar)
-{
-    if (tma) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // (after this warp's accesses to the box)
-        __syncwarp();
-        if (lane == 0) {
-            mbar_expect(bar, kBox);
-            asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-                             box),
-                         "l"(tm), "r"(smem_addr(bar)), "r"(col), "r"(row)
-                         : "memory");
-        }
-    } else {
-        const bool in_n = col + lane < N;
-        const uint16_t *p = in + (int64_t)row * ld + col + lane;
+    } else if (col + lane < N) {
+        uint16_t *o = s.p + row * s.ld + col + lane;
+        const int rows = min(32, M - row);
 #pragma unroll 8
-        for (int r = 0; r < 32; ++r) {
-            const uint16_t v = in_n && row + r < M ? p[r * ld] : (uint16_t)0;
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(box_at(box, r, lane >> 3) + (lane & 7) * 2), "h"(v) : "memory");
+        for (int r = 0; r < rows; ++r, o += s.ld) {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box_at(box, r, lane >> 3) + (lane & 7) * 2) : "memory");
+            *o = v;
         }
-        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-        __syncwarp();
     }
+    __syncwarp();
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -318,12 +308,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     uint64_t *empty = full + kStages;
     uint64_t *acc_full = empty + kStages;  // [2]
     uint64_t *acc_empty = acc_full + 2;    // [2], used in the first CTA
-    uint64_t *in_full = acc_empty + 2;     // [8][2], one per box
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(in_full + 2 * kEpiWarps);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init1(full + s), mbar_init1(empty + s);
         for (int s = 0; s < 2; ++s) mbar_init1(acc_full + s), mbar_init(acc_empty + s, 2 * kEpiWarps);
-        for (int s = 0; s < 2 * kEpiWarps; ++s) mbar_init1(in_full + s);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -420,15 +408,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         const int q = warp & 3, half = warp >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t box0 = base + kStages * kStageBytes + (uint32_t)warp * 2 * kBox, box1 = box0 + kBox;
-        uint64_t *bar0 = in_full + 2 * warp, *bar1 = bar0 + 1;
-        uint32_t fetched = 0; // fetches into each box so far
         const Epi &e = p.e;
-        Epi e_out = e; // (fp32 outputs: z has been kept by its own pass)
-        e_out.out2 = nullptr;
-        const bool aux = e.out2 || e.out3, has_in = MODE == EPI_DACT || (MODE == EPI_LINEAR && e.res && !e.out32), two = MODE == EPI_DACT && e.in2;
-        const uint16_t *in1 = MODE == EPI_DACT ? e.in1 : static_cast<const uint16_t *>(e.res);
-        const int64_t ldi1 = MODE == EPI_DACT ? e.ldi1 : e.ldr;
-        const bool t_in1 = (e.vec & (MODE == EPI_DACT ? V_IN1 : V_RES)) != 0;
+        const bool two = MODE == EPI_DACT && e.in2, out32 = MODE == EPI_LINEAR && e.out32;
+        const bool has_in = MODE == EPI_DACT || (MODE == EPI_LINEAR && e.res && !out32);
+        const Strip out = {static_cast<uint16_t *>(e.out), e.ldo, (e.vec & V_OUT) != 0};
+        const Strip out2 = {e.out2, e.ld2, (e.vec & V_OUT2) != 0}, out3 = {e.out3, e.ld3, (e.vec & V_OUT3) != 0};
+        const Strip in1 = MODE == EPI_DACT ? Strip{const_cast<uint16_t *>(e.in1), e.ldi1, (e.vec & V_IN1) != 0}
+                                           : Strip{static_cast<uint16_t *>(const_cast<void *>(e.res)), e.ldr, (e.vec & V_RES) != 0};
+        const Strip in2 = {const_cast<uint16_t *>(e.in2), e.ldi2, (e.vec & V_IN2) != 0};
         constexpr int kCols = kOutN / 2; // of this warp
         for (uint32_t it = 0; ok && walk.next(w); ++it) {
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
@@ -436,18 +423,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             tile_at(w.tile, p.tm, p.tn, mi, ni);
             const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * kOutN + half * kCols;
             const bool whole = w.slot < 0;
-            auto fetch = [&](int col) {
-                box_wait_read(lane, true); // (what was sent from the boxes has been read)
-                box_fetch(box0, lane, &p.min1, t_in1, in1, ldi1, row0, col, p.M, p.N, bar0);
-                if (two) box_fetch(box1, lane, &p.min2, e.vec & V_IN2, e.in2, e.ldi2, row0, col, p.M, p.N, bar1);
-                ++fetched;
-            };
-            const bool early = whole && has_in && row0 < p.M && col0 < p.N;
-            if (early) fetch(col0); // in flight while the products finish
+            uint4 q1[4], q2[4]; // the next chunk's inputs
+            if (whole && has_in) { // in flight while the products finish
+                strip_load(in1, lane, row0, col0, p.M, p.N, q1);
+                if (two) strip_load(in2, lane, row0, col0, p.M, p.N, q2);
+            }
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + buf, ph, p));
             if (!ok) break;
             tc_after();
             const uint32_t ta = lane_addr + buf * 256u;
+            bool released = false;
             if (!whole) {
                 const int r = (int)rank * 128 + q * 32 + lane; // row within the tile
                 float *dst = p.part + ((size_t)w.slot * kTile + r) * kTile;
@@ -466,104 +451,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 for (int c = 0; c < kCols; c += 32) {
                     const int col = col0 + c;
                     if (col >= p.N) break;
-                    const bool last = c + 32 >= kCols || col + 32 >= p.N;
+                    float v[32], u[MODE == EPI_GATED ? 32 : 1];
+                    tmem_ld32(ta + half * kCols + c, v);
+                    if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
+                    if (c + 32 >= kCols || col + 32 >= p.N) {
+                        // the accumulator is in registers: the next tile's products may begin
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
+                        released = true;
+                    }
                     if (has_in) {
-                        if (c) fetch(col);
-                        ok = mbar_wait_bounded(bar0, (fetched - 1) & 1, p) && (!two || mbar_wait_bounded(bar1, (fetched - 1) & 1, p));
-                        ok = __all_sync(0xffffffffu, ok);
-                    }
-                    const uint32_t box = has_in || aux || !((c >> 5) & 1) ? box0 : box1;
-                    if (!has_in) box_wait_read(lane, aux);
-                    // passes over the chunk: the pre-activation g or z, u (only if they are kept), then the output
-                    const int pass0 = e.out2 && MODE != EPI_DACT ? 0 : e.out3 ? 1 : 2;
-#pragma unroll 1
-                    for (int pass = pass0; pass < 3; ++pass) {
-                        if (pass == 1 && !e.out3) continue;
-                        if (pass == 1 && pass0 == 0) box_wait_read(lane, true);
-#pragma unroll 1
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t rv[8], ru[8];
-                            float v[8], u[8];
-                            tmem_ld8(ta + half * kCols + c + 8 * j, rv);
-                            if (MODE == EPI_GATED) tmem_ld8(ta + 128 + half * kCols + c + 8 * j, ru);
-                            tmem_wait();
-                            to_float(rv, v);
-                            if (MODE == EPI_GATED) to_float(ru, u);
-                            if (last && j == 3 && pass == 2) {
-                                // the accumulator has been read: the next tile's products may begin
-                                tc_before();
-                                __syncwarp();
-                                if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
-                            }
-                            const int cj = col + 8 * j;
-                            if (MODE == EPI_LINEAR && e.out32 && pass == 2) {
-                                if (row0 + lane < p.M && cj < p.N) epilogue8<T, MODE>(e_out, p.N, row0 + lane, cj, v, v);
-                                continue;
-                            }
-                            if (MODE != EPI_DACT && e.bias) {
-                                float b[8];
-                                load8<T>(e.bias + cj, p.N - cj, e.vec & V_BIAS, b);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] += b[i];
-                            }
-                            if (MODE == EPI_GATED && e.bias2) {
-                                float b[8];
-                                load8<T>(e.bias2 + cj, p.N - cj, e.vec & V_BIAS2, b);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) u[i] += b[i];
-                            }
-                            if (pass == 0) {
-                                box_put<T>(box1, lane, j, v);
-                                continue;
-                            }
-                            if (MODE == EPI_GATED && pass == 1) {
-                                box_put<T>(box1, lane, j, u);
-                                continue;
-                            }
-                            if (MODE == EPI_LINEAR) {
-                                act8(e.fn, v);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] *= e.scale;
-                                if (has_in) {
-                                    float r[8];
-                                    box_get<T>(box0, lane, j, r);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) v[i] += r[i];
-                                }
-                            } else if (MODE == EPI_GATED) {
-                                act8(e.fn, v);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] *= u[i];
-                            } else {
-                                float g[8], f[8], df[8];
-                                box_get<T>(box0, lane, j, g);
-                                both8(e.fn, g, f, df);
-                                if (two) {
-                                    box_get<T>(box1, lane, j, u);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) f[i] *= v[i], v[i] *= u[i] * df[i];
-                                    box_put<T>(box1, lane, j, f); // du
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) v[i] *= e.scale * df[i];
-                                }
-                            }
-                            box_put<T>(box, lane, j, v);
+                        strip_to_box(box0, lane, q1);
+                        if (two) strip_to_box(box1, lane, q2);
+                        if (!released) {
+                            strip_load(in1, lane, row0, col + 32, p.M, p.N, q1);
+                            if (two) strip_load(in2, lane, row0, col + 32, p.M, p.N, q2);
                         }
-                        if (pass == 0) box_send(box1, lane, &p.mout2, e.vec & V_OUT2, e.out2, e.ld2, row0, col, p.M, p.N);
-                        if (pass == 1) box_send(box1, lane, &p.mout3, e.vec & V_OUT3, e.out3, e.ld3, row0, col, p.M, p.N);
+                        __syncwarp();
                     }
-                    if (MODE == EPI_LINEAR && e.out32) continue;
-                    if (two) box_send(box1, lane, &p.mout2, e.vec & V_OUT2, e.out2, e.ld2, row0, col, p.M, p.N);
-                    box_send(box, lane, &p.mout, e.vec & V_OUT, static_cast<uint16_t *>(e.out), e.ldo, row0, col, p.M, p.N);
+                    if (MODE != EPI_DACT && e.bias) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float b[8];
+                            load8<T>(e.bias + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS, b);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
+                        }
+                    }
+                    if (MODE == EPI_GATED && e.bias2) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float b[8];
+                            load8<T>(e.bias2 + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS2, b);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) u[(8 * j + i) % (MODE == EPI_GATED ? 32 : 1)] += b[i];
+                        }
+                    }
+                    if (MODE != EPI_DACT && e.out2) {
+                        box_put<T>(box1, lane, v);
+                        box_send(box1, out2, lane, row0, col, p.M, p.N);
+                    }
+                    if (MODE == EPI_GATED && e.out3) {
+                        box_put<T>(box1, lane, *reinterpret_cast<float(*)[32]>(u));
+                        box_send(box1, out3, lane, row0, col, p.M, p.N);
+                    }
+                    if (MODE == EPI_DACT) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float g[8], f[8], df[8];
+                            unpack8<T>(lds16(box_at(box0, lane, j)), g);
+                            both8(e.fn, g, f, df);
+                            if (two) {
+                                float s[8];
+                                unpack8<T>(lds16(box_at(box1, lane, j)), s);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) f[i] *= v[8 * j + i], v[8 * j + i] *= s[i] * df[i];
+                                sts16(box_at(box1, lane, j), pack8<T>(f)); // du
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[8 * j + i] *= e.scale * df[i];
+                            }
+                        }
+                        if (two) box_send(box1, out2, lane, row0, col, p.M, p.N);
+                    } else {
+                        acts(e.fn, v);
+                        if (MODE == EPI_GATED) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= u[i % (MODE == EPI_GATED ? 32 : 1)];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= e.scale;
+                            if (out32) {
+                                if (row0 + lane < p.M)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        const int cj = col + 8 * j;
+                                        if (cj >= p.N) break;
+                                        float(&x)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * j);
+                                        if (e.res) {
+                                            float r[8];
+                                            load8f(static_cast<const float *>(e.res) + (int64_t)(row0 + lane) * e.ldr + cj, p.N - cj, e.vec & V_RES, r);
+#pragma unroll
+                                            for (int i = 0; i < 8; ++i) x[i] += r[i];
+                                        }
+                                        store8f(static_cast<float *>(e.out) + (int64_t)(row0 + lane) * e.ldo + cj, p.N - cj, e.vec & V_OUT, x);
+                                    }
+                                continue;
+                            }
+                            if (has_in) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    float r[8];
+                                    unpack8<T>(lds16(box_at(box0, lane, j)), r);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) v[8 * j + i] += r[i];
+                                }
+                            }
+                        }
+                    }
+                    box_put<T>(box0, lane, v);
+                    box_send(box0, out, lane, row0, col, p.M, p.N);
                 }
-                if (col0 < p.N) continue; // (released above)
             }
-            tc_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
+            if (!released) {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
+            }
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // everything sent is written
     }
     __syncwarp();
     if (*(volatile int *)p.abort_flag) linger();
@@ -648,7 +644,7 @@ cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K)
 
 template <typename T, int MODE> cudaError_t run(const TcParams &p, int pairs, cudaStream_t s)
 {
-    constexpr int smem = kStages * kStageBytes + kBoxes + (2 * kStages + 4 + 2 * kEpiWarps) * 8 + 16;
+    constexpr int smem = kStages * kStageBytes + kBoxes + (2 * kStages + 4) * 8 + 16;
     auto kern = gemm_tc<T, MODE>;
     static std::atomic<uint64_t> ready{0}; // devices whose limit has been raised
     int dev = 0;
@@ -693,19 +689,6 @@ cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws)
     const int nb = g.mode == EPI_GATED ? 2 : g.segs;
     for (int i = 0; i < nb && e == cudaSuccess; ++i)
         e = map_of(&p.mb[i], g.b[i], g.N, g.K[g.mode == EPI_GATED ? 0 : i]);
-    // the epilogue's boxes
-    auto boxes = [&](CUtensorMap *m, const void *base, int64_t ld, unsigned bit) {
-        if (e == cudaSuccess && base && (g.e.vec & bit))
-            e = encode_map(m, base, (uint64_t)g.N, (uint64_t)g.M, (uint64_t)ld * 2, 32, 32);
-    };
-    if (!g.e.out32) {
-        boxes(&p.mout, g.e.out, g.e.ldo, V_OUT);
-        boxes(&p.min1, g.e.res, g.e.ldr, V_RES);
-    }
-    boxes(&p.mout2, g.e.out2, g.e.ld2, V_OUT2);
-    boxes(&p.mout3, g.e.out3, g.e.ld3, V_OUT3);
-    boxes(&p.min1, g.e.in1, g.e.ldi1, V_IN1);
-    boxes(&p.min2, g.e.in2, g.e.ldi2, V_IN2);
     if (e != cudaSuccess) return e;
     const int pairs = std::min(v.sms / 2, std::max(std::min(p.nfull, v.sms / 2), p.parts));
     return bf16 ? run_mode<__nv_bfloat16>(g, p, pairs, v.stream) : run_mode<__half>(g, p, pairs, v.stream);

@@ -263,10 +263,9 @@ cudaError_t launch_rmsnorm_rows(const PredParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_predict_batch(const PredParams &p, bool bf16, int sms, cudaStream_t s);
 // the list of every neuron 0..n-1 (dense steps), with its trace copies
 cudaError_t launch_list_all(const PredParams &p, cudaStream_t s);
-// a 2D TMA map over a row-major 16-bit matrix: box = 64 columns (128-byte
-// swizzle) or 32 (64-byte swizzle) x box_rows rows
+// a 2D TMA map over a row-major 16-bit matrix: box = 64 columns x box_rows rows, 128-byte swizzle
 cudaError_t encode_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
-                       uint32_t box_rows, uint32_t box_cols = 64);
+                       uint32_t box_rows);
 
 cudaError_t launch_permute_rows(const void *src, void *dst, const int32_t *perm, int rows, size_t rowBytes,
                                 cudaStream_t s, size_t dstStride = 0);
