@@ -35,6 +35,17 @@ template <> struct C16<__nv_bfloat16> {
 // smooth functions below equal their limits in fp32, and inf * 0 is avoided.
 __device__ __forceinline__ float clampn(float z, float lim) { return z < -lim ? -lim : (z > lim ? lim : z); }
 
+// 1 - Phi(x) for x >= 0, as half of erfc(x / sqrt 2) by the rational
+// approximation 7.1.26 of Abramowitz and Stegun (absolute error 1.5e-7); ex =
+// exp(-x^2 / 2), which the derivative needs too.
+__device__ __forceinline__ float upper_tail(float x, float &ex)
+{
+    ex = __expf(-0.5f * x * x);
+    const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678f, x, 1.f));
+    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    return 0.5f * q * ex;
+}
+
 // fn(z), and with both also fn'(z), which shares its exponential.  __expf's
 // error is a few units in the last place for the arguments that matter, far
 // below the 16-bit rounding that follows every use.
@@ -44,7 +55,11 @@ template <int FN> __device__ __forceinline__ float act_one(float z)
     if (FN == PI_FN_SQRELU) return z < 0.f ? 0.f : z * z;
     if (FN == PI_FN_SIGMOID) return __fdividef(1.f, 1.f + __expf(-z)); // (0 below -87)
     if (FN == PI_FN_SILU) return z < -80.f ? -0.f : __fdividef(z, 1.f + __expf(-z));
-    if (FN == PI_FN_GELU) return z < -30.f ? -0.f : 0.5f * z * (1.f + erff(z * 0.70710678f));
+    if (FN == PI_FN_GELU) {
+        float ex;
+        const float q = upper_tail(fabsf(clampn(z, 30.f)), ex);
+        return z < -30.f ? -0.f : z * (z < 0.f ? q : 1.f - q);
+    }
     if (FN == PI_FN_GELU_TANH) { // z (1 + tanh t) / 2 = z / (1 + exp(-2 t))
         const float c = clampn(z, 30.f);
         const float t = 0.79788456f * (c + 0.044715f * c * c * c);
@@ -64,9 +79,10 @@ template <int FN> __device__ __forceinline__ void act_both(float z, float &f, fl
         else f = z < -80.f ? -0.f : z * p, df = p * (1.f + c * (1.f - p));
     } else if (FN == PI_FN_GELU) {
         const float c = clampn(z, 30.f);
-        const float p = 0.5f * (1.f + erff(c * 0.70710678f));
+        float ex;
+        const float q = upper_tail(fabsf(c), ex), p = z < 0.f ? q : 1.f - q;
         f = z < -30.f ? -0.f : z * p;
-        df = p + 0.39894228f * c * __expf(-0.5f * c * c);
+        df = fmaf(0.39894228f * c, ex, p);
     } else if (FN == PI_FN_GELU_TANH) {
         const float c = clampn(z, 10.f);
         const float t = 0.79788456f * (c + 0.044715f * c * c * c);

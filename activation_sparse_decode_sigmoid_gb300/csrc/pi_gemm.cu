@@ -59,6 +59,7 @@ constexpr uint32_t kAtom = 8192;                // MN-major: 64 rows x 64 k
 constexpr int kTile = 256;
 constexpr uint32_t kBox = 2048;                 // 32 rows x 32 columns of an epilogue warp
 constexpr uint32_t kBoxes = kEpiWarps * 2 * kBox;
+constexpr uint32_t kBiasB = 256;                // a warp's 128 bias values (gated: 64 of each)
 
 struct TcParams {
     CUtensorMap ma[2], mb[2];
@@ -304,17 +305,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile; // output columns of a tile
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kBoxes); // used in the first CTA
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kBoxes + kEpiWarps * kBiasB); // used in the first CTA
     uint64_t *empty = full + kStages;
     uint64_t *acc_full = empty + kStages;  // [2]
     uint64_t *acc_empty = acc_full + 2;    // [2], used in the first CTA
     uint32_t *tslot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    if (warp == kEpiWarps && lane == 0) {
+        // the maps are on their way while the rest is set up
+        prefetch_map(&p.ma[0]), prefetch_map(&p.mb[0]);
+        if (p.kt0 < p.KT || MODE == EPI_GATED) prefetch_map(&p.ma[1]), prefetch_map(&p.mb[1]);
+    }
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init1(full + s), mbar_init1(empty + s);
         for (int s = 0; s < 2; ++s) mbar_init1(acc_full + s), mbar_init(acc_empty + s, 2 * kEpiWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0) {
+    if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)),
                      "r"(512u));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -331,48 +337,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     Work w;
     bool ok = true;
     if (warp == kEpiWarps) {
-        if (lane == 0) {
-            const CUtensorMap *mb_gated = &p.mb[MODE == EPI_GATED ? rank : 0];
-            Cur cur(0, kStages);
-            uint32_t round = 0;
-            while (ok && walk.next(w)) {
-                int mi, ni;
-                tile_at(w.tile, p.tm, p.tn, mi, ni);
-                const int m0 = mi * kTile + (int)rank * 128;
-                const int n0 = ni * kOutN + (MODE == EPI_GATED ? 0 : (int)rank * 128);
-                for (int k = w.k0; k < w.k1; ++k) {
-                    if (round >= kStages && !mbar_wait_bounded(empty + cur.s, cur.ph ^ 1u, p)) {
+        const uint32_t full0 = in_first(smem_addr(full));
+        Cur cur(0, kStages);
+        uint32_t round = 0;
+        while (ok && walk.next(w)) {
+            int mi, ni;
+            tile_at(w.tile, p.tm, p.tn, mi, ni);
+            const int m0 = mi * kTile + (int)rank * 128;
+            const int n0 = ni * kOutN + (MODE == EPI_GATED ? 0 : (int)rank * 128);
+            for (int seg = 0; seg < 2; ++seg) {
+                const int lo = seg ? p.kt0 : 0, ka = max(w.k0, lo), kb = min(w.k1, seg ? p.KT : p.kt0);
+                const CUtensorMap *ma = &p.ma[seg], *mb = &p.mb[MODE == EPI_GATED ? (int)rank : seg];
+                for (int k = ka; k < kb; ++k) {
+                    if (round >= kStages && !mbar_wait_all(empty + cur.s, cur.ph ^ 1u, p)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = in_first(smem_addr(full + cur.s));
-                    if (rank == 0) mbar_expect(full + cur.s, 2 * kStageBytes);
-                    const int seg = k >= p.kt0 ? 1 : 0;
-                    const int kc = (k - (seg ? p.kt0 : 0)) * kBK;
-                    const CUtensorMap *ma = &p.ma[seg], *mb = MODE == EPI_GATED ? mb_gated : &p.mb[seg];
-                    const uint32_t sa = base + cur.s * kStageBytes, sb = sa + kOpBytes;
-                    if (p.a_mn) {
-                        pair_load(sa, ma, m0, kc, bar);
-                        pair_load(sa + kAtom, ma, m0 + 64, kc, bar);
-                    } else
-                        pair_load(sa, ma, kc, m0, bar);
-                    if (p.b_mn) {
-                        pair_load(sb, mb, n0, kc, bar);
-                        pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
-                    } else
-                        pair_load(sb, mb, kc, n0, bar);
+                    if (elect_one()) {
+                        const uint32_t bar = full0 + cur.s * 8, sa = base + cur.s * kStageBytes, sb = sa + kOpBytes;
+                        const int kc = (k - lo) * kBK;
+                        if (rank == 0) mbar_expect(full + cur.s, 2 * kStageBytes);
+                        if (p.a_mn) {
+                            pair_load(sa, ma, m0, kc, bar);
+                            pair_load(sa + kAtom, ma, m0 + 64, kc, bar);
+                        } else
+                            pair_load(sa, ma, kc, m0, bar);
+                        if (p.b_mn) {
+                            pair_load(sb, mb, n0, kc, bar);
+                            pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
+                        } else
+                            pair_load(sb, mb, kc, n0, bar);
+                    }
+                    __syncwarp();
                     cur.next(kStages);
                     ++round;
                 }
             }
-            // the MMAs' arrivals on this CTA's barriers land before it leaves
-            for (uint32_t i = min(round, (uint32_t)kStages); ok && i > 0; --i) {
-                const Cur last(round - i, kStages);
-                ok = mbar_wait_bounded(empty + last.s, last.ph, p);
-            }
+        }
+        // the MMAs' arrivals on this CTA's barriers land before it leaves
+        for (uint32_t i = min(round, (uint32_t)kStages); ok && i > 0; --i) {
+            const Cur last(round - i, kStages);
+            ok = mbar_wait_all(empty + last.s, last.ph, p);
         }
     } else if (warp == kEpiWarps + 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             const uint32_t id = idesc(H::fmt, (uint32_t)p.a_mn, (uint32_t)p.b_mn, 256, 256);
             // descriptors of stage 0; a byte offset o adds o / 16 (the start address field)
             const uint64_t da = p.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
@@ -381,26 +389,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             Cur cur(0, kStages);
             for (uint32_t it = 0; ok && walk.next(w); ++it) {
                 const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-                if (it >= 2 && !mbar_wait_bounded(acc_empty + buf, ph ^ 1u, p)) {
+                if (it >= 2 && !mbar_wait_all(acc_empty + buf, ph ^ 1u, p)) {
                     ok = false;
                     break;
                 }
                 tc_after();
                 const uint32_t d = tmem + buf * 256u;
                 for (int k = w.k0; k < w.k1; ++k) {
-                    if (!mbar_wait_bounded(full + cur.s, cur.ph, p)) {
+                    if (!mbar_wait_all(full + cur.s, cur.ph, p)) {
                         ok = false;
                         break;
                     }
                     tc_after();
-                    const uint32_t so = (cur.s * kStageBytes) >> 4;
+                    if (elect_one()) {
+                        const uint32_t so = (cur.s * kStageBytes) >> 4;
 #pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j)
-                        mma2(d, da + so + j * ka, db + so + j * kb, id, (k > w.k0 || j > 0) ? 1u : 0u);
-                    commit2(empty + cur.s);
+                        for (int j = 0; j < kBK / 16; ++j)
+                            mma2(d, da + so + j * ka, db + so + j * kb, id, (k > w.k0 || j > 0) ? 1u : 0u);
+                        commit2(empty + cur.s);
+                    }
+                    __syncwarp();
                     cur.next(kStages);
                 }
-                if (ok) commit2(acc_full + buf);
+                if (ok && elect_one()) commit2(acc_full + buf);
+                __syncwarp();
             }
         }
     } else {
@@ -417,6 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                                            : Strip{static_cast<uint16_t *>(const_cast<void *>(e.res)), e.ldr, (e.vec & V_RES) != 0};
         const Strip in2 = {const_cast<uint16_t *>(e.in2), e.ldi2, (e.vec & V_IN2) != 0};
         constexpr int kCols = kOutN / 2; // of this warp
+        const uint32_t bias = base + kStages * kStageBytes + kBoxes + (uint32_t)warp * kBiasB;
+        const bool biased = MODE != EPI_DACT && (e.bias || e.bias2);
         for (uint32_t it = 0; ok && walk.next(w); ++it) {
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
             int mi, ni;
@@ -428,7 +442,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 strip_load(in1, lane, row0, col0, p.M, p.N, q1);
                 if (two) strip_load(in2, lane, row0, col0, p.M, p.N, q2);
             }
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + buf, ph, p));
+            if (whole && biased) { // 4 values a lane
+                const int h = MODE == EPI_GATED ? lane >> 4 : 0, k = (MODE == EPI_GATED ? lane & 15 : lane) * 4;
+                const uint16_t *src = h ? e.bias2 : e.bias;
+                uint32_t b[2] = {};
+                if (src) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (col0 + k + i < p.N) b[i >> 1] |= (uint32_t)src[col0 + k + i] << (16 * (i & 1));
+                }
+                __syncwarp();
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(bias + lane * 8), "r"(b[0]), "r"(b[1]) : "memory");
+                __syncwarp();
+            }
+            ok = warp_wait(acc_full + buf, ph, p, lane);
             if (!ok) break;
             tc_after();
             const uint32_t ta = lane_addr + buf * 256u;
@@ -470,22 +497,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                         }
                         __syncwarp();
                     }
-                    if (MODE != EPI_DACT && e.bias) {
+                    if (biased) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             float b[8];
-                            load8<T>(e.bias + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS, b);
+                            unpack8<T>(lds16(bias + 2 * (c + 8 * j)), b);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
-                        }
-                    }
-                    if (MODE == EPI_GATED && e.bias2) {
+                            if (MODE == EPI_GATED) {
+                                unpack8<T>(lds16(bias + 128 + 2 * (c + 8 * j)), b);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float b[8];
-                            load8<T>(e.bias2 + col + 8 * j, p.N - col - 8 * j, e.vec & V_BIAS2, b);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) u[(8 * j + i) % (MODE == EPI_GATED ? 32 : 1)] += b[i];
+                                for (int i = 0; i < 8; ++i) u[(8 * j + i) % (MODE == EPI_GATED ? 32 : 1)] += b[i];
+                            }
                         }
                     }
                     if (MODE != EPI_DACT && e.out2) {
@@ -567,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     __syncthreads();
     cluster_sync(); // neither CTA leaves while the other still reads its shared or tensor memory
     tc_after();
-    if (warp == 0)
+    if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
@@ -644,7 +667,7 @@ cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K)
 
 template <typename T, int MODE> cudaError_t run(const TcParams &p, int pairs, cudaStream_t s)
 {
-    constexpr int smem = kStages * kStageBytes + kBoxes + (2 * kStages + 4) * 8 + 16;
+    constexpr int smem = kStages * kStageBytes + kBoxes + kEpiWarps * kBiasB + (2 * kStages + 4) * 8 + 16;
     auto kern = gemm_tc<T, MODE>;
     static std::atomic<uint64_t> ready{0}; // devices whose limit has been raised
     int dev = 0;

@@ -64,6 +64,7 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
     uint64_t *empty = full + kMaxRing;
     uint64_t *acc_full = empty + kMaxRing, *acc_empty = acc_full + 2;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    if (tid == 128) prefetch_map(&p.mw[0]), prefetch_map(&p.mx);
     if (tid == 0) {
         for (uint32_t s = 0; s < S; ++s) mbar_init1(full + s), mbar_init1(empty + s);
         for (int s = 0; s < 2; ++s) mbar_init1(acc_full + s), mbar_init(acc_empty + s, 4);
@@ -77,76 +78,80 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
     const uint32_t base = smem_addr(smem);
     bool ok = true;
     if (warp == 4) {
-        if (lane == 0) {
-            Cur cur(0, S);
-            uint32_t round = 0;
-            const uint32_t bytes = kWTile + (uint32_t)p.Tp * 128u;
-            int tile = (int)(u / p.KT), k = (int)(u - (int64_t)tile * p.KT);
-            auto load_w = [&](uint32_t s) {
-                const int m = tile >= p.tn ? 1 : 0;
-                mbar_expect(full + s, bytes);
-                tile_load(base + s * p.slotB, &p.mw[m], k * kBK, (tile - m * p.tn) * 128, full + s);
-            };
-            if (p.early) {
-                // fill the ring's weights while the launch before finishes, then their tokens
-                const int k0 = k;
-                for (; u < u1 && round < S; ++u, ++round) {
-                    load_w(round);
-                    if (++k == p.KT) k = 0, ++tile;
-                }
-                pdl_enter();
-                int kx = k0;
-                for (uint32_t s = 0; s < round; ++s) {
-                    tile_load(base + s * p.slotB + kWTile, &p.mx, kx * kBK, 0, full + s);
-                    if (++kx == p.KT) kx = 0;
-                }
-                cur = Cur(round, S);
+        Cur cur(0, S);
+        uint32_t round = 0;
+        const uint32_t bytes = kWTile + (uint32_t)p.Tp * 128u;
+        int tile = (int)(u / p.KT), k = (int)(u - (int64_t)tile * p.KT);
+        auto load_w = [&](uint32_t s) {
+            const int m = tile >= p.tn ? 1 : 0;
+            mbar_expect(full + s, bytes);
+            tile_load(base + s * p.slotB, &p.mw[m], k * kBK, (tile - m * p.tn) * 128, full + s);
+        };
+        if (p.early) {
+            // fill the ring's weights while the launch before finishes, then their tokens
+            int kx = k;
+            for (; u < u1 && round < S; ++u, ++round) {
+                if (elect_one()) load_w(round);
+                __syncwarp();
+                if (++k == p.KT) k = 0, ++tile;
             }
-            for (; u < u1; ++u) {
-                if (round >= S && !mbar_wait_bounded(empty + cur.s, cur.ph ^ 1u, p)) {
+            pdl_enter();
+            for (uint32_t s = 0; s < round; ++s) {
+                if (elect_one()) tile_load(base + s * p.slotB + kWTile, &p.mx, kx * kBK, 0, full + s);
+                __syncwarp();
+                if (++kx == p.KT) kx = 0;
+            }
+            cur = Cur(round, S);
+        }
+        for (; u < u1; ++u) {
+            if (round >= S && !mbar_wait_all(empty + cur.s, cur.ph ^ 1u, p)) {
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
+                load_w(cur.s);
+                tile_load(base + cur.s * p.slotB + kWTile, &p.mx, k * kBK, 0, full + cur.s);
+            }
+            __syncwarp();
+            cur.next(S);
+            ++round;
+            if (++k == p.KT) k = 0, ++tile;
+        }
+        for (uint32_t i = round < S ? round : S; ok && i > 0; --i) { // nothing of its own is left in flight
+            const Cur last(round - i, S);
+            ok = mbar_wait_all(empty + last.s, last.ph, p);
+        }
+    } else if (warp == 5) {
+        const uint32_t id = idesc(H::fmt, 0, 0, 128, (uint32_t)p.Tp);
+        const uint64_t d0 = sdesc(base, 16, 1024);
+        Cur cur(0, S);
+        for (uint32_t it = 0; ok && u < u1; ++it) {
+            const uint32_t buf = it & 1, ph = (it >> 1) & 1;
+            if (it >= 2 && !mbar_wait_all(acc_empty + buf, ph ^ 1u, p)) break;
+            tc_after();
+            const int64_t end = min(u1, (u / p.KT + 1) * p.KT);
+            for (bool first = true; u < end; ++u, first = false) {
+                if (!mbar_wait_all(full + cur.s, cur.ph, p)) {
                     ok = false;
                     break;
                 }
-                load_w(cur.s);
-                tile_load(base + cur.s * p.slotB + kWTile, &p.mx, k * kBK, 0, full + cur.s);
-                cur.next(S);
-                ++round;
-                if (++k == p.KT) k = 0, ++tile;
-            }
-            for (uint32_t i = round < S ? round : S; ok && i > 0; --i) { // nothing of its own is left in flight
-                const Cur last(round - i, S);
-                ok = mbar_wait_bounded(empty + last.s, last.ph, p);
-            }
-        }
-    } else if (warp == 5) {
-        if (lane == 0) {
-            const uint32_t id = idesc(H::fmt, 0, 0, 128, (uint32_t)p.Tp);
-            const uint64_t d0 = sdesc(base, 16, 1024);
-            Cur cur(0, S);
-            for (uint32_t it = 0; ok && u < u1; ++it) {
-                const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-                if (it >= 2 && !mbar_wait_bounded(acc_empty + buf, ph ^ 1u, p)) break;
                 tc_after();
-                const int64_t end = min(u1, (u / p.KT + 1) * p.KT);
-                for (bool first = true; u < end; ++u, first = false) {
-                    if (!mbar_wait_bounded(full + cur.s, cur.ph, p)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_after();
+                if (elect_one()) {
                     const uint64_t a = d0 + ((cur.s * p.slotB) >> 4), b = a + (kWTile >> 4);
 #pragma unroll
                     for (int j = 0; j < kBK / 16; ++j) mma(tmem + buf * 64u, a + 2 * j, b + 2 * j, id, (!first || j > 0) ? 1u : 0u);
                     mma_commit(empty + cur.s);
-                    cur.next(S);
                 }
-                if (ok) mma_commit(acc_full + buf);
+                __syncwarp();
+                cur.next(S);
             }
+            if (ok && elect_one()) mma_commit(acc_full + buf);
+            __syncwarp();
         }
     } else {
         for (uint32_t it = 0; ok && u < u1; ++it) {
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + buf, ph, p));
+            ok = warp_wait(acc_full + buf, ph, p, lane);
             if (!ok) break;
             tc_after();
             const int tile = (int)(u / p.KT);

@@ -82,6 +82,33 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *b, uint32_t parity, 
     }
 }
 
+// The same for a warp that runs its role's loop in all lanes: one answer for all.
+template <typename P>
+__device__ __forceinline__ bool mbar_wait_all(uint64_t *b, uint32_t parity, const P &p)
+{
+    return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity, p));
+}
+
+// One lane of a converged warp.  A role's loop runs in all lanes and only
+// issues its copies or MMAs under this: their operands then stay in uniform
+// registers.  (In a branch on the lane number instead, the issue of a
+// 256 x 256 x 64 step of a CTA pair took up to 1.4 times the step's 512 cycles.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
+// The same for a warp whose waits are long: lane 0 polls for all.
+template <typename P>
+__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, const P &p, int lane)
+{
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait_bounded(b, parity, p);
+    return __shfl_sync(0xffffffffu, ok, 0);
+}
+
 // Bounded wait that ignores the abort flag: a CTA lets its own copies land
 // before it exits, even after a failure elsewhere.  Copies land within
 // microseconds; the limit only guards against a device that stopped.
@@ -272,6 +299,11 @@ __device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap *tm, int
                  " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
                  "l"(tm), "r"(smem_addr(bar)), "r"(col), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                  : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *tm)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tm) : "memory");
 }
 
 // a box of 64 columns x box-rows rows at (col, row)
