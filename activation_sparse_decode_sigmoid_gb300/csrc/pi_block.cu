@@ -27,10 +27,10 @@ __global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t ld
     pdl_enter();
     const int ncb = (cols + 255) / 256;
     const int c = (int)(blockIdx.x % ncb) * 256 + threadIdx.x;
-    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * 32;
+    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * 8;
     if (c >= cols) return;
 #pragma unroll 8
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 8; ++i)
         if (r0 + i < rows) dst[(r0 + i) * ldd + c] = src[(r0 + i) * lds + c];
 }
 
@@ -525,7 +525,7 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
 
 cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
 {
-    const int64_t blocks = (int64_t)((rows + 31) / 32) * ((cols + 255) / 256);
+    const int64_t blocks = (int64_t)((rows + 7) / 8) * ((cols + 255) / 256);
     if (!blocks) return cudaSuccess;
     return launch_pdl(pack_rows, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t *)src, lds, (uint16_t *)dst, ldd, rows,
                       cols);

@@ -65,7 +65,7 @@ cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
 // Products of up to this many rows of A go to skinny_tc (pi_skinny.cu) where
 // both operands lie along k.
-constexpr int kSkinnyRows = 64;
+constexpr int kSkinnyRows = 128;
 bool skinny_takes(const Gemm &g);
 size_t skinny_workspace(const Gemm &g, const CtxView &v);
 cudaError_t launch_skinny(const Gemm &g, bool bf16, const CtxView &v, void *ws);

@@ -1,16 +1,18 @@
-// The matrix product of the block operators for few tokens (M <= 64 rows of A):
+// The matrix product of the block operators for few tokens (M <= 128 rows of A):
 //     D[t][f] = sum_k X[t][k] W[f][k]
 //
 // Bound by HBM: every weight is read once for 2 M operations.  The weights
 // are the MMA's 128-row operand and the tokens its columns (M rounded up to
-// 16), so no part of the product is spent on rows that are not there; one CTA
-// per SM streams its share of W through a ring of 128 x 64 tiles that fills
-// shared memory (about 200 KB in flight per SM, whatever the token count).
-// The work is cut by bytes, not by tiles: all (tile, k step) pairs end to
-// end, in equal ranges, one per CTA.  Each CTA writes the fp32 partial sums of
-// its one to three tiles, [tokens][128], and skinny_join adds the parts of a
-// tile in the order of k and runs the epilogue - bias, activation, gate,
-// residual - on 8 features at a time.
+// 16), so no part of the product is spent on rows that are not there; a CTA
+// per SM streams its share of W through a ring of boxes that fills shared
+// memory (about 200 KB in flight per SM, whatever the token count).
+// The work is cut by bytes, not by tiles: all (128-feature tile, k step) pairs
+// end to end, in equal ranges, one per CTA.  Each CTA writes the fp32 partial
+// sums of its tiles, [tokens][128], and skinny_join adds the parts of a tile in
+// the order of k and runs the epilogue on 8 features at a time.  (Whole rows
+// per CTA, without the second launch, lost: an MMA of 128 x 16 x 16 takes about
+// 100 cycles however few of its rows count, so 56 rows of K = 28672 took 101 us
+// against 80.)
 //
 // One token, and up to four of a smaller matrix (gemv_takes), take one launch
 // of gemv_rows instead: dot products on the CUDA cores, no workspace.
@@ -70,7 +72,7 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
         for (int s = 0; s < 2; ++s) mbar_init1(acc_full + s), mbar_init(acc_empty + s, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const uint32_t tmem = tmem_alloc(tslot, 128); // two accumulators of up to 64 columns
+    const uint32_t tmem = tmem_alloc(tslot, 256); // two accumulators of up to 128 columns
     if (!(p.early && warp == 4)) pdl_enter();
     const int64_t units = (int64_t)p.tiles * p.KT;
     int64_t u = sk_range(units, (int)blockIdx.x, p.parts);
@@ -139,7 +141,7 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
                 if (elect_one()) {
                     const uint64_t a = d0 + ((cur.s * p.slotB) >> 4), b = a + (kWTile >> 4);
 #pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j) mma(tmem + buf * 64u, a + 2 * j, b + 2 * j, id, (!first || j > 0) ? 1u : 0u);
+                    for (int j = 0; j < kBK / 16; ++j) mma(tmem + buf * 128u, a + 2 * j, b + 2 * j, id, (!first || j > 0) ? 1u : 0u);
                     mma_commit(empty + cur.s);
                 }
                 __syncwarp();
@@ -157,7 +159,7 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
             const int tile = (int)(u / p.KT);
             const int slot = (int)blockIdx.x - sk_part_of(units, (int64_t)tile * p.KT, p.parts);
             float *dst = p.part + ((size_t)tile * p.smax + slot) * (size_t)p.T * 128 + warp * 32 + lane;
-            const uint32_t ta = tmem + ((uint32_t)(warp * 32) << 16) + buf * 64u;
+            const uint32_t ta = tmem + ((uint32_t)(warp * 32) << 16) + buf * 128u;
             for (int t0 = 0; t0 < p.T; t0 += 16) {
                 float v[16];
                 tmem_ld16(ta + t0, v);
@@ -177,7 +179,7 @@ template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc
         while (gtimer() - t0 < 5000000ull) {
         }
     }
-    tmem_free(tmem, 128);
+    tmem_free(tmem, 256);
 }
 
 template <typename T, int MODE> __global__ void __launch_bounds__(128) skinny_join(const __grid_constant__ SkParams p)
@@ -194,7 +196,7 @@ template <typename T, int MODE> __global__ void __launch_bounds__(128) skinny_jo
         const int tile = f / 128 + m * p.tn;
         const int cnt = sk_part_of(units, (int64_t)(tile + 1) * p.KT - 1, p.parts) - sk_part_of(units, (int64_t)tile * p.KT, p.parts) + 1;
         const float *src = p.part + ((size_t)tile * p.smax * p.T + t) * 128 + (f & 127);
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < cnt; ++s) {
             float w[8];
             load8f(src + (size_t)s * p.T * 128, 8, true, w);
@@ -203,6 +205,19 @@ template <typename T, int MODE> __global__ void __launch_bounds__(128) skinny_jo
         }
     }
     epilogue8<T, MODE>(p.e, p.N, t, f, v[0], v[1]);
+}
+
+// the device's shared-memory limit for a kernel, raised once per device
+template <typename K> cudaError_t raise_limit(K kern, std::atomic<uint64_t> &ready)
+{
+    int dev = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
+        e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
+    }
+    return e;
 }
 
 // ------------------------------------------------------------------ one token, or few and a smaller matrix
@@ -339,7 +354,7 @@ SkParams plan(const Gemm &g, const CtxView &v)
     p.tiles = p.tn * (g.mode == EPI_GATED ? 2 : 1);
     p.KT = (g.K[0] + kBK - 1) / kBK;
     const int64_t units = (int64_t)p.tiles * p.KT;
-    p.parts = (int)std::min<int64_t>(v.sms, std::max<int64_t>(1, units / 2)); // at least two k steps each
+    p.parts = (int)std::min<int64_t>(v.sms, std::max<int64_t>(1, units / 6)); // at least six k steps each
     p.smax = (int)std::min<int64_t>(p.parts, p.KT / (units / p.parts) + 2);
     p.slotB = kWTile + (uint32_t)p.Tp * 128u;
     p.slots = std::min(kMaxRing, (v.smem_optin - 1024) / (int)p.slotB);
@@ -353,14 +368,8 @@ template <typename T, int MODE> cudaError_t run(const SkParams &p, cudaStream_t 
 {
     auto kern = skinny_tc<T>;
     const int smem = p.slots * (int)p.slotB + (2 * kMaxRing + 4) * 8 + 16;
-    static std::atomic<uint64_t> ready{0}; // devices whose shared-memory limit has been raised
-    int dev = 0, most = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
-        e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
-    }
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = raise_limit(kern, ready);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(p.parts), dim3(kSkThreads), smem, s, p);
     if (e != cudaSuccess) return e;
     const int64_t threads = (int64_t)p.T * p.tn * 16;
