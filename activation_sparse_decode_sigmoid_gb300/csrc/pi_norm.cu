@@ -710,7 +710,8 @@ struct BwdStat {
 // tensor memory, where each thread adds to its own columns' values: in
 // registers they took half of what 512 threads have (8000 x 8192 layer norms:
 // 345 us with 512 threads and spills, 271 us with 256 threads of 32 columns).
-template <typename T, bool X32, int V, bool FULL>
+// RG: a gate row per token, in the ring.
+template <typename T, bool X32, int V, bool FULL, bool RG>
 __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
 {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -731,7 +732,8 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
     int issued = r0;
     if (tid == 0)
         for (; issued < min(r1, r0 + S); ++issued) issue_row(p, q, ring, full, issued - r0, issued);
-    const bool row_gate = q.off_gate >= 0, pre = p.dh != nullptr, post = p.y && p.post != PI_NORM_NONE;
+    constexpr bool row_gate = RG;
+    const bool pre = p.dh != nullptr, post = p.y && p.post != PI_NORM_NONE;
     const bool lpre = FULL && p.pre == PI_NORM_LAYER, lpost = FULL && p.post == PI_NORM_LAYER;
     uint4 wp[V], wq[V];
     int c[V];
@@ -788,30 +790,30 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
         // statistics of x' and y, and the sums of dh w and dh w xh, about the warp's means
         BwdStat st = {};
         float wmx = 0.f, wmy = 0.f;
-        if (FULL) {
+        float x[V][8], y[V][8]; // x' and y, later normalised in place
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float v[8], u[8];
-                ring8x<T, X32>(row, c[i], v);
-                ring8<T>(row + q.off_y, c[i], u);
+        for (int i = 0; i < V; ++i) {
+            ring8x<T, X32>(row, c[i], x[i]);
+            ring8<T>(row + q.off_y, c[i], y[i]);
+            if (FULL) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) st.sx += v[j], st.sy += u[j];
+                for (int j = 0; j < 8; ++j) st.sx += x[i][j], st.sy += y[i][j];
             }
+        }
+        if (FULL) {
             st.sx = warp_add(st.sx), st.sy = warp_add(st.sy);
             if (lpre && nel > 0.f) wmx = st.sx / nel;
             if (lpost && nel > 0.f) wmy = st.sy / nel;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float v[8], h[8], u[8], w[8];
-            ring8x<T, X32>(row, c[i], v);
+            float h[8], w[8];
             ring8<T>(row + q.off_dh, c[i], h);
-            ring8<T>(row + q.off_y, c[i], u);
             unpack8<T>(wp[i], w);
             const float mx = on[i] ? wmx : 0.f, my = on[i] ? wmy : 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float e = FULL ? v[j] - mx : v[j], f = FULL ? u[j] - my : u[j], k = h[j] * w[j];
+                const float e = FULL ? x[i][j] - mx : x[i][j], f = FULL ? y[i][j] - my : y[i][j], k = h[j] * w[j];
                 st.mx = fmaf(e, e, st.mx);
                 if (FULL) st.sq += k;
                 st.sqx = fmaf(k, e, st.sqx);
@@ -849,12 +851,11 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             float v[8], h[8], w[8], a[16]; // a: P1, P0
             tmem_ld16(sums + 32 * i, a);
             ring8x<T, X32>(row + q.off_dxo, c[i], D[i]);
-            ring8x<T, X32>(row, c[i], v);
             ring8<T>(row + q.off_dh, c[i], h);
             unpack8<T>(wp[i], w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float xh = FULL ? (v[j] - mx) * rx : v[j] * rx;
+                const float xh = FULL ? (x[i][j] - mx) * rx : x[i][j] * rx;
                 float e = fmaf(rx * h[j], w[j], D[i][j]);
                 if (FULL) e += k0;
                 D[i][j] = fmaf(kx, xh, e);
@@ -867,16 +868,17 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float y[8], w[8], g[8], a[16]; // a: S1, S0
+            float w[8], g[8], a[16]; // a: S1, S0
             tmem_ld16(sums + 32 * i + 16, a);
-            ring8<T>(row + q.off_y, c[i], y);
             ring8<T>(gate, c[i], g);
             unpack8<T>(wq[i], w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[i][j] = FULL ? (y[i][j] - my) * ry : y[i][j] * ry;
             if (row_gate && p.dgate && on[i]) {
                 float b[8], o[8];
                 unpack8<T>(param8<T>(p.b_post, c[i], d, 0.f), b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = p.bs * D[i][j] * fmaf((y[j] - my) * ry, w[j], b[j]);
+                for (int j = 0; j < 8; ++j) o[j] = p.bs * D[i][j] * fmaf(y[i][j], w[j], b[j]);
                 const int64_t at = (int64_t)t * d + c[i];
                 if (p.acc) {
                     float old[8];
@@ -888,13 +890,12 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float yh = FULL ? (y[j] - my) * ry : y[j] * ry;
                 const float k = row_gate ? g[j] * D[i][j] : D[i][j]; // (what S1 and S0 sum)
                 D[i][j] *= p.bs * g[j];                            // dv from here on
                 const float e = D[i][j] * w[j];
                 if (FULL) s1 += e;
-                s2 = fmaf(e, yh, s2);
-                a[j] = fmaf(k, yh, a[j]);
+                s2 = fmaf(e, y[i][j], s2);
+                a[j] = fmaf(k, y[i][j], a[j]);
                 if (FULL) a[8 + j] += k;
             }
             tm_st16(sums + 32 * i + 16, a);
@@ -913,17 +914,15 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float y[8], w[8];
-                ring8<T>(row + q.off_y, c[i], y);
+                float w[8];
                 unpack8<T>(wq[i], w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float yh = FULL ? (y[j] - my) * ry : y[j] * ry;
                     float e = D[i][j] * w[j];
                     if (FULL) e -= k1;
-                    y[j] = ry * fmaf(-k2, yh, e);
+                    y[i][j] = ry * fmaf(-k2, y[i][j], e);
                 }
-                if (on[i]) store8<T>(p.dy + (int64_t)t * p.ldy + c[i], 8, true, y);
+                if (on[i]) store8<T>(p.dy + (int64_t)t * p.ldy + c[i], 8, true, y[i]);
             }
         }
         flip ^= 1;
@@ -1096,7 +1095,11 @@ template <typename T> cudaError_t fwd(const NormP &p, const CtxView &c)
 
 template <typename T, bool X32, bool FULL> cudaError_t bwd_pipe(const NormP &p, const Pipe &o, cudaStream_t s)
 {
-    return o.v == 1 ? run_pipe(norm_bwd_pipe<T, X32, 1, FULL>, p, o, s) : run_pipe(norm_bwd_pipe<T, X32, 2, FULL>, p, o, s);
+    if (o.q.off_gate >= 0)
+        return o.v == 1 ? run_pipe(norm_bwd_pipe<T, X32, 1, FULL, true>, p, o, s)
+                        : run_pipe(norm_bwd_pipe<T, X32, 2, FULL, true>, p, o, s);
+    return o.v == 1 ? run_pipe(norm_bwd_pipe<T, X32, 1, FULL, false>, p, o, s)
+                    : run_pipe(norm_bwd_pipe<T, X32, 2, FULL, false>, p, o, s);
 }
 
 template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &c)
