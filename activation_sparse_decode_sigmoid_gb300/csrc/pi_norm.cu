@@ -444,6 +444,7 @@ struct PipeP {
     int off_hold;                         // after the ring: the current gate row
     uint32_t row_bytes;                   // bytes of a row's copies in all
     uint32_t tcols;                       // backward: tensor memory columns
+    int clear;                            // some columns or rows of the ring are not copied: zeros
     int *status, *abort_flag;
     unsigned long long wait_ns;
 };
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     uint8_t *hold = ring + q.off_hold;
-    clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
+    if (q.clear) clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
     __syncthreads();
     pdl_enter();
     int issued = r0;
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     uint8_t *hold = ring + q.off_hold;
-    clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
+    if (q.clear) clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
     const uint32_t tmem = tmem_alloc(&tslot, q.tcols);
     pdl_enter();
     int issued = r0;
@@ -946,37 +947,48 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
     tmem_free(tmem, q.tcols);
 }
 
-// The CTAs' partials in order: 32 columns a CTA, 16 lanes that share the parts.
+// The CTAs' partials in a fixed order: 32 columns a CTA, 32 lanes that share the parts.
 // Tokens of gate row g lie in CTAs c0 .. c1 of the row kernel; partial slot
-// c + g.  blockIdx.y 0: the parameters' gradients; y > 0: gate rows y - 1,
-// y - 1 + (gridDim.y - 1), ...
-constexpr int kJoinLanes = 16;
+// c + g.  blockIdx.y 0: the parameters' gradients; y > 0: gate rows.
+constexpr int kJoinLanes = 32;
+constexpr int kMaxCtas = 2048; // of the row kernel
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_constant__ NormP p, int G, int groups, int sums)
+__global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_constant__ NormP p, int G, int groups, int sums, int lpg)
 {
     __shared__ float red[kJoinLanes][6][32];
+    __shared__ int first[kMaxCtas], last[kMaxCtas]; // gate rows of a CTA's tokens
+    if (blockIdx.y == 0) {
+        for (int i = threadIdx.x; i < G; i += blockDim.x) {
+            first[i] = p.per_token ? 0 : row_of(p.Tn, i, G) / p.gate_rows;
+            last[i] = p.per_token ? 0 : (row_of(p.Tn, i + 1, G) - 1) / p.gate_rows;
+        }
+        __syncthreads();
+    }
     pdl_enter();
     const int l = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + l, d = p.d;
     const bool in = c < d;
     const float *S = p.part + (int64_t)G * 2 * d;
     const float w = in && p.w_post ? C16<T>::one(p.w_post[c]) : 1.f, b = in && p.b_post ? C16<T>::one(p.b_post[c]) : 0.f;
     if (blockIdx.y > 0) {
-        for (int g = (int)blockIdx.y - 1; g < groups; g += (int)gridDim.y - 1) {
-            const int c0 = cta_of(p, g * (int64_t)p.gate_rows, G);
-            const int c1 = cta_of(p, min((int64_t)p.Tn, (g + 1) * (int64_t)p.gate_rows) - 1, G);
+        // lpg lanes to a gate row, kJoinLanes / lpg gate rows at a time
+        const int per = kJoinLanes / lpg, sub = k % lpg;
+        for (int g0 = ((int)blockIdx.y - 1) * per; g0 < groups; g0 += ((int)gridDim.y - 1) * per) {
+            const int g = g0 + k / lpg;
             float a = 0.f, z = 0.f;
-            if (in) {
+            if (in && g < groups) {
+                const int c0 = cta_of(p, g * (int64_t)p.gate_rows, G);
+                const int c1 = cta_of(p, min((int64_t)p.Tn, (g + 1) * (int64_t)p.gate_rows) - 1, G);
 #pragma unroll 4
-                for (int i = c0 + k; i <= c1; i += kJoinLanes) {
+                for (int i = c0 + sub; i <= c1; i += lpg) {
                     a += S[(int64_t)(i + g) * 2 * d + c];
                     if (sums) z += S[((int64_t)(i + g) * 2 + 1) * d + c];
                 }
             }
             red[k][0][l] = a, red[k][1][l] = z;
             __syncthreads();
-            if (in && k == 0) {
-                for (int j = 1; j < kJoinLanes; ++j) a += red[j][0][l], z += red[j][1][l];
+            if (in && sub == 0 && g < groups) {
+                for (int j = 1; j < lpg; ++j) a += red[k + j][0][l], z += red[k + j][1][l];
                 put<T>(p, p.dgate, (int64_t)g * d + c, p.bs * fmaf(w, a, b * z));
             }
             __syncthreads();
@@ -984,23 +996,26 @@ __global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_co
         return;
     }
     float v[6] = {}; // P1, P0, gate S1, gate S0, S1, S0
+    auto add_s = [&](int i, int g) {
+        const float gate = p.gate && !p.per_token ? C16<T>::one(p.gate[(int64_t)g * p.ldgate + c]) : 1.f;
+        const float a = S[(int64_t)(i + g) * 2 * d + c], z = sums ? S[((int64_t)(i + g) * 2 + 1) * d + c] : 0.f;
+        v[2] = fmaf(gate, a, v[2]);
+        v[3] = fmaf(gate, z, v[3]);
+        v[4] += a;
+        v[5] += z;
+    };
     if (in) {
-#pragma unroll 2
+#pragma unroll 4
         for (int i = k; i < G; i += kJoinLanes) {
             v[0] += p.part[(int64_t)i * 2 * d + c];
             if (sums) v[1] += p.part[((int64_t)i * 2 + 1) * d + c];
-            if (!p.y) continue;
-            const int r0 = row_of(p.Tn, i, G), r1 = row_of(p.Tn, i + 1, G);
-            const int g0 = p.per_token ? 0 : r0 / p.gate_rows, g1 = p.per_token ? 0 : (r1 - 1) / p.gate_rows;
+        }
+        if (p.y) {
+            // most CTAs meet one gate row: their loads first, all in flight
 #pragma unroll 4
-            for (int g = g0; g <= g1; ++g) {
-                const float gate = p.gate && !p.per_token ? C16<T>::one(p.gate[(int64_t)g * p.ldgate + c]) : 1.f;
-                const float a = S[(int64_t)(i + g) * 2 * d + c], z = sums ? S[((int64_t)(i + g) * 2 + 1) * d + c] : 0.f;
-                v[2] = fmaf(gate, a, v[2]);
-                v[3] = fmaf(gate, z, v[3]);
-                v[4] += a;
-                v[5] += z;
-            }
+            for (int i = k; i < G; i += kJoinLanes) add_s(i, first[i]);
+            for (int i = k; i < G; i += kJoinLanes)
+                for (int g = first[i] + 1; g <= last[i]; ++g) add_s(i, g);
         }
     }
 #pragma unroll
@@ -1053,6 +1068,7 @@ bool plan_pipe(const NormP &p, bool backward, bool row_gate, const CtxView &c, P
     q.slotB = at;
     q.row_bytes = (uint32_t)p.d * ((p.x ? xe : 0) + (backward && p.dxo ? xe : 0) + (backward && p.dh ? 2 : 0) + (p.y ? 2 : 0) +
                                    (row_gate ? 2 : 0));
+    q.clear = wide != p.d || !p.x || !p.y || (backward && (!p.dxo || !p.dh));
     const int budget = c.smem_optin - 2048 - hB;
     int per_sm = std::min(8, kPipeThreads / o.threads);
     while (per_sm > 1 && per_sm * (2 * q.slotB + hB + 4096) > budget) --per_sm;
@@ -1063,7 +1079,7 @@ bool plan_pipe(const NormP &p, bool backward, bool row_gate, const CtxView &c, P
     // (a power of two from 32 up; at most 256 a CTA of 16 warps, so that the CTAs of an SM fit its 512)
     q.tcols = 32;
     while (q.tcols < (uint32_t)(o.threads / 32 + 3) / 4 * 32 * o.v) q.tcols *= 2;
-    o.grid = std::min(p.Tn, c.sms * per_sm);
+    o.grid = std::min({p.Tn, c.sms * per_sm, kMaxCtas});
     q.status = c.status, q.abort_flag = c.abort_flag, q.wait_ns = c.wait_ns;
     return true;
 }
@@ -1113,9 +1129,12 @@ template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &
                                     : (full ? bwd_pipe<T, false, true>(p, o, s) : bwd_pipe<T, false, false>(p, o, s));
         if (e != cudaSuccess || !cols) return e;
         const int groups = p.per_token ? 1 : (int)((p.Tn + (int64_t)p.gate_rows - 1) / p.gate_rows);
-        const int gy = p.dgate && !p.per_token && groups > 1 ? std::min(groups, 64) : 0;
+        int lpg = 1;
+        while (2 * lpg * groups <= kJoinLanes) lpg *= 2;
+        const int sets = (groups + kJoinLanes / lpg - 1) / (kJoinLanes / lpg);
+        const int gy = p.dgate && !p.per_token && groups > 1 ? std::min(sets, 64) : 0;
         return launch_pdl(norm_bwd_join<T>, dim3((p.d + 31) / 32, 1 + gy), dim3(32 * kJoinLanes), 0, s, p, o.grid, groups,
-                          (int)full);
+                          (int)full, lpg);
     }
     const int nt = std::min(512, ((p.d + 7) / 8 + 31) / 32 * 32);
     cudaError_t e = launch_pdl(norm_bwd_rows<T>, dim3(p.Tn), dim3(nt), 0, s, p);
