@@ -21,17 +21,38 @@ namespace {
 constexpr int kMaxT = 1 << 22, kMaxDim = 1 << 20;
 
 // ------------------------------------------------------------------ kernels
-// 256 columns a CTA by 8 rows at a time: lanes along a row.
-__global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd, int rows, int cols)
+// Rows of 16-bit elements that may start on odd ones, by 32-bit words: a lane
+// reads one aligned word of the row, takes the next one's low half from its
+// neighbour where the row starts in the middle of a word, and writes one word
+// of the (aligned) copy.  Only words that lie inside the row are read whole.
+// 8 rows of 256 words a CTA.
+__global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t lds, uint32_t *dst, int64_t ldd, int rows, int cols)
 {
     pdl_enter();
-    const int ncb = (cols + 255) / 256;
-    const int c = (int)(blockIdx.x % ncb) * 256 + threadIdx.x;
+    const int nw = (cols + 1) / 2, ncb = (nw + 247) / 248; // (31 words a warp: lane 31 only lends its word)
+    const int lane = threadIdx.x & 31, w = (int)(blockIdx.x % ncb) * 248 + (threadIdx.x >> 5) * 31 + lane;
     const int64_t r0 = (int64_t)(blockIdx.x / ncb) * 8;
-    if (c >= cols) return;
-#pragma unroll 8
-    for (int i = 0; i < 8; ++i)
-        if (r0 + i < rows) dst[(r0 + i) * ldd + c] = src[(r0 + i) * lds + c];
+    uint32_t q[8];
+    bool odd[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = 0, odd[i] = false;
+        if (r0 + i >= rows) continue;
+        const uint16_t *row = src + (r0 + i) * lds;
+        odd[i] = ((uintptr_t)row & 2) != 0;
+        const int c = 2 * w - odd[i]; // the word's first column
+        if (c >= 0 && c + 1 < cols) q[i] = *reinterpret_cast<const uint32_t *>(row + c);
+        else {
+            if (c >= 0 && c < cols) q[i] = row[c];
+            if (c + 1 >= 0 && c + 1 < cols) q[i] |= (uint32_t)row[c + 1] << 16;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t next = __shfl_down_sync(0xffffffffu, q[i], 1);
+        const uint32_t v = odd[i] ? (q[i] >> 16) | (next << 16) : q[i];
+        if (lane < 31 && w < nw && r0 + i < rows) dst[(r0 + i) * (ldd / 2) + w] = v;
+    }
 }
 
 // Column sums in two launches: a CTA sums some rows of 256 columns (8 per
@@ -525,9 +546,9 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
 
 cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
 {
-    const int64_t blocks = (int64_t)((rows + 7) / 8) * ((cols + 255) / 256);
+    const int64_t blocks = (int64_t)((rows + 7) / 8) * (((cols + 1) / 2 + 247) / 248);
     if (!blocks) return cudaSuccess;
-    return launch_pdl(pack_rows, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t *)src, lds, (uint16_t *)dst, ldd, rows,
+    return launch_pdl(pack_rows, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t *)src, lds, (uint32_t *)dst, ldd, rows,
                       cols);
 }
 

@@ -263,12 +263,22 @@ __device__ __forceinline__ void strip_to_box(uint32_t box, int lane, const uint4
     for (int i = 0; i < 4; ++i) sts16(box_at(box, i * 8 + (lane >> 2), lane & 3), q[i]);
 }
 
-// The box into rows [row, row + 32), columns [col, col + 32); what lies outside is left out.
-__device__ __forceinline__ void box_send(uint32_t box, const Strip &s, int lane, int row, int col, int M, int N)
+// The box into rows [row, row + 32), columns [col, col + 32); what lies
+// outside is left out.  inside: nothing does.
+__device__ __forceinline__ void box_send(uint32_t box, const Strip &s, int lane, int row, int col, int M, int N, bool inside)
 {
     __syncwarp();
     const int c = col + (lane & 3) * 8, n = N - c;
-    if (s.vec) {
+    if (s.vec && inside) {
+        // (rows 8 apart lie 512 bytes apart in the box, their chunks alike)
+        const uint32_t at = box_at(box, lane >> 2, lane & 3);
+        uint16_t *p = s.p + (int64_t)(row + (lane >> 2)) * s.ld + c;
+        uint4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = lds16(at + 512 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i, p += 8 * s.ld) *reinterpret_cast<uint4 *>(p) = q[i];
+    } else if (s.vec) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = row + i * 8 + (lane >> 2);
@@ -478,6 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 for (int c = 0; c < kCols; c += 32) {
                     const int col = col0 + c;
                     if (col >= p.N) break;
+                    const bool inside = row0 + 32 <= p.M && col + 32 <= p.N;
                     float v[32], u[MODE == EPI_GATED ? 32 : 1];
                     tmem_ld32(ta + half * kCols + c, v);
                     if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
@@ -513,11 +524,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     }
                     if (MODE != EPI_DACT && e.out2) {
                         box_put<T>(box1, lane, v);
-                        box_send(box1, out2, lane, row0, col, p.M, p.N);
+                        box_send(box1, out2, lane, row0, col, p.M, p.N, inside);
                     }
                     if (MODE == EPI_GATED && e.out3) {
                         box_put<T>(box1, lane, *reinterpret_cast<float(*)[32]>(u));
-                        box_send(box1, out3, lane, row0, col, p.M, p.N);
+                        box_send(box1, out3, lane, row0, col, p.M, p.N, inside);
                     }
                     if (MODE == EPI_DACT) {
 #pragma unroll
@@ -536,15 +547,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                                 for (int i = 0; i < 8; ++i) v[8 * j + i] *= e.scale * df[i];
                             }
                         }
-                        if (two) box_send(box1, out2, lane, row0, col, p.M, p.N);
+                        if (two) box_send(box1, out2, lane, row0, col, p.M, p.N, inside);
                     } else {
-                        acts(e.fn, v);
+                        if (e.fn != PI_FN_NONE) acts(e.fn, v);
                         if (MODE == EPI_GATED) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] *= u[i % (MODE == EPI_GATED ? 32 : 1)];
                         } else {
+                            if (e.scale != 1.f) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= e.scale;
+                                for (int i = 0; i < 32; ++i) v[i] *= e.scale;
+                            }
                             if (out32) {
                                 if (row0 + lane < p.M)
 #pragma unroll
@@ -574,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                         }
                     }
                     box_put<T>(box0, lane, v);
-                    box_send(box0, out, lane, row0, col, p.M, p.N);
+                    box_send(box0, out, lane, row0, col, p.M, p.N, inside);
                 }
             }
             if (!released) {

@@ -28,7 +28,14 @@ namespace pi {
 namespace {
 
 constexpr int kMaxT = 1 << 22, kMaxNormD = 16384;
-constexpr int kUnitRows = 64; // tokens whose column sums one unit adds up
+
+// Tokens whose column sums one unit of norm_bwd_cols adds up: enough units for
+// eight CTAs of 1024 columns on every SM, 4 to 64 tokens each.
+int unit_rows(int T, int d)
+{
+    const int64_t want = (int64_t)T * ((d + 1023) / 1024) / 1216;
+    return (int)std::min<int64_t>(64, std::max<int64_t>(4, want));
+}
 
 struct NormP {
     int Tn, d, pre, post, x32;
@@ -49,6 +56,7 @@ struct NormP {
     float *stats;               // [T][8]: mean_x, r_x, c1, c2, mean_y, r_y
     float *part;                // [units][4][d]: P1, P0, S1, S0
     int units, per_group;       // units in all, and per gate row
+    int unit;                   // tokens of a unit
     int per_token;              // a gate row per token: S1, S0 carry the gate, dgate is written by the row kernel
     void *dgate, *dw_pre, *db_pre, *dw_post, *db_post;
     int g32, acc;
@@ -349,12 +357,12 @@ template <typename T> __global__ void __launch_bounds__(512) norm_bwd_rows(const
 }
 
 // Tokens of unit u: [t0, t1) (all of one gate row unless per_token).
-__device__ __forceinline__ void unit_rows(const NormP &p, int u, int &t0, int &t1)
+__device__ __forceinline__ void unit_tokens(const NormP &p, int u, int &t0, int &t1)
 {
     const int g = u / p.per_group, k = u % p.per_group;
     const int end = p.per_token ? p.Tn : (int)min((int64_t)p.Tn, (int64_t)(g + 1) * p.gate_rows);
-    t0 = (p.per_token ? 0 : g * p.gate_rows) + k * kUnitRows;
-    t1 = min(end, t0 + kUnitRows);
+    t0 = (p.per_token ? 0 : g * p.gate_rows) + k * p.unit;
+    t1 = min(end, t0 + p.unit);
 }
 
 // Backward, columns: one CTA adds up one unit's tokens over 1024 columns.
@@ -365,7 +373,7 @@ template <typename T> __global__ void __launch_bounds__(128) norm_bwd_cols(const
     const int u = blockIdx.x / ncb, c = (blockIdx.x % ncb) * 1024 + threadIdx.x * 8;
     if (c >= p.d) return;
     int t0, t1;
-    unit_rows(p, u, t0, t1);
+    unit_tokens(p, u, t0, t1);
     float P1[8] = {}, P0[8] = {}, S1[8] = {}, S0[8] = {};
     for (int64_t t = t0; t < t1; ++t) {
         float st[6], D[8], xh[8], dh[8], yh[8], g[8];
@@ -407,33 +415,65 @@ template <typename T> __device__ __forceinline__ void put(const NormP &p, void *
     }
 }
 
-// Backward, the units' partials in order: parameter gradients and dgate.
-template <typename T> __global__ void norm_bwd_sum(const __grid_constant__ NormP p)
+// Backward, the units' partials in a fixed order: 32 columns a CTA, 16 lanes
+// that share them.  blockIdx.y 0: the parameters' gradients; y > 0: the gate
+// rows y - 1, y - 1 + (gridDim.y - 1), ...
+constexpr int kSumLanes = 16;
+
+template <typename T> __global__ void __launch_bounds__(32 * kSumLanes) norm_bwd_sum(const __grid_constant__ NormP p, int groups)
 {
+    __shared__ float red[kSumLanes][4][32];
     pdl_enter();
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= p.d) return;
-    const float w = p.w_post ? C16<T>::one(p.w_post[c]) : 1.f, b = p.b_post ? C16<T>::one(p.b_post[c]) : 0.f;
-    float p1 = 0.f, p0 = 0.f, dw = 0.f, db = 0.f;
-    for (int g = 0; g * p.per_group < p.units; ++g) {
-        float s1 = 0.f, s0 = 0.f;
-        for (int k = 0; k < p.per_group && g * p.per_group + k < p.units; ++k) {
-            const float *o = p.part + (int64_t)(g * p.per_group + k) * 4 * p.d + c;
-            p1 += o[0];
-            p0 += o[p.d];
-            s1 += o[2 * (int64_t)p.d];
-            s0 += o[3 * (int64_t)p.d];
+    const int l = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
+    const bool in = c < p.d;
+    const int64_t d = p.d;
+    if (blockIdx.y > 0) {
+        const float w = in && p.w_post ? C16<T>::one(p.w_post[c]) : 1.f, b = in && p.b_post ? C16<T>::one(p.b_post[c]) : 0.f;
+        for (int g = (int)blockIdx.y - 1; g < groups; g += (int)gridDim.y - 1) {
+            float s1 = 0.f, s0 = 0.f;
+            if (in) {
+#pragma unroll 4
+                for (int i = k; i < p.per_group; i += kSumLanes) {
+                    const float *o = p.part + ((int64_t)g * p.per_group + i) * 4 * d + c;
+                    s1 += o[2 * d];
+                    s0 += o[3 * d];
+                }
+            }
+            red[k][0][l] = s1, red[k][1][l] = s0;
+            __syncthreads();
+            if (in && k == 0) {
+                for (int j = 1; j < kSumLanes; ++j) s1 += red[j][0][l], s0 += red[j][1][l];
+                put<T>(p, p.dgate, g * d + c, p.bs * fmaf(w, s1, b * s0));
+            }
+            __syncthreads();
         }
-        const float gate = p.gate && !p.per_token ? C16<T>::one(p.gate[g * p.ldgate + c]) : 1.f;
-        dw = fmaf(p.bs * gate, s1, dw);
-        db = fmaf(p.bs * gate, s0, db);
-        if (p.dgate && !p.per_token) put<T>(p, p.dgate, (int64_t)g * p.d + c, p.bs * fmaf(w, s1, b * s0));
+        return;
     }
-    put<T>(p, p.dw_pre, c, p1);
-    put<T>(p, p.db_pre, c, p0);
-    put<T>(p, p.dw_post, c, dw);
-    put<T>(p, p.db_post, c, db);
+    float v[4] = {}; // P1, P0, gate S1, gate S0
+    if (in) {
+#pragma unroll 4
+        for (int i = k; i < p.units; i += kSumLanes) {
+            const float *o = p.part + (int64_t)i * 4 * d + c;
+            const float gate = p.gate && !p.per_token ? C16<T>::one(p.gate[(int64_t)(i / p.per_group) * p.ldgate + c]) : 1.f;
+            v[0] += o[0];
+            v[1] += o[d];
+            v[2] = fmaf(gate, o[2 * d], v[2]);
+            v[3] = fmaf(gate, o[3 * d], v[3]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[k][i][l] = v[i];
+    __syncthreads();
+    if (!in || k) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        for (int j = 1; j < kSumLanes; ++j) v[i] += red[j][i][l];
+    put<T>(p, p.dw_pre, c, v[0]);
+    put<T>(p, p.db_pre, c, v[1]);
+    put<T>(p, p.dw_post, c, p.bs * v[2]);
+    put<T>(p, p.db_post, c, p.bs * v[3]);
 }
+
 
 // ------------------------------------------------------------------ pipelined rows
 constexpr int kPipeThreads = 512, kPipeMaxD = 8192;
@@ -1142,7 +1182,8 @@ template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &
     const int64_t blocks = (int64_t)p.units * ((p.d + 1023) / 1024);
     e = launch_pdl(norm_bwd_cols<T>, dim3((unsigned)blocks), dim3(128), 0, s, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_bwd_sum<T>, dim3((p.d + 63) / 64), dim3(64), 0, s, p);
+    const int groups = p.units / p.per_group, gy = p.dgate && !p.per_token ? std::min(groups, 64) : 0;
+    return launch_pdl(norm_bwd_sum<T>, dim3((p.d + 31) / 32, 1 + gy), dim3(32 * kSumLanes), 0, s, p, groups);
 }
 
 bool norm_kind(int k) { return k == PI_NORM_NONE || k == PI_NORM_RMS || k == PI_NORM_LAYER; }
@@ -1196,7 +1237,7 @@ NormP params(const pi_norm_residual_desc &d, const pi_norm_residual_params *q)
 
 // The units of the column sums, and the workspace.
 struct Units {
-    int units, per_group;
+    int units, per_group, unit;
     bool per_token;
     size_t stats, part;
 };
@@ -1206,7 +1247,8 @@ Units plan_units(const pi_norm_residual_desc &d, bool gate, int sms)
     Units u;
     const int gr = gate && d.gate_rows ? d.gate_rows : std::max(1, d.T);
     u.per_token = gate && gr == 1 && d.T > 1;
-    u.per_group = ((u.per_token ? d.T : std::min(gr, std::max(1, d.T))) + kUnitRows - 1) / kUnitRows;
+    u.unit = unit_rows(d.T, d.d);
+    u.per_group = ((u.per_token ? d.T : std::min(gr, std::max(1, d.T))) + u.unit - 1) / u.unit;
     const int64_t groups = u.per_token ? 1 : (d.T + (int64_t)gr - 1) / gr;
     // the last gate row may have fewer tokens, and units without any add zeros
     u.units = (int)(groups * u.per_group);
@@ -1298,7 +1340,7 @@ pi_status pi_norm_residual_bwd(pi_ctx *c, const pi_norm_residual_desc *desc, con
     p.dgate = gr->dgate, p.dw_pre = gr->dw_pre, p.db_pre = gr->db_pre, p.dw_post = gr->dw_post, p.db_post = gr->db_post;
     p.g32 = d.grad_dtype == PI_F32, p.acc = accumulate != 0;
     const Units u = plan_units(d, p.gate != nullptr, v.sms);
-    p.units = u.units, p.per_group = u.per_group, p.per_token = u.per_token;
+    p.units = u.units, p.per_group = u.per_group, p.unit = u.unit, p.per_token = u.per_token;
     if (!p.gate) p.gate_rows = d.T;
     if (want) {
         const size_t need = u.stats + u.part;
