@@ -241,8 +241,8 @@ pi_status check_ws(pi_ctx *c, const void *ws, size_t have, size_t need)
     return PI_OK;
 }
 
-// Products run one after the other on one stream, so their workspaces share
-// one region.
+// Launches follow one another on one stream, so their workspaces share one
+// region.
 struct Plan {
     Gemm g[5];
     int n = 0;
@@ -254,9 +254,11 @@ struct Plan {
         g[n].e.scale = 1.f;
         return g[n++];
     }
-    void size(const CtxView &v)
+    // products [0, first) run alone, the rest in one launch
+    void size(const CtxView &v, int first)
     {
-        for (int i = 0; i < n; ++i) bytes = std::max(bytes, gemm_workspace(g[i], v));
+        for (int i = 0; i < first; ++i) bytes = std::max(bytes, gemm_workspace(g[i], v));
+        if (n > first) bytes = std::max(bytes, gemms_workspace(g + first, n - first, v));
     }
 };
 
@@ -311,7 +313,7 @@ LinearFwd plan_linear(const pi_linear_desc &d, const CtxView &v, const void *x, 
     e.bias = (const uint16_t *)b, e.res = r, e.ldr = d.ldr, e.out = y, e.ldo = d.ldy;
     e.out2 = (uint16_t *)z, e.ld2 = d.ldz;
     set_vec(e);
-    f.p.size(v);
+    f.p.size(v, f.p.n);
     f.gws = a.take(f.p.bytes);
     f.bytes = a.used;
     return f;
@@ -324,7 +326,6 @@ struct LinearBwd {
     int64_t lddz;
     void *part;
     Plan p;
-    int i_dx = -1, i_dw = -1;
     void *gws;
     size_t bytes;
 };
@@ -347,7 +348,6 @@ LinearBwd plan_linear_bwd(const pi_linear_desc &d, const CtxView &v, const void 
     if (dx) f.w = stage(a, w, d.ldw, d.N, d.K, 1);
     f.part = db ? a.take(colsum_bytes(d.T, d.N)) : nullptr;
     if (dx) {
-        f.i_dx = f.p.n;
         Gemm &g = f.p.add();
         g.mode = EPI_LINEAR;
         g.M = d.T, g.N = d.K, g.K[0] = d.N;
@@ -356,7 +356,6 @@ LinearBwd plan_linear_bwd(const pi_linear_desc &d, const CtxView &v, const void 
         set_vec(g.e);
     }
     if (dw) {
-        f.i_dw = f.p.n;
         Gemm &g = f.p.add();
         g.mode = EPI_LINEAR;
         g.M = d.N, g.N = d.K, g.K[0] = d.T;
@@ -366,7 +365,7 @@ LinearBwd plan_linear_bwd(const pi_linear_desc &d, const CtxView &v, const void 
         if (acc) g.e.res = dw, g.e.ldr = d.lddw;
         set_vec(g.e);
     }
-    f.p.size(v);
+    f.p.size(v, 0);
     f.gws = a.take(f.p.bytes);
     f.bytes = a.used;
     return f;
@@ -455,7 +454,7 @@ FfnFwd plan_ffn(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated_ffn
     h.e.bias = (const uint16_t *)w.b_down;
     h.e.out = y, h.e.ldo = d.ldy;
     set_vec(h.e);
-    f.p.size(v);
+    f.p.size(v, f.p.n);
     f.gws = ar.take(f.p.bytes);
     f.bytes = ar.used;
     return f;
@@ -467,7 +466,7 @@ struct FfnBwd {
     int64_t ldd;
     void *part;
     Plan p;
-    int i_da = -1, i_dx = -1, i_wg = -1, i_wu = -1, i_wd = -1;
+    bool da = false; // the first product is da; the others follow it
     void *gws;
     size_t bytes;
 };
@@ -493,7 +492,7 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
     f.part = gr.b_up || gr.b_gate || gr.b_down ? ar.take(std::max(colsum_bytes(d.T, d.n), colsum_bytes(d.T, d.d))) : nullptr;
     const int g32 = d.grad_dtype == PI_F32;
     if (want_d) {
-        f.i_da = f.p.n;
+        f.da = true;
         Gemm &g = f.p.add();
         g.mode = EPI_DACT;
         g.M = d.T, g.N = d.n, g.K[0] = d.d;
@@ -511,7 +510,6 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
         set_vec(g.e);
     }
     if (dx) {
-        f.i_dx = f.p.n;
         Gemm &g = f.p.add();
         g.mode = EPI_LINEAR;
         g.M = d.T, g.N = d.d;
@@ -533,10 +531,10 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
         if (acc) g.e.res = out, g.e.ldr = N;
         set_vec(g.e);
     };
-    if (gr.w_gate) f.i_wg = f.p.n, wgrad(f.p.add(), {f.dg, f.ldd, 1}, d.n, d.d, f.x.m, gr.w_gate);
-    if (gr.w_up) f.i_wu = f.p.n, wgrad(f.p.add(), {f.du, f.ldd, 1}, d.n, d.d, f.x.m, gr.w_up);
-    if (gr.w_down) f.i_wd = f.p.n, wgrad(f.p.add(), f.dy.m, d.d, d.n, f.a.m, gr.w_down);
-    f.p.size(v);
+    if (gr.w_gate) wgrad(f.p.add(), {f.dg, f.ldd, 1}, d.n, d.d, f.x.m, gr.w_gate);
+    if (gr.w_up) wgrad(f.p.add(), {f.du, f.ldd, 1}, d.n, d.d, f.x.m, gr.w_up);
+    if (gr.w_down) wgrad(f.p.add(), f.dy.m, d.d, d.n, f.a.m, gr.w_down);
+    f.p.size(v, f.da);
     f.gws = ar.take(f.p.bytes);
     f.bytes = ar.used;
     return f;
@@ -587,13 +585,17 @@ pi_status pi_linear_workspace(pi_ctx *c, const pi_linear_desc *desc, int32_t bac
     if (!bytes) return ctx_fail(c, PI_ERR_ARG, "bytes is NULL");
     pi_linear_desc d;
     if (pi_status st = check_linear(c, desc, d)) return st;
-    // the most that a call with this desc takes, all outputs wanted: with
-    // `unaligned`, every operand is copied
+    // the most that a call with this desc takes: with `unaligned`, every
+    // operand is copied
     const CtxView v = ctx_view(c);
     const void *odd = (const void *)(uintptr_t)(d.unaligned ? 2 : 16);
     if (backward) {
-        const size_t a = plan_linear_bwd(d, v, odd, odd, odd, odd, (void *)odd, odd, 1, nullptr).bytes;
-        *bytes = d.T ? a : 0;
+        // (fewer outputs may be cut differently)
+        *bytes = 0;
+        for (int want = 0; d.T && want < 4; ++want) {
+            void *dx = want & 1 ? (void *)odd : nullptr, *dw = want & 2 ? (void *)odd : nullptr;
+            *bytes = std::max(*bytes, plan_linear_bwd(d, v, odd, odd, odd, dx, dw, odd, 1, nullptr).bytes);
+        }
     } else
         *bytes = d.T ? plan_linear(d, v, odd, odd, odd, odd, (void *)odd, (void *)odd, nullptr).bytes : 0;
     return PI_OK;
@@ -650,11 +652,8 @@ pi_status pi_linear_bwd(pi_ctx *c, const pi_linear_desc *desc, const void *dy, c
         if (db) CUB(launch_colsum(dy, 0, d.ldy, d.T, d.N, 1.f, db, g32, accumulate, bf, f.part, v.stream));
     }
     if (dw) CUB(run_copy(f.x, v.stream));
-    if (dx) {
-        CUB(run_copy(f.w, v.stream));
-        CUB(launch_gemm(f.p.g[f.i_dx], bf, v, f.gws));
-    }
-    if (dw) CUB(launch_gemm(f.p.g[f.i_dw], bf, v, f.gws));
+    if (dx) CUB(run_copy(f.w, v.stream));
+    if (f.p.n) CUB(launch_gemms(f.p.g, f.p.n, bf, v, f.gws));
     return PI_OK;
 }
 
@@ -668,11 +667,15 @@ pi_status pi_gated_ffn_workspace(pi_ctx *c, const pi_gated_ffn_desc *desc, int32
     void *odd = (void *)(uintptr_t)(d.unaligned ? 2 : 16);
     void *gate = d.gated ? odd : nullptr;
     const pi_gated_ffn_weights w = {gate, odd, odd, gate, odd, odd};
-    const pi_gated_ffn_grads gr = {gate, odd, odd, gate, odd, odd};
     const pi_gated_ffn_save s = {gate, odd, odd}, none = {nullptr, nullptr, nullptr};
     if (d.T == 0) *bytes = 0;
-    else if (backward) *bytes = plan_ffn_bwd(d, v, w, odd, odd, s, odd, gr, 1, nullptr).bytes;
-    else
+    else if (backward) {
+        *bytes = 0;
+        for (int want = 0; want < 16; ++want) {
+            const pi_gated_ffn_grads gr = {want & 1 ? gate : nullptr, want & 2 ? odd : nullptr, want & 4 ? odd : nullptr, gate, odd, odd};
+            *bytes = std::max(*bytes, plan_ffn_bwd(d, v, w, odd, odd, s, want & 8 ? odd : nullptr, gr, 1, nullptr).bytes);
+        }
+    } else
         *bytes = std::max(plan_ffn(d, v, w, odd, s, odd, nullptr).bytes, plan_ffn(d, v, w, odd, none, odd, nullptr).bytes);
     return PI_OK;
 }
@@ -738,11 +741,8 @@ pi_status pi_gated_ffn_bwd(pi_ctx *c, const pi_gated_ffn_desc *desc, const pi_ga
     DeviceGuard g(v.device);
     const Staged *copies[] = {&f.dy, &f.wd, &f.wg, &f.wu, &f.x, &f.a};
     for (const Staged *s : copies) CUB(run_copy(*s, v.stream));
-    if (f.i_da >= 0) CUB(launch_gemm(f.p.g[f.i_da], bf, v, f.gws));
-    if (f.i_dx >= 0) CUB(launch_gemm(f.p.g[f.i_dx], bf, v, f.gws));
-    if (f.i_wg >= 0) CUB(launch_gemm(f.p.g[f.i_wg], bf, v, f.gws));
-    if (f.i_wu >= 0) CUB(launch_gemm(f.p.g[f.i_wu], bf, v, f.gws));
-    if (f.i_wd >= 0) CUB(launch_gemm(f.p.g[f.i_wd], bf, v, f.gws));
+    if (f.da) CUB(launch_gemm(f.p.g[0], bf, v, f.gws));
+    if (f.p.n > f.da) CUB(launch_gemms(f.p.g + f.da, f.p.n - f.da, bf, v, f.gws));
     if (gr.b_gate) CUB(launch_colsum(f.dg, 0, f.ldd, d.T, d.n, 1.f, gr.b_gate, g32, accumulate, bf, f.part, v.stream));
     if (gr.b_up) CUB(launch_colsum(f.du, 0, f.ldd, d.T, d.n, 1.f, gr.b_up, g32, accumulate, bf, f.part, v.stream));
     if (gr.b_down) CUB(launch_colsum(dy, 0, d.ldy, d.T, d.d, 1.f, gr.b_down, g32, accumulate, bf, f.part, v.stream));

@@ -63,6 +63,11 @@ struct Gemm {
 size_t gemm_workspace(const Gemm &g, const CtxView &v);
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
+// The same for up to four products that are independent of one another, in one
+// launch; their epilogues are EPI_LINEAR without bias, activation, scale or z.
+size_t gemms_workspace(const Gemm *g, int n, const CtxView &v);
+cudaError_t launch_gemms(const Gemm *g, int n, bool bf16, const CtxView &v, void *ws);
+
 // Products of up to this many rows of A go to skinny_tc (pi_skinny.cu) where
 // both operands lie along k.
 constexpr int kSkinnyRows = 128;

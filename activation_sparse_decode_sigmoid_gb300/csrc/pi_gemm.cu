@@ -16,6 +16,11 @@
 // of the previous tile out of the other half of tensor memory (2 x 256
 // columns).  Six stages of 32 KB.
 //
+// One launch takes up to four products that do not wait for one another (a
+// backward pass's gradients of x and of the weights): their tiles are dealt to
+// the pairs longest first, so that one product's last, partly filled wave is
+// filled by the next.
+//
 // Tiles past the last whole wave are split along k: their steps, put end to
 // end, are cut into equal ranges, one per pair; each pair writes its fp32
 // partial tile(s), and gemm_fixup adds them in order and runs the epilogue.
@@ -61,18 +66,36 @@ constexpr uint32_t kBox = 2048;                 // 32 rows x 32 columns of an ep
 constexpr uint32_t kBoxes = kEpiWarps * 2 * kBox;
 constexpr uint32_t kBiasB = 256;                // a warp's 128 bias values (gated: 64 of each)
 
-struct TcParams {
+constexpr int kMaxProbs = 4;
+
+struct Prob {
     CUtensorMap ma[2], mb[2];
     int M, N, tm, tn;     // tiles along M and N
     int kt0, KT;          // k steps of the first segment, and of all
     int a_mn, b_mn;
-    int nfull;            // tiles computed whole (the first ones)
-    int nsplit, parts;    // tiles split along k, and pairs that share them
+    Epi e;
+};
+
+// Tiles tile0 + i, i < count, of a product, computed whole: by pair (pair0 + i mod npairs) mod all pairs.
+struct Deal {
+    int prob, tile0, count, pair0, npairs;
+};
+
+// How a group of products is cut.
+struct Sched {
+    Deal deal[2 * kMaxProbs];
+    int ndeal, pairs;     // pairs that tiles are dealt to
+    int sprob, stile0;    // the product whose last tiles are split along k, the first of them
+    int nsplit, parts;    // how many, and pairs that share them
     int smax;             // partial tiles kept per split tile
+};
+
+template <int NP> struct TcParams {
+    Prob prob[NP];
+    Sched s;
     float *part;          // [nsplit][smax][256][256]
     int *status, *abort_flag;
     unsigned long long wait_ns;
-    Epi e;
 };
 
 // ------------------------------------------------------------------ schedule
@@ -95,33 +118,47 @@ __host__ __device__ inline int part_of(int64_t units, int64_t u, int parts)
 }
 
 struct Work {
-    int tile, k0, k1, slot; // slot < 0: a whole tile
+    int prob, tile, k0, k1, slot; // slot < 0: a whole tile
 };
 
-// The work of pair c of n, in order; every role of both CTAs walks it alike.
-struct Walk {
-    const TcParams &p;
-    int t, n, u, u1, c;
-    __device__ __forceinline__ Walk(const TcParams &q, int c_, int n_) : p(q), t(c_), n(n_), u(0), u1(0), c(c_)
+// The work of pair c, in order; every role of both CTAs walks it alike.
+template <int NP> struct Walk {
+    const TcParams<NP> &p;
+    int c, d, i, u, u1;
+    __device__ __forceinline__ Walk(const TcParams<NP> &q, int c_) : p(q), c(c_), d(0), u(0), u1(0)
     {
-        if (c < p.parts) {
-            const int64_t units = (int64_t)p.nsplit * p.KT;
-            u = range_at(units, c, p.parts);
-            u1 = range_at(units, c + 1, p.parts);
+        i = first(0);
+        if (c < p.s.parts) {
+            const int64_t units = (int64_t)p.s.nsplit * p.prob[NP == 1 ? 0 : p.s.sprob].KT;
+            u = range_at(units, c, p.s.parts);
+            u1 = range_at(units, c + 1, p.s.parts);
         }
+    }
+    // this pair's first index in deal d
+    __device__ __forceinline__ int first(int d_) const
+    {
+        const Deal &e = p.s.deal[d_];
+        int pos = c - e.pair0;
+        pos += pos < 0 ? p.s.pairs : 0;
+        return pos < e.npairs ? pos : 0x7fffffff;
     }
     __device__ __forceinline__ bool next(Work &w)
     {
-        if (t < p.nfull) {
-            w = {t, 0, p.KT, -1};
-            t += n;
-            return true;
+        while (d < p.s.ndeal) {
+            const Deal &e = p.s.deal[d];
+            if (i < e.count) {
+                w = {NP == 1 ? 0 : e.prob, e.tile0 + i, 0, p.prob[NP == 1 ? 0 : e.prob].KT, -1};
+                i += e.npairs;
+                return true;
+            }
+            if (++d < p.s.ndeal) i = first(d);
         }
         if (u >= u1) return false;
-        const int r = u / p.KT, k0 = u - r * p.KT;
-        const int k1 = min(p.KT, k0 + u1 - u);
-        const int first = part_of((int64_t)p.nsplit * p.KT, (int64_t)r * p.KT, p.parts);
-        w = {p.nfull + r, k0, k1, r * p.smax + (c - first)};
+        const int KT = p.prob[NP == 1 ? 0 : p.s.sprob].KT;
+        const int r = u / KT, k0 = u - r * KT;
+        const int k1 = min(KT, k0 + u1 - u);
+        const int lead = part_of((int64_t)p.s.nsplit * KT, (int64_t)r * KT, p.s.parts);
+        w = {p.s.sprob, p.s.stile0 + r, k0, k1, r * p.s.smax + (c - lead)};
         u += k1 - k0;
         return true;
     }
@@ -307,12 +344,13 @@ __device__ __forceinline__ void box_send(uint32_t box, const Strip &s, int lane,
 }
 
 // ------------------------------------------------------------------ the kernel
-template <typename T, int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gemm_tc(const __grid_constant__ TcParams p)
+template <typename T, int MODE, int NP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gemm_tc(const __grid_constant__ TcParams<NP> p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     using H = H16<T>;
     constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile; // output columns of a tile
+    constexpr bool kPlain = NP > 1; // a backward pass's products: no bias, activation, scale or z
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kBoxes + kEpiWarps * kBiasB); // used in the first CTA
@@ -322,8 +360,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     uint32_t *tslot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     if (warp == kEpiWarps && lane == 0) {
         // the maps are on their way while the rest is set up
-        prefetch_map(&p.ma[0]), prefetch_map(&p.mb[0]);
-        if (p.kt0 < p.KT || MODE == EPI_GATED) prefetch_map(&p.ma[1]), prefetch_map(&p.mb[1]);
+        const Prob &pr = p.prob[NP == 1 ? 0 : p.s.ndeal ? p.s.deal[0].prob : p.s.sprob];
+        prefetch_map(&pr.ma[0]), prefetch_map(&pr.mb[0]);
+        if (MODE == EPI_GATED) prefetch_map(&pr.mb[1]);
     }
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init1(full + s), mbar_init1(empty + s);
@@ -343,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
     pdl_enter();
 
     const uint32_t base = smem_addr(smem);
-    Walk walk(p, (int)blockIdx.x >> 1, (int)gridDim.x >> 1);
+    Walk<NP> walk(p, (int)blockIdx.x >> 1);
     Work w;
     bool ok = true;
     if (warp == kEpiWarps) {
@@ -351,13 +390,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         Cur cur(0, kStages);
         uint32_t round = 0;
         while (ok && walk.next(w)) {
+            const Prob &pr = p.prob[NP == 1 ? 0 : w.prob];
             int mi, ni;
-            tile_at(w.tile, p.tm, p.tn, mi, ni);
+            tile_at(w.tile, pr.tm, pr.tn, mi, ni);
             const int m0 = mi * kTile + (int)rank * 128;
             const int n0 = ni * kOutN + (MODE == EPI_GATED ? 0 : (int)rank * 128);
             for (int seg = 0; seg < 2; ++seg) {
-                const int lo = seg ? p.kt0 : 0, ka = max(w.k0, lo), kb = min(w.k1, seg ? p.KT : p.kt0);
-                const CUtensorMap *ma = &p.ma[seg], *mb = &p.mb[MODE == EPI_GATED ? (int)rank : seg];
+                const int lo = seg ? pr.kt0 : 0, ka = max(w.k0, lo), kb = min(w.k1, seg ? pr.KT : pr.kt0);
+                const CUtensorMap *ma = &pr.ma[seg], *mb = &pr.mb[MODE == EPI_GATED ? (int)rank : seg];
                 for (int k = ka; k < kb; ++k) {
                     if (round >= kStages && !mbar_wait_all(empty + cur.s, cur.ph ^ 1u, p)) {
                         ok = false;
@@ -367,12 +407,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                         const uint32_t bar = full0 + cur.s * 8, sa = base + cur.s * kStageBytes, sb = sa + kOpBytes;
                         const int kc = (k - lo) * kBK;
                         if (rank == 0) mbar_expect(full + cur.s, 2 * kStageBytes);
-                        if (p.a_mn) {
+                        if (pr.a_mn) {
                             pair_load(sa, ma, m0, kc, bar);
                             pair_load(sa + kAtom, ma, m0 + 64, kc, bar);
                         } else
                             pair_load(sa, ma, kc, m0, bar);
-                        if (p.b_mn) {
+                        if (pr.b_mn) {
                             pair_load(sb, mb, n0, kc, bar);
                             pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
                         } else
@@ -391,13 +431,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         }
     } else if (warp == kEpiWarps + 1) {
         if (rank == 0) {
-            const uint32_t id = idesc(H::fmt, (uint32_t)p.a_mn, (uint32_t)p.b_mn, 256, 256);
-            // descriptors of stage 0; a byte offset o adds o / 16 (the start address field)
-            const uint64_t da = p.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
-            const uint64_t db = p.b_mn ? sdesc(base + kOpBytes, kAtom, 1024) : sdesc(base + kOpBytes, 16, 1024);
-            const uint32_t ka = p.a_mn ? 128 : 2, kb = p.b_mn ? 128 : 2; // 16 elements of k
             Cur cur(0, kStages);
             for (uint32_t it = 0; ok && walk.next(w); ++it) {
+                const Prob &pr = p.prob[NP == 1 ? 0 : w.prob];
+                const uint32_t id = idesc(H::fmt, (uint32_t)pr.a_mn, (uint32_t)pr.b_mn, 256, 256);
+                // descriptors of stage 0; a byte offset o adds o / 16 (the start address field)
+                const uint64_t da = pr.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
+                const uint64_t db = pr.b_mn ? sdesc(base + kOpBytes, kAtom, 1024) : sdesc(base + kOpBytes, 16, 1024);
+                const uint32_t ka = pr.a_mn ? 128 : 2, kb = pr.b_mn ? 128 : 2; // 16 elements of k
                 const uint32_t buf = it & 1, ph = (it >> 1) & 1;
                 if (it >= 2 && !mbar_wait_all(acc_empty + buf, ph ^ 1u, p)) {
                     ok = false;
@@ -430,27 +471,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         const int q = warp & 3, half = warp >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t box0 = base + kStages * kStageBytes + (uint32_t)warp * 2 * kBox, box1 = box0 + kBox;
-        const Epi &e = p.e;
-        const bool two = MODE == EPI_DACT && e.in2, out32 = MODE == EPI_LINEAR && e.out32;
-        const bool has_in = MODE == EPI_DACT || (MODE == EPI_LINEAR && e.res && !out32);
-        const Strip out = {static_cast<uint16_t *>(e.out), e.ldo, (e.vec & V_OUT) != 0};
-        const Strip out2 = {e.out2, e.ld2, (e.vec & V_OUT2) != 0}, out3 = {e.out3, e.ld3, (e.vec & V_OUT3) != 0};
-        const Strip in1 = MODE == EPI_DACT ? Strip{const_cast<uint16_t *>(e.in1), e.ldi1, (e.vec & V_IN1) != 0}
-                                           : Strip{static_cast<uint16_t *>(const_cast<void *>(e.res)), e.ldr, (e.vec & V_RES) != 0};
-        const Strip in2 = {const_cast<uint16_t *>(e.in2), e.ldi2, (e.vec & V_IN2) != 0};
         constexpr int kCols = kOutN / 2; // of this warp
         const uint32_t bias = base + kStages * kStageBytes + kBoxes + (uint32_t)warp * kBiasB;
-        const bool biased = MODE != EPI_DACT && (e.bias || e.bias2);
         for (uint32_t it = 0; ok && walk.next(w); ++it) {
+            const Prob &pr = p.prob[NP == 1 ? 0 : w.prob];
+            const int M = pr.M, N = pr.N;
+            const Epi &e = pr.e;
+            const bool two = MODE == EPI_DACT && e.in2, out32 = MODE == EPI_LINEAR && e.out32;
+            const bool has_in = MODE == EPI_DACT || (MODE == EPI_LINEAR && e.res && !out32);
+            const Strip out = {static_cast<uint16_t *>(e.out), e.ldo, (e.vec & V_OUT) != 0};
+            const Strip out2 = {e.out2, e.ld2, (e.vec & V_OUT2) != 0}, out3 = {e.out3, e.ld3, (e.vec & V_OUT3) != 0};
+            const Strip in1 = MODE == EPI_DACT ? Strip{const_cast<uint16_t *>(e.in1), e.ldi1, (e.vec & V_IN1) != 0}
+                                               : Strip{static_cast<uint16_t *>(const_cast<void *>(e.res)), e.ldr, (e.vec & V_RES) != 0};
+            const Strip in2 = {const_cast<uint16_t *>(e.in2), e.ldi2, (e.vec & V_IN2) != 0};
+            const bool biased = !kPlain && MODE != EPI_DACT && (e.bias || e.bias2);
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
             int mi, ni;
-            tile_at(w.tile, p.tm, p.tn, mi, ni);
+            tile_at(w.tile, pr.tm, pr.tn, mi, ni);
             const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * kOutN + half * kCols;
             const bool whole = w.slot < 0;
             uint4 q1[4], q2[4]; // the next chunk's inputs
             if (whole && has_in) { // in flight while the products finish
-                strip_load(in1, lane, row0, col0, p.M, p.N, q1);
-                if (two) strip_load(in2, lane, row0, col0, p.M, p.N, q2);
+                strip_load(in1, lane, row0, col0, M, N, q1);
+                if (two) strip_load(in2, lane, row0, col0, M, N, q2);
             }
             if (whole && biased) { // 4 values a lane
                 const int h = MODE == EPI_GATED ? lane >> 4 : 0, k = (MODE == EPI_GATED ? lane & 15 : lane) * 4;
@@ -459,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 if (src) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (col0 + k + i < p.N) b[i >> 1] |= (uint32_t)src[col0 + k + i] << (16 * (i & 1));
+                        if (col0 + k + i < N) b[i >> 1] |= (uint32_t)src[col0 + k + i] << (16 * (i & 1));
                 }
                 __syncwarp();
                 asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(bias + lane * 8), "r"(b[0]), "r"(b[1]) : "memory");
@@ -477,22 +520,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 for (int c = half * 128; c < half * 128 + 128; c += 32) {
                     float v[32];
                     tmem_ld32(ta + c, v);
-                    if (row0 + lane < p.M) {
+                    if (row0 + lane < M) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
-            } else if (row0 < p.M) {
+            } else if (row0 < M) {
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += 32) {
                     const int col = col0 + c;
-                    if (col >= p.N) break;
-                    const bool inside = row0 + 32 <= p.M && col + 32 <= p.N;
+                    if (col >= N) break;
+                    const bool inside = row0 + 32 <= M && col + 32 <= N;
                     float v[32], u[MODE == EPI_GATED ? 32 : 1];
                     tmem_ld32(ta + half * kCols + c, v);
                     if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
-                    if (c + 32 >= kCols || col + 32 >= p.N) {
+                    if (c + 32 >= kCols || col + 32 >= N) {
                         // the accumulator is in registers: the next tile's products may begin
                         tc_before();
                         __syncwarp();
@@ -503,8 +546,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                         strip_to_box(box0, lane, q1);
                         if (two) strip_to_box(box1, lane, q2);
                         if (!released) {
-                            strip_load(in1, lane, row0, col + 32, p.M, p.N, q1);
-                            if (two) strip_load(in2, lane, row0, col + 32, p.M, p.N, q2);
+                            strip_load(in1, lane, row0, col + 32, M, N, q1);
+                            if (two) strip_load(in2, lane, row0, col + 32, M, N, q2);
                         }
                         __syncwarp();
                     }
@@ -522,13 +565,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                             }
                         }
                     }
-                    if (MODE != EPI_DACT && e.out2) {
+                    if (!kPlain && MODE != EPI_DACT && e.out2) {
                         box_put<T>(box1, lane, v);
-                        box_send(box1, out2, lane, row0, col, p.M, p.N, inside);
+                        box_send(box1, out2, lane, row0, col, M, N, inside);
                     }
                     if (MODE == EPI_GATED && e.out3) {
                         box_put<T>(box1, lane, *reinterpret_cast<float(*)[32]>(u));
-                        box_send(box1, out3, lane, row0, col, p.M, p.N, inside);
+                        box_send(box1, out3, lane, row0, col, M, N, inside);
                     }
                     if (MODE == EPI_DACT) {
 #pragma unroll
@@ -547,31 +590,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                                 for (int i = 0; i < 8; ++i) v[8 * j + i] *= e.scale * df[i];
                             }
                         }
-                        if (two) box_send(box1, out2, lane, row0, col, p.M, p.N, inside);
+                        if (two) box_send(box1, out2, lane, row0, col, M, N, inside);
                     } else {
-                        if (e.fn != PI_FN_NONE) acts(e.fn, v);
+                        if (!kPlain && e.fn != PI_FN_NONE) acts(e.fn, v);
                         if (MODE == EPI_GATED) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] *= u[i % (MODE == EPI_GATED ? 32 : 1)];
                         } else {
-                            if (e.scale != 1.f) {
+                            if (!kPlain && e.scale != 1.f) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) v[i] *= e.scale;
                             }
                             if (out32) {
-                                if (row0 + lane < p.M)
+                                if (row0 + lane < M)
 #pragma unroll
                                     for (int j = 0; j < 4; ++j) {
                                         const int cj = col + 8 * j;
-                                        if (cj >= p.N) break;
+                                        if (cj >= N) break;
                                         float(&x)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * j);
                                         if (e.res) {
                                             float r[8];
-                                            load8f(static_cast<const float *>(e.res) + (int64_t)(row0 + lane) * e.ldr + cj, p.N - cj, e.vec & V_RES, r);
+                                            load8f(static_cast<const float *>(e.res) + (int64_t)(row0 + lane) * e.ldr + cj, N - cj, e.vec & V_RES, r);
 #pragma unroll
                                             for (int i = 0; i < 8; ++i) x[i] += r[i];
                                         }
-                                        store8f(static_cast<float *>(e.out) + (int64_t)(row0 + lane) * e.ldo + cj, p.N - cj, e.vec & V_OUT, x);
+                                        store8f(static_cast<float *>(e.out) + (int64_t)(row0 + lane) * e.ldo + cj, N - cj, e.vec & V_OUT, x);
                                     }
                                 continue;
                             }
@@ -587,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                         }
                     }
                     box_put<T>(box0, lane, v);
-                    box_send(box0, out, lane, row0, col, p.M, p.N, inside);
+                    box_send(box0, out, lane, row0, col, M, N, inside);
                 }
             }
             if (!released) {
@@ -609,20 +652,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
 
 // The split tiles: partials added in the order of k, then the epilogue.
 // 256 threads take 8 columns each of 8 (gated: 16) rows.
-template <typename T, int MODE> __global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcParams p)
+template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcParams<NP> p)
 {
     pdl_enter();
+    const Prob &pr = p.prob[NP == 1 ? 0 : p.s.sprob];
     constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile, kCols = kOutN / 8, kRows = 256 / kCols;
     const int per = kTile / kRows, r = (int)blockIdx.x / per;
     const int row = ((int)blockIdx.x % per) * kRows + threadIdx.x / kCols, c = (threadIdx.x % kCols) * 8;
     int mi, ni;
-    tile_at(p.nfull + r, p.tm, p.tn, mi, ni);
+    tile_at(p.s.stile0 + r, pr.tm, pr.tn, mi, ni);
     const int grow = mi * kTile + row, gcol = ni * kOutN + c;
-    if (grow >= p.M || gcol >= p.N) return;
-    const int64_t units = (int64_t)p.nsplit * p.KT;
-    const int cnt = part_of(units, (int64_t)(r + 1) * p.KT - 1, p.parts) - part_of(units, (int64_t)r * p.KT, p.parts) + 1;
+    if (grow >= pr.M || gcol >= pr.N) return;
+    const int64_t units = (int64_t)p.s.nsplit * pr.KT;
+    const int cnt = part_of(units, (int64_t)(r + 1) * pr.KT - 1, p.s.parts) - part_of(units, (int64_t)r * pr.KT, p.s.parts) + 1;
     float v[8] = {}, u[8] = {};
-    const float *src = p.part + ((size_t)r * p.smax * kTile + row) * kTile + c;
+    const float *src = p.part + ((size_t)r * p.s.smax * kTile + row) * kTile + c;
     for (int s = 0; s < cnt; ++s, src += kTile * kTile) {
         float t[8];
         load8f(src, 8, true, t);
@@ -634,42 +678,73 @@ template <typename T, int MODE> __global__ void __launch_bounds__(256) gemm_fixu
             for (int i = 0; i < 8; ++i) u[i] += t[i];
         }
     }
-    epilogue8<T, MODE>(p.e, p.N, grow, gcol, v, u);
+    epilogue8<T, MODE>(pr.e, pr.N, grow, gcol, v, u);
 }
 
 // ------------------------------------------------------------------ host
-// The tiles that are split along k, and over how many pairs.  A last wave of
-// `rem` tiles on n pairs would take KT steps; split, it takes rem KT / n and
-// the fixup launch with its traffic, worth about kFixupSteps steps.
+// A last wave of `rem` tiles on n pairs takes KT steps; split along k, it takes
+// rem KT / n and the fixup launch with its traffic, worth about kFixupSteps steps.
 constexpr int kFixupSteps = 32;
 constexpr int kMinShare = 4; // k steps per pair, at least
 
-struct Split {
-    int tm, tn, KT, kt0, nfull, nsplit, parts, smax;
+struct Plan {
+    Sched s;
+    int order[kMaxProbs]; // products by falling k steps
+    int tm[kMaxProbs], tn[kMaxProbs], kt0[kMaxProbs], KT[kMaxProbs]; // in that order
+    int launched;         // pairs
     size_t bytes;
 };
 
-Split plan_split(const Gemm &g, int sms)
+Plan plan_group(const Gemm *g, int n, int sms)
 {
-    Split s = {};
-    const int n = sms / 2, outn = g.mode == EPI_GATED ? 128 : kTile;
-    s.tm = (g.M + kTile - 1) / kTile;
-    s.tn = (g.N + outn - 1) / outn;
-    s.kt0 = (g.K[0] + kBK - 1) / kBK;
-    s.KT = s.kt0 + (g.segs > 1 ? (g.K[1] + kBK - 1) / kBK : 0);
-    const int tiles = s.tm * s.tn, rem = tiles % n;
-    s.nfull = tiles;
-    s.smax = 1;
-    if (rem && (int64_t)s.KT * (n - rem) > (int64_t)kFixupSteps * n) {
-        s.nfull = tiles - rem;
-        s.nsplit = rem;
-        const int64_t units = (int64_t)rem * s.KT;
-        s.parts = (int)std::min<int64_t>(n, std::max<int64_t>(1, units / kMinShare));
-        const int share = (int)(units / s.parts); // the smallest range
-        s.smax = s.KT / share + 2;
-        s.bytes = (size_t)rem * s.smax * kTile * kTile * sizeof(float);
+    Plan q = {};
+    const int P = sms / 2;
+    int KT[kMaxProbs];
+    for (int i = 0; i < n; ++i) {
+        KT[i] = (g[i].K[0] + kBK - 1) / kBK + (g[i].segs > 1 ? (g[i].K[1] + kBK - 1) / kBK : 0);
+        q.order[i] = i;
     }
-    return s;
+    std::stable_sort(q.order, q.order + n, [&](int a, int b) { return KT[a] > KT[b]; });
+    Sched &s = q.s;
+    s.pairs = P;
+    s.smax = 1;
+    // Pairs base .. base + high - 1 (mod P) are ahead of the others by `gap` steps.
+    int base = 0, high = 0, gap = 0, used = 0;
+    for (int j = 0; j < n; ++j) {
+        const Gemm &x = g[q.order[j]];
+        const int outn = x.mode == EPI_GATED ? 128 : kTile;
+        q.tm[j] = (x.M + kTile - 1) / kTile;
+        q.tn[j] = (x.N + outn - 1) / outn;
+        q.kt0[j] = (x.K[0] + kBK - 1) / kBK;
+        q.KT[j] = KT[q.order[j]];
+        int t0 = 0, m = q.tm[j] * q.tn[j];
+        if (high && gap >= q.KT[j]) { // the pairs behind catch up first
+            const int lo = P - high;
+            const int cnt = (int)std::min<int64_t>(m, (int64_t)(gap / q.KT[j]) * lo);
+            s.deal[s.ndeal++] = {j, t0, cnt, (base + high) % P, lo};
+            used = P;
+            t0 += cnt, m -= cnt;
+            gap -= (cnt + lo - 1) / lo * q.KT[j];
+        }
+        if (!m) continue;
+        const int rem = m % P, from = (base + high) % P;
+        if (j == n - 1 && rem && (int64_t)q.KT[j] * (P - rem) > (int64_t)kFixupSteps * P) {
+            s.sprob = j, s.stile0 = t0 + m - rem, s.nsplit = rem;
+            const int64_t units = (int64_t)rem * q.KT[j];
+            s.parts = (int)std::min<int64_t>(P, std::max<int64_t>(1, units / kMinShare));
+            s.smax = q.KT[j] / (int)(units / s.parts) + 2;
+            q.bytes = (size_t)rem * s.smax * kTile * kTile * sizeof(float);
+            m -= rem;
+            used = std::max(used, s.parts);
+        }
+        if (m) {
+            s.deal[s.ndeal++] = {j, t0, m, from, P};
+            used = from ? P : std::max(used, std::min(m, P));
+        }
+        base = from, high = m % P, gap = q.KT[j];
+    }
+    q.launched = used;
+    return q;
 }
 
 cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K)
@@ -678,56 +753,71 @@ cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K)
                 : encode_map(m, a.p, (uint64_t)K, (uint64_t)rows, (uint64_t)a.ld * 2, 128);
 }
 
-template <typename T, int MODE> cudaError_t run(const TcParams &p, int pairs, cudaStream_t s)
+template <typename T, int MODE, int NP> cudaError_t run(const Gemm *g, int n, const CtxView &v, void *ws)
 {
+    const Plan q = plan_group(g, n, v.sms);
+    TcParams<NP> p = {};
+    p.s = q.s;
+    cudaError_t e = cudaSuccess;
+    for (int j = 0; j < n; ++j) {
+        const Gemm &x = g[q.order[j]];
+        Prob &pr = p.prob[j];
+        pr.M = x.M, pr.N = x.N, pr.tm = q.tm[j], pr.tn = q.tn[j], pr.kt0 = q.kt0[j], pr.KT = q.KT[j];
+        pr.a_mn = x.a[0].mn, pr.b_mn = x.b[0].mn;
+        pr.e = x.e;
+        for (int i = 0; i < x.segs && e == cudaSuccess; ++i) e = map_of(&pr.ma[i], x.a[i], x.M, x.K[i]);
+        const int nb = MODE == EPI_GATED ? 2 : x.segs;
+        for (int i = 0; i < nb && e == cudaSuccess; ++i) e = map_of(&pr.mb[i], x.b[i], x.N, x.K[MODE == EPI_GATED ? 0 : i]);
+    }
+    if (e != cudaSuccess) return e;
+    p.part = static_cast<float *>(ws);
+    p.status = v.status, p.abort_flag = v.abort_flag, p.wait_ns = v.wait_ns;
+
     constexpr int smem = kStages * kStageBytes + kBoxes + kEpiWarps * kBiasB + (2 * kStages + 4) * 8 + 16;
-    auto kern = gemm_tc<T, MODE>;
+    auto kern = gemm_tc<T, MODE, NP>;
     static std::atomic<uint64_t> ready{0}; // devices whose limit has been raised
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
     }
-    if (e == cudaSuccess) e = launch_pdl(kern, dim3(2 * pairs), dim3(kGemmThreads), smem, s, p);
-    if (e != cudaSuccess || !p.nsplit) return e;
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(2 * q.launched), dim3(kGemmThreads), smem, v.stream, p);
+    if (e != cudaSuccess || !p.s.nsplit) return e;
     constexpr int kCols = (MODE == EPI_GATED ? 128 : kTile) / 8;
-    return launch_pdl(gemm_fixup<T, MODE>, dim3(p.nsplit * kTile / (256 / kCols)), dim3(256), 0, s, p);
+    return launch_pdl(gemm_fixup<T, MODE, NP>, dim3(p.s.nsplit * kTile / (256 / kCols)), dim3(256), 0, v.stream, p);
 }
 
-template <typename T> cudaError_t run_mode(const Gemm &g, const TcParams &p, int pairs, cudaStream_t s)
+template <typename T> cudaError_t run_mode(const Gemm *g, int n, const CtxView &v, void *ws)
 {
-    return g.mode == EPI_LINEAR ? run<T, EPI_LINEAR>(p, pairs, s)
-           : g.mode == EPI_GATED ? run<T, EPI_GATED>(p, pairs, s)
-                                 : run<T, EPI_DACT>(p, pairs, s);
+    if (n > 1) return run<T, EPI_LINEAR, kMaxProbs>(g, n, v, ws);
+    return g->mode == EPI_LINEAR  ? run<T, EPI_LINEAR, 1>(g, 1, v, ws)
+           : g->mode == EPI_GATED ? run<T, EPI_GATED, 1>(g, 1, v, ws)
+                                  : run<T, EPI_DACT, 1>(g, 1, v, ws);
 }
 
 } // namespace
 
 size_t gemm_workspace(const Gemm &g, const CtxView &v)
 {
-    return skinny_takes(g) ? skinny_workspace(g, v) : plan_split(g, v.sms).bytes;
+    return skinny_takes(g) ? skinny_workspace(g, v) : plan_group(&g, 1, v.sms).bytes;
 }
 
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws)
 {
     if (skinny_takes(g)) return launch_skinny(g, bf16, v, ws);
-    const Split s = plan_split(g, v.sms);
-    TcParams p = {};
-    p.M = g.M, p.N = g.N, p.tm = s.tm, p.tn = s.tn, p.kt0 = s.kt0, p.KT = s.KT;
-    p.a_mn = g.a[0].mn, p.b_mn = g.b[0].mn;
-    p.nfull = s.nfull, p.nsplit = s.nsplit, p.parts = s.parts, p.smax = s.smax;
-    p.part = static_cast<float *>(ws);
-    p.status = v.status, p.abort_flag = v.abort_flag, p.wait_ns = v.wait_ns;
-    p.e = g.e;
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < g.segs && e == cudaSuccess; ++i) e = map_of(&p.ma[i], g.a[i], g.M, g.K[i]);
-    const int nb = g.mode == EPI_GATED ? 2 : g.segs;
-    for (int i = 0; i < nb && e == cudaSuccess; ++i)
-        e = map_of(&p.mb[i], g.b[i], g.N, g.K[g.mode == EPI_GATED ? 0 : i]);
-    if (e != cudaSuccess) return e;
-    const int pairs = std::min(v.sms / 2, std::max(std::min(p.nfull, v.sms / 2), p.parts));
-    return bf16 ? run_mode<__nv_bfloat16>(g, p, pairs, v.stream) : run_mode<__half>(g, p, pairs, v.stream);
+    return bf16 ? run_mode<__nv_bfloat16>(&g, 1, v, ws) : run_mode<__half>(&g, 1, v, ws);
+}
+
+size_t gemms_workspace(const Gemm *g, int n, const CtxView &v)
+{
+    return n == 1 ? gemm_workspace(*g, v) : plan_group(g, n, v.sms).bytes;
+}
+
+cudaError_t launch_gemms(const Gemm *g, int n, bool bf16, const CtxView &v, void *ws)
+{
+    if (n == 1) return launch_gemm(*g, bf16, v, ws);
+    return bf16 ? run_mode<__nv_bfloat16>(g, n, v, ws) : run_mode<__half>(g, n, v, ws);
 }
 
 } // namespace pi
