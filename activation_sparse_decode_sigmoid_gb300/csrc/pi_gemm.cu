@@ -232,6 +232,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// The same without the wait: tmem_wait32 before the values are used.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+                   "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                   "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+// (the registers are operands, so that no use of them moves in front of the wait)
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
 // After a failure: copies and MMAs in flight finish within microseconds; the
 // CTA stays for a bounded time that covers them.
 __device__ __forceinline__ void linger()
@@ -339,6 +364,44 @@ __device__ __forceinline__ void box_send(uint32_t box, const Strip &s, int lane,
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(box_at(box, r, lane >> 3) + (lane & 7) * 2) : "memory");
             *o = v;
         }
+    }
+    __syncwarp();
+}
+
+// A warp's 32 x 128 values, rounded and nothing else, all inside the output:
+// the next 32 columns are on their way out of tensor memory while these go
+// through their box.  `last` runs once the accumulator has been read.
+template <typename T, typename F>
+__device__ __forceinline__ void plain_strip(uint32_t ta, uint32_t box0, uint32_t box1, const Strip &s, int lane, int row, int col, F last)
+{
+    uint32_t r[2][32];
+    tmem_ld32_async(ta, r[0]);
+    tmem_wait32(r[0]);
+    const int rr = lane >> 2;
+    uint16_t *p = s.p + (int64_t)(row + rr) * s.ld + col + (lane & 3) * 8;
+    const int64_t ld8 = 8 * s.ld;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t(&v)[32] = r[c & 1];
+        if (c < 3) tmem_ld32_async(ta + 32 * (c + 1), r[(c + 1) & 1]);
+        else last();
+        const uint32_t box = c & 1 ? box1 : box0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * j + i]);
+            sts16(box_at(box, lane, j), pack8<T>(x));
+        }
+        __syncwarp();
+        const uint32_t at = box_at(box, rr, lane & 3);
+        uint4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = lds16(at + 512 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(p + 32 * c + i * ld8) = q[i];
+        // (the other box was read before the barrier above)
+        if (c < 3) tmem_wait32(r[(c + 1) & 1]);
     }
     __syncwarp();
 }
@@ -485,6 +548,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                                                : Strip{static_cast<uint16_t *>(const_cast<void *>(e.res)), e.ldr, (e.vec & V_RES) != 0};
             const Strip in2 = {const_cast<uint16_t *>(e.in2), e.ldi2, (e.vec & V_IN2) != 0};
             const bool biased = !kPlain && MODE != EPI_DACT && (e.bias || e.bias2);
+            const bool simple = MODE == EPI_LINEAR && !has_in && !out32 && out.vec &&
+                                (kPlain || (!biased && !e.out2 && e.fn == PI_FN_NONE && e.scale == 1.f));
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
             int mi, ni;
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
@@ -526,6 +591,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                             *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
+            } else if (simple && row0 + 32 <= M && col0 + kCols <= N) {
+                plain_strip<T>(ta + half * kCols, box0, box1, out, lane, row0, col0, [&]() {
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
+                });
+                released = true;
             } else if (row0 < M) {
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += 32) {
@@ -684,6 +756,7 @@ template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) g
 // ------------------------------------------------------------------ host
 // A last wave of `rem` tiles on n pairs takes KT steps; split along k, it takes
 // rem KT / n and the fixup launch with its traffic, worth about kFixupSteps steps.
+// One product of a group may be split: the longest that the others do not fill up.
 constexpr int kFixupSteps = 32;
 constexpr int kMinShare = 4; // k steps per pair, at least
 
@@ -708,8 +781,7 @@ Plan plan_group(const Gemm *g, int n, int sms)
     Sched &s = q.s;
     s.pairs = P;
     s.smax = 1;
-    // Pairs base .. base + high - 1 (mod P) are ahead of the others by `gap` steps.
-    int base = 0, high = 0, gap = 0, used = 0;
+    int64_t later = 0; // steps of the products that follow
     for (int j = 0; j < n; ++j) {
         const Gemm &x = g[q.order[j]];
         const int outn = x.mode == EPI_GATED ? 128 : kTile;
@@ -717,6 +789,12 @@ Plan plan_group(const Gemm *g, int n, int sms)
         q.tn[j] = (x.N + outn - 1) / outn;
         q.kt0[j] = (x.K[0] + kBK - 1) / kBK;
         q.KT[j] = KT[q.order[j]];
+        later += (int64_t)q.tm[j] * q.tn[j] * q.KT[j];
+    }
+    // Pairs base .. base + high - 1 (mod P) are ahead of the others by `gap` steps.
+    int base = 0, high = 0, gap = 0, used = 0;
+    for (int j = 0; j < n; ++j) {
+        later -= (int64_t)q.tm[j] * q.tn[j] * q.KT[j];
         int t0 = 0, m = q.tm[j] * q.tn[j];
         if (high && gap >= q.KT[j]) { // the pairs behind catch up first
             const int lo = P - high;
@@ -727,21 +805,24 @@ Plan plan_group(const Gemm *g, int n, int sms)
             gap -= (cnt + lo - 1) / lo * q.KT[j];
         }
         if (!m) continue;
-        const int rem = m % P, from = (base + high) % P;
-        if (j == n - 1 && rem && (int64_t)q.KT[j] * (P - rem) > (int64_t)kFixupSteps * P) {
+        int rem = m % P;
+        const int from = (base + high) % P;
+        // (what follows fills the pairs that the last wave leaves idle, as far as it goes)
+        if (!s.nsplit && rem && (int64_t)q.KT[j] * (P - rem) - later > (int64_t)kFixupSteps * P) {
             s.sprob = j, s.stile0 = t0 + m - rem, s.nsplit = rem;
             const int64_t units = (int64_t)rem * q.KT[j];
             s.parts = (int)std::min<int64_t>(P, std::max<int64_t>(1, units / kMinShare));
             s.smax = q.KT[j] / (int)(units / s.parts) + 2;
             q.bytes = (size_t)rem * s.smax * kTile * kTile * sizeof(float);
             m -= rem;
+            rem = 0;
             used = std::max(used, s.parts);
         }
         if (m) {
             s.deal[s.ndeal++] = {j, t0, m, from, P};
             used = from ? P : std::max(used, std::min(m, P));
         }
-        base = from, high = m % P, gap = q.KT[j];
+        base = from, high = rem, gap = q.KT[j];
     }
     q.launched = used;
     return q;

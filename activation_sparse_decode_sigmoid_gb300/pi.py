@@ -641,9 +641,12 @@ class Context:
                 plans.clear()
         return got
 
-    def _ws(self, n: int):
-        import torch
-        return torch.empty(n, dtype=torch.uint8, device=self.torch_device) if n else None
+    def _ws(self, like, n: int):
+        """Workspace of n bytes, as a tensor of `like`'s type, and its address."""
+        if not n:
+            return None, 0
+        t = like.new_empty(-(-n // like.element_size()))
+        return t, t.data_ptr()
 
     def _grad_buffers(self, given: dict, accumulate: bool, shapes: dict, dtype):
         """Checks gradient buffers: packed, one type; returns that type."""
@@ -681,9 +684,9 @@ class Context:
         py, ldy = self._at("y", y, (T, N), y.dtype)
         desc, n = self._plan(pi_linear_desc, (T, K, N, code, out, code, fn, scale, (px | pw) & 15 != 0, ldx, ldw, ldz, ldr,
                                               ldy, 0, 0), pi_linear_workspace, False)
-        ws = self._ws(n)
+        ws, pws = self._ws(x, n)
         self._s()
-        rc = _lib.pi_linear(self.handle, ctypes.addressof(desc), px, pw, pb, pr, pz, py, _ptr(ws), n)
+        rc = _lib.pi_linear(self.handle, ctypes.addressof(desc), px, pw, pb, pr, pz, py, pws, n)
         if rc:
             _check(self.handle, rc, "pi_linear")
         return y
@@ -714,24 +717,22 @@ class Context:
         desc, n = self._plan(pi_linear_desc, (T, K, N, code, self._code(dy.dtype), grad, fn, scale,
                                               (pdy | px | pw) & 15 != 0, ldx, ldw, ldz, 0, ldy, lddx, lddw),
                              pi_linear_workspace, True)
-        ws = self._ws(n)
+        ws, pws = self._ws(x, n)
         self._s()
         rc = _lib.pi_linear_bwd(self.handle, ctypes.addressof(desc), pdy, px, pw, pz, pdx, pdw, pdb,
-                                          int(accumulate), _ptr(ws), n)
+                                          int(accumulate), pws, n)
         if rc:
             _check(self.handle, rc, "pi_linear_bwd")
         return dx, dw, db
 
     def gated_ffn_save(self, x, w_gate, w_up):
         """Buffers (g, u, a) for ``gated_ffn`` to leave for its backward pass,
-        [T][n] with rows that start on 128-byte boundaries (g None if not gated)."""
+        [T][n] with rows that start on 16-byte boundaries (g None if not gated)."""
         T, n = x.shape[0], w_up.shape[0]
-        wide = (n + 63) // 64 * 64
-
-        def new():
-            t = x.new_empty((T, wide))
-            return t if wide == n else t[:, :n]
-
+        if n % 8 == 0:
+            return (x.new_empty((T, n)) if w_gate is not None else None), x.new_empty((T, n)), x.new_empty((T, n))
+        wide = (n + 7) // 8 * 8
+        new = lambda: x.new_empty((T, wide)).as_strided((T, n), (wide, 1))
         return (new() if w_gate is not None else None), new(), new()
 
     def gated_ffn(self, x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, *, fn=PI_FN_RELU, save=None,
@@ -760,10 +761,10 @@ class Context:
                                                   (px | pwg | pwu | pwd | pa) & 15 != 0, ldx, ldy, ldwg, ldwu, ldwd, ldg,
                                                   ldu, lda), pi_gated_ffn_workspace, False)
         wts, sv = pi_gated_ffn_weights(pwg, pwu, pwd, pbg, pbu, pbd), pi_gated_ffn_save(pg, pu, pa)
-        ws = self._ws(nb)
+        ws, pws = self._ws(x, nb)
         self._s()
         rc = _lib.pi_gated_ffn(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px,
-                                         ctypes.addressof(sv), py, _ptr(ws), nb)
+                                         ctypes.addressof(sv), py, pws, nb)
         if rc:
             _check(self.handle, rc, "pi_gated_ffn")
         return y
@@ -780,14 +781,16 @@ class Context:
         g, u, a = save
         T, d = self._dims("x", x)
         n, gated = self._dims("w_up", w_up)[0], w_gate is not None
-        shapes = {"w_gate": (n, d), "w_up": (n, d), "w_down": (d, n), "b_gate": (n,), "b_up": (n,), "b_down": (d,)}
         if grads is None:
             if accumulate:
                 raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
-            out = {k: x.new_empty(s) if (weight_grads if k[0] == "w" else bias_grads) and (gated or k[2:] != "gate")
-                   else None for k, s in shapes.items()}
+            new, w, b = x.new_empty, weight_grads, bias_grads
+            out = {"w_gate": new((n, d)) if w and gated else None, "w_up": new((n, d)) if w else None,
+                   "w_down": new((d, n)) if w else None, "b_gate": new(n) if b and gated else None,
+                   "b_up": new(n) if b else None, "b_down": new(d) if b else None}
             gdt = dt
         else:
+            shapes = {"w_gate": (n, d), "w_up": (n, d), "w_down": (d, n), "b_gate": (n,), "b_up": (n,), "b_down": (d,)}
             out = {k: grads.get(k) for k in shapes}
             gdt = self._grad_buffers(out, accumulate, shapes, dt)
         pdy, ldy = self._at("dy", dy, (T, d), dt)
@@ -806,11 +809,11 @@ class Context:
                                                   ldg, ldu, lda), pi_gated_ffn_workspace, True)
         wts, sv = pi_gated_ffn_weights(pwg, pwu, pwd, 0, 0, 0), pi_gated_ffn_save(pg, pu, pa)
         gr = pi_gated_ffn_grads(*(_ptr(v) for v in out.values()))
-        ws = self._ws(nb)
+        ws, pws = self._ws(x, nb)
         self._s()
         rc = _lib.pi_gated_ffn_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px, pdy,
                                              ctypes.addressof(sv), _ptr(dx), ctypes.addressof(gr), int(accumulate),
-                                             _ptr(ws), nb)
+                                             pws, nb)
         if rc:
             _check(self.handle, rc, "pi_gated_ffn_bwd")
         return {"dx": dx, **out}
@@ -892,10 +895,10 @@ class Context:
                                                      branch_scale, eps, 0, ldxo, ldy, ldh, ldg),
                              pi_norm_residual_bwd_workspace)
         gr = pi_norm_residual_grads(dx.data_ptr(), _ptr(dy), *(_ptr(v) for v in out.values()))
-        ws = self._ws(n)
+        ws, pws = self._ws(x_out, n)
         self._s()
         rc = _lib.pi_norm_residual_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(par), pdxo, pdh, px,
-                                                 py, pg, ctypes.addressof(gr), int(accumulate), _ptr(ws), n)
+                                                 py, pg, ctypes.addressof(gr), int(accumulate), pws, n)
         if rc:
             _check(self.handle, rc, "pi_norm_residual_bwd")
         return {"dx": dx, "dy": dy, **out}
