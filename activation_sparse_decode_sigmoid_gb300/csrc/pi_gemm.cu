@@ -458,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
             const int m0 = mi * kTile + (int)rank * 128;
             const int n0 = ni * kOutN + (MODE == EPI_GATED ? 0 : (int)rank * 128);
-            for (int seg = 0; seg < 2; ++seg) {
+            for (int seg = 0; seg < 2 && ok; ++seg) {
                 const int lo = seg ? pr.kt0 : 0, ka = max(w.k0, lo), kb = min(w.k1, seg ? pr.KT : pr.kt0);
                 const CUtensorMap *ma = &pr.ma[seg], *mb = &pr.mb[MODE == EPI_GATED ? (int)rank : seg];
                 for (int k = ka; k < kb; ++k) {

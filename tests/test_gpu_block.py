@@ -93,6 +93,45 @@ def test_linear_adds_into_an_fp32_stream(c, T, K, N):
     assert r.equal(y)
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 72, 40), (3, 264, 130), (40, 72, 130), (128, 264, 515), (300, 136, 264)])
+def test_linear_adds_into_its_residual(c, T, K, N):
+    m = Maker(6)
+    x, w, r = m(T, K), m(N, K, std=K ** -0.5), m(T, N)
+    want = c.linear(x, w, residual=r, fn=pi.PI_FN_SILU)
+    c.linear(x, w, residual=r, fn=pi.PI_FN_SILU, y=r)
+    assert r.equal(want)
+
+
+# more tiles than CTA pairs: one round and a bit, several rounds, and a split
+# last wave behind whole ones; odd edges
+@pytest.mark.parametrize("T,K,N", [(2600, 136, 2056), (5200, 72, 2049), (2600, 4096, 2056)])
+def test_linear_of_many_tiles(c, T, K, N):
+    m = Maker(7)
+    x, w, b, r = m(T, K, dt=BF16), m(N, K, dt=BF16, std=K ** -0.5), m(N, dt=BF16), m(T, N, dt=BF16)
+    z = torch.empty(T, N, dtype=BF16, device="cuda")
+    want = R.linear(x, w, b, "gelu_tanh", 1.0, r, BF16)
+    y = c.linear(x, w, b, fn=pi.PI_FN_GELU_TANH, residual=r, z=z)
+    R.check(y, want["y"], "y")
+    R.check(z, want["z"], "z")
+    R.check(c.linear(x, w), R.linear(x, w, None, "none", 1.0, None, BF16)["y"], "plain")
+
+
+# backward passes whose products fill up each other's waves, or are split
+@pytest.mark.parametrize("T,K,N", [(2304, 1544, 4104), (300, 4104, 2056), (4100, 520, 2056), (200, 264, 9000)])
+def test_linear_bwd_of_many_tiles(c, T, K, N):
+    m = Maker(8)
+    x, w, z, dy = m(T, K), m(N, K, std=K ** -0.5), m(T, N), m(T, N)
+    want = R.linear_bwd(dy, x, w, z, "silu", 1.0, F16)
+    got = c.linear_bwd(dy, x, w, z, fn=pi.PI_FN_SILU)
+    for k, v in zip(("dx", "dw", "db"), got):
+        R.check(v, want[k], k)
+    for need in ((True, False, False), (False, True, False)):  # alone, each is cut differently
+        part = c.linear_bwd(dy, x, w, z, fn=pi.PI_FN_SILU, need=need)
+        for k, v in zip(("dx", "dw", "db"), part):
+            if v is not None:
+                R.check(v, want[k], k + " alone")
+
+
 @pytest.mark.parametrize("fn", R.FNS)
 def test_linear_activations_at_their_ends(c, fn):
     """Pre-activations from 0 over the type's range, infinities and NaN:
@@ -241,6 +280,36 @@ def test_gated_ffn_and_backward(c, T, d, n, gated, dt):
         R.check(gr[k], (val + 2, e + 2.0 ** -22 * (2 + val.abs())), k)
 
 
+def test_gated_ffn_of_many_tiles(c):
+    m = Maker(19)
+    T, d, n = 700, 776, 3080
+    wts = ffn_weights(m, d, n, BF16, True, True)
+    x, dy = m(T, d, dt=BF16), m(T, d, dt=BF16)
+    save = c.gated_ffn_save(x, wts[0], wts[1])
+    want = R.ffn(x, *wts, "none")
+    R.check(c.gated_ffn(x, *wts, fn=pi.PI_FN_NONE, save=save), want["y"], "y")
+    want = R.ffn_bwd(dy, x, *wts[:3], *save, "none", BF16)
+    got = c.gated_ffn_bwd(dy, x, *wts[:3], save, fn=pi.PI_FN_NONE)
+    for k in want:
+        R.check(got[k], want[k], k)
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_gradients_accumulate_in_16_bits(c, T):
+    m = Maker(20)
+    d, n = 136, 264
+    wts = ffn_weights(m, d, n, F16, True, True)
+    x, dy = m(T, d), m(T, d)
+    save = c.gated_ffn_save(x, wts[0], wts[1])
+    c.gated_ffn(x, *wts, fn=pi.PI_FN_GELU, save=save)
+    want = R.ffn_bwd(dy, x, *wts[:3], *save, "gelu", F32)
+    gr = {k: torch.full_like(want[k][0], 2.0, dtype=F16) for k in want if k != "dx"}
+    c.gated_ffn_bwd(dy, x, *wts[:3], save, fn=pi.PI_FN_GELU, grads=gr, accumulate=True)
+    for k in gr:
+        val, e = want[k][0] + 2, want[k][1]
+        R.check(gr[k], (val, e + 2.0 ** -22 * (2 + val.abs()) + R.rnd(val, F16)), k)
+
+
 def test_gated_ffn_partial_gradients(c):
     m = Maker(9)
     wts = ffn_weights(m, 72, 130, BF16, True, False)
@@ -259,7 +328,12 @@ def test_gated_ffn_partial_gradients(c):
 
 # ------------------------------------------------------------------ norms
 NORM = [(1, 8, 0), (1, 8192, 0), (1, 16384, 1), (3, 1, 2), (5, 33, 1), (64, 1000, 0), (65, 256, 7), (130, 1001, 64),
-        (200, 2048, 70), (33, 8200, 5)]
+        (200, 2048, 70), (33, 8200, 5), (5, 64, 100)]
+# rows that follow one another through the rings of the pipelined kernels: many
+# per CTA, gate rows that end inside a CTA's tokens and that span several CTAs,
+# more gate rows than lanes that join them
+NORM_LONG = [(310, 8192, 0), (400, 4104, 100), (620, 1000, 7), (1000, 2048, 70), (700, 8192, 1), (2000, 72, 3),
+             (5000, 8, 0), (1400, 4096, 701)]
 
 
 @pytest.mark.parametrize("T,d,rows", NORM)
@@ -267,6 +341,17 @@ NORM = [(1, 8, 0), (1, 8192, 0), (1, 16384, 1), (3, 1, 2), (5, 33, 1), (64, 1000
                                       ("layer", "none"), ("none", "none")])
 @pytest.mark.parametrize("xdt,dt", [(F32, BF16), (F16, F16), (F32, F16)])
 def test_norm_residual_and_backward(c, T, d, rows, pre, post, xdt, dt):
+    norm_case(c, T, d, rows, pre, post, xdt, dt)
+
+
+@pytest.mark.parametrize("T,d,rows", NORM_LONG)
+@pytest.mark.parametrize("pre,post,xdt,dt", [("rms", "rms", F32, BF16), ("layer", "layer", BF16, BF16), ("rms", "none", F16, F16),
+                                             ("layer", "none", F32, F16), ("none", "layer", F32, BF16)])
+def test_norm_of_many_rows(c, T, d, rows, pre, post, xdt, dt):
+    norm_case(c, T, d, rows, pre, post, xdt, dt)
+
+
+def norm_case(c, T, d, rows, pre, post, xdt, dt):
     m = Maker(T + d)
     eps = 1e-3  # (a row of one element has no variance)
     x, y = m(T, d, dt=xdt, std=2.0), m(T, d, dt=dt)
@@ -510,6 +595,29 @@ def test_captured_and_replayed_beside_eager_calls(c):
     for want, got in zip(eager + [eager[0]], outs + [other]):
         for a, b in zip(want, got):
             assert a.equal(b)
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_a_wait_that_runs_out_is_reported(T):
+    """With a wait limit of a nanosecond the products' waits run out: the
+    kernels return, the status says so, and the context goes on working."""
+    ctx = G.ctx()
+    try:
+        m = Maker(21)
+        x, w = m(T, 2048), m(512, 2048, std=0.02)
+        want = ctx.linear(x, w)
+        ctx.check()
+        pi.pi_debug_set_wait_limit(ctx.handle, 1)
+        status = 0
+        for _ in range(5):  # (a wait may be over before the clock is read)
+            ctx.linear(x, w)
+            status = ctx.sync_status() or status  # (which also clears it)
+        assert status == pi.PI_ERR_TIMEOUT
+        pi.pi_debug_set_wait_limit(ctx.handle, 2_000_000_000)
+        assert ctx.linear(x, w).equal(want)
+        ctx.check()
+    finally:
+        ctx.close()
 
 
 def test_same_block_as_the_loaded_layer(c):
