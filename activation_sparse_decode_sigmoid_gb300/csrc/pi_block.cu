@@ -25,22 +25,22 @@ constexpr int kMaxT = 1 << 22, kMaxDim = 1 << 20;
 // reads one aligned word of the row, takes the next one's low half from its
 // neighbour where the row starts in the middle of a word, and writes one word
 // of the (aligned) copy.  Only words that lie inside the row are read whole.
-// 8 rows of 256 words a CTA.
+// 16 rows of 8 x 31 words a CTA.
+constexpr int kPackRows = 16;
+
 __global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t lds, uint32_t *dst, int64_t ldd, int rows, int cols)
 {
     pdl_enter();
     const int nw = (cols + 1) / 2, ncb = (nw + 247) / 248; // (31 words a warp: lane 31 only lends its word)
     const int lane = threadIdx.x & 31, w = (int)(blockIdx.x % ncb) * 248 + (threadIdx.x >> 5) * 31 + lane;
-    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * 8;
-    uint32_t q[8];
-    bool odd[8];
+    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * kPackRows;
+    uint32_t q[kPackRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        q[i] = 0, odd[i] = false;
+    for (int i = 0; i < kPackRows; ++i) {
+        q[i] = 0;
         if (r0 + i >= rows) continue;
         const uint16_t *row = src + (r0 + i) * lds;
-        odd[i] = ((uintptr_t)row & 2) != 0;
-        const int c = 2 * w - odd[i]; // the word's first column
+        const int c = 2 * w - (((uintptr_t)row & 2) ? 1 : 0); // the word's first column
         if (c >= 0 && c + 1 < cols) q[i] = *reinterpret_cast<const uint32_t *>(row + c);
         else {
             if (c >= 0 && c < cols) q[i] = row[c];
@@ -48,11 +48,36 @@ __global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t ld
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kPackRows; ++i) {
         const uint32_t next = __shfl_down_sync(0xffffffffu, q[i], 1);
-        const uint32_t v = odd[i] ? (q[i] >> 16) | (next << 16) : q[i];
-        if (lane < 31 && w < nw && r0 + i < rows) dst[(r0 + i) * (ldd / 2) + w] = v;
+        const bool odd = ((uintptr_t)(src + (r0 + i) * lds) & 2) != 0;
+        if (lane < 31 && w < nw && r0 + i < rows) dst[(r0 + i) * (ldd / 2) + w] = odd ? (q[i] >> 16) | (next << 16) : q[i];
     }
+}
+
+// The same for rows that are 8-byte aligned (strides of 4 elements): 8 bytes a thread.
+__global__ void __launch_bounds__(256) pack_rows8(const uint16_t *src, int64_t lds, uint2 *dst, int64_t ldd, int rows, int cols)
+{
+    pdl_enter();
+    const int nq = cols / 4, ncb = (nq + 256) / 256; // (the last, partial 8 bytes included)
+    const int w = (int)(blockIdx.x % ncb) * 256 + threadIdx.x;
+    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * kPackRows;
+    if (w > nq) return;
+    uint2 q[kPackRows];
+#pragma unroll
+    for (int i = 0; i < kPackRows; ++i) {
+        if (r0 + i >= rows) continue;
+        const uint16_t *row = src + (r0 + i) * lds;
+        if (w < nq) q[i] = *reinterpret_cast<const uint2 *>(row + 4 * w);
+        else {
+            uint32_t v[2] = {};
+            for (int j = 0; j < (cols & 3); ++j) v[j >> 1] |= (uint32_t)row[4 * w + j] << (16 * (j & 1));
+            q[i] = make_uint2(v[0], v[1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPackRows; ++i)
+        if (r0 + i < rows && (w < nq || (cols & 3))) dst[(r0 + i) * (ldd / 4) + w] = q[i];
 }
 
 // Column sums in two launches: a CTA sums some rows of 256 columns (8 per
@@ -544,10 +569,13 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
 
 cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
 {
-    const int64_t blocks = (int64_t)((rows + 7) / 8) * (((cols + 1) / 2 + 247) / 248);
-    if (!blocks) return cudaSuccess;
-    return launch_pdl(pack_rows, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t *)src, lds, (uint32_t *)dst, ldd, rows,
-                      cols);
+    const int64_t groups = (rows + kPackRows - 1) / kPackRows;
+    if (!rows || !cols) return cudaSuccess;
+    if (((uintptr_t)src & 7) == 0 && lds % 4 == 0)
+        return launch_pdl(pack_rows8, dim3((unsigned)(groups * ((cols / 4 + 256) / 256))), dim3(256), 0, s, (const uint16_t *)src, lds,
+                          (uint2 *)dst, ldd, rows, cols);
+    return launch_pdl(pack_rows, dim3((unsigned)(groups * (((cols + 1) / 2 + 247) / 248))), dim3(256), 0, s, (const uint16_t *)src, lds,
+                      (uint32_t *)dst, ldd, rows, cols);
 }
 
 size_t colsum_bytes(int T, int N)

@@ -86,7 +86,8 @@ struct Sched {
     Deal deal[2 * kMaxProbs];
     int ndeal, pairs;     // pairs that tiles are dealt to
     int sprob, stile0;    // the product whose last tiles are split along k, the first of them
-    int nsplit, parts;    // how many, and pairs that share them
+    int nsplit, parts;    // how many, and pairs that share them (each lane's)
+    int lanes;            // tile rows that are cut apart and alike, so that their pairs read the same of B at a time
     int smax;             // partial tiles kept per split tile
 };
 
@@ -128,10 +129,10 @@ template <int NP> struct Walk {
     __device__ __forceinline__ Walk(const TcParams<NP> &q, int c_) : p(q), c(c_), d(0), u(0), u1(0)
     {
         i = first(0);
-        if (c < p.s.parts) {
-            const int64_t units = (int64_t)p.s.nsplit * p.prob[NP == 1 ? 0 : p.s.sprob].KT;
-            u = range_at(units, c, p.s.parts);
-            u1 = range_at(units, c + 1, p.s.parts);
+        if (c < p.s.parts * p.s.lanes) {
+            const int64_t units = (int64_t)(p.s.nsplit / p.s.lanes) * p.prob[NP == 1 ? 0 : p.s.sprob].KT;
+            u = range_at(units, c / p.s.lanes, p.s.parts);
+            u1 = range_at(units, c / p.s.lanes + 1, p.s.parts);
         }
     }
     // this pair's first index in deal d
@@ -155,10 +156,10 @@ template <int NP> struct Walk {
         }
         if (u >= u1) return false;
         const int KT = p.prob[NP == 1 ? 0 : p.s.sprob].KT;
-        const int r = u / KT, k0 = u - r * KT;
-        const int k1 = min(KT, k0 + u1 - u);
-        const int lead = part_of((int64_t)p.s.nsplit * KT, (int64_t)r * KT, p.s.parts);
-        w = {p.s.sprob, p.s.stile0 + r, k0, k1, r * p.s.smax + (c - lead)};
+        const int q = u / KT, k0 = u - q * KT, lane = c % p.s.lanes;
+        const int k1 = min(KT, k0 + u1 - u), r = q * p.s.lanes + lane;
+        const int lead = part_of((int64_t)(p.s.nsplit / p.s.lanes) * KT, (int64_t)q * KT, p.s.parts);
+        w = {p.s.sprob, p.s.stile0 + r, k0, k1, r * p.s.smax + (c / p.s.lanes - lead)};
         u += k1 - k0;
         return true;
     }
@@ -735,8 +736,8 @@ template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) g
     tile_at(p.s.stile0 + r, pr.tm, pr.tn, mi, ni);
     const int grow = mi * kTile + row, gcol = ni * kOutN + c;
     if (grow >= pr.M || gcol >= pr.N) return;
-    const int64_t units = (int64_t)p.s.nsplit * pr.KT;
-    const int cnt = part_of(units, (int64_t)(r + 1) * pr.KT - 1, p.s.parts) - part_of(units, (int64_t)r * pr.KT, p.s.parts) + 1;
+    const int64_t units = (int64_t)(p.s.nsplit / p.s.lanes) * pr.KT, u0 = (int64_t)(r / p.s.lanes) * pr.KT;
+    const int cnt = part_of(units, u0 + pr.KT - 1, p.s.parts) - part_of(units, u0, p.s.parts) + 1;
     float v[8] = {}, u[8] = {};
     const float *src = p.part + ((size_t)r * p.s.smax * kTile + row) * kTile + c;
     for (int s = 0; s < cnt; ++s, src += kTile * kTile) {
@@ -759,6 +760,7 @@ template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) g
 // One product of a group may be split: the longest that the others do not fill up.
 constexpr int kFixupSteps = 32;
 constexpr int kMinShare = 4; // k steps per pair, at least
+constexpr int kTileSteps = 8; // a tile's epilogue takes as long as about this many steps, which it hides behind
 
 struct Plan {
     Sched s;
@@ -780,8 +782,9 @@ Plan plan_group(const Gemm *g, int n, int sms)
     std::stable_sort(q.order, q.order + n, [&](int a, int b) { return KT[a] > KT[b]; });
     Sched &s = q.s;
     s.pairs = P;
-    s.smax = 1;
+    s.smax = 1, s.lanes = 1;
     int64_t later = 0; // steps of the products that follow
+    int cost[kMaxProbs];
     for (int j = 0; j < n; ++j) {
         const Gemm &x = g[q.order[j]];
         const int outn = x.mode == EPI_GATED ? 128 : kTile;
@@ -789,20 +792,21 @@ Plan plan_group(const Gemm *g, int n, int sms)
         q.tn[j] = (x.N + outn - 1) / outn;
         q.kt0[j] = (x.K[0] + kBK - 1) / kBK;
         q.KT[j] = KT[q.order[j]];
-        later += (int64_t)q.tm[j] * q.tn[j] * q.KT[j];
+        cost[j] = std::max(q.KT[j], kTileSteps);
+        later += (int64_t)q.tm[j] * q.tn[j] * cost[j];
     }
     // Pairs base .. base + high - 1 (mod P) are ahead of the others by `gap` steps.
     int base = 0, high = 0, gap = 0, used = 0;
     for (int j = 0; j < n; ++j) {
-        later -= (int64_t)q.tm[j] * q.tn[j] * q.KT[j];
+        later -= (int64_t)q.tm[j] * q.tn[j] * cost[j];
         int t0 = 0, m = q.tm[j] * q.tn[j];
-        if (high && gap >= q.KT[j]) { // the pairs behind catch up first
+        if (high && gap >= cost[j]) { // the pairs behind catch up first
             const int lo = P - high;
-            const int cnt = (int)std::min<int64_t>(m, (int64_t)(gap / q.KT[j]) * lo);
+            const int cnt = (int)std::min<int64_t>(m, (int64_t)(gap / cost[j]) * lo);
             s.deal[s.ndeal++] = {j, t0, cnt, (base + high) % P, lo};
             used = P;
             t0 += cnt, m -= cnt;
-            gap -= (cnt + lo - 1) / lo * q.KT[j];
+            gap -= (cnt + lo - 1) / lo * cost[j];
         }
         if (!m) continue;
         int rem = m % P;
@@ -810,19 +814,22 @@ Plan plan_group(const Gemm *g, int n, int sms)
         // (what follows fills the pairs that the last wave leaves idle, as far as it goes)
         if (!s.nsplit && rem && (int64_t)q.KT[j] * (P - rem) - later > (int64_t)kFixupSteps * P) {
             s.sprob = j, s.stile0 = t0 + m - rem, s.nsplit = rem;
-            const int64_t units = (int64_t)rem * q.KT[j];
-            s.parts = (int)std::min<int64_t>(P, std::max<int64_t>(1, units / kMinShare));
+            // a product of up to 8 tile rows that is split as a whole: rows apart
+            // (512 x 8192 x 28672: cut end to end, its two rows read B twice, 194 us)
+            s.lanes = m == rem && m == q.tm[j] * q.tn[j] && q.tm[j] <= 8 ? q.tm[j] : 1;
+            const int64_t units = (int64_t)(rem / s.lanes) * q.KT[j];
+            s.parts = (int)std::min<int64_t>(P / s.lanes, std::max<int64_t>(1, units / kMinShare));
             s.smax = q.KT[j] / (int)(units / s.parts) + 2;
             q.bytes = (size_t)rem * s.smax * kTile * kTile * sizeof(float);
             m -= rem;
             rem = 0;
-            used = std::max(used, s.parts);
+            used = std::max(used, s.parts * s.lanes);
         }
         if (m) {
             s.deal[s.ndeal++] = {j, t0, m, from, P};
             used = from ? P : std::max(used, std::min(m, P));
         }
-        base = from, high = rem, gap = q.KT[j];
+        base = from, high = rem, gap = cost[j];
     }
     q.launched = used;
     return q;
