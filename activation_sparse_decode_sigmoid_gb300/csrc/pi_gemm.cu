@@ -46,6 +46,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <numeric>
 
 #include "pi_block.h"
 #include "pi_epi.cuh"
@@ -88,7 +89,7 @@ struct Sched {
     int ndeal, pairs;     // pairs that tiles are dealt to
     int sprob, stile0;    // the product whose last tiles are split along k, the first of them
     int nsplit, parts;    // how many, and pairs that share them (each lane's)
-    int lanes;            // tile rows that are cut apart and alike, so that their pairs read the same of B at a time
+    int lanes;            // split tiles in a row that are cut alike, each by pairs of its own
     int smax;             // partial tiles kept per split tile
 };
 
@@ -826,9 +827,13 @@ Plan plan_group(const Gemm *g, int n, int sms)
         // (what follows fills the pairs that the last wave leaves idle, as far as it goes)
         if (!s.nsplit && rem && (int64_t)q.KT[j] * (P - rem) - later > (int64_t)kFixupSteps * P) {
             s.sprob = j, s.stile0 = t0 + m - rem, s.nsplit = rem;
-            // a product of up to 8 tile rows that is split as a whole: rows apart
-            // (512 x 8192 x 28672: cut end to end, its two rows read B twice, 194 us)
-            s.lanes = m == rem && m == q.tm[j] * q.tn[j] && q.tm[j] <= 8 ? q.tm[j] : 1;
+            // the split tiles of a column (they lie together, see tile_at) are
+            // cut alike, where they come in whole groups: pairs that work on
+            // one column then read the same of B at a time.  (512 x 8192 x
+            // 28672: cut end to end, its two rows read B twice, 194 us instead of 149)
+            const int rows = q.tm[j] <= 8 ? q.tm[j] : q.tm[j] % 8 ? 1 : 8;
+            s.lanes = std::gcd(std::gcd(rows, s.stile0), rem);
+            while (s.lanes % 2 == 0 && P % s.lanes) s.lanes /= 2; // (no pair left over)
             const int64_t units = (int64_t)(rem / s.lanes) * q.KT[j];
             s.parts = (int)std::min<int64_t>(P / s.lanes, std::max<int64_t>(1, units / kMinShare));
             s.smax = q.KT[j] / (int)(units / s.parts) + 2;
