@@ -641,11 +641,16 @@ class Context:
                 plans.clear()
         return got
 
-    def _ws(self, like, n: int):
-        """Workspace of n bytes, as a tensor of `like`'s type, and its address."""
+    def _new(self, shape, dtype):
+        import torch
+        return torch.empty(shape, dtype=dtype, device=self.torch_device)
+
+    def _ws(self, n: int):
+        """Workspace of n bytes and its address."""
         if not n:
             return None, 0
-        t = like.new_empty(-(-n // like.element_size()))
+        import torch
+        t = torch.empty(n, dtype=torch.uint8, device=self.torch_device)
         return t, t.data_ptr()
 
     def _grad_buffers(self, given: dict, accumulate: bool, shapes: dict, dtype):
@@ -674,7 +679,7 @@ class Context:
         T, K = self._dims("x", x)
         N = self._dims("w", w)[0]
         if y is None:
-            y = x.new_empty((T, N), dtype=dt if residual is None else residual.dtype)
+            y = self._new((T, N), dt if residual is None else residual.dtype)
         out = self._code(y.dtype)
         px, ldx = self._at("x", x, (T, K), dt)
         pw, ldw = self._at("w", w, (N, K), dt)
@@ -684,7 +689,7 @@ class Context:
         py, ldy = self._at("y", y, (T, N), y.dtype)
         desc, n = self._plan(pi_linear_desc, (T, K, N, code, out, code, fn, scale, (px | pw) & 15 != 0, ldx, ldw, ldz, ldr,
                                               ldy, 0, 0), pi_linear_workspace, False)
-        ws, pws = self._ws(x, n)
+        ws, pws = self._ws(n)
         self._s()
         rc = _lib.pi_linear(self.handle, ctypes.addressof(desc), px, pw, pb, pr, pz, py, pws, n)
         if rc:
@@ -704,9 +709,9 @@ class Context:
             raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
         gdt = dt if not (need[1] or need[2]) else next((t.dtype for t in (dw, db) if t is not None), dt)
         grad = self._code(gdt)
-        dx = (x.new_empty((T, K)) if dx is None else dx) if need[0] else None
-        dw = (x.new_empty((N, K), dtype=gdt) if dw is None else dw) if need[1] else None
-        db = (x.new_empty(N, dtype=gdt) if db is None else db) if need[2] else None
+        dx = (self._new((T, K), dt) if dx is None else dx) if need[0] else None
+        dw = (self._new((N, K), gdt) if dw is None else dw) if need[1] else None
+        db = (self._new((N,), gdt) if db is None else db) if need[2] else None
         pdy, ldy = self._at("dy", dy, (T, N), dy.dtype)
         px, ldx = self._at("x", x, (T, K), dt)
         pw, ldw = self._at("w", w, (N, K), dt)
@@ -717,7 +722,7 @@ class Context:
         desc, n = self._plan(pi_linear_desc, (T, K, N, code, self._code(dy.dtype), grad, fn, scale,
                                               (pdy | px | pw) & 15 != 0, ldx, ldw, ldz, 0, ldy, lddx, lddw),
                              pi_linear_workspace, True)
-        ws, pws = self._ws(x, n)
+        ws, pws = self._ws(n)
         self._s()
         rc = _lib.pi_linear_bwd(self.handle, ctypes.addressof(desc), pdy, px, pw, pz, pdx, pdw, pdb,
                                           int(accumulate), pws, n)
@@ -728,11 +733,9 @@ class Context:
     def gated_ffn_save(self, x, w_gate, w_up):
         """Buffers (g, u, a) for ``gated_ffn`` to leave for its backward pass,
         [T][n] with rows that start on 16-byte boundaries (g None if not gated)."""
+        import torch
         T, n = x.shape[0], w_up.shape[0]
-        if n % 8 == 0:
-            return (x.new_empty((T, n)) if w_gate is not None else None), x.new_empty((T, n)), x.new_empty((T, n))
-        wide = (n + 7) // 8 * 8
-        new = lambda: x.new_empty((T, wide)).as_strided((T, n), (wide, 1))
+        new = lambda: torch.empty_strided((T, n), ((n + 7) // 8 * 8, 1), dtype=x.dtype, device=x.device)
         return (new() if w_gate is not None else None), new(), new()
 
     def gated_ffn(self, x, w_gate, w_up, w_down, b_gate=None, b_up=None, b_down=None, *, fn=PI_FN_RELU, save=None,
@@ -745,7 +748,7 @@ class Context:
         T, d = self._dims("x", x)
         n = self._dims("w_up", w_up)[0]
         if y is None:
-            y = x.new_empty((T, d))
+            y = self._new((T, d), dt)
         g, u, a = save if save is not None else (None, None, None)
         px, ldx = self._at("x", x, (T, d), dt)
         pwg, ldwg = self._at("w_gate", w_gate, (n, d), dt)
@@ -761,7 +764,7 @@ class Context:
                                                   (px | pwg | pwu | pwd | pa) & 15 != 0, ldx, ldy, ldwg, ldwu, ldwd, ldg,
                                                   ldu, lda), pi_gated_ffn_workspace, False)
         wts, sv = pi_gated_ffn_weights(pwg, pwu, pwd, pbg, pbu, pbd), pi_gated_ffn_save(pg, pu, pa)
-        ws, pws = self._ws(x, nb)
+        ws, pws = self._ws(nb)
         self._s()
         rc = _lib.pi_gated_ffn(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px,
                                          ctypes.addressof(sv), py, pws, nb)
@@ -784,10 +787,10 @@ class Context:
         if grads is None:
             if accumulate:
                 raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
-            new, w, b = x.new_empty, weight_grads, bias_grads
-            out = {"w_gate": new((n, d)) if w and gated else None, "w_up": new((n, d)) if w else None,
-                   "w_down": new((d, n)) if w else None, "b_gate": new(n) if b and gated else None,
-                   "b_up": new(n) if b else None, "b_down": new(d) if b else None}
+            new, w, b = self._new, weight_grads, bias_grads
+            out = {"w_gate": new((n, d), dt) if w and gated else None, "w_up": new((n, d), dt) if w else None,
+                   "w_down": new((d, n), dt) if w else None, "b_gate": new((n,), dt) if b and gated else None,
+                   "b_up": new((n,), dt) if b else None, "b_down": new((d,), dt) if b else None}
             gdt = dt
         else:
             shapes = {"w_gate": (n, d), "w_up": (n, d), "w_down": (d, n), "b_gate": (n,), "b_up": (n,), "b_down": (d,)}
@@ -797,7 +800,7 @@ class Context:
         px, ldx = self._at("x", x, (T, d), dt)
         dx = None
         if need_dx:  # (x and dx share their stride)
-            dx = x.new_empty((T, d)) if ldx in (0, d) else x.new_empty((T, ldx))[:, :d]
+            dx = self._new((T, d), dt) if ldx in (0, d) else self._new((T, ldx), dt)[:, :d]
         pwg, ldwg = self._at("w_gate", w_gate, (n, d), dt)
         pwu, ldwu = self._at("w_up", w_up, (n, d), dt)
         pwd, ldwd = self._at("w_down", w_down, (d, n), dt)
@@ -809,7 +812,7 @@ class Context:
                                                   ldg, ldu, lda), pi_gated_ffn_workspace, True)
         wts, sv = pi_gated_ffn_weights(pwg, pwu, pwd, 0, 0, 0), pi_gated_ffn_save(pg, pu, pa)
         gr = pi_gated_ffn_grads(*(_ptr(v) for v in out.values()))
-        ws, pws = self._ws(x, nb)
+        ws, pws = self._ws(nb)
         self._s()
         rc = _lib.pi_gated_ffn_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), px, pdy,
                                              ctypes.addressof(sv), _ptr(dx), ctypes.addressof(gr), int(accumulate),
@@ -834,9 +837,9 @@ class Context:
         code = self._code16(dtype)
         T, d = self._dims("x", x)
         if x_out is None:
-            x_out = x.new_empty((T, d))
+            x_out = self._new((T, d), xdt)
         if h is None and pre != PI_NORM_NONE:
-            h = x.new_empty((T, d), dtype=dtype)
+            h = self._new((T, d), dtype)
         px, ldx = self._at("x", x, (T, d), dtype if xcode != PI_F32 else xdt)
         py, ldy = self._at("y", y, (T, d), dtype)
         pg, ldg = self._at("gate", gate, (1 if gate_rows == 0 else -(-T // max(gate_rows, 1)), d), dtype)
@@ -872,7 +875,7 @@ class Context:
         if grads is None:
             if accumulate:
                 raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
-            out = {k: None if v is None else v.new_empty(v.shape) for k, v in given.items()}
+            out = {k: None if v is None else self._new(v.shape, dtype) for k, v in given.items()}
             gdt = dtype
         else:
             out = {k: grads.get(k) for k in given}
@@ -888,14 +891,14 @@ class Context:
         pg, ldg = self._at("gate", gate, (rows, d), dtype)
         par = pi_norm_residual_params(self._at("w_pre", w_pre, (d,), dtype)[0], self._at("b_pre", b_pre, (d,), dtype)[0],
                                       self._at("w_post", w_post, (d,), dtype)[0], self._at("b_post", b_post, (d,), dtype)[0])
-        dx = x_out.new_empty((T, d))
+        dx = self._new((T, d), xdt)
         # (y and dy share their stride)
-        dy = None if y is None else y.new_empty((T, d)) if ldy in (0, d) else y.new_empty((T, ldy))[:, :d]
+        dy = None if y is None else self._new((T, d), dtype) if ldy in (0, d) else self._new((T, ldy), dtype)[:, :d]
         desc, n = self._plan(pi_norm_residual_desc, (T, d, xcode, code, self._code(gdt), pre, post, gate_rows, res_scale,
                                                      branch_scale, eps, 0, ldxo, ldy, ldh, ldg),
                              pi_norm_residual_bwd_workspace)
         gr = pi_norm_residual_grads(dx.data_ptr(), _ptr(dy), *(_ptr(v) for v in out.values()))
-        ws, pws = self._ws(x_out, n)
+        ws, pws = self._ws(n)
         self._s()
         rc = _lib.pi_norm_residual_bwd(self.handle, ctypes.addressof(desc), ctypes.addressof(par), pdxo, pdh, px,
                                                  py, pg, ctypes.addressof(gr), int(accumulate), pws, n)
