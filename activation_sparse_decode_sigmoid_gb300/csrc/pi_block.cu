@@ -25,18 +25,16 @@ constexpr int kMaxT = 1 << 22, kMaxDim = 1 << 20;
 // reads one aligned word of the row, takes the next one's low half from its
 // neighbour where the row starts in the middle of a word, and writes one word
 // of the (aligned) copy.  Only words that lie inside the row are read whole.
-// 16 rows of 8 x 31 words a CTA.
-constexpr int kPackRows = 16;
-
-__global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t lds, uint32_t *dst, int64_t ldd, int rows, int cols)
+// R rows of 8 x 31 words a CTA: 16 of a large matrix (loads in flight), 4 of a small one (CTAs).
+template <int R> __global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t lds, uint32_t *dst, int64_t ldd, int rows, int cols)
 {
     pdl_enter();
     const int nw = (cols + 1) / 2, ncb = (nw + 247) / 248; // (31 words a warp: lane 31 only lends its word)
     const int lane = threadIdx.x & 31, w = (int)(blockIdx.x % ncb) * 248 + (threadIdx.x >> 5) * 31 + lane;
-    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * kPackRows;
-    uint32_t q[kPackRows];
+    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * R;
+    uint32_t q[R];
 #pragma unroll
-    for (int i = 0; i < kPackRows; ++i) {
+    for (int i = 0; i < R; ++i) {
         q[i] = 0;
         if (r0 + i >= rows) continue;
         const uint16_t *row = src + (r0 + i) * lds;
@@ -48,7 +46,7 @@ __global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t ld
         }
     }
 #pragma unroll
-    for (int i = 0; i < kPackRows; ++i) {
+    for (int i = 0; i < R; ++i) {
         const uint32_t next = __shfl_down_sync(0xffffffffu, q[i], 1);
         const bool odd = ((uintptr_t)(src + (r0 + i) * lds) & 2) != 0;
         if (lane < 31 && w < nw && r0 + i < rows) dst[(r0 + i) * (ldd / 2) + w] = odd ? (q[i] >> 16) | (next << 16) : q[i];
@@ -56,16 +54,16 @@ __global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t ld
 }
 
 // The same for rows that are 8-byte aligned (strides of 4 elements): 8 bytes a thread.
-__global__ void __launch_bounds__(256) pack_rows8(const uint16_t *src, int64_t lds, uint2 *dst, int64_t ldd, int rows, int cols)
+template <int R> __global__ void __launch_bounds__(256) pack_rows8(const uint16_t *src, int64_t lds, uint2 *dst, int64_t ldd, int rows, int cols)
 {
     pdl_enter();
     const int nq = cols / 4, ncb = (nq + 256) / 256; // (the last, partial 8 bytes included)
     const int w = (int)(blockIdx.x % ncb) * 256 + threadIdx.x;
-    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * kPackRows;
+    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * R;
     if (w > nq) return;
-    uint2 q[kPackRows];
+    uint2 q[R];
 #pragma unroll
-    for (int i = 0; i < kPackRows; ++i) {
+    for (int i = 0; i < R; ++i) {
         if (r0 + i >= rows) continue;
         const uint16_t *row = src + (r0 + i) * lds;
         if (w < nq) q[i] = *reinterpret_cast<const uint2 *>(row + 4 * w);
@@ -76,7 +74,7 @@ __global__ void __launch_bounds__(256) pack_rows8(const uint16_t *src, int64_t l
         }
     }
 #pragma unroll
-    for (int i = 0; i < kPackRows; ++i)
+    for (int i = 0; i < R; ++i)
         if (r0 + i < rows && (w < nq || (cols & 3))) dst[(r0 + i) * (ldd / 4) + w] = q[i];
 }
 
@@ -567,15 +565,22 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
 
 } // namespace
 
+template <int R>
+static cudaError_t pack(const uint16_t *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
+{
+    const int64_t groups = (rows + R - 1) / R;
+    if (((uintptr_t)src & 7) == 0 && lds % 4 == 0)
+        return launch_pdl(pack_rows8<R>, dim3((unsigned)(groups * ((cols / 4 + 256) / 256))), dim3(256), 0, s, src, lds, (uint2 *)dst, ldd,
+                          rows, cols);
+    return launch_pdl(pack_rows<R>, dim3((unsigned)(groups * (((cols + 1) / 2 + 247) / 248))), dim3(256), 0, s, src, lds,
+                      (uint32_t *)dst, ldd, rows, cols);
+}
+
 cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
 {
-    const int64_t groups = (rows + kPackRows - 1) / kPackRows;
     if (!rows || !cols) return cudaSuccess;
-    if (((uintptr_t)src & 7) == 0 && lds % 4 == 0)
-        return launch_pdl(pack_rows8, dim3((unsigned)(groups * ((cols / 4 + 256) / 256))), dim3(256), 0, s, (const uint16_t *)src, lds,
-                          (uint2 *)dst, ldd, rows, cols);
-    return launch_pdl(pack_rows, dim3((unsigned)(groups * (((cols + 1) / 2 + 247) / 248))), dim3(256), 0, s, (const uint16_t *)src, lds,
-                      (uint32_t *)dst, ldd, rows, cols);
+    return (int64_t)rows * cols > (4 << 20) ? pack<16>((const uint16_t *)src, lds, dst, ldd, rows, cols, s)
+                                            : pack<4>((const uint16_t *)src, lds, dst, ldd, rows, cols, s);
 }
 
 size_t colsum_bytes(int T, int N)
