@@ -6,8 +6,9 @@ module raises on first use -- build it with
 
 Tensors are torch tensors on the context's device (PyTorch supplies device
 memory and streams only).  16-bit data may be passed as float16 / bfloat16 or
-as int16 / uint16 views of the bit patterns.  Every compute call is issued on
-torch's current CUDA stream.
+as int16 / uint16 views of the bit patterns; the block operators (linear,
+gated FFN, norms) take float16, bfloat16 and float32 tensors as they are.  Every
+compute call is issued on torch's current CUDA stream.
 """
 from __future__ import annotations
 
