@@ -30,12 +30,13 @@
 // MN-major forms, 128-byte swizzle), so the backward products read dz, W and
 // x as they lie.
 //
-// A thread of the epilogue holds one row of the accumulator; outputs, and the
-// inputs that the epilogue needs (the residual, or g and u), pass through
-// shared memory in boxes of 32 x 32 per warp, so that memory sees 64
-// consecutive bytes per row.  (Straight from the registers, 16 bytes in each
-// of 32 rows at a time, or by TMA stores of such boxes, a 256 x 256 tile took
-// 6.5 us or more; its products take 4.3 us at 1024 values of k.)
+// A thread of the epilogue holds one row of the accumulator.  Plain outputs
+// leave through shared memory by TMA stores of 32 x 64 boxes; the others, and
+// the inputs that the epilogue needs (the residual, or g and u), pass through
+// boxes of 32 x 32 per warp, so that memory sees 64 consecutive bytes per row.
+// (Straight from the registers, 16 bytes in each of 32 rows at a time, or by
+// TMA stores of 32 x 32 boxes, a 256 x 256 tile took 6.5 us or more; its
+// products take 4.3 us at 1024 values of k.)
 //
 // Every wait is bounded; after one that ran out a pair stops issuing, waits
 // for what it has in flight, frees its tensor memory and returns.

@@ -481,7 +481,7 @@ constexpr int kPipeThreads = 512, kPipeMaxD = 8192;
 struct PipeP {
     int slots, slotB;                     // ring
     int off_dxo, off_dh, off_y, off_gate; // regions of a slot (x at 0); off_gate -1: one gate row for many tokens
-    int off_hold;                         // after the ring: the current gate row
+    int off_hold, holdB;                  // after the ring: the current gate row
     uint32_t row_bytes;                   // bytes of a row's copies in all
     uint32_t tcols;                       // backward: tensor memory columns
     int clear;                            // some columns or rows of the ring are not copied: zeros
@@ -546,6 +546,29 @@ template <typename T, int V> __device__ __forceinline__ void hold_gate(const Nor
         if (c < p.d)
             *reinterpret_cast<uint4 *>(hold + 2 * c) = param8<T>(p.gate ? p.gate + (int64_t)group * p.ldgate : nullptr, c, p.d, 1.f);
     }
+}
+
+// The same for the backward pass, as fp32 factors bs gate w_post (zeros past
+// the row): a chunk's 8 values in two planes of 16 bytes per thread.
+template <typename T, int V> __device__ __forceinline__ void hold_factors(const NormP &p, uint8_t *hold, int group)
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        float g[8], w[8];
+        unpack8<T>(param8<T>(p.gate ? p.gate + (int64_t)group * p.ldgate : nullptr, c, p.d, 1.f), g);
+        unpack8<T>(param8<T>(p.w_post, c, p.d, 1.f), w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = c < p.d ? p.bs * g[j] * w[j] : 0.f;
+        float4 *o = reinterpret_cast<float4 *>(hold) + 2 * i * blockDim.x + threadIdx.x;
+        o[0] = make_float4(g[0], g[1], g[2], g[3]), o[blockDim.x] = make_float4(g[4], g[5], g[6], g[7]);
+    }
+}
+
+__device__ __forceinline__ void load8f2(const float *a, const float *b, float (&v)[8])
+{
+    const float4 p = *reinterpret_cast<const float4 *>(a), q = *reinterpret_cast<const float4 *>(b);
+    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
 }
 
 __device__ __forceinline__ float warp_add(float a)
@@ -618,7 +641,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     uint8_t *hold = ring + q.off_hold;
-    if (q.clear) clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
+    if (q.clear) clear_ring(ring, q.off_hold + q.holdB);
     __syncthreads();
     pdl_enter();
     int issued = r0;
@@ -737,6 +760,21 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const float (&v)[16])
                  "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
                  : "memory");
 }
+// The load of 16 columns starts; tm_have16 before its values are used (they
+// are operands there, so that no use moves in front of the wait).
+__device__ __forceinline__ void tm_ld16(uint32_t at, float (&v)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+                   "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tm_have16(float (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
 __device__ __forceinline__ void tm_settle() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // What a warp publishes of a row in the backward pass.
@@ -751,6 +789,9 @@ struct BwdStat {
 // tensor memory, where each thread adds to its own columns' values: in
 // registers they took half of what 512 threads have (8000 x 8192 layer norms:
 // 345 us with 512 threads and spills, 271 us with 256 threads of 32 columns).
+// Bound by instruction issue, so what one gate row's tokens share, bs gate
+// w_post, is multiplied once, and each element's value is kept in the form
+// that its next use wants (FIG).
 // RG: a gate row per token, in the ring.
 template <typename T, bool X32, int V, bool FULL, bool RG>
 __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
@@ -767,7 +808,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     uint8_t *hold = ring + q.off_hold;
-    if (q.clear) clear_ring(ring, q.off_hold + (int)blockDim.x * V * 16);
+    if (q.clear) clear_ring(ring, q.off_hold + q.holdB);
     const uint32_t tmem = tmem_alloc(&tslot, q.tcols);
     pdl_enter();
     int issued = r0;
@@ -819,19 +860,17 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
     };
     for (int t = r0; t < r1; ++t) {
         ok = mbar_wait_bounded(full + slot, par, q);
-        if (!__syncthreads_and(ok)) break; // also: every thread is done with the previous row's slot
-        if (tid == 0 && t > r0 && issued < r1) issue_row(p, q, ring, full, slot ? slot - 1 : S - 1, issued), ++issued;
-        const uint8_t *row = ring + slot * q.slotB, *gate = row_gate ? row + q.off_gate : hold;
+        const uint8_t *row = ring + slot * q.slotB;
         tm_settle(); // (the previous row's sums are in tensor memory)
         if (!row_gate && t / p.gate_rows != group) {
             if (group >= 0 && p.part) flush();
             group = t / p.gate_rows;
-            hold_gate<T, V>(p, hold, group);
+            hold_factors<T, V>(p, hold, group);
         }
         // statistics of x' and y, and the sums of dh w and dh w xh, about the warp's means
         BwdStat st = {};
         float wmx = 0.f, wmy = 0.f;
-        float x[V][8], y[V][8]; // x' and y, later normalised in place
+        float x[V][8], y[V][8]; // x' and y, then less the warp's means, then normalised
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             ring8x<T, X32>(row, c[i], x[i]);
@@ -854,17 +893,18 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             const float mx = on[i] ? wmx : 0.f, my = on[i] ? wmy : 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float e = FULL ? x[i][j] - mx : x[i][j], f = FULL ? y[i][j] - my : y[i][j], k = h[j] * w[j];
-                st.mx = fmaf(e, e, st.mx);
+                const float k = h[j] * w[j];
+                if (FULL) x[i][j] -= mx, y[i][j] -= my;
+                st.mx = fmaf(x[i][j], x[i][j], st.mx);
                 if (FULL) st.sq += k;
-                st.sqx = fmaf(k, e, st.sqx);
-                st.my = fmaf(f, f, st.my);
+                st.sqx = fmaf(k, x[i][j], st.sqx);
+                st.my = fmaf(y[i][j], y[i][j], st.my);
             }
         }
         st.mx = warp_add(st.mx), st.sqx = warp_add(st.sqx), st.my = warp_add(st.my);
         if (FULL) st.sq = warp_add(st.sq);
         if (lane == 0) red[flip][warp] = st;
-        __syncthreads();
+        if (!__syncthreads_and(ok)) break;
         float mx = 0.f, rx, c1 = 0.f, c2, my = 0.f, ry;
         {
             BwdStat z = {};
@@ -883,40 +923,51 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             ry = post ? 1.f / sqrtf(half_add(z.my) * inv_d + p.eps) : 1.f;
             c2 = half_add(z.sqx) * rx * inv_d;
         }
+        // (the warp's mean lies within sqrt(d / its elements) deviations of the row's: x rx + cx cancels little)
+        const float cx = (wmx - mx) * rx, cy = (wmy - my) * ry;
         // D, dx, the column sums, and the sums for y's gradient
-        float D[V][8];
+        float D[V][8]; // later D bs gate w_post, the gradient of y's normalised row
         float s1 = 0.f, s2 = 0.f;
         const float k0 = -rx * c1, kx = -rx * c2;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float v[8], h[8], w[8], a[16]; // a: P1, P0
-            tmem_ld16(sums + 32 * i, a);
+            tm_ld16(sums + 32 * i, a);
             ring8x<T, X32>(row + q.off_dxo, c[i], D[i]);
             ring8<T>(row + q.off_dh, c[i], h);
             unpack8<T>(wp[i], w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float xh = FULL ? (x[i][j] - mx) * rx : x[i][j] * rx;
+                const float xh = FULL ? fmaf(x[i][j], rx, cx) : x[i][j] * rx;
                 float e = fmaf(rx * h[j], w[j], D[i][j]);
                 if (FULL) e += k0;
                 D[i][j] = fmaf(kx, xh, e);
-                a[j] = fmaf(h[j], xh, a[j]);
-                if (FULL) a[8 + j] += h[j];
                 v[j] = p.rs * D[i][j];
+                x[i][j] = xh;
+            }
+            tm_have16(a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] = fmaf(h[j], x[i][j], a[j]);
+                if (FULL) a[8 + j] += h[j];
             }
             tm_st16(sums + 32 * i, a);
             if (p.dx && on[i]) storex8<T>(p.dx, X32, (int64_t)t * p.lddx + c[i], 8, true, v);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float w[8], g[8], a[16]; // a: S1, S0
-            tmem_ld16(sums + 32 * i + 16, a);
-            ring8<T>(gate, c[i], g);
-            unpack8<T>(wq[i], w);
+            float g[8], a[16]; // g: the gate, or bs gate w_post; a: S1, S0
+            tm_ld16(sums + 32 * i + 16, a);
+            if (row_gate) ring8<T>(row + q.off_gate, c[i], g);
+            else {
+                const float *o = reinterpret_cast<const float *>(hold) + (2 * i * blockDim.x + tid) * 4;
+                load8f2(o, o + 4 * blockDim.x, g);
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[i][j] = FULL ? (y[i][j] - my) * ry : y[i][j] * ry;
+            for (int j = 0; j < 8; ++j) y[i][j] = FULL ? fmaf(y[i][j], ry, cy) : y[i][j] * ry;
             if (row_gate && p.dgate && on[i]) {
-                float b[8], o[8];
+                float b[8], o[8], w[8];
+                unpack8<T>(wq[i], w);
                 unpack8<T>(param8<T>(p.b_post, c[i], d, 0.f), b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = p.bs * D[i][j] * fmaf(y[i][j], w[j], b[j]);
@@ -929,40 +980,44 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
                 }
                 storex8<T>(p.dgate, p.g32, at, 8, true, o);
             }
+            float w[8];
+            if (row_gate) unpack8<T>(wq[i], w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float k = row_gate ? g[j] * D[i][j] : D[i][j]; // (what S1 and S0 sum)
-                D[i][j] *= p.bs * g[j];                            // dv from here on
-                const float e = D[i][j] * w[j];
-                if (FULL) s1 += e;
-                s2 = fmaf(e, y[i][j], s2);
-                a[j] = fmaf(k, y[i][j], a[j]);
-                if (FULL) a[8 + j] += k;
+                D[i][j] = row_gate ? p.bs * k * w[j] : k * g[j];
+                if (FULL) s1 += D[i][j];
+                s2 = fmaf(D[i][j], y[i][j], s2);
+                g[j] = k;
+            }
+            tm_have16(a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] = fmaf(g[j], y[i][j], a[j]);
+                if (FULL) a[8 + j] += g[j];
             }
             tm_st16(sums + 32 * i + 16, a);
         }
+        if (post) {
+            s2 = warp_add(s2);
+            if (FULL) s1 = warp_add(s1);
+            if (lane == 0) red2[flip][warp] = make_float2(s1, s2);
+        }
+        __syncthreads(); // also: every thread is done with the row's slot
+        if (tid == 0 && issued < r1) issue_row(p, q, ring, full, slot, issued), ++issued;
         if (p.dy) {
             float k1 = 0.f, k2 = 0.f;
             if (post) {
-                s2 = warp_add(s2);
-                if (FULL) s1 = warp_add(s1);
-                if (lane == 0) red2[flip][warp] = make_float2(s1, s2);
-                __syncthreads();
                 float2 z = make_float2(0.f, 0.f);
                 if ((lane & 15) < nw) z = red2[flip][lane & 15];
                 if (lpost) k1 = half_add(z.x) * inv_d;
                 k2 = half_add(z.y) * inv_d;
             }
+            k1 *= -ry, k2 *= -ry;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float w[8];
-                unpack8<T>(wq[i], w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float e = D[i][j] * w[j];
-                    if (FULL) e -= k1;
-                    y[i][j] = ry * fmaf(-k2, y[i][j], e);
-                }
+                for (int j = 0; j < 8; ++j) y[i][j] = fmaf(k2, y[i][j], FULL ? fmaf(ry, D[i][j], k1) : ry * D[i][j]);
                 if (on[i]) store8<T>(p.dy + (int64_t)t * p.ldy + c[i], 8, true, y[i]);
             }
         }
@@ -1109,13 +1164,14 @@ bool plan_pipe(const NormP &p, bool backward, bool row_gate, const CtxView &c, P
     q.row_bytes = (uint32_t)p.d * ((p.x ? xe : 0) + (backward && p.dxo ? xe : 0) + (backward && p.dh ? 2 : 0) + (p.y ? 2 : 0) +
                                    (row_gate ? 2 : 0));
     q.clear = wide != p.d || !p.x || !p.y || (backward && (!p.dxo || !p.dh));
-    const int budget = c.smem_optin - 2048 - hB;
+    q.holdB = row_gate ? 0 : backward ? 2 * hB : hB; // (16 bits, or factors of 32)
+    const int budget = c.smem_optin - 2048 - q.holdB;
     int per_sm = std::min(8, kPipeThreads / o.threads);
-    while (per_sm > 1 && per_sm * (2 * q.slotB + hB + 4096) > budget) --per_sm;
-    q.slots = std::min(4, (budget / per_sm - (per_sm > 1 ? hB + 4096 : 0)) / q.slotB);
+    while (per_sm > 1 && per_sm * (2 * q.slotB + q.holdB + 4096) > budget) --per_sm;
+    q.slots = std::min(4, (budget / per_sm - (per_sm > 1 ? q.holdB + 4096 : 0)) / q.slotB);
     if (q.slots < 2) return false;
     q.off_hold = q.slots * q.slotB;
-    o.smem = q.off_hold + hB;
+    o.smem = q.off_hold + q.holdB;
     // (a power of two from 32 up; at most 256 a CTA of 16 warps, so that the CTAs of an SM fit its 512)
     q.tcols = 32;
     while (q.tcols < (uint32_t)(o.threads / 32 + 3) / 4 * 32 * o.v) q.tcols *= 2;

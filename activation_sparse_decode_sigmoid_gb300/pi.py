@@ -654,7 +654,7 @@ class Context:
         t = torch.empty(n, dtype=torch.uint8, device=self.torch_device)
         return t, t.data_ptr()
 
-    def _grad_buffers(self, given: dict, accumulate: bool, shapes: dict, dtype):
+    def _grad_buffers(self, given: dict, shapes: dict, dtype):
         """Checks gradient buffers: packed, one type; returns that type."""
         kind = None
         for k, t in given.items():
@@ -796,7 +796,7 @@ class Context:
         else:
             shapes = {"w_gate": (n, d), "w_up": (n, d), "w_down": (d, n), "b_gate": (n,), "b_up": (n,), "b_down": (d,)}
             out = {k: grads.get(k) for k in shapes}
-            gdt = self._grad_buffers(out, accumulate, shapes, dt)
+            gdt = self._grad_buffers(out, shapes, dt)
         pdy, ldy = self._at("dy", dy, (T, d), dt)
         px, ldx = self._at("x", x, (T, d), dt)
         dx = None
@@ -880,7 +880,7 @@ class Context:
             gdt = dtype
         else:
             out = {k: grads.get(k) for k in given}
-            gdt = self._grad_buffers(out, accumulate, {k: (rows, d) if k == "gate" else (d,) for k in given}, dtype)
+            gdt = self._grad_buffers(out, {k: (rows, d) if k == "gate" else (d,) for k in given}, dtype)
         if xcode != PI_F32 and xdt != dtype:
             raise PiError(PI_ERR_ARG, f"x_out is {xdt}, expected {dtype} or float32")
         px, ldxo = self._at("x_out", x_out, (T, d), xdt)
