@@ -777,10 +777,29 @@ __device__ __forceinline__ void tm_have16(float (&v)[16])
 }
 __device__ __forceinline__ void tm_settle() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// What a warp publishes of a row in the backward pass.
-struct BwdStat {
-    float sx, mx, sq, sqx, sy, my;
-};
+// Sums over the warp of several values at once: lanes that have added two
+// halves carry on with different values, so that two sums take 6 shuffles
+// instead of 10 and four take 6 instead of 20.  (Half of the backward pass's
+// instructions were such sums and what joins them: FIG2.)
+__device__ __forceinline__ float pair_sum(float a, float b, int lane) // a's in lanes 0-15, b's in 16-31
+{
+    float v = (lane & 16 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : b, 16);
+    return half_add(v);
+}
+__device__ __forceinline__ float quad_sum(float a, float b, float c, float d, int lane) // in lanes 0-7, 8-15, ...
+{
+    const float v = (lane & 16 ? c : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : c, 16);
+    const float w = (lane & 16 ? d : b) + __shfl_xor_sync(0xffffffffu, lane & 16 ? b : d, 16);
+    float u = (lane & 8 ? w : v) + __shfl_xor_sync(0xffffffffu, lane & 8 ? v : w, 8);
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    return u;
+}
+__device__ __forceinline__ float lane_of(float v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
+
+// What a warp publishes of a row in the backward pass: the sums of x' and y,
+// then about its own means of x'^2, dh w x', y^2 and dh w.
+enum { ST_SX, ST_SY, ST_MX, ST_SQX, ST_MY, ST_SQ, ST_N = 9 }; // (9: no bank conflicts)
 
 // FULL: layer norms, and the plain sums P0 and S0 (biases); else RMS norms
 // without them.  Per row two barriers: each warp publishes its share of the
@@ -791,15 +810,15 @@ struct BwdStat {
 // 345 us with 512 threads and spills, 271 us with 256 threads of 32 columns).
 // Bound by instruction issue, so what one gate row's tokens share, bs gate
 // w_post, is multiplied once, and each element's value is kept in the form
-// that its next use wants (FIG).
+// that its next use wants (209 -> 196 us; the next row's statistics computed ahead
+// of the same barrier took 235 us, the registers being full).
 // RG: a gate row per token, in the ring.
 template <typename T, bool X32, int V, bool FULL, bool RG>
 __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[8];
-    __shared__ BwdStat red[2][16];
-    __shared__ float2 red2[2][16];
+    __shared__ float red[2][16][ST_N], red2[2][16][2];
     __shared__ uint32_t tslot;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5, S = q.slots, d = p.d;
     const int r0 = row_of(p.Tn, blockIdx.x, gridDim.x), r1 = row_of(p.Tn, blockIdx.x + 1, gridDim.x);
@@ -833,7 +852,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) tm_st16(sums + 16 * i, z);
     }
-    const float nel = warp_elems<V>(d), inv_d = 1.f / (float)d;
+    const float nel = warp_elems<V>(d), inv_nel = nel > 0.f ? 1.f / nel : 0.f, inv_d = 1.f / (float)d;
     // elements of warp (lane mod 16), whose share this lane joins
     float nz = 0.f;
 #pragma unroll
@@ -868,8 +887,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             hold_factors<T, V>(p, hold, group);
         }
         // statistics of x' and y, and the sums of dh w and dh w xh, about the warp's means
-        BwdStat st = {};
-        float wmx = 0.f, wmy = 0.f;
+        float wmx = 0.f, wmy = 0.f, sx = 0.f, sy = 0.f, qx = 0.f, qy = 0.f, sq = 0.f, sqx = 0.f;
         float x[V][8], y[V][8]; // x' and y, then less the warp's means, then normalised
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -877,13 +895,14 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             ring8<T>(row + q.off_y, c[i], y[i]);
             if (FULL) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) st.sx += x[i][j], st.sy += y[i][j];
+                for (int j = 0; j < 8; ++j) sx += x[i][j], sy += y[i][j];
             }
         }
         if (FULL) {
-            st.sx = warp_add(st.sx), st.sy = warp_add(st.sy);
-            if (lpre && nel > 0.f) wmx = st.sx / nel;
-            if (lpost && nel > 0.f) wmy = st.sy / nel;
+            const float v = pair_sum(sx, sy, lane);
+            if ((lane & 15) == 0) red[flip][warp][lane ? ST_SY : ST_SX] = v;
+            if (lpre) wmx = lane_of(v, 0) * inv_nel;
+            if (lpost) wmy = lane_of(v, 16) * inv_nel;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -895,33 +914,39 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             for (int j = 0; j < 8; ++j) {
                 const float k = h[j] * w[j];
                 if (FULL) x[i][j] -= mx, y[i][j] -= my;
-                st.mx = fmaf(x[i][j], x[i][j], st.mx);
-                if (FULL) st.sq += k;
-                st.sqx = fmaf(k, x[i][j], st.sqx);
-                st.my = fmaf(y[i][j], y[i][j], st.my);
+                qx = fmaf(x[i][j], x[i][j], qx);
+                if (FULL) sq += k;
+                sqx = fmaf(k, x[i][j], sqx);
+                qy = fmaf(y[i][j], y[i][j], qy);
             }
         }
-        st.mx = warp_add(st.mx), st.sqx = warp_add(st.sqx), st.my = warp_add(st.my);
-        if (FULL) st.sq = warp_add(st.sq);
-        if (lane == 0) red[flip][warp] = st;
-        if (!__syncthreads_and(ok)) break;
-        float mx = 0.f, rx, c1 = 0.f, c2, my = 0.f, ry;
         {
-            BwdStat z = {};
-            if ((lane & 15) < nw) z = red[flip][lane & 15];
-            if (lpre) {
-                mx = half_add(z.sx) * inv_d, c1 = half_add(z.sq) * inv_d;
-                const float e = z.sx * inv_nz - mx;
-                z.mx = fmaf(nz * e, e, z.mx), z.sqx = fmaf(e, z.sq, z.sqx);
+            const float v = quad_sum(qx, sqx, qy, sq, lane);
+            if ((lane & 7) == 0) red[flip][warp][ST_MX + (lane >> 3)] = v;
+        }
+        if (!__syncthreads_and(ok)) break;
+        // all warps' shares: those of x' in lanes 0-15, of y in lanes 16-31
+        float mx = 0.f, my = 0.f, c1 = 0.f, rx, ry, c2;
+        {
+            const bool hi = lane & 16, in = (lane & 15) < nw;
+            const float *z = red[flip][lane & 15];
+            float m = in ? z[hi ? ST_MY : ST_MX] : 0.f, k = in ? z[hi ? ST_SQ : ST_SQX] : 0.f;
+            float mean = 0.f;
+            if (FULL) {
+                const float u = in ? z[hi ? ST_SY : ST_SX] : 0.f, all = half_add(u);
+                if (hi ? lpost : lpre) {
+                    mean = all * inv_d;
+                    const float e = u * inv_nz - mean;
+                    m = fmaf(nz * e, e, m);
+                    if (!hi && in) k = fmaf(e, z[ST_SQ], k);
+                }
+                mx = lane_of(mean, 0), my = lane_of(mean, 16);
             }
-            if (lpost) {
-                my = half_add(z.sy) * inv_d;
-                const float e = z.sy * inv_nz - my;
-                z.my = fmaf(nz * e, e, z.my);
-            }
-            rx = pre ? 1.f / sqrtf(half_add(z.mx) * inv_d + p.eps) : 0.f;
-            ry = post ? 1.f / sqrtf(half_add(z.my) * inv_d + p.eps) : 1.f;
-            c2 = half_add(z.sqx) * rx * inv_d;
+            m = half_add(m), k = half_add(k);
+            const float r = (hi ? post : pre) ? 1.f / sqrtf(m * inv_d + p.eps) : hi ? 1.f : 0.f;
+            rx = lane_of(r, 0), ry = lane_of(r, 16);
+            c2 = lane_of(k, 0) * rx * inv_d;
+            if (lpre) c1 = lane_of(k, 16) * inv_d;
         }
         // (the warp's mean lies within sqrt(d / its elements) deviations of the row's: x rx + cx cancels little)
         const float cx = (wmx - mx) * rx, cy = (wmy - my) * ry;
@@ -999,19 +1024,17 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_co
             tm_st16(sums + 32 * i + 16, a);
         }
         if (post) {
-            s2 = warp_add(s2);
-            if (FULL) s1 = warp_add(s1);
-            if (lane == 0) red2[flip][warp] = make_float2(s1, s2);
+            const float v = pair_sum(s1, s2, lane);
+            if ((lane & 15) == 0) red2[flip][warp][lane >> 4] = v;
         }
         __syncthreads(); // also: every thread is done with the row's slot
         if (tid == 0 && issued < r1) issue_row(p, q, ring, full, slot, issued), ++issued;
         if (p.dy) {
             float k1 = 0.f, k2 = 0.f;
             if (post) {
-                float2 z = make_float2(0.f, 0.f);
-                if ((lane & 15) < nw) z = red2[flip][lane & 15];
-                if (lpost) k1 = half_add(z.x) * inv_d;
-                k2 = half_add(z.y) * inv_d;
+                const float v = half_add((lane & 15) < nw ? red2[flip][lane & 15][lane >> 4] : 0.f);
+                if (lpost) k1 = lane_of(v, 0) * inv_d;
+                k2 = lane_of(v, 16) * inv_d;
             }
             k1 *= -ry, k2 *= -ry;
 #pragma unroll
