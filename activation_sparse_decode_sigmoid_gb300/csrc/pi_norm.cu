@@ -779,8 +779,8 @@ __device__ __forceinline__ void tm_settle() { asm volatile("tcgen05.wait::st.syn
 
 // Sums over the warp of several values at once: lanes that have added two
 // halves carry on with different values, so that two sums take 6 shuffles
-// instead of 10 and four take 6 instead of 20.  (Half of the backward pass's
-// instructions were such sums and what joins them: FIG2.)
+// instead of 10 and four take 6 instead of 20.  (A good part of the backward pass's
+// instructions were such sums and what joins them: 8000 x 8192 196 -> 178 us.)
 __device__ __forceinline__ float pair_sum(float a, float b, int lane) // a's in lanes 0-15, b's in 16-31
 {
     float v = (lane & 16 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : b, 16);
@@ -810,8 +810,8 @@ enum { ST_SX, ST_SY, ST_MX, ST_SQX, ST_MY, ST_SQ, ST_N = 9 }; // (9: no bank con
 // 345 us with 512 threads and spills, 271 us with 256 threads of 32 columns).
 // Bound by instruction issue, so what one gate row's tokens share, bs gate
 // w_post, is multiplied once, and each element's value is kept in the form
-// that its next use wants (209 -> 196 us; the next row's statistics computed ahead
-// of the same barrier took 235 us, the registers being full).
+// that its next use wants (209 -> 196 us), and sums share shuffles (178 us).  (The next row's statistics computed ahead
+// of the same barrier took 235 instead of 196 us, the registers being full.)
 // RG: a gate row per token, in the ring.
 template <typename T, bool X32, int V, bool FULL, bool RG>
 __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
@@ -1075,7 +1075,8 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_constant__ NormP p, int G, int groups, int sums, int lpg)
 {
     __shared__ float red[kJoinLanes][6][32];
-    __shared__ int first[kMaxCtas], last[kMaxCtas]; // gate rows of a CTA's tokens
+    extern __shared__ __align__(128) uint8_t ring[];
+    int *first = reinterpret_cast<int *>(ring), *last = first + G; // gate rows of a CTA's tokens
     if (blockIdx.y == 0) {
         for (int i = threadIdx.x; i < G; i += blockDim.x) {
             first[i] = p.per_token ? 0 : row_of(p.Tn, i, G) / p.gate_rows;
@@ -1139,10 +1140,16 @@ __global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_co
 #pragma unroll
     for (int i = 0; i < 6; ++i) red[k][i][l] = v[i];
     __syncthreads();
+    if (k < 6) { // a warp each
+        float a = red[0][k][l];
+#pragma unroll
+        for (int j = 1; j < kJoinLanes; ++j) a += red[j][k][l];
+        red[0][k][l] = a;
+    }
+    __syncthreads();
     if (!in || k) return;
 #pragma unroll
-    for (int i = 0; i < 6; ++i)
-        for (int j = 1; j < kJoinLanes; ++j) v[i] += red[j][i][l];
+    for (int i = 0; i < 6; ++i) v[i] = red[0][i][l];
     put<T>(p, p.dw_pre, c, v[0]);
     put<T>(p, p.db_pre, c, v[1]);
     put<T>(p, p.dw_post, c, p.bs * v[2]);
@@ -1252,8 +1259,8 @@ template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &
         while (2 * lpg * groups <= kJoinLanes) lpg *= 2;
         const int sets = (groups + kJoinLanes / lpg - 1) / (kJoinLanes / lpg);
         const int gy = p.dgate && !p.per_token && groups > 1 ? std::min(sets, 64) : 0;
-        return launch_pdl(norm_bwd_join<T>, dim3((p.d + 31) / 32, 1 + gy), dim3(32 * kJoinLanes), 0, s, p, o.grid, groups,
-                          (int)full, lpg);
+        return launch_pdl(norm_bwd_join<T>, dim3((p.d + 31) / 32, 1 + gy), dim3(32 * kJoinLanes), o.grid * 8, s, p, o.grid,
+                          groups, (int)full, lpg);
     }
     const int nt = std::min(512, ((p.d + 7) / 8 + 31) / 32 * 32);
     cudaError_t e = launch_pdl(norm_bwd_rows<T>, dim3(p.Tn), dim3(nt), 0, s, p);
