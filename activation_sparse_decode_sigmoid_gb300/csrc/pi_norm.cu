@@ -571,13 +571,6 @@ __device__ __forceinline__ void load8f2(const float *a, const float *b, float (&
     v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
 }
 
-__device__ __forceinline__ float warp_add(float a)
-{
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    return a;
-}
-
 // sum over 16 lanes (both halves hold the same values)
 __device__ __forceinline__ float half_add(float a)
 {
@@ -586,25 +579,29 @@ __device__ __forceinline__ float half_add(float a)
     return a;
 }
 
-// Row statistics without a second pass over the CTA: each warp publishes the
-// sum s of its n elements and the squares m about its own mean; the whole
-// row's squares about its mean are sum (m_w + n_w (mean_w - mean)^2).
-struct WarpStat {
-    float s, m, n;
-};
-
-// mean and 1 / sqrt(... + eps) from this lane's warp's share (lanes l and l + 16 alike, 0 past the warps)
-__device__ __forceinline__ void join_stats(int kind, const WarpStat &w, int d, float eps, float &mean, float &r)
+// Row statistics in one exchange between the warps: each publishes the sum of
+// its n elements and the squares m about its own mean; the row's squares about
+// its mean are sum (m_w + n_w (mean_w - mean)^2).
+//
+// Sums over the warp of several values at once: lanes that have added two
+// halves carry on with different values, so that two sums take 6 shuffles
+// instead of 10 and four take 6 instead of 20.  (A good part of the backward pass's
+// instructions were such sums and what joins them: 8000 x 8192 196 -> 178 us.)
+__device__ __forceinline__ float pair_sum(float a, float b, int lane) // a's in lanes 0-15, b's in 16-31
 {
-    mean = 0.f;
-    float m = w.m;
-    if (kind == PI_NORM_LAYER) {
-        mean = half_add(w.s) / (float)d;
-        const float e = w.n > 0.f ? w.s / w.n - mean : 0.f;
-        m = fmaf(w.n * e, e, m);
-    }
-    r = 1.f / sqrtf(half_add(m) / (float)d + eps);
+    float v = (lane & 16 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : b, 16);
+    return half_add(v);
 }
+__device__ __forceinline__ float quad_sum(float a, float b, float c, float d, int lane) // in lanes 0-7, 8-15, ...
+{
+    const float v = (lane & 16 ? c : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : c, 16);
+    const float w = (lane & 16 ? d : b) + __shfl_xor_sync(0xffffffffu, lane & 16 ? b : d, 16);
+    float u = (lane & 8 ? w : v) + __shfl_xor_sync(0xffffffffu, lane & 8 ? v : w, 8);
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    return u;
+}
+__device__ __forceinline__ float lane_of(float v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
 
 __device__ __forceinline__ int row_of(int64_t Tn, int c, int G) { return (int)(Tn * c / G); }
 
@@ -628,12 +625,15 @@ __device__ __forceinline__ void pipe_settle()
     }
 }
 
+// One barrier a row: behind it lie all warps' shares of the statistics of x'
+// and, computed ahead about each warp's own mean, of the next row's y (4096 x
+// 7168 with both norms: 72 us, 84 % of the copy rate; with three barriers 75).
 template <typename T, bool X32, int V>
 __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[8];
-    __shared__ WarpStat red[2][2][16];
+    __shared__ float red[2][16][5]; // a warp's sums of x' and of y, then of the squares about its means
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = blockDim.x >> 5, S = q.slots, d = p.d;
     const int r0 = row_of(p.Tn, blockIdx.x, gridDim.x), r1 = row_of(p.Tn, blockIdx.x + 1, gridDim.x);
     if (tid == 0) {
@@ -658,96 +658,119 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_co
         wq[i] = param8<T>(p.w_post, c[i], d, 1.f), bq[i] = param8<T>(p.b_post, c[i], d, 0.f);
     }
     const bool post = p.y && p.post != PI_NORM_NONE;
-    const float nel = warp_elems<V>(d);
+    const bool lpre = p.pre == PI_NORM_LAYER, lpost = post && p.post == PI_NORM_LAYER;
+    const float nel = warp_elems<V>(d), inv_nel = nel > 0.f ? 1.f / nel : 0.f, inv_d = 1.f / (float)d;
+    float nz = 0.f; // elements of warp (lane mod 16), whose share this lane joins
+#pragma unroll
+    for (int i = 0; i < V; ++i) nz += (float)max(0, min(256, d - (int)((lane & 15) * 256 + i * blockDim.x * 8)));
+    if ((lane & 15) >= nw) nz = 0.f;
+    const float inv_nz = nz > 0.f ? 1.f / nz : 0.f;
     int group = -1, slot = 0, flip = 0;
     uint32_t par = 0;
+    float x[V][8] = {}, z[V][8]; // x' of this row, y of the next, less the warp's means
+    float rx = 0.f, cx = 0.f, rz = 0.f, cz = 0.f; // normalised: x rx + cx, z rz + cz
+    float wmx = 0.f, wmz = 0.f;
+    auto load_y = [&](const uint8_t *row) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) ring8<T>(row + q.off_y, c[i], z[i]);
+    };
+    auto publish = [&]() {
+        if (lpre || lpost) {
+            float sx = 0.f, sz = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sx += x[i][j], sz += z[i][j];
+            const float v = pair_sum(sx, sz, lane);
+            if ((lane & 15) == 0) red[flip][warp][lane >> 4] = v;
+            if (lpre) wmx = lane_of(v, 0) * inv_nel;
+            if (lpost) wmz = lane_of(v, 16) * inv_nel;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (on[i]) x[i][j] -= wmx, z[i][j] -= wmz;
+        }
+        float qx = 0.f, qz = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) qx = fmaf(x[i][j], x[i][j], qx), qz = fmaf(z[i][j], z[i][j], qz);
+        const float v = pair_sum(qx, qz, lane);
+        if ((lane & 15) == 0) red[flip][warp][2 + (lane >> 4)] = v;
+    };
+    // all warps' shares: those of x' in lanes 0-15, of y in lanes 16-31
+    auto join = [&]() {
+        const int hi = lane >> 4;
+        const bool in = (lane & 15) < nw;
+        const float *w = red[flip][lane & 15];
+        float m = in ? w[2 + hi] : 0.f, mean = 0.f;
+        if (lpre || lpost) {
+            const float u = in ? w[hi] : 0.f, all = half_add(u);
+            if (hi ? lpost : lpre) {
+                mean = all * inv_d;
+                const float e = u * inv_nz - mean;
+                m = fmaf(nz * e, e, m);
+            }
+        }
+        m = half_add(m);
+        const float r = (hi ? post : p.h != nullptr) ? 1.f / sqrtf(m * inv_d + p.eps) : 1.f;
+        // (the warp's mean lies within sqrt(d / its elements) deviations of the row's: x rx + cx cancels little)
+        rx = lane_of(r, 0), rz = lane_of(r, 16);
+        cx = (wmx - lane_of(mean, 0)) * rx, cz = (wmz - lane_of(mean, 16)) * rz;
+    };
     bool ok = true;
-    for (int t = r0; t < r1; ++t) {
-        ok = mbar_wait_bounded(full + slot, par, q);
-        if (!__syncthreads_and(ok)) break; // also: every thread is done with the previous row's slot
-        if (tid == 0 && t > r0 && issued < r1) issue_row(p, q, ring, full, slot ? slot - 1 : S - 1, issued), ++issued;
+    if (r0 < r1) {
+        ok = mbar_wait_bounded(full, 0, q);
+        load_y(ring);
+        publish();
+    }
+    ok = __syncthreads_and(ok);
+    if (ok && r0 < r1) join();
+    flip = 1;
+    for (int t = r0; ok && t < r1; ++t) {
         const uint8_t *row = ring + slot * q.slotB, *gate = q.off_gate >= 0 ? row + q.off_gate : hold;
         if (q.off_gate < 0 && t / p.gate_rows != group) {
             group = t / p.gate_rows;
             hold_gate<T, V>(p, hold, group);
         }
-        float x[V][8], y[V][8];
-#pragma unroll
-        for (int i = 0; i < V; ++i) ring8<T>(row + q.off_y, c[i], y[i]);
-        if (post) {
-            WarpStat w = {0.f, 0.f, nel};
-            float mean = 0.f, r;
-            if (p.post == PI_NORM_LAYER) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) w.s += y[i][j];
-                w.s = warp_add(w.s);
-                mean = nel > 0.f ? w.s / nel : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float m = on[i] ? mean : 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w.m = fmaf(y[i][j] - m, y[i][j] - m, w.m);
-            }
-            w.m = warp_add(w.m);
-            if (lane == 0) red[0][flip][warp] = w;
-            __syncthreads();
-            WarpStat z = {0.f, 0.f, 0.f};
-            if ((lane & 15) < nw) z = red[0][flip][lane & 15];
-            join_stats(p.post, z, d, p.eps, mean, r);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float w8[8], b8[8];
-                unpack8<T>(wq[i], w8), unpack8<T>(bq[i], b8);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[i][j] = fmaf((y[i][j] - mean) * r, w8[j], b8[j]);
-            }
-        }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float g[8];
+            if (post) {
+                float w8[8], b8[8];
+                unpack8<T>(wq[i], w8), unpack8<T>(bq[i], b8);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[i][j] = fmaf(fmaf(z[i][j], rz, cz), w8[j], b8[j]);
+            }
             ring8x<T, X32>(row, c[i], x[i]);
             ring8<T>(gate, c[i], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] = fmaf(p.bs * g[j], y[i][j], p.rs * x[i][j]);
+            for (int j = 0; j < 8; ++j) x[i][j] = fmaf(p.bs * g[j], z[i][j], p.rs * x[i][j]);
             if (p.xo && on[i]) storex8<T>(p.xo, X32, (int64_t)t * p.ldxo + c[i], 8, true, x[i]);
         }
+        const int done = slot;
+        if (++slot == S) slot = 0, par ^= 1u;
+        if (t + 1 < r1) {
+            ok = mbar_wait_bounded(full + slot, par, q);
+            load_y(ring + slot * q.slotB);
+        }
+        publish();
+        ok = __syncthreads_and(ok); // also: every thread is done with this row's slot
+        if (!ok) break;
+        if (tid == 0 && issued < r1) issue_row(p, q, ring, full, done, issued), ++issued;
+        join();
         if (p.h) {
-            WarpStat w = {0.f, 0.f, nel};
-            float mean = 0.f, r;
-            if (p.pre == PI_NORM_LAYER) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) w.s += x[i][j];
-                w.s = warp_add(w.s);
-                mean = nel > 0.f ? w.s / nel : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float m = on[i] ? mean : 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w.m = fmaf(x[i][j] - m, x[i][j] - m, w.m);
-            }
-            w.m = warp_add(w.m);
-            if (lane == 0) red[1][flip][warp] = w;
-            __syncthreads();
-            WarpStat z = {0.f, 0.f, 0.f};
-            if ((lane & 15) < nw) z = red[1][flip][lane & 15];
-            join_stats(p.pre, z, d, p.eps, mean, r);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float w8[8], b8[8];
                 unpack8<T>(wp[i], w8), unpack8<T>(bp[i], b8);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = fmaf((x[i][j] - mean) * r, w8[j], b8[j]);
+                for (int j = 0; j < 8; ++j) x[i][j] = fmaf(fmaf(x[i][j], rx, cx), w8[j], b8[j]);
                 if (on[i]) store8<T>(p.h + (int64_t)t * p.ldh + c[i], 8, true, x[i]);
             }
         }
         flip ^= 1;
-        if (++slot == S) slot = 0, par ^= 1u;
     }
     if (!ok || *(volatile int *)q.abort_flag) pipe_settle();
 }
@@ -776,26 +799,6 @@ __device__ __forceinline__ void tm_have16(float (&v)[16])
                    "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
 __device__ __forceinline__ void tm_settle() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Sums over the warp of several values at once: lanes that have added two
-// halves carry on with different values, so that two sums take 6 shuffles
-// instead of 10 and four take 6 instead of 20.  (A good part of the backward pass's
-// instructions were such sums and what joins them: 8000 x 8192 196 -> 178 us.)
-__device__ __forceinline__ float pair_sum(float a, float b, int lane) // a's in lanes 0-15, b's in 16-31
-{
-    float v = (lane & 16 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : b, 16);
-    return half_add(v);
-}
-__device__ __forceinline__ float quad_sum(float a, float b, float c, float d, int lane) // in lanes 0-7, 8-15, ...
-{
-    const float v = (lane & 16 ? c : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : c, 16);
-    const float w = (lane & 16 ? d : b) + __shfl_xor_sync(0xffffffffu, lane & 16 ? b : d, 16);
-    float u = (lane & 8 ? w : v) + __shfl_xor_sync(0xffffffffu, lane & 8 ? v : w, 8);
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    return u;
-}
-__device__ __forceinline__ float lane_of(float v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
 
 // What a warp publishes of a row in the backward pass: the sums of x' and y,
 // then about its own means of x'^2, dh w x', y^2 and dh w.
