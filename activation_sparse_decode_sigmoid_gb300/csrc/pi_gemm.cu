@@ -97,7 +97,7 @@ struct Sched {
 template <int NP> struct TcParams {
     Prob prob[NP];
     Sched s;
-    float *part;          // [nsplit][smax][256][256]
+    float *part;          // [nsplit][smax][256 / 4 columns][256 rows][4]: a warp's 32 rows write 512 bytes in a row
     int *status, *abort_flag;
     unsigned long long wait_ns;
 };
@@ -593,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             bool released = false;
             if (!whole) {
                 const int r = (int)rank * 128 + q * 32 + lane; // row within the tile
-                float *dst = p.part + ((size_t)w.slot * kTile + r) * kTile;
+                float4 *dst = reinterpret_cast<float4 *>(p.part) + (size_t)w.slot * (kTile * kTile / 4) + r;
 #pragma unroll 1
                 for (int c = half * 128; c < half * 128 + 128; c += 32) {
                     float v[32];
@@ -601,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     if (row0 + lane < M) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            dst[(c + i) / 4 * kTile] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
             } else if (simple && row0 + 32 <= M && col0 + kCols <= N) {
@@ -737,15 +737,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
+__device__ __forceinline__ void load4x2(const float4 *a, const float4 *b, float (&v)[8])
+{
+    const float4 p = *a, q = *b;
+    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
+}
+
 // The split tiles: partials added in the order of k, then the epilogue.
-// 256 threads take 8 columns each of 8 (gated: 16) rows.
+// 256 threads take 8 columns each of 8 (gated: 16) rows; a warp's 8 rows x 32
+// columns are 128 bytes in a row of the partials, 64 of the output.
 template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcParams<NP> p)
 {
     pdl_enter();
     const Prob &pr = p.prob[NP == 1 ? 0 : p.s.sprob];
     constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile, kCols = kOutN / 8, kRows = 256 / kCols;
     const int per = kTile / kRows, r = (int)blockIdx.x / per;
-    const int row = ((int)blockIdx.x % per) * kRows + threadIdx.x / kCols, c = (threadIdx.x % kCols) * 8;
+    constexpr int kWarps = kOutN / 32; // that share 8 rows
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = ((int)blockIdx.x % per) * kRows + warp / kWarps * 8 + (lane & 7), c = warp % kWarps * 32 + (lane >> 3) * 8;
     int mi, ni;
     tile_at(p.s.stile0 + r, pr.tm, pr.tn, mi, ni);
     const int grow = mi * kTile + row, gcol = ni * kOutN + c;
@@ -753,14 +762,14 @@ template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) g
     const int64_t units = (int64_t)(p.s.nsplit / p.s.lanes) * pr.KT, u0 = (int64_t)(r / p.s.lanes) * pr.KT;
     const int cnt = part_of(units, u0 + pr.KT - 1, p.s.parts) - part_of(units, u0, p.s.parts) + 1;
     float v[8] = {}, u[8] = {};
-    const float *src = p.part + ((size_t)r * p.s.smax * kTile + row) * kTile + c;
-    for (int s = 0; s < cnt; ++s, src += kTile * kTile) {
+    const float4 *src = reinterpret_cast<const float4 *>(p.part) + (size_t)r * p.s.smax * (kTile * kTile / 4) + c / 4 * kTile + row;
+    for (int s = 0; s < cnt; ++s, src += kTile * kTile / 4) {
         float t[8];
-        load8f(src, 8, true, t);
+        load4x2(src, src + kTile, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += t[i];
         if (MODE == EPI_GATED) {
-            load8f(src + 128, 8, true, t);
+            load4x2(src + 32 * kTile, src + 33 * kTile, t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) u[i] += t[i];
         }
