@@ -3,7 +3,8 @@
 //     D[m][n] = sum_k A(m, k) B(n, k)   (one or two segments of k)
 //
 // Bound by the tensor cores for more than about 300 rows of A and of B (2 M N
-// K operations on (M K + N K) 2 bytes), by HBM below.  One tile is 256 x 256,
+// K operations on (M K + N K) 2 bytes), by HBM below.  One tile is 256 x 256
+// (256 x 128 where those would leave half of the SMs idle, see plan_group),
 // computed by a pair of CTAs on two SMs (cta_group::2): each holds 128 rows of
 // A and 128 of B per 64-element step of k in shared memory, so a step costs
 // each SM 32 KB of loads for 256 x 256 x 64 products - half of what a CTA of
@@ -97,6 +98,7 @@ struct Sched {
 template <int NP> struct TcParams {
     Prob prob[NP];
     Sched s;
+    int wide;             // columns of a tile's accumulator: 256 or 128
     float *part;          // [nsplit][smax][256 / 4 columns][256 rows][4]: a warp's 32 rows write 512 bytes in a row
     int *status, *abort_flag;
     unsigned long long wait_ns;
@@ -379,42 +381,48 @@ __device__ __forceinline__ void box_settle(int lane)
     __syncwarp();
 }
 
-// A warp's 32 x 128 values, rounded and nothing else, all inside the output:
-// 64 columns at a time through the warp's 4 KB (128-byte swizzle) and out by a
-// TMA store, the next 32 columns on their way out of tensor memory meanwhile.
-// (By the warps' own stores, 64 bytes a row, a tile took 2.7 us.)  `last` runs
-// once the accumulator has been read.
+// A warp's 32 x 64 `boxes` values, rounded and nothing else, all inside the
+// output: 64 columns at a time through the warp's 4 KB (128-byte swizzle) and
+// out by a TMA store, the next 32 columns on their way out of tensor memory
+// meanwhile.  (By the warps' own stores, 64 bytes a row, a tile of 256 x 256
+// took 2.7 us.)  `last` runs once the accumulator has been read.
+template <typename T> __device__ __forceinline__ void box_half(uint32_t box, int lane, int h, const uint32_t (&v)[32])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * j + i]);
+        sts16(box + lane * 128 + (((h * 4 + j) ^ (lane & 7)) << 4), pack8<T>(x));
+    }
+}
+
 template <typename T, typename F>
-__device__ __forceinline__ void plain_strip(uint32_t ta, uint32_t box, const CUtensorMap *mo, int lane, int row, int col, F last)
+__device__ __forceinline__ void plain_strip(uint32_t ta, int boxes, uint32_t box, const CUtensorMap *mo, int lane, int row, int col,
+                                            F last)
 {
     uint32_t r[2][32];
     tmem_ld32_async(ta, r[0]);
     box_settle(lane);
     tmem_wait32(r[0]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t(&v)[32] = r[c & 1];
-        if (c < 3) tmem_ld32_async(ta + 32 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll 1
+    for (int b = 1; b <= boxes; ++b, ta += 64, col += 64) {
+        tmem_ld32_async(ta + 32, r[1]);
+        if (b > 1) box_settle(lane);
+        box_half<T>(box, lane, 0, r[0]);
+        tmem_wait32(r[1]);
+        if (b < boxes) tmem_ld32_async(ta + 64, r[0]);
         else last();
-        if (c == 2) box_settle(lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * j + i]);
-            sts16(box + lane * 128 + ((((c & 1) * 4 + j) ^ (lane & 7)) << 4), pack8<T>(x));
+        box_half<T>(box, lane, 1, r[1]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(mo), "r"(box),
+                         "r"(col), "r"(row)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
-        if (c & 1) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(mo), "r"(box),
-                             "r"(col + 64 * (c >> 1)), "r"(row)
-                             : "memory");
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-        }
-        if (c < 3) tmem_wait32(r[(c + 1) & 1]);
+        if (b < boxes) tmem_wait32(r[0]);
     }
     __syncwarp();
 }
@@ -425,7 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     using H = H16<T>;
-    constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile; // output columns of a tile
+    const int wide = MODE == EPI_GATED ? kTile : p.wide;
+    const int outn = MODE == EPI_GATED ? 128 : wide; // output columns of a tile
     constexpr bool kPlain = NP > 1; // a backward pass's products: no bias, activation, scale or z
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
@@ -470,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             int mi, ni;
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
             const int m0 = mi * kTile + (int)rank * 128;
-            const int n0 = ni * kOutN + (MODE == EPI_GATED ? 0 : (int)rank * 128);
+            const int n0 = ni * outn + (MODE == EPI_GATED ? 0 : (int)rank * (wide / 2));
             for (int seg = 0; seg < 2 && ok; ++seg) {
                 const int lo = seg ? pr.kt0 : 0, ka = max(w.k0, lo), kb = min(w.k1, seg ? pr.KT : pr.kt0);
                 const CUtensorMap *ma = &pr.ma[seg], *mb = &pr.mb[MODE == EPI_GATED ? (int)rank : seg];
@@ -482,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     if (elect_one()) {
                         const uint32_t bar = full0 + cur.s * 8, sa = base + cur.s * kStageBytes, sb = sa + kOpBytes;
                         const int kc = (k - lo) * kBK;
-                        if (rank == 0) mbar_expect(full + cur.s, 2 * kStageBytes);
+                        if (rank == 0) mbar_expect(full + cur.s, 2 * kOpBytes + (uint32_t)wide * (kBK * 2));
                         if (pr.a_mn) {
                             pair_load(sa, ma, m0, kc, bar);
                             pair_load(sa + kAtom, ma, m0 + 64, kc, bar);
@@ -490,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                             pair_load(sa, ma, kc, m0, bar);
                         if (pr.b_mn) {
                             pair_load(sb, mb, n0, kc, bar);
-                            pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
+                            if (wide == kTile) pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
                         } else
                             pair_load(sb, mb, kc, n0, bar);
                     }
@@ -510,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             Cur cur(0, kStages);
             for (uint32_t it = 0; ok && walk.next(w); ++it) {
                 const Prob &pr = p.prob[NP == 1 ? 0 : w.prob];
-                const uint32_t id = idesc(H::fmt, (uint32_t)pr.a_mn, (uint32_t)pr.b_mn, 256, 256);
+                const uint32_t id = idesc(H::fmt, (uint32_t)pr.a_mn, (uint32_t)pr.b_mn, 256, (uint32_t)wide);
                 // descriptors of stage 0; a byte offset o adds o / 16 (the start address field)
                 const uint64_t da = pr.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
                 const uint64_t db = pr.b_mn ? sdesc(base + kOpBytes, kAtom, 1024) : sdesc(base + kOpBytes, 16, 1024);
@@ -547,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         const int q = warp & 3, half = warp >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t box0 = base + kStages * kStageBytes + (uint32_t)warp * 2 * kBox, box1 = box0 + kBox;
-        constexpr int kCols = kOutN / 2; // of this warp
+        const int cols = outn / 2; // of this warp
         const uint32_t bias = base + kStages * kStageBytes + kBoxes + (uint32_t)warp * kBiasB;
         for (uint32_t it = 0; ok && walk.next(w); ++it) {
             const Prob &pr = p.prob[NP == 1 ? 0 : w.prob];
@@ -566,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
             int mi, ni;
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
-            const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * kOutN + half * kCols;
+            const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * outn + half * cols;
             const bool whole = w.slot < 0;
             uint4 q1[4], q2[4]; // the next chunk's inputs
             if (whole && has_in) { // in flight while the products finish
@@ -595,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 const int r = (int)rank * 128 + q * 32 + lane; // row within the tile
                 float4 *dst = reinterpret_cast<float4 *>(p.part) + (size_t)w.slot * (kTile * kTile / 4) + r;
 #pragma unroll 1
-                for (int c = half * 128; c < half * 128 + 128; c += 32) {
+                for (int c = half * (wide / 2); c < (half + 1) * (wide / 2); c += 32) {
                     float v[32];
                     tmem_ld32(ta + c, v);
                     if (row0 + lane < M) {
@@ -604,8 +613,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                             dst[(c + i) / 4 * kTile] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
-            } else if (simple && row0 + 32 <= M && col0 + kCols <= N) {
-                plain_strip<T>(ta + half * kCols, box0, &pr.mo, lane, row0, col0, [&]() {
+            } else if (simple && row0 + 32 <= M && col0 + cols <= N) {
+                plain_strip<T>(ta + half * cols, cols / 64, box0, &pr.mo, lane, row0, col0, [&]() {
                     tc_before();
                     __syncwarp();
                     if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
@@ -614,14 +623,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             } else if (row0 < M) {
                 if (MODE == EPI_LINEAR) box_settle(lane);
 #pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
+                for (int c = 0; c < cols; c += 32) {
                     const int col = col0 + c;
                     if (col >= N) break;
                     const bool inside = row0 + 32 <= M && col + 32 <= N;
                     float v[32], u[MODE == EPI_GATED ? 32 : 1];
-                    tmem_ld32(ta + half * kCols + c, v);
-                    if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
-                    if (c + 32 >= kCols || col + 32 >= N) {
+                    tmem_ld32(ta + half * cols + c, v);
+                    if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * cols + c, *reinterpret_cast<float(*)[32]>(u));
+                    if (c + 32 >= cols || col + 32 >= N) {
                         // the accumulator is in registers: the next tile's products may begin
                         tc_before();
                         __syncwarp();
@@ -751,14 +760,15 @@ template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) g
     pdl_enter();
     const Prob &pr = p.prob[NP == 1 ? 0 : p.s.sprob];
     constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile, kCols = kOutN / 8, kRows = 256 / kCols;
+    const int outn = MODE == EPI_GATED ? 128 : p.wide;
     const int per = kTile / kRows, r = (int)blockIdx.x / per;
     constexpr int kWarps = kOutN / 32; // that share 8 rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = ((int)blockIdx.x % per) * kRows + warp / kWarps * 8 + (lane & 7), c = warp % kWarps * 32 + (lane >> 3) * 8;
     int mi, ni;
     tile_at(p.s.stile0 + r, pr.tm, pr.tn, mi, ni);
-    const int grow = mi * kTile + row, gcol = ni * kOutN + c;
-    if (grow >= pr.M || gcol >= pr.N) return;
+    const int grow = mi * kTile + row, gcol = ni * outn + c;
+    if (grow >= pr.M || gcol >= pr.N || c >= outn) return;
     const int64_t units = (int64_t)(p.s.nsplit / p.s.lanes) * pr.KT, u0 = (int64_t)(r / p.s.lanes) * pr.KT;
     const int cnt = part_of(units, u0 + pr.KT - 1, p.s.parts) - part_of(units, u0, p.s.parts) + 1;
     float v[8] = {}, u[8] = {};
@@ -790,6 +800,7 @@ struct Plan {
     int order[kMaxProbs]; // products by falling k steps
     int tm[kMaxProbs], tn[kMaxProbs], kt0[kMaxProbs], KT[kMaxProbs]; // in that order
     int launched;         // pairs
+    int wide;             // columns of a tile
     size_t bytes;
 };
 
@@ -803,6 +814,18 @@ Plan plan_group(const Gemm *g, int n, int sms)
         q.order[i] = i;
     }
     std::stable_sort(q.order, q.order + n, [&](int a, int b) { return KT[a] > KT[b]; });
+    // Where tiles of 256 x 256 would leave half of the pairs idle, ones of 256
+    // x 128 use them: a step of k takes about 2 / 3 as long (24 instead of 32 KB
+    // of loads, which bound it, and half of the epilogue).  512 x 4096 x 4096:
+    // 20 us, 256 wide 24; 300 rows, K 1024, N 4096: 9.1, 10.9.  A long k is
+    // better split (129 x 28672 x 8192: 256 wide and split 89 us, 128 wide 108).
+    int64_t tiles = 0, steps = 0, longest = 0;
+    for (int i = 0; i < n; ++i) {
+        const int64_t t = (int64_t)((g[i].M + kTile - 1) / kTile) * ((g[i].N + kTile - 1) / kTile);
+        tiles += t, steps += t * KT[i], longest = std::max<int64_t>(longest, KT[i]);
+    }
+    q.wide = g[0].mode != EPI_GATED && tiles <= P / 2 && 2 * longest < 3 * (steps / P + kFixupSteps) ? 128 : kTile;
+    const int fixup = q.wide == kTile ? kFixupSteps : 2 * kFixupSteps;
     Sched &s = q.s;
     s.pairs = P;
     s.smax = 1, s.lanes = 1;
@@ -810,7 +833,7 @@ Plan plan_group(const Gemm *g, int n, int sms)
     int cost[kMaxProbs];
     for (int j = 0; j < n; ++j) {
         const Gemm &x = g[q.order[j]];
-        const int outn = x.mode == EPI_GATED ? 128 : kTile;
+        const int outn = x.mode == EPI_GATED ? 128 : q.wide;
         q.tm[j] = (x.M + kTile - 1) / kTile;
         q.tn[j] = (x.N + outn - 1) / outn;
         q.kt0[j] = (x.K[0] + kBK - 1) / kBK;
@@ -835,7 +858,7 @@ Plan plan_group(const Gemm *g, int n, int sms)
         int rem = m % P;
         const int from = (base + high) % P;
         // (what follows fills the pairs that the last wave leaves idle, as far as it goes)
-        if (!s.nsplit && rem && (int64_t)q.KT[j] * (P - rem) - later > (int64_t)kFixupSteps * P) {
+        if (!s.nsplit && rem && (int64_t)q.KT[j] * (P - rem) - later > (int64_t)fixup * P) {
             s.sprob = j, s.stile0 = t0 + m - rem, s.nsplit = rem;
             // the split tiles of a column (they lie together, see tile_at) are
             // cut alike, where they come in whole groups: pairs that work on
@@ -862,17 +885,18 @@ Plan plan_group(const Gemm *g, int n, int sms)
     return q;
 }
 
-cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K)
+// box: rows of a stage
+cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K, int box)
 {
     return a.mn ? encode_map(m, a.p, (uint64_t)rows, (uint64_t)K, (uint64_t)a.ld * 2, 64)
-                : encode_map(m, a.p, (uint64_t)K, (uint64_t)rows, (uint64_t)a.ld * 2, 128);
+                : encode_map(m, a.p, (uint64_t)K, (uint64_t)rows, (uint64_t)a.ld * 2, box);
 }
 
 template <typename T, int MODE, int NP> cudaError_t run(const Gemm *g, int n, const CtxView &v, void *ws)
 {
     const Plan q = plan_group(g, n, v.sms);
     TcParams<NP> p = {};
-    p.s = q.s;
+    p.s = q.s, p.wide = q.wide;
     cudaError_t e = cudaSuccess;
     for (int j = 0; j < n; ++j) {
         const Gemm &x = g[q.order[j]];
@@ -880,11 +904,11 @@ template <typename T, int MODE, int NP> cudaError_t run(const Gemm *g, int n, co
         pr.M = x.M, pr.N = x.N, pr.tm = q.tm[j], pr.tn = q.tn[j], pr.kt0 = q.kt0[j], pr.KT = q.KT[j];
         pr.a_mn = x.a[0].mn, pr.b_mn = x.b[0].mn;
         pr.e = x.e;
-        for (int i = 0; i < x.segs && e == cudaSuccess; ++i) e = map_of(&pr.ma[i], x.a[i], x.M, x.K[i]);
+        for (int i = 0; i < x.segs && e == cudaSuccess; ++i) e = map_of(&pr.ma[i], x.a[i], x.M, x.K[i], 128);
         const int nb = MODE == EPI_GATED ? 2 : x.segs;
         if (MODE == EPI_LINEAR && !x.e.out32 && (x.e.vec & V_OUT) && e == cudaSuccess)
             e = encode_map(&pr.mo, x.e.out, (uint64_t)x.N, (uint64_t)x.M, (uint64_t)x.e.ldo * 2, 32);
-        for (int i = 0; i < nb && e == cudaSuccess; ++i) e = map_of(&pr.mb[i], x.b[i], x.N, x.K[MODE == EPI_GATED ? 0 : i]);
+        for (int i = 0; i < nb && e == cudaSuccess; ++i) e = map_of(&pr.mb[i], x.b[i], x.N, x.K[MODE == EPI_GATED ? 0 : i], MODE == EPI_GATED ? 128 : q.wide / 2);
     }
     if (e != cudaSuccess) return e;
     p.part = static_cast<float *>(ws);
