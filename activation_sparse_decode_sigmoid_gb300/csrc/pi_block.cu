@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "pi.h"
 #include "pi_block.h"
@@ -26,12 +27,12 @@ constexpr int kMaxT = 1 << 22, kMaxDim = 1 << 20;
 // neighbour where the row starts in the middle of a word, and writes one word
 // of the (aligned) copy.  Only words that lie inside the row are read whole.
 // R rows of 8 x 31 words a CTA: 16 of a large matrix (loads in flight), 4 of a small one (CTAs).
-template <int R> __global__ void __launch_bounds__(256) pack_rows(const uint16_t *src, int64_t lds, uint32_t *dst, int64_t ldd, int rows, int cols)
+template <int R>
+__device__ __forceinline__ void pack_rows(unsigned block, const uint16_t *src, int64_t lds, uint32_t *dst, int64_t ldd, int rows, int cols)
 {
-    pdl_enter();
     const int nw = (cols + 1) / 2, ncb = (nw + 247) / 248; // (31 words a warp: lane 31 only lends its word)
-    const int lane = threadIdx.x & 31, w = (int)(blockIdx.x % ncb) * 248 + (threadIdx.x >> 5) * 31 + lane;
-    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * R;
+    const int lane = threadIdx.x & 31, w = (int)(block % ncb) * 248 + (threadIdx.x >> 5) * 31 + lane;
+    const int64_t r0 = (int64_t)(block / ncb) * R;
     uint32_t q[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -54,12 +55,12 @@ template <int R> __global__ void __launch_bounds__(256) pack_rows(const uint16_t
 }
 
 // The same for rows that are 8-byte aligned (strides of 4 elements): 8 bytes a thread.
-template <int R> __global__ void __launch_bounds__(256) pack_rows8(const uint16_t *src, int64_t lds, uint2 *dst, int64_t ldd, int rows, int cols)
+template <int R>
+__device__ __forceinline__ void pack_rows8(unsigned block, const uint16_t *src, int64_t lds, uint2 *dst, int64_t ldd, int rows, int cols)
 {
-    pdl_enter();
     const int nq = cols / 4, ncb = (nq + 256) / 256; // (the last, partial 8 bytes included)
-    const int w = (int)(blockIdx.x % ncb) * 256 + threadIdx.x;
-    const int64_t r0 = (int64_t)(blockIdx.x / ncb) * R;
+    const int w = (int)(block % ncb) * 256 + threadIdx.x;
+    const int64_t r0 = (int64_t)(block / ncb) * R;
     if (w > nq) return;
     uint2 q[R];
 #pragma unroll
@@ -78,6 +79,36 @@ template <int R> __global__ void __launch_bounds__(256) pack_rows8(const uint16_
         if (r0 + i < rows && (w < nq || (cols & 3))) dst[(r0 + i) * (ldd / 4) + w] = q[i];
 }
 
+// All copies of a call in one launch: of small operands, each costs more as a launch than as a copy.
+constexpr int kMaxCopies = 6;
+struct CopySet {
+    struct One {
+        const uint16_t *src;
+        void *dst;
+        int64_t lds, ldd;
+        int rows, cols;
+        unsigned block0; // its first block
+        bool large, by8;
+    } m[kMaxCopies];
+    int n;
+};
+
+__global__ void __launch_bounds__(256) pack_set(const __grid_constant__ CopySet s)
+{
+    pdl_enter();
+    int i = 0;
+    while (i + 1 < s.n && blockIdx.x >= s.m[i + 1].block0) ++i;
+    const CopySet::One &m = s.m[i];
+    const unsigned block = blockIdx.x - m.block0;
+    if (m.by8) {
+        if (m.large) pack_rows8<16>(block, m.src, m.lds, static_cast<uint2 *>(m.dst), m.ldd, m.rows, m.cols);
+        else pack_rows8<4>(block, m.src, m.lds, static_cast<uint2 *>(m.dst), m.ldd, m.rows, m.cols);
+    } else {
+        if (m.large) pack_rows<16>(block, m.src, m.lds, static_cast<uint32_t *>(m.dst), m.ldd, m.rows, m.cols);
+        else pack_rows<4>(block, m.src, m.lds, static_cast<uint32_t *>(m.dst), m.ldd, m.rows, m.cols);
+    }
+}
+
 // Column sums in two launches: a CTA sums some rows of 256 columns (8 per
 // thread, 8 row lanes), then the row blocks' partials are added in order.
 // Rows per CTA: enough CTAs for four on every SM (152), at least 8 rows; a
@@ -92,14 +123,13 @@ int sum_rows(int T, int N)
 // column sums of the unrounded values over the CTA's rows into part [row
 // block][N] unless that is NULL.
 template <typename T>
-__global__ void __launch_bounds__(256) dact_rows(const void *dy, int dy32, int64_t ldy, const uint16_t *z, int64_t ldz,
-                                                 int fn, float scale, uint16_t *dz, int64_t lddz, int Trows, int N,
-                                                 float *part, int vec, int rpb)
+__device__ __forceinline__ void dact_block(unsigned block, const void *dy, int dy32, int64_t ldy, const uint16_t *z, int64_t ldz,
+                                           int fn, float scale, uint16_t *dz, int64_t lddz, int Trows, int N, float *part, int vec,
+                                           int rpb)
 {
     __shared__ float red[8][256];
-    pdl_enter();
     const int nb = (N + 255) / 256;
-    const int rb = (int)(blockIdx.x / nb), cb = (int)(blockIdx.x % nb);
+    const int rb = (int)(block / nb), cb = (int)(block % nb);
     const int lane = threadIdx.x & 31, wr = threadIdx.x >> 5;
     const int c = cb * 256 + lane * 8, n = N - c;
     const int r1 = (int)min((int64_t)Trows, (rb + 1) * (int64_t)rpb);
@@ -134,13 +164,21 @@ __global__ void __launch_bounds__(256) dact_rows(const void *dy, int dy32, int64
     if (cc < N) part[(int64_t)rb * N + cc] = s;
 }
 
+template <typename T>
+__global__ void __launch_bounds__(256) dact_rows(const void *dy, int dy32, int64_t ldy, const uint16_t *z, int64_t ldz,
+                                                 int fn, float scale, uint16_t *dz, int64_t lddz, int Trows, int N,
+                                                 float *part, int vec, int rpb)
+{
+    pdl_enter();
+    dact_block<T>(blockIdx.x, dy, dy32, ldy, z, ldz, fn, scale, dz, lddz, Trows, N, part, vec, rpb);
+}
+
 // 32 columns a CTA, 8 lanes that share the parts.
 template <typename T>
-__global__ void __launch_bounds__(256) sum_parts(const float *part, int nparts, int N, void *out, int out32, int accumulate)
+__device__ __forceinline__ void sum_block(unsigned block, const float *part, int nparts, int N, void *out, int out32, int accumulate)
 {
     __shared__ float red[8][32];
-    pdl_enter();
-    const int l = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
+    const int l = threadIdx.x & 31, k = threadIdx.x >> 5, c = block * 32 + l;
     float s = 0.f;
     if (c < N) {
 #pragma unroll 4
@@ -157,6 +195,44 @@ __global__ void __launch_bounds__(256) sum_parts(const float *part, int nparts, 
         uint16_t *o = static_cast<uint16_t *>(out);
         o[c] = C16<T>::round(accumulate ? C16<T>::one(o[c]) + s : s);
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts(const float *part, int nparts, int N, void *out, int out32, int accumulate)
+{
+    pdl_enter();
+    sum_block<T>(blockIdx.x, part, nparts, N, out, out32, accumulate);
+}
+
+// The column sums of up to three 16-bit matrices of T rows in two launches.
+struct SumSet {
+    struct One {
+        const uint16_t *src;
+        void *out;
+        float *part;
+        int64_t ld;
+        int N, rpb, nparts, vec;
+        unsigned block0, join0; // its first block of either launch
+    } m[3];
+    int n, T, out32, accumulate;
+};
+
+template <typename T> __global__ void __launch_bounds__(256) col_sums(const __grid_constant__ SumSet s)
+{
+    pdl_enter();
+    int i = 0;
+    while (i + 1 < s.n && blockIdx.x >= s.m[i + 1].block0) ++i;
+    const SumSet::One &m = s.m[i];
+    dact_block<T>(blockIdx.x - m.block0, m.src, 0, m.ld, nullptr, 0, PI_FN_NONE, 1.f, nullptr, 0, s.T, m.N, m.part, m.vec, m.rpb);
+}
+
+template <typename T> __global__ void __launch_bounds__(256) join_sums(const __grid_constant__ SumSet s)
+{
+    pdl_enter();
+    int i = 0;
+    while (i + 1 < s.n && blockIdx.x >= s.m[i + 1].join0) ++i;
+    const SumSet::One &m = s.m[i];
+    sum_block<T>(blockIdx.x - m.join0, m.part, m.nparts, m.N, m.out, s.out32, s.accumulate);
 }
 
 bool aligned16(const void *p, int64_t ld, int elem) { return ((uintptr_t)p & 15) == 0 && (ld * elem) % 16 == 0; }
@@ -233,9 +309,21 @@ Staged stage(Arena &ws, const void *p, int64_t ld, int rows, int cols, int mn)
     return s;
 }
 
-cudaError_t run_copy(const Staged &s, cudaStream_t st)
+// The copies of the operands that need one.
+cudaError_t run_copies(std::initializer_list<const Staged *> list, cudaStream_t st)
 {
-    return s.copy ? launch_pack(s.src, s.lds, const_cast<void *>(s.m.p), s.m.ld, s.rows, s.cols, st) : cudaSuccess;
+    CopySet c = {};
+    uint64_t blocks = 0;
+    for (const Staged *s : list) {
+        if (!s->copy) continue;
+        CopySet::One &m = c.m[c.n++];
+        m = {(const uint16_t *)s->src, const_cast<void *>(s->m.p), s->lds, s->m.ld, s->rows, s->cols, (unsigned)blocks,
+             (int64_t)s->rows * s->cols > (4 << 20), ((uintptr_t)s->src & 7) == 0 && s->lds % 4 == 0};
+        const int64_t r = m.large ? 16 : 4;
+        blocks += (uint64_t)((m.rows + r - 1) / r) * (m.by8 ? (m.cols / 4 + 256) / 256 : ((m.cols + 1) / 2 + 247) / 248);
+    }
+    if (!c.n) return cudaSuccess;
+    return launch_pdl(pack_set, dim3((unsigned)blocks), dim3(256), 0, st, c);
 }
 
 unsigned vbit(const void *p, int64_t ld, int elem, unsigned bit) { return p && aligned16(p, ld, elem) ? bit : 0; }
@@ -512,7 +600,9 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
     }
     if (gr.w_up || gr.w_gate) f.x = stage(ar, x, d.ldx, d.T, d.d, 1);
     if (gr.w_down) f.a = stage(ar, s.a, d.lda, d.T, d.n, 1);
-    f.part = gr.b_up || gr.b_gate || gr.b_down ? ar.take(std::max(colsum_bytes(d.T, d.n), colsum_bytes(d.T, d.d))) : nullptr;
+    const size_t part = (gr.b_gate ? colsum_bytes(d.T, d.n) : 0) + (gr.b_up ? colsum_bytes(d.T, d.n) : 0) +
+                        (gr.b_down ? colsum_bytes(d.T, d.d) : 0);
+    f.part = part ? ar.take(part) : nullptr;
     const int g32 = d.grad_dtype == PI_F32;
     if (want_d) {
         f.da = true;
@@ -565,24 +655,6 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
 
 } // namespace
 
-template <int R>
-static cudaError_t pack(const uint16_t *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
-{
-    const int64_t groups = (rows + R - 1) / R;
-    if (((uintptr_t)src & 7) == 0 && lds % 4 == 0)
-        return launch_pdl(pack_rows8<R>, dim3((unsigned)(groups * ((cols / 4 + 256) / 256))), dim3(256), 0, s, src, lds, (uint2 *)dst, ldd,
-                          rows, cols);
-    return launch_pdl(pack_rows<R>, dim3((unsigned)(groups * (((cols + 1) / 2 + 247) / 248))), dim3(256), 0, s, src, lds,
-                      (uint32_t *)dst, ldd, rows, cols);
-}
-
-cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s)
-{
-    if (!rows || !cols) return cudaSuccess;
-    return (int64_t)rows * cols > (4 << 20) ? pack<16>((const uint16_t *)src, lds, dst, ldd, rows, cols, s)
-                                            : pack<4>((const uint16_t *)src, lds, dst, ldd, rows, cols, s);
-}
-
 size_t colsum_bytes(int T, int N)
 {
     const int rpb = sum_rows(T, N);
@@ -599,11 +671,29 @@ cudaError_t launch_dact(const void *dy, int dy32, int64_t ldy, const void *z, in
                                  s);
 }
 
-cudaError_t launch_colsum(const void *src, int src32, int64_t lds, int T, int N, float scale, void *out, int out32,
-                          int accumulate, bool bf16, void *part, cudaStream_t s)
+// One more matrix whose column sums are wanted (out NULL: not wanted).  part: its partials.
+void add_sum(SumSet &s, const void *src, int64_t ld, int N, void *out, void *&part)
 {
-    return launch_dact(src, src32, lds, nullptr, 0, PI_FN_NONE, scale, nullptr, 0, T, N, out, out32, accumulate, bf16,
-                       part, s);
+    if (!out) return;
+    SumSet::One &m = s.m[s.n];
+    const int rpb = sum_rows(s.T, N), nparts = (s.T + rpb - 1) / rpb;
+    m = {(const uint16_t *)src, out, (float *)part, ld, N, rpb, nparts, aligned16(src, ld, 2) ? 1 : 0, 0, 0};
+    if (s.n) {
+        const SumSet::One &l = s.m[s.n - 1];
+        m.block0 = l.block0 + (unsigned)l.nparts * ((l.N + 255) / 256), m.join0 = l.join0 + (l.N + 31) / 32;
+    }
+    part = (uint8_t *)part + colsum_bytes(s.T, N);
+    ++s.n;
+}
+
+cudaError_t launch_sums(const SumSet &s, bool bf16, cudaStream_t st)
+{
+    if (!s.n) return cudaSuccess;
+    const SumSet::One &l = s.m[s.n - 1];
+    const dim3 blocks(l.block0 + (unsigned)l.nparts * ((l.N + 255) / 256)), joins(l.join0 + (l.N + 31) / 32);
+    cudaError_t e = bf16 ? launch_pdl(col_sums<__nv_bfloat16>, blocks, dim3(256), 0, st, s) : launch_pdl(col_sums<__half>, blocks, dim3(256), 0, st, s);
+    if (e != cudaSuccess) return e;
+    return bf16 ? launch_pdl(join_sums<__nv_bfloat16>, joins, dim3(256), 0, st, s) : launch_pdl(join_sums<__half>, joins, dim3(256), 0, st, s);
 }
 
 } // namespace pi
@@ -646,8 +736,7 @@ pi_status pi_linear(pi_ctx *c, const pi_linear_desc *desc, const void *x, const 
     const LinearFwd f = plan_linear(d, v, x, w, b, residual, z, y, ws);
     if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes)) return st;
     DeviceGuard g(v.device);
-    CUB(run_copy(f.x, v.stream));
-    CUB(run_copy(f.w, v.stream));
+    CUB(run_copies({&f.x, &f.w}, v.stream));
     CUB(launch_gemm(f.p.g[0], d.dtype == PI_BF16, v, f.gws));
     return PI_OK;
 }
@@ -677,15 +766,16 @@ pi_status pi_linear_bwd(pi_ctx *c, const pi_linear_desc *desc, const void *dy, c
     if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes)) return st;
     DeviceGuard g(v.device);
     const int dy32 = d.out_dtype == PI_F32;
+    CUB(run_copies({&f.dz, &f.x, &f.w}, v.stream));
     if (!f.direct) {
         CUB(launch_dact(dy, dy32, d.ldy, z, d.ldz, d.fn, d.scale, f.dzbuf, f.lddz, d.T, d.N, db, g32, accumulate, bf,
                         f.part, v.stream));
     } else {
-        CUB(run_copy(f.dz, v.stream));
-        if (db) CUB(launch_colsum(dy, 0, d.ldy, d.T, d.N, 1.f, db, g32, accumulate, bf, f.part, v.stream));
+        SumSet sums = {{}, 0, d.T, g32, accumulate};
+        void *part = f.part;
+        add_sum(sums, dy, d.ldy, d.N, db, part);
+        CUB(launch_sums(sums, bf, v.stream));
     }
-    if (dw) CUB(run_copy(f.x, v.stream));
-    if (dx) CUB(run_copy(f.w, v.stream));
     if (f.p.n) CUB(launch_gemms(f.p.g, f.p.n, bf, v, f.gws));
     return PI_OK;
 }
@@ -730,12 +820,9 @@ pi_status pi_gated_ffn(pi_ctx *c, const pi_gated_ffn_desc *desc, const pi_gated_
     const FfnFwd f = plan_ffn(d, v, *w, x, s, y, ws);
     if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes)) return st;
     DeviceGuard g(v.device);
-    CUB(run_copy(f.x, v.stream));
-    if (d.gated) CUB(run_copy(f.wg, v.stream));
-    CUB(run_copy(f.wu, v.stream));
-    CUB(run_copy(f.wd, v.stream));
+    CUB(run_copies({&f.x, &f.wg, &f.wu, &f.wd}, v.stream));
     CUB(launch_gemm(f.p.g[0], bf, v, f.gws));
-    CUB(run_copy(f.a, v.stream)); // (the caller's a, written by the product above)
+    CUB(run_copies({&f.a}, v.stream)); // (the caller's a, written by the product above)
     CUB(launch_gemm(f.p.g[1], bf, v, f.gws));
     return PI_OK;
 }
@@ -772,13 +859,15 @@ pi_status pi_gated_ffn_bwd(pi_ctx *c, const pi_gated_ffn_desc *desc, const pi_ga
     const FfnBwd f = plan_ffn_bwd(d, v, *w, x, dy, *save, dx, gr, accumulate, ws);
     if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes)) return st;
     DeviceGuard g(v.device);
-    const Staged *copies[] = {&f.dy, &f.wd, &f.wg, &f.wu, &f.x, &f.a};
-    for (const Staged *s : copies) CUB(run_copy(*s, v.stream));
+    CUB(run_copies({&f.dy, &f.wd, &f.wg, &f.wu, &f.x, &f.a}, v.stream));
     if (f.da) CUB(launch_gemm(f.p.g[0], bf, v, f.gws));
     if (f.p.n > f.da) CUB(launch_gemms(f.p.g + f.da, f.p.n - f.da, bf, v, f.gws));
-    if (gr.b_gate) CUB(launch_colsum(f.dg, 0, f.ldd, d.T, d.n, 1.f, gr.b_gate, g32, accumulate, bf, f.part, v.stream));
-    if (gr.b_up) CUB(launch_colsum(f.du, 0, f.ldd, d.T, d.n, 1.f, gr.b_up, g32, accumulate, bf, f.part, v.stream));
-    if (gr.b_down) CUB(launch_colsum(dy, 0, d.ldy, d.T, d.d, 1.f, gr.b_down, g32, accumulate, bf, f.part, v.stream));
+    SumSet sums = {{}, 0, d.T, g32, accumulate};
+    void *part = f.part;
+    add_sum(sums, f.dg, f.ldd, d.n, gr.b_gate, part);
+    add_sum(sums, f.du, f.ldd, d.n, gr.b_up, part);
+    add_sum(sums, dy, d.ldy, d.d, gr.b_down, part);
+    CUB(launch_sums(sums, bf, v.stream));
     return PI_OK;
 }
 

@@ -75,14 +75,8 @@ bool skinny_takes(const Gemm &g);
 size_t skinny_workspace(const Gemm &g, const CtxView &v);
 cudaError_t launch_skinny(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
-// dst [rows][cols] (row stride ldd) = src (row stride lds), 16-bit elements
-cudaError_t launch_pack(const void *src, int64_t lds, void *dst, int64_t ldd, int rows, int cols, cudaStream_t s);
-
-// out [N] (fp32 or 16-bit; += when accumulate) = column sums of src [T][N]
-// (16-bit, or fp32 when src32), times scale.  part: colsum_bytes(T, N) bytes.
+// Bytes of the partial column sums of a matrix [T][N].
 size_t colsum_bytes(int T, int N);
-cudaError_t launch_colsum(const void *src, int src32, int64_t lds, int T, int N, float scale, void *out, int out32,
-                          int accumulate, bool bf16, void *part, cudaStream_t s);
 
 // dz = scale * dy * fn'(z) [T][N], 16-bit, and its column sums into db (NULL:
 // none; the fp32 values before their rounding are summed)
