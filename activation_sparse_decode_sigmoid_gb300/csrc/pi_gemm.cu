@@ -98,7 +98,6 @@ struct Sched {
 template <int NP> struct TcParams {
     Prob prob[NP];
     Sched s;
-    int wide;             // columns of a tile's accumulator: 256 or 128
     float *part;          // [nsplit][smax][256 / 4 columns][256 rows][4]: a warp's 32 rows write 512 bytes in a row
     int *status, *abort_flag;
     unsigned long long wait_ns;
@@ -381,60 +380,54 @@ __device__ __forceinline__ void box_settle(int lane)
     __syncwarp();
 }
 
-// A warp's 32 x 64 `boxes` values, rounded and nothing else, all inside the
-// output: 64 columns at a time through the warp's 4 KB (128-byte swizzle) and
-// out by a TMA store, the next 32 columns on their way out of tensor memory
-// meanwhile.  (By the warps' own stores, 64 bytes a row, a tile of 256 x 256
-// took 2.7 us.)  `last` runs once the accumulator has been read.
-template <typename T> __device__ __forceinline__ void box_half(uint32_t box, int lane, int h, const uint32_t (&v)[32])
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * j + i]);
-        sts16(box + lane * 128 + (((h * 4 + j) ^ (lane & 7)) << 4), pack8<T>(x));
-    }
-}
-
-template <typename T, typename F>
-__device__ __forceinline__ void plain_strip(uint32_t ta, int boxes, uint32_t box, const CUtensorMap *mo, int lane, int row, int col,
-                                            F last)
+// A warp's 32 x COLS values, rounded and nothing else, all inside the output:
+// 64 columns at a time through the warp's 4 KB (128-byte swizzle) and out by a
+// TMA store, the next 32 columns on their way out of tensor memory meanwhile.
+// (By the warps' own stores, 64 bytes a row, a tile took 2.7 us.)  `last` runs
+// once the accumulator has been read.
+template <typename T, int COLS, typename F>
+__device__ __forceinline__ void plain_strip(uint32_t ta, uint32_t box, const CUtensorMap *mo, int lane, int row, int col, F last)
 {
     uint32_t r[2][32];
     tmem_ld32_async(ta, r[0]);
     box_settle(lane);
     tmem_wait32(r[0]);
-#pragma unroll 1
-    for (int b = 1; b <= boxes; ++b, ta += 64, col += 64) {
-        tmem_ld32_async(ta + 32, r[1]);
-        if (b > 1) box_settle(lane);
-        box_half<T>(box, lane, 0, r[0]);
-        tmem_wait32(r[1]);
-        if (b < boxes) tmem_ld32_async(ta + 64, r[0]);
+#pragma unroll
+    for (int c = 0; c < COLS / 32; ++c) {
+        uint32_t(&v)[32] = r[c & 1];
+        if (c < COLS / 32 - 1) tmem_ld32_async(ta + 32 * (c + 1), r[(c + 1) & 1]);
         else last();
-        box_half<T>(box, lane, 1, r[1]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(mo), "r"(box),
-                         "r"(col), "r"(row)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        if (c && !(c & 1)) box_settle(lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[8 * j + i]);
+            sts16(box + lane * 128 + ((((c & 1) * 4 + j) ^ (lane & 7)) << 4), pack8<T>(x));
         }
-        if (b < boxes) tmem_wait32(r[0]);
+        if (c & 1) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(mo), "r"(box),
+                             "r"(col + 64 * (c >> 1)), "r"(row)
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+        }
+        if (c < COLS / 32 - 1) tmem_wait32(r[(c + 1) & 1]);
     }
     __syncwarp();
 }
 
 // ------------------------------------------------------------------ the kernel
-template <typename T, int MODE, int NP>
+// WIDE: columns of a tile's accumulator, 256 or 128.
+template <typename T, int MODE, int NP, int WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gemm_tc(const __grid_constant__ TcParams<NP> p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     using H = H16<T>;
-    const int wide = MODE == EPI_GATED ? kTile : p.wide;
-    const int outn = MODE == EPI_GATED ? 128 : wide; // output columns of a tile
+    constexpr int kOutN = MODE == EPI_GATED ? 128 : WIDE; // output columns of a tile
     constexpr bool kPlain = NP > 1; // a backward pass's products: no bias, activation, scale or z
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
@@ -479,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             int mi, ni;
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
             const int m0 = mi * kTile + (int)rank * 128;
-            const int n0 = ni * outn + (MODE == EPI_GATED ? 0 : (int)rank * (wide / 2));
+            const int n0 = ni * kOutN + (MODE == EPI_GATED ? 0 : (int)rank * (WIDE / 2));
             for (int seg = 0; seg < 2 && ok; ++seg) {
                 const int lo = seg ? pr.kt0 : 0, ka = max(w.k0, lo), kb = min(w.k1, seg ? pr.KT : pr.kt0);
                 const CUtensorMap *ma = &pr.ma[seg], *mb = &pr.mb[MODE == EPI_GATED ? (int)rank : seg];
@@ -491,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                     if (elect_one()) {
                         const uint32_t bar = full0 + cur.s * 8, sa = base + cur.s * kStageBytes, sb = sa + kOpBytes;
                         const int kc = (k - lo) * kBK;
-                        if (rank == 0) mbar_expect(full + cur.s, 2 * kOpBytes + (uint32_t)wide * (kBK * 2));
+                        if (rank == 0) mbar_expect(full + cur.s, 2 * kOpBytes + WIDE * kBK * 2);
                         if (pr.a_mn) {
                             pair_load(sa, ma, m0, kc, bar);
                             pair_load(sa + kAtom, ma, m0 + 64, kc, bar);
@@ -499,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                             pair_load(sa, ma, kc, m0, bar);
                         if (pr.b_mn) {
                             pair_load(sb, mb, n0, kc, bar);
-                            if (wide == kTile) pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
+                            if (WIDE == kTile) pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
                         } else
                             pair_load(sb, mb, kc, n0, bar);
                     }
@@ -519,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             Cur cur(0, kStages);
             for (uint32_t it = 0; ok && walk.next(w); ++it) {
                 const Prob &pr = p.prob[NP == 1 ? 0 : w.prob];
-                const uint32_t id = idesc(H::fmt, (uint32_t)pr.a_mn, (uint32_t)pr.b_mn, 256, (uint32_t)wide);
+                const uint32_t id = idesc(H::fmt, (uint32_t)pr.a_mn, (uint32_t)pr.b_mn, 256, WIDE);
                 // descriptors of stage 0; a byte offset o adds o / 16 (the start address field)
                 const uint64_t da = pr.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
                 const uint64_t db = pr.b_mn ? sdesc(base + kOpBytes, kAtom, 1024) : sdesc(base + kOpBytes, 16, 1024);
@@ -556,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
         const int q = warp & 3, half = warp >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t box0 = base + kStages * kStageBytes + (uint32_t)warp * 2 * kBox, box1 = box0 + kBox;
-        const int cols = outn / 2; // of this warp
+        constexpr int kCols = kOutN / 2; // of this warp
         const uint32_t bias = base + kStages * kStageBytes + kBoxes + (uint32_t)warp * kBiasB;
         for (uint32_t it = 0; ok && walk.next(w); ++it) {
             const Prob &pr = p.prob[NP == 1 ? 0 : w.prob];
@@ -575,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
             int mi, ni;
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
-            const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * outn + half * cols;
+            const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * kOutN + half * kCols;
             const bool whole = w.slot < 0;
             uint4 q1[4], q2[4]; // the next chunk's inputs
             if (whole && has_in) { // in flight while the products finish
@@ -604,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                 const int r = (int)rank * 128 + q * 32 + lane; // row within the tile
                 float4 *dst = reinterpret_cast<float4 *>(p.part) + (size_t)w.slot * (kTile * kTile / 4) + r;
 #pragma unroll 1
-                for (int c = half * (wide / 2); c < (half + 1) * (wide / 2); c += 32) {
+                for (int c = half * (WIDE / 2); c < (half + 1) * (WIDE / 2); c += 32) {
                     float v[32];
                     tmem_ld32(ta + c, v);
                     if (row0 + lane < M) {
@@ -613,8 +606,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
                             dst[(c + i) / 4 * kTile] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                 }
-            } else if (simple && row0 + 32 <= M && col0 + cols <= N) {
-                plain_strip<T>(ta + half * cols, cols / 64, box0, &pr.mo, lane, row0, col0, [&]() {
+            } else if (simple && row0 + 32 <= M && col0 + kCols <= N) {
+                plain_strip<T, kCols>(ta + half * kCols, box0, &pr.mo, lane, row0, col0, [&]() {
                     tc_before();
                     __syncwarp();
                     if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
@@ -623,14 +616,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1) gem
             } else if (row0 < M) {
                 if (MODE == EPI_LINEAR) box_settle(lane);
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 32) {
+                for (int c = 0; c < kCols; c += 32) {
                     const int col = col0 + c;
                     if (col >= N) break;
                     const bool inside = row0 + 32 <= M && col + 32 <= N;
                     float v[32], u[MODE == EPI_GATED ? 32 : 1];
-                    tmem_ld32(ta + half * cols + c, v);
-                    if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * cols + c, *reinterpret_cast<float(*)[32]>(u));
-                    if (c + 32 >= cols || col + 32 >= N) {
+                    tmem_ld32(ta + half * kCols + c, v);
+                    if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
+                    if (c + 32 >= kCols || col + 32 >= N) {
                         // the accumulator is in registers: the next tile's products may begin
                         tc_before();
                         __syncwarp();
@@ -755,12 +748,13 @@ __device__ __forceinline__ void load4x2(const float4 *a, const float4 *b, float 
 // The split tiles: partials added in the order of k, then the epilogue.
 // 256 threads take 8 columns each of 8 (gated: 16) rows; a warp's 8 rows x 32
 // columns are 128 bytes in a row of the partials, 64 of the output.
-template <typename T, int MODE, int NP> __global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcParams<NP> p)
+template <typename T, int MODE, int NP>
+__global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcParams<NP> p, int wide)
 {
     pdl_enter();
     const Prob &pr = p.prob[NP == 1 ? 0 : p.s.sprob];
     constexpr int kOutN = MODE == EPI_GATED ? 128 : kTile, kCols = kOutN / 8, kRows = 256 / kCols;
-    const int outn = MODE == EPI_GATED ? 128 : p.wide;
+    const int outn = MODE == EPI_GATED ? 128 : wide;
     const int per = kTile / kRows, r = (int)blockIdx.x / per;
     constexpr int kWarps = kOutN / 32; // that share 8 rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -892,11 +886,10 @@ cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K, int box)
                 : encode_map(m, a.p, (uint64_t)K, (uint64_t)rows, (uint64_t)a.ld * 2, box);
 }
 
-template <typename T, int MODE, int NP> cudaError_t run(const Gemm *g, int n, const CtxView &v, void *ws)
+template <typename T, int MODE, int NP, int WIDE> cudaError_t run_plan(const Gemm *g, int n, const Plan &q, const CtxView &v, void *ws)
 {
-    const Plan q = plan_group(g, n, v.sms);
     TcParams<NP> p = {};
-    p.s = q.s, p.wide = q.wide;
+    p.s = q.s;
     cudaError_t e = cudaSuccess;
     for (int j = 0; j < n; ++j) {
         const Gemm &x = g[q.order[j]];
@@ -908,14 +901,14 @@ template <typename T, int MODE, int NP> cudaError_t run(const Gemm *g, int n, co
         const int nb = MODE == EPI_GATED ? 2 : x.segs;
         if (MODE == EPI_LINEAR && !x.e.out32 && (x.e.vec & V_OUT) && e == cudaSuccess)
             e = encode_map(&pr.mo, x.e.out, (uint64_t)x.N, (uint64_t)x.M, (uint64_t)x.e.ldo * 2, 32);
-        for (int i = 0; i < nb && e == cudaSuccess; ++i) e = map_of(&pr.mb[i], x.b[i], x.N, x.K[MODE == EPI_GATED ? 0 : i], MODE == EPI_GATED ? 128 : q.wide / 2);
+        for (int i = 0; i < nb && e == cudaSuccess; ++i) e = map_of(&pr.mb[i], x.b[i], x.N, x.K[MODE == EPI_GATED ? 0 : i], MODE == EPI_GATED ? 128 : WIDE / 2);
     }
     if (e != cudaSuccess) return e;
     p.part = static_cast<float *>(ws);
     p.status = v.status, p.abort_flag = v.abort_flag, p.wait_ns = v.wait_ns;
 
     constexpr int smem = kStages * kStageBytes + kBoxes + kEpiWarps * kBiasB + (2 * kStages + 4) * 8 + 16;
-    auto kern = gemm_tc<T, MODE, NP>;
+    auto kern = gemm_tc<T, MODE, NP, WIDE>;
     static std::atomic<uint64_t> ready{0}; // devices whose limit has been raised
     int dev = 0;
     e = cudaGetDevice(&dev);
@@ -926,7 +919,15 @@ template <typename T, int MODE, int NP> cudaError_t run(const Gemm *g, int n, co
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(2 * q.launched), dim3(kGemmThreads), smem, v.stream, p);
     if (e != cudaSuccess || !p.s.nsplit) return e;
     constexpr int kCols = (MODE == EPI_GATED ? 128 : kTile) / 8;
-    return launch_pdl(gemm_fixup<T, MODE, NP>, dim3(p.s.nsplit * kTile / (256 / kCols)), dim3(256), 0, v.stream, p);
+    return launch_pdl(gemm_fixup<T, MODE, NP>, dim3(p.s.nsplit * kTile / (256 / kCols)), dim3(256), 0, v.stream, p, WIDE);
+}
+
+template <typename T, int MODE, int NP> cudaError_t run(const Gemm *g, int n, const CtxView &v, void *ws)
+{
+    const Plan q = plan_group(g, n, v.sms);
+    if constexpr (MODE != EPI_GATED)
+        if (q.wide != kTile) return run_plan<T, MODE, NP, 128>(g, n, q, v, ws);
+    return run_plan<T, MODE, NP, kTile>(g, n, q, v, ws);
 }
 
 template <typename T> cudaError_t run_mode(const Gemm *g, int n, const CtxView &v, void *ws)
