@@ -174,6 +174,17 @@ def _stream_ptr(device) -> int:
     return _raw_stream(device.index)
 
 
+_torch = None
+
+
+def _import_torch():
+    """The module, imported on first use (an import statement in a call's path costs 0.3 us)."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 _CODES: dict = {}
 
 
@@ -643,14 +654,13 @@ class Context:
         return got
 
     def _new(self, shape, dtype):
-        import torch
-        return torch.empty(shape, dtype=dtype, device=self.torch_device)
+        return (_torch or _import_torch()).empty(shape, dtype=dtype, device=self.torch_device)
 
     def _ws(self, n: int):
         """Workspace of n bytes and its address."""
         if not n:
             return None, 0
-        import torch
+        torch = _torch or _import_torch()
         t = torch.empty(n, dtype=torch.uint8, device=self.torch_device)
         return t, t.data_ptr()
 
@@ -734,7 +744,7 @@ class Context:
     def gated_ffn_save(self, x, w_gate, w_up):
         """Buffers (g, u, a) for ``gated_ffn`` to leave for its backward pass,
         [T][n] with rows that start on 16-byte boundaries (g None if not gated)."""
-        import torch
+        torch = _torch or _import_torch()
         T, n = x.shape[0], w_up.shape[0]
         new = lambda: torch.empty_strided((T, n), ((n + 7) // 8 * 8, 1), dtype=x.dtype, device=x.device)
         return (new() if w_gate is not None else None), new(), new()
