@@ -813,12 +813,16 @@ Plan plan_group(const Gemm *g, int n, int sms)
     // of loads, which bound it, and half of the epilogue).  512 x 4096 x 4096:
     // 20 us, 256 wide 24; 300 rows, K 1024, N 4096: 9.1, 10.9.  A long k is
     // better split (129 x 28672 x 8192: 256 wide and split 89 us, 128 wide 108).
+    // Outputs of up to 128 columns fill no wider tile.
     int64_t tiles = 0, steps = 0, longest = 0;
+    bool thin = true;
     for (int i = 0; i < n; ++i) {
+        thin = thin && g[i].N <= 128;
         const int64_t t = (int64_t)((g[i].M + kTile - 1) / kTile) * ((g[i].N + kTile - 1) / kTile);
         tiles += t, steps += t * KT[i], longest = std::max<int64_t>(longest, KT[i]);
     }
-    q.wide = g[0].mode != EPI_GATED && tiles <= P / 2 && 2 * longest < 3 * (steps / P + kFixupSteps) ? 128 : kTile;
+    const bool idle = tiles <= P / 2 && 2 * longest < 3 * (steps / P + kFixupSteps);
+    q.wide = g[0].mode != EPI_GATED && (thin || idle) ? 128 : kTile;
     const int fixup = q.wide == kTile ? kFixupSteps : 2 * kFixupSteps;
     Sched &s = q.s;
     s.pairs = P;

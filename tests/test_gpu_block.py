@@ -132,6 +132,24 @@ def test_linear_bwd_of_many_tiles(c, T, K, N):
                 R.check(v, want[k], k + " alone")
 
 
+# fewer tiles than half of the CTA pairs: narrower ones; thin outputs, whose
+# tiles are narrow and split; few tiles of a long k, wide and split
+@pytest.mark.parametrize("T,K,N", [(300, 640, 1000), (140, 2056, 300), (9728, 9600, 100), (30000, 136, 128), (200, 12296, 520)])
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_linear_and_backward_of_few_or_thin_tiles(c, T, K, N, dt):
+    m = Maker(9)
+    x, w, b, r = m(T, K, dt=dt), m(N, K, dt=dt, std=K ** -0.5), m(N, dt=dt), m(T, N, dt=dt)
+    z, dy = m(T, N, dt=dt), m(T, N, dt=dt)
+    R.check(c.linear(x, w), R.linear(x, w, None, "none", 1.0, None, dt)["y"], "plain")
+    R.check(c.linear(x, w, b, fn=pi.PI_FN_SILU, residual=r), R.linear(x, w, b, "silu", 1.0, r, dt)["y"], "y")
+    want = R.linear_bwd(dy, x, w, z, "relu", 1.0, dt)
+    for need in ((True, True, True), (True, False, False), (False, True, False)):
+        got = c.linear_bwd(dy, x, w, z, fn=pi.PI_FN_RELU, need=need)
+        for k, v in zip(("dx", "dw", "db"), got):
+            if v is not None:
+                R.check(v, want[k], k)
+
+
 @pytest.mark.parametrize("fn", R.FNS)
 def test_linear_activations_at_their_ends(c, fn):
     """Pre-activations from 0 over the type's range, infinities and NaN:
