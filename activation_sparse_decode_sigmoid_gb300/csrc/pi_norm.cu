@@ -10,7 +10,8 @@
 //     P1 = sum dh xh, P0 = sum dh  over tokens: dw_pre, db_pre
 //     S1 = sum D yh, S0 = sum D    over the tokens of one gate row:
 //         dgate = bs (w_post S1 + b_post S0),  dw_post += bs gate S1,  db_post += bs gate S0
-// All of it is bound by HBM: a few operations per 16-bit or fp32 element.
+// The forward pass is bound by HBM (a few operations per element), the
+// backward pass, about 50 instructions per element of six arrays, by their issue.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -811,10 +812,11 @@ enum { ST_SX, ST_SY, ST_MX, ST_SQX, ST_MY, ST_SQ, ST_N = 9 }; // (9: no bank con
 // tensor memory, where each thread adds to its own columns' values: in
 // registers they took half of what 512 threads have (8000 x 8192 layer norms:
 // 345 us with 512 threads and spills, 271 us with 256 threads of 32 columns).
-// Bound by instruction issue, so what one gate row's tokens share, bs gate
-// w_post, is multiplied once, and each element's value is kept in the form
-// that its next use wants (209 -> 196 us), and sums share shuffles (178 us).  (The next row's statistics computed ahead
-// of the same barrier took 235 instead of 196 us, the registers being full.)
+// Bound by instruction issue: what one gate row's tokens share, bs gate
+// w_post, is multiplied once, each element's value is kept in the form that its
+// next use wants (209 -> 196 us), and sums share shuffles (178 us; 172 with the
+// join below; 4.6 TB/s).  (The next row's statistics computed ahead of the same
+// barrier took 235 instead of 196 us, the registers being full.)
 // RG: a gate row per token, in the ring.
 template <typename T, bool X32, int V, bool FULL, bool RG>
 __global__ void __launch_bounds__(kPipeThreads, 1) norm_bwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)

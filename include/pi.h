@@ -407,8 +407,8 @@ pi_status pi_layerwise_min_batch(pi_ctx *ctx, int32_t layer, int32_t *min_batch)
  *     *_workspace function gives for the same desc, 16-byte aligned (NULL if
  *     0 bytes).  With `unaligned` set in the desc those bytes have room for
  *     copies of every operand, else only of those whose stride is not a
- *     multiple of 16 bytes.  It holds nothing between calls; calls that may run at the
- *     same time (two streams, two captured graphs) need their own.
+ *     multiple of 16 bytes.  It holds nothing between calls; calls that may
+ *     run at the same time (two streams, two captured graphs) need their own.
  *   - The calls launch kernels on the context's stream only and can be
  *     captured into a CUDA graph.
  *   - Products are accumulated in fp32; bias, activation, residual and
