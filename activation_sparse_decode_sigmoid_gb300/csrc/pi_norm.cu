@@ -104,7 +104,8 @@ __device__ __forceinline__ float2 cta_sum2(float a, float b, float *buf, int &fl
 }
 
 // mean and 1 / sqrt(variance or mean square + eps) of a row held in V chunks
-// of 8 per thread (two passes over the registers for a layer norm)
+// of 8 per thread (two passes over the registers for a layer norm).  Elements
+// behind the row count nowhere: a norm without weight and gate leaves -mean r there.
 template <int V>
 __device__ __forceinline__ void row_stats(int kind, const float (&v)[V][8], int d, float eps, float *buf, int &flip,
                                           float &mean, float &r)
@@ -113,9 +114,11 @@ __device__ __forceinline__ void row_stats(int kind, const float (&v)[V][8], int 
     if (kind == PI_NORM_LAYER) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            const int c = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += v[i][j];
+            for (int j = 0; j < 8; ++j) s += c + j < d ? v[i][j] : 0.f;
+        }
         mean = cta_sum2(s, 0.f, buf, flip).x / (float)d;
     }
     float q = 0.f;
@@ -194,7 +197,6 @@ template <typename T, int V> __global__ void __launch_bounds__(1024) norm_fwd(co
         if (p.xo) storex8<T>(p.xo, p.x32, t * p.ldxo + c, n, p.vec & NV_XO, x[i]);
     }
     if (!p.h) return;
-    // (chunks past the row hold zeros; a layer norm's statistics skip them)
     row_stats<V>(p.pre, x, p.d, p.eps, buf, flip, mean, r);
     apply_norm<T, V>(p, x, p.w_pre, p.b_pre, mean, r);
 #pragma unroll

@@ -420,6 +420,33 @@ def test_norm_without_a_block_and_without_parameters(c, T, d):
                                   BF16)["dx"], "dx")
 
 
+@pytest.mark.parametrize("T,d", [(5, 1), (9, 33), (9, 65), (7, 1001), (3, 8200), (400, 33), (400, 1000), (310, 4104)])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+@pytest.mark.parametrize("given", ["", "w", "b"])
+def test_norm_around_a_block_without_gate_and_without_parameters(c, T, d, pre, post, given):
+    """Weights, biases and gate that are not there stand for 1, 0 and 1; y
+    has a mean, so that what a layer norm takes away shows wherever it stays."""
+    m = Maker(T + d)
+    x, y = m(T, d, dt=F32, std=2.0), m(T, d, dt=BF16) + 3
+    par = lambda kind, which: m(d, dt=BF16) if kind != "none" and given == which else None
+    wp, wq, bp, bq = par(pre, "w"), par(post, "w"), par(pre, "b"), par(post, "b")
+    kw = dict(pre=KIND[pre], post=KIND[post], w_pre=wp, b_pre=bp, w_post=wq, b_post=bq, eps=1e-3)
+    want = R.norm_fwd(x, y, None, 0, pre, post, wp, bp, wq, bq, 1.0, 1.0, 1e-3, BF16)
+    xo, h = c.norm_residual(x, y, **kw)
+    R.check(xo, want["x"], "x")
+    if h is not None:
+        R.check(h, want["h"], "h")
+    dxo, dh = m(T, d, dt=F32), (m(T, d, dt=BF16) if pre != "none" else None)
+    want = R.norm_bwd(dxo, dh, xo, y, None, 0, pre, post, wp, wq, bq, 1.0, 1.0, 1e-3, BF16, BF16)
+    got = c.norm_residual_bwd(dxo, dh, xo, y, **kw)
+    assert set(k for k in got if got[k] is not None) == \
+        {"dx", "dy"} | {k for k, v in dict(w_pre=wp, b_pre=bp, w_post=wq, b_post=bq).items() if v is not None}
+    for k in want:
+        if got[k] is not None:
+            R.check(got[k], want[k], k)
+
+
 @pytest.mark.parametrize("off,pad", [(1, 2), (8, 8)])
 def test_norm_of_slices(c, off, pad):
     """Rows that start anywhere in wider ones, and outputs that leave the rest alone."""
