@@ -3,6 +3,9 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
 
 #include "pi.h"
 
@@ -32,6 +35,23 @@ struct CtxView {
     int *abort_flag;
     unsigned long long wait_ns;
 };
+
+// Raises a kernel's limit of dynamic shared memory on the current device to all
+// that its static arrays leave, once per device (`ready`: the kernel's own,
+// devices by bit).  The limit belongs to the function, not to a launch: lowered
+// to one call's size, it could make a launch of another thread's context fail.
+inline cudaError_t raise_limit(const void *kern, std::atomic<uint64_t> &ready)
+{
+    int dev = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kern);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)a.sharedSizeBytes);
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
+    return e;
+}
 
 CtxView ctx_view(pi_ctx *c);
 pi_status ctx_fail(pi_ctx *c, pi_status code, const char *fmt, ...);

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "pi.h"
@@ -1219,10 +1220,11 @@ bool plan_pipe(const NormP &p, bool backward, bool row_gate, const CtxView &c, P
     return true;
 }
 
-template <typename K> cudaError_t run_pipe(K kern, const NormP &p, const Pipe &o, cudaStream_t s)
+template <auto KERN> cudaError_t run_pipe(const NormP &p, const Pipe &o, cudaStream_t s)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, o.smem);
-    return e != cudaSuccess ? e : launch_pdl(kern, dim3(o.grid), dim3(o.threads), o.smem, s, p, o.q);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = raise_limit((const void *)KERN, ready);
+    return e != cudaSuccess ? e : launch_pdl(KERN, dim3(o.grid), dim3(o.threads), o.smem, s, p, o.q);
 }
 
 // Tokens from which the pipelined forward kernel runs: below two per SM
@@ -1236,10 +1238,10 @@ template <typename T> cudaError_t fwd(const NormP &p, const CtxView &c)
     const bool row_gate = p.gate && p.gate_rows == 1;
     if (p.Tn >= kPipeRows * c.sms && plan_pipe(p, false, row_gate, c, o)) {
         if (p.x32)
-            return o.v == 1 ? run_pipe(norm_fwd_pipe<T, true, 1>, p, o, c.stream)
-                            : run_pipe(norm_fwd_pipe<T, true, 2>, p, o, c.stream);
-        return o.v == 1 ? run_pipe(norm_fwd_pipe<T, false, 1>, p, o, c.stream)
-                        : run_pipe(norm_fwd_pipe<T, false, 2>, p, o, c.stream);
+            return o.v == 1 ? run_pipe<norm_fwd_pipe<T, true, 1>>(p, o, c.stream)
+                            : run_pipe<norm_fwd_pipe<T, true, 2>>(p, o, c.stream);
+        return o.v == 1 ? run_pipe<norm_fwd_pipe<T, false, 1>>(p, o, c.stream)
+                        : run_pipe<norm_fwd_pipe<T, false, 2>>(p, o, c.stream);
     }
     return p.d <= 8192 ? launch_fwd<T, 1>(p, c.stream) : launch_fwd<T, 2>(p, c.stream);
 }
@@ -1247,10 +1249,10 @@ template <typename T> cudaError_t fwd(const NormP &p, const CtxView &c)
 template <typename T, bool X32, bool FULL> cudaError_t bwd_pipe(const NormP &p, const Pipe &o, cudaStream_t s)
 {
     if (o.q.off_gate >= 0)
-        return o.v == 1 ? run_pipe(norm_bwd_pipe<T, X32, 1, FULL, true>, p, o, s)
-                        : run_pipe(norm_bwd_pipe<T, X32, 2, FULL, true>, p, o, s);
-    return o.v == 1 ? run_pipe(norm_bwd_pipe<T, X32, 1, FULL, false>, p, o, s)
-                    : run_pipe(norm_bwd_pipe<T, X32, 2, FULL, false>, p, o, s);
+        return o.v == 1 ? run_pipe<norm_bwd_pipe<T, X32, 1, FULL, true>>(p, o, s)
+                        : run_pipe<norm_bwd_pipe<T, X32, 2, FULL, true>>(p, o, s);
+    return o.v == 1 ? run_pipe<norm_bwd_pipe<T, X32, 1, FULL, false>>(p, o, s)
+                    : run_pipe<norm_bwd_pipe<T, X32, 2, FULL, false>>(p, o, s);
 }
 
 template <typename T> cudaError_t bwd(const NormP &p, bool cols, const CtxView &c)

@@ -207,19 +207,6 @@ template <typename T, int MODE> __global__ void __launch_bounds__(128) skinny_jo
     epilogue8<T, MODE>(p.e, p.N, t, f, v[0], v[1]);
 }
 
-// the device's shared-memory limit for a kernel, raised once per device
-template <typename K> cudaError_t raise_limit(K kern, std::atomic<uint64_t> &ready)
-{
-    int dev = 0, most = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1))) {
-        e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
-    }
-    return e;
-}
-
 // ------------------------------------------------------------------ one token, or few and a smaller matrix
 // A group of `wpr` warps of a CTA computes R features (gated: their g and u)
 // for all tokens: lanes take chunks of 8 elements of the rows, 4 loads or
@@ -369,7 +356,7 @@ template <typename T, int MODE> cudaError_t run(const SkParams &p, cudaStream_t 
     auto kern = skinny_tc<T>;
     const int smem = p.slots * (int)p.slotB + (2 * kMaxRing + 4) * 8 + 16;
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = raise_limit(kern, ready);
+    cudaError_t e = raise_limit((const void *)kern, ready);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(p.parts), dim3(kSkThreads), smem, s, p);
     if (e != cudaSuccess) return e;
     const int64_t threads = (int64_t)p.T * p.tn * 16;

@@ -4,6 +4,7 @@ tests/_block.py derives from the arithmetic."""
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -663,6 +664,44 @@ def test_a_wait_that_runs_out_is_reported(T):
         ctx.check()
     finally:
         ctx.close()
+
+
+def test_two_threads_with_a_context_each():
+    """A context belongs to one thread, two contexts of a device need not: calls
+    of one size do not disturb the launches of another (a kernel's
+    shared-memory limit belongs to the function, not to the call).  The C entry
+    point itself is called, so that the threads spend their time in the library."""
+    lib, sizes, T = pi.load_library(), (64, 4096), 400
+    ctxs = [G.ctx() for _ in sizes]
+    failed = []
+    m = Maker(22)
+    bufs = {d: [m(T, d), m(T, d), torch.empty(T, d, dtype=F16, device="cuda"), torch.empty(T, d, dtype=F16, device="cuda")]
+            for d in sizes}
+    torch.cuda.synchronize()
+
+    def work(ctx, d):
+        desc = pi.pi_norm_residual_desc(T, d, 0, 0, 0, pi.PI_NORM_RMS, 0, 0, 1.0, 1.0, 1e-5, *[0] * 5)
+        par = pi.pi_norm_residual_params()
+        x, y, xo, h = (t.data_ptr() for t in bufs[d])
+        call = (ctx.handle, pi._ref(desc), pi._ref(par), x, y, None, xo, h)
+        failed.extend(d for _ in range(5000) if lib.pi_norm_residual(*call))
+
+    try:
+        threads = [threading.Thread(target=work, args=a) for a in zip(ctxs, sizes)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        for ctx in ctxs:
+            ctx.check()
+        assert not failed, (len(failed), pi.pi_last_error(ctxs[1].handle))
+        for x, y, xo, h in bufs.values():
+            want = R.norm_fwd(x, y, None, 0, "rms", "none", None, None, None, None, 1.0, 1.0, 1e-5, F16)
+            R.check(xo, want["x"], "x")
+            R.check(h, want["h"], "h")
+    finally:
+        for ctx in ctxs:
+            ctx.close()
 
 
 def test_same_block_as_the_loaded_layer(c):
