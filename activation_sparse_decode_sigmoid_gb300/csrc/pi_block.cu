@@ -734,6 +734,8 @@ pi_status pi_linear(pi_ctx *c, const pi_linear_desc *desc, const void *x, const 
     if (pi_status st = check_linear(c, desc, d)) return st;
     if (d.T == 0) return PI_OK;
     if (!x || !w || !y) return ctx_fail(c, PI_ERR_ARG, "x, w or y is NULL");
+    if (pi_status st = check_elements(c, 2, {x, w, b, z})) return st;
+    if (pi_status st = check_elements(c, d.out_dtype == PI_F32 ? 4 : 2, {residual, y})) return st;
     const CtxView v = ctx_view(c);
     const LinearFwd f = plan_linear(d, v, x, w, b, residual, z, y, ws);
     if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes)) return st;
@@ -764,6 +766,9 @@ pi_status pi_linear_bwd(pi_ctx *c, const pi_linear_desc *desc, const void *dy, c
     if (!dx && !dw && !db) return PI_OK;
     if (!dy || (dw && !x) || (dx && !w) || (d.fn != PI_FN_NONE && !z))
         return ctx_fail(c, PI_ERR_ARG, "dy, x, w or z is NULL but needed");
+    if (pi_status st = check_elements(c, 2, {x, w, z, dx})) return st;
+    if (pi_status st = check_elements(c, d.out_dtype == PI_F32 ? 4 : 2, {dy})) return st;
+    if (pi_status st = check_elements(c, g32 ? 4 : 2, {dw, db})) return st;
     const LinearBwd f = plan_linear_bwd(d, v, dy, x, w, dx, dw, db, accumulate, ws);
     if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes)) return st;
     DeviceGuard g(v.device);
@@ -817,6 +822,8 @@ pi_status pi_gated_ffn(pi_ctx *c, const pi_gated_ffn_desc *desc, const pi_gated_
     if (!d.gated && s.g) return ctx_fail(c, PI_ERR_ARG, "save->g given, but gated is 0");
     if (d.T == 0) return PI_OK;
     if (!x || !y) return ctx_fail(c, PI_ERR_ARG, "x or y is NULL");
+    if (pi_status st = check_elements(c, 2, {x, w->w_gate, w->w_up, w->w_down, w->b_gate, w->b_up, w->b_down, s.g, s.u, s.a, y}))
+        return st;
     const CtxView v = ctx_view(c);
     const bool bf = d.dtype == PI_BF16;
     const FfnFwd f = plan_ffn(d, v, *w, x, s, y, ws);
@@ -858,6 +865,8 @@ pi_status pi_gated_ffn_bwd(pi_ctx *c, const pi_gated_ffn_desc *desc, const pi_ga
     if (!dy || ((gr.w_up || gr.w_gate) && !x)) return ctx_fail(c, PI_ERR_ARG, "dy or x is NULL but needed");
     if (!save || (want_d && (!save->u || (d.gated && !save->g))) || (gr.w_down && !save->a))
         return ctx_fail(c, PI_ERR_ARG, "save, or what is needed of it, is NULL");
+    if (pi_status st = check_elements(c, 2, {x, dy, w->w_gate, w->w_up, w->w_down, save->g, save->u, save->a, dx})) return st;
+    if (pi_status st = check_elements(c, g32 ? 4 : 2, {gr.w_gate, gr.w_up, gr.w_down, gr.b_gate, gr.b_up, gr.b_down})) return st;
     const FfnBwd f = plan_ffn_bwd(d, v, *w, x, dy, *save, dx, gr, accumulate, ws);
     if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes)) return st;
     DeviceGuard g(v.device);

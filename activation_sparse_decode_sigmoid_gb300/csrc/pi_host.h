@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "pi.h"
 
@@ -55,5 +56,15 @@ inline cudaError_t raise_limit(const void *kern, std::atomic<uint64_t> &ready)
 
 CtxView ctx_view(pi_ctx *c);
 pi_status ctx_fail(pi_ctx *c, pi_status code, const char *fmt, ...);
+
+// Refuses buffers of elements of `elem` bytes that start between two elements:
+// a kernel's access there would fault.
+inline pi_status check_elements(pi_ctx *c, int elem, std::initializer_list<const void *> buffers)
+{
+    for (const void *p : buffers)
+        if ((uintptr_t)p % elem)
+            return ctx_fail(c, PI_ERR_ARG, "address %p is not a multiple of the element's %d bytes", p, elem);
+    return PI_OK;
+}
 
 } // namespace pi

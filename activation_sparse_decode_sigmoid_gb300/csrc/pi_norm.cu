@@ -1383,6 +1383,8 @@ pi_status pi_norm_residual(pi_ctx *c, const pi_norm_residual_desc *desc, const p
     if (!h && !x_out) return PI_OK;
     const CtxView v = ctx_view(c);
     NormP p = params(d, q);
+    if (pi_status st = check_elements(c, p.x32 ? 4 : 2, {x, x_out})) return st;
+    if (pi_status st = check_elements(c, 2, {y, gate, h, p.w_pre, p.b_pre, p.w_post, p.b_post})) return st;
     p.x = x, p.y = (const uint16_t *)y, p.gate = y ? (const uint16_t *)gate : nullptr, p.xo = x_out, p.h = (uint16_t *)h;
     const int xe = p.x32 ? 4 : 2;
     p.vec |= vb(x, p.ldx, xe, NV_X) | vb(x_out, p.ldxo, xe, NV_XO) | vb(y, p.ldy, 2, NV_Y) | vb(h, p.ldh, 2, NV_H) |
@@ -1432,6 +1434,10 @@ pi_status pi_norm_residual_bwd(pi_ctx *c, const pi_norm_residual_desc *desc, con
     if (!y && (gr->dy || gr->dgate || gr->dw_post || gr->db_post)) return ctx_fail(c, PI_ERR_ARG, "y is NULL but needed");
     if (!gate && gr->dgate) return ctx_fail(c, PI_ERR_ARG, "dgate wanted without a gate");
     NormP p = params(d, q);
+    if (pi_status st = check_elements(c, p.x32 ? 4 : 2, {dx_out, x_out, gr->dx})) return st;
+    if (pi_status st = check_elements(c, 2, {dh, y, gate, gr->dy, p.w_pre, p.b_pre, p.w_post, p.b_post})) return st;
+    if (pi_status st = check_elements(c, d.grad_dtype == PI_F32 ? 4 : 2, {gr->dgate, gr->dw_pre, gr->db_pre, gr->dw_post, gr->db_post}))
+        return st;
     p.x = x_out, p.y = (const uint16_t *)y, p.gate = y ? (const uint16_t *)gate : nullptr;
     p.dxo = dx_out, p.dh = (const uint16_t *)dh, p.dx = gr->dx, p.dy = (uint16_t *)gr->dy;
     p.dgate = gr->dgate, p.dw_pre = gr->dw_pre, p.db_pre = gr->db_pre, p.dw_post = gr->dw_post, p.db_post = gr->db_post;

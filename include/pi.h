@@ -397,7 +397,8 @@ pi_status pi_layerwise_min_batch(pi_ctx *ctx, int32_t layer, int32_t *min_batch)
  * Common rules
  *   - All pointers are device pointers; 16-bit data is `dtype` (PI_F16 or
  *     PI_BF16).  Row strides (ld*) count elements; 0 means packed rows.
- *     Rows may start anywhere and have any stride of at least their length;
+ *     Rows may start at any element (an address that is not a multiple of the
+ *     element's size is PI_ERR_ARG) and have any stride of at least their length;
  *     buffers whose base and stride are multiples of 16 bytes are read in
  *     place, others are first copied (by a kernel) into the workspace.
  *   - T counts tokens and may be 0: forward calls then do nothing, backward

@@ -545,6 +545,50 @@ def test_library_refuses_bad_arguments(c):
     c.check()
 
 
+def test_library_refuses_addresses_between_two_elements(c):
+    """Every buffer of every call, moved by one byte (16-bit elements) or by
+    two (fp32): refused before anything is planned or launched."""
+    t = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    lib, h, p = pi.load_library(), c.handle, t.data_ptr()
+
+    def each(fun, args, at):
+        """fun with args, moved in one place at a time; at: {index in args: bytes}"""
+        for i, by in at.items():
+            moved = list(args)
+            moved[i] += by
+            assert fun(*moved) == pi.PI_ERR_ARG, i
+            assert "element" in pi.pi_last_error(h), i
+
+    lin = pi.pi_linear_desc(2, 8, 8, 0, pi.PI_F32, pi.PI_F32, pi.PI_FN_RELU, 1.0, 1, *[0] * 7)
+    each(lambda *a: lib.pi_linear(h, pi._ref(lin), *a, p, 1 << 16), [p] * 6, {0: 1, 1: 1, 2: 1, 3: 2, 4: 1, 5: 2})
+    each(lambda *a: lib.pi_linear_bwd(h, pi._ref(lin), *a, 0, p, 1 << 16), [p] * 7, {0: 2, 1: 1, 2: 1, 3: 1, 4: 1, 5: 2, 6: 2})
+    ffn = pi.pi_gated_ffn_desc(2, 8, 8, 0, pi.PI_F32, pi.PI_FN_RELU, 1, 1, *[0] * 8)
+
+    def ffn_fwd(*a):
+        w, s = pi.pi_gated_ffn_weights(*a[:6]), pi.pi_gated_ffn_save(*a[6:9])
+        return lib.pi_gated_ffn(h, pi._ref(ffn), pi._ref(w), a[9], pi._ref(s), a[10], p, 1 << 16)
+
+    def ffn_bwd(*a):
+        w, s, g = pi.pi_gated_ffn_weights(*a[:3], None, None, None), pi.pi_gated_ffn_save(*a[3:6]), pi.pi_gated_ffn_grads(*a[6:12])
+        return lib.pi_gated_ffn_bwd(h, pi._ref(ffn), pi._ref(w), a[12], a[13], pi._ref(s), a[14], pi._ref(g), 0, p, 1 << 16)
+
+    each(ffn_fwd, [p] * 11, {i: 1 for i in range(11)})
+    each(ffn_bwd, [p] * 15, {i: 2 if 6 <= i < 12 else 1 for i in range(15)})
+    nd = pi.pi_norm_residual_desc(2, 8, pi.PI_F32, 0, pi.PI_F32, 1, 1, 0, 1.0, 1.0, 1e-5, *[0] * 5)
+
+    def norm(*a):
+        par = pi.pi_norm_residual_params(*a[:4])
+        return lib.pi_norm_residual(h, pi._ref(nd), pi._ref(par), *a[4:])
+
+    def norm_bwd(*a):
+        par, g = pi.pi_norm_residual_params(*a[:4]), pi.pi_norm_residual_grads(*a[9:])
+        return lib.pi_norm_residual_bwd(h, pi._ref(nd), pi._ref(par), *a[4:9], pi._ref(g), 0, p, 1 << 16)
+
+    each(norm, [p] * 9, {**{i: 1 for i in range(9)}, 4: 2, 7: 2})
+    each(norm_bwd, [p] * 16, {**{i: 1 for i in range(9)}, 4: 2, 6: 2, 9: 2, 10: 1, **{i: 2 for i in range(11, 16)}})
+    c.check()
+
+
 def block(c, x, y0, gate, wts, w, fn):
     """x' and h after the norm, the FFN of h, and the next norm's outputs."""
     x1, h1 = c.norm_residual(x, y0, gate, w_pre=w)
