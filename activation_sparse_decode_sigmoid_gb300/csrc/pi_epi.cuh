@@ -72,11 +72,13 @@ template <int FN> __device__ __forceinline__ void act_both(float z, float &f, fl
 {
     if (FN == PI_FN_RELU) f = z < 0.f ? 0.f : z, df = z > 0.f ? 1.f : 0.f;
     else if (FN == PI_FN_SQRELU) f = z < 0.f ? 0.f : z * z, df = z < 0.f ? 0.f : 2.f * z;
-    else if (FN == PI_FN_SIGMOID || FN == PI_FN_SILU) {
+    else if (FN == PI_FN_SIGMOID) { // p (1 - p) = e q^2, the same on both sides: 1 - p has nothing left of it above 17
+        const float e = __expf(-fabsf(z)), q = __fdividef(1.f, 1.f + e);
+        f = z < 0.f ? e * q : q, df = e * q * q;
+    } else if (FN == PI_FN_SILU) {
         const float c = clampn(z, 80.f);
         const float p = __fdividef(1.f, 1.f + __expf(-c));
-        if (FN == PI_FN_SIGMOID) f = p, df = p * (1.f - p);
-        else f = z < -80.f ? -0.f : z * p, df = p * (1.f + c * (1.f - p));
+        f = z < -80.f ? -0.f : z * p, df = p * (1.f + c * (1.f - p));
     } else if (FN == PI_FN_GELU) {
         const float c = clampn(z, 30.f);
         float ex;

@@ -172,6 +172,25 @@ def test_linear_activations_at_their_ends(c, fn):
     assert bool((y == (0.0 if fn != "none" else float("-inf"))).all()), y
 
 
+def test_sigmoid_derivative_on_both_sides(c):
+    """p (1 - p) to within its rounding, however near p is to 0 or 1.  The
+    exponential is off by at most 2 + 1.173 |z| steps of 2^-23, 1 / (1 + e) by
+    2.5, and three products round: below (1.2 |z| + 10) 2^-23 of the value."""
+    z = torch.tensor([0.0, 0.5, 4.0, 8.0, 12.0, 16.0, 20.0, 40.0, 80.0], device="cuda")
+    z = torch.cat([z, -z]).to(BF16)[None]
+    n = z.shape[1]
+    dy, x, w = torch.ones(1, n, dtype=BF16, device="cuda"), torch.zeros(1, n, dtype=BF16, device="cuda"), torch.eye(n, device="cuda").to(BF16)
+    db = torch.empty(n, device="cuda")
+    kw = dict(fn=pi.PI_FN_SIGMOID)
+    c.linear_bwd(dy, x, w, z, need=(False, False, True), db=db, **kw)       # dz itself
+    dx = c.linear_bwd(dy, x, w, z, need=(True, False, False), **kw)[0][0]   # dz rounded
+    e = torch.exp(-z[0].double().abs())
+    want = e / (1 + e) ** 2
+    rel = (1.2 * z[0].double().abs() + 10) * 2.0 ** -23
+    R.check(db, (want, rel * want), "dz")
+    R.check(dx, (want, (rel + R.U[BF16]) * want), "dz rounded")
+
+
 @pytest.mark.parametrize("T,K,N,pad,off", LINEAR)
 @pytest.mark.parametrize("dt", [F16, BF16])
 def test_linear_bwd(c, T, K, N, pad, off, dt):
