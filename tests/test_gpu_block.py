@@ -4,6 +4,7 @@ tests/_block.py derives from the arithmetic."""
 from __future__ import annotations
 
 import ctypes
+import math
 import threading
 
 import numpy as np
@@ -189,6 +190,32 @@ def test_sigmoid_derivative_on_both_sides(c):
     rel = (1.2 * z[0].double().abs() + 10) * 2.0 ** -23
     R.check(db, (want, rel * want), "dz")
     R.check(dx, (want, (rel + R.U[BF16]) * want), "dz rounded")
+
+
+@pytest.mark.parametrize("T", [1, 18, 300])
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+def test_gelu_keeps_its_precision_in_the_tail(c, T, dt):
+    """z Phi(z) and its derivative Phi(z) + z phi(z), term by term within
+    (8 + 4 z^2) 2^-23: the exponential's argument z^2 / 2 rounds twice, the
+    exponential is off by 2 + 1.173 z^2 / 2 steps and the factor behind it by
+    1.1 (1 + 0.6 z^2), then two products and a division.  An identity product
+    hands z over exactly."""
+    v = [0.125, 0.5, 1.0, 2.0, 3.0, 3.5, 4.0] + ([] if dt == F16 else [4.5, 5.0, 6.0, 7.5, 9.0, 11.0, 12.5])  # (f16: normal values)
+    v = torch.tensor(v + [-a for a in v], device="cuda")
+    n, t16 = v.numel(), F16 if dt == F16 else BF16
+    x = v.expand(T, n).to(t16)
+    w = torch.eye(n, device="cuda").to(t16)
+    y = c.linear(x.contiguous(), w, fn=pi.PI_FN_GELU, y=torch.empty(T, n, dtype=dt, device="cuda"))
+    z = v.double()
+    phi, Phi = torch.exp(-z * z / 2) / (2 * math.pi) ** 0.5, torch.special.erfc(-z / 2 ** 0.5) / 2
+    rel = (8 + 4 * z * z) * 2.0 ** -23
+    want = z * Phi
+    R.check(y, (want.expand(T, n), ((rel + R.U[dt]) * want.abs()).expand(T, n)), "y")
+    db = torch.empty(n, device="cuda")
+    dy = torch.zeros(T, n, dtype=t16, device="cuda")
+    dy[0] = 1
+    c.linear_bwd(dy, x.contiguous(), w, x.contiguous(), fn=pi.PI_FN_GELU, need=(False, False, True), db=db)
+    R.check(db, (Phi + z * phi, rel * (Phi + z.abs() * phi)), "derivative")
 
 
 @pytest.mark.parametrize("T,K,N,pad,off", LINEAR)
