@@ -48,7 +48,7 @@ struct NormP {
     const uint16_t *w_pre, *b_pre, *w_post, *b_post;
     void *xo;                   // forward: x' (or NULL)
     uint16_t *h;                // or NULL
-    int64_t ldx, ldxo, ldy, ldh, ldgate, lddx; // (ldx: of `x`)
+    int64_t ldx, ldxo, ldy, ldh, ldgate, lddx; // (ldx: of `x`, ldxo: of xo or dxo)
     unsigned vec;               // 16-byte accesses: 1 x, 2 xo, 4 y, 8 h, 16 gate, 32.. parameters, 64 dx, 128 dy, 256 dxo
     // backward
     const void *dxo;
@@ -1306,6 +1306,8 @@ pi_status check(pi_ctx *c, const pi_norm_residual_desc *d, pi_norm_residual_desc
         if (!*l) *l = o.d;
         if (*l < o.d) return ctx_fail(c, PI_ERR_SHAPE, "row stride %lld below the row's %d elements", (long long)*l, o.d);
     }
+    if (!o.lddxo) o.lddxo = o.ldxo;
+    if (o.lddxo < o.d) return ctx_fail(c, PI_ERR_SHAPE, "row stride %lld below the row's %d elements", (long long)o.lddxo, o.d);
     return PI_OK;
 }
 
@@ -1453,7 +1455,7 @@ pi_status pi_norm_residual_bwd(pi_ctx *c, const pi_norm_residual_desc *desc, con
         p.stats = (float *)ws;
         p.part = (float *)((uint8_t *)ws + u.stats);
     }
-    p.lddx = d.ldx, p.ldx = d.ldxo;
+    p.lddx = d.ldx, p.ldx = d.ldxo, p.ldxo = d.lddxo;
     if (p.pre == PI_NORM_NONE) p.x = nullptr; // (not needed)
     const int xe = p.x32 ? 4 : 2;
     p.vec |= vb(x_out, p.ldx, xe, NV_X) | vb(y, p.ldy, 2, NV_Y) | vb(dh, p.ldh, 2, NV_H) | vb(gate, p.ldgate, 2, NV_GATE) |

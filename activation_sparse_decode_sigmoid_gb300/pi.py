@@ -84,7 +84,7 @@ pi_gated_ffn_grads = _struct("pi_gated_ffn_grads", ptr=("w_gate", "w_up", "w_dow
 pi_norm_residual_desc = _struct("pi_norm_residual_desc",
                                 ("T", "d", "x_dtype", "dtype", "grad_dtype", "pre", "post", "gate_rows", "res_scale",
                                  "branch_scale", "eps"), ("res_scale", "branch_scale", "eps"),
-                                ("ldx", "ldxo", "ldy", "ldh", "ldgate"))
+                                ("ldx", "ldxo", "ldy", "ldh", "ldgate", "lddxo"))
 pi_norm_residual_params = _struct("pi_norm_residual_params", ptr=("w_pre", "b_pre", "w_post", "b_post"))
 pi_norm_residual_grads = _struct("pi_norm_residual_grads",
                                  ptr=("dx", "dy", "dgate", "dw_pre", "db_pre", "dw_post", "db_post"))
@@ -895,8 +895,6 @@ class Context:
             raise PiError(PI_ERR_ARG, f"x_out is {xdt}, expected {dtype} or float32")
         px, ldxo = self._at("x_out", x_out, (T, d), xdt)
         pdxo, lddxo = self._at("dx_out", dx_out, (T, d), xdt)
-        if dx_out is not None and lddxo != ldxo:
-            raise PiError(PI_ERR_ARG, "dx_out and x_out differ in their row stride")
         pdh, ldh = self._at("dh", dh, (T, d), dtype)
         py, ldy = self._at("y", y, (T, d), dtype)
         pg, ldg = self._at("gate", gate, (rows, d), dtype)
@@ -906,7 +904,7 @@ class Context:
         # (y and dy share their stride)
         dy = None if y is None else self._new((T, d), dtype) if ldy in (0, d) else self._new((T, ldy), dtype)[:, :d]
         desc, n = self._plan(pi_norm_residual_desc, (T, d, xcode, code, self._code(gdt), pre, post, gate_rows, res_scale,
-                                                     branch_scale, eps, 0, ldxo, ldy, ldh, ldg),
+                                                     branch_scale, eps, 0, ldxo, ldy, ldh, ldg, lddxo or d),
                              pi_norm_residual_bwd_workspace)
         gr = pi_norm_residual_grads(dx.data_ptr(), _ptr(dy), *(_ptr(v) for v in out.values()))
         ws, pws = self._ws(n)

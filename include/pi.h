@@ -539,7 +539,8 @@ typedef struct {
     int32_t pre, post;  /* pi_norm */
     int32_t gate_rows;
     float res_scale, branch_scale, eps; /* finite, eps >= 0 */
-    int64_t ldx, ldxo, ldy, ldh, ldgate; /* backward: ldx dx's, ldxo x_out's and dx_out's, ldy y's and dy's, ldh dh's */
+    int64_t ldx, ldxo, ldy, ldh, ldgate; /* backward: ldx dx's, ldxo x_out's, ldy y's and dy's, ldh dh's */
+    int64_t lddxo;                       /* backward: dx_out's; 0: as x_out's */
 } pi_norm_residual_desc;
 
 typedef struct {

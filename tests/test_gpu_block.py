@@ -515,6 +515,18 @@ def test_norm_of_slices(c, off, pad):
         R.check(got[k], want[k], k)
 
 
+@pytest.mark.parametrize("T,d", [(1, 40), (9, 120), (400, 1000), (400, 33)])
+@pytest.mark.parametrize("wide", ["x_out", "dx_out"])
+def test_norm_bwd_of_a_stream_and_a_gradient_with_their_own_strides(c, T, d, wide):
+    m = Maker(23)
+    x, dxo = m(T, d, dt=F32, pad=8 * (wide == "x_out")), m(T, d, dt=F32, pad=4 * (wide == "dx_out"))
+    y, dh, w = m(T, d), m(T, d), m(d)
+    want = R.norm_bwd(dxo, dh, x, y, None, 0, "rms", "none", w, None, None, 1.0, 1.0, 1e-5, F16, F16)
+    got = c.norm_residual_bwd(dxo, dh, x, y, w_pre=w)
+    for k in ("dx", "dy", "w_pre"):
+        R.check(got[k], want[k], k)
+
+
 def test_norm_rows_of_zeros_and_of_nan(c):
     x = torch.zeros(4, 64, device="cuda")
     x[1] = float("nan")
