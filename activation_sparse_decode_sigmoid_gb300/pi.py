@@ -871,7 +871,8 @@ class Context:
                           grads=None, accumulate=False):
         """Gradients of ``norm_residual`` for the gradients dx_out of x' (None:
         0) and dh of h, as a dict with keys dx, dy, gate, w_pre, b_pre,
-        w_post, b_post; a parameter that was not given has none.  grads:
+        w_post, b_post; a parameter that was not given, or that no norm or
+        block used, has none.  grads:
         buffers for gate and the parameters, packed, in h's type or float32
         (all alike), used instead of new ones and added to with `accumulate`."""
         xdt = x_out.dtype
@@ -886,7 +887,9 @@ class Context:
         if grads is None:
             if accumulate:
                 raise PiError(PI_ERR_ARG, "accumulate needs the buffers that it adds to")
-            out = {k: None if v is None else self._new(v.shape, dtype) for k, v in given.items()}
+            used = {"gate": y is not None, "pre": pre != PI_NORM_NONE, "post": y is not None and post != PI_NORM_NONE}
+            out = {k: self._new(v.shape, dtype) if v is not None and used[k[2:] if k != "gate" else k] else None
+                   for k, v in given.items()}
             gdt = dtype
         else:
             out = {k: grads.get(k) for k in given}

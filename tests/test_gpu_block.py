@@ -527,6 +527,38 @@ def test_norm_bwd_of_a_stream_and_a_gradient_with_their_own_strides(c, T, d, wid
         R.check(got[k], want[k], k)
 
 
+def test_norm_parameters_that_nothing_uses_have_no_gradient(c):
+    """The forward pass ignores the parameters of a norm that is not there, and
+    the gate and the norm of a block that is not there; so does the backward pass."""
+    m = Maker(24)
+    T, d = 6, 40
+    x, y, dxo, dh, w, b, gate = m(T, d, dt=F32), m(T, d), m(T, d, dt=F32), m(T, d), m(d), m(d), m(1, d)
+    par = dict(w_pre=w, b_pre=b, w_post=w, b_post=b)
+    # no post norm
+    xo, h = c.norm_residual(x, y, gate, **par)
+    want = R.norm_bwd(dxo, dh, xo, y, gate, 0, "rms", "none", w, w, b, 1.0, 1.0, 1e-5, F16, F16)
+    got = c.norm_residual_bwd(dxo, dh, xo, y, gate, **par)
+    assert set(k for k in got if got[k] is not None) == {"dx", "dy", "gate", "w_pre", "b_pre"} == set(want)
+    for k in want:
+        R.check(got[k], want[k], k)
+    # no pre norm
+    kw = dict(pre=pi.PI_NORM_NONE, post=pi.PI_NORM_LAYER)
+    xo, h = c.norm_residual(x, y, gate, **par, **kw)
+    want = R.norm_bwd(dxo, None, xo, y, gate, 0, "none", "layer", None, w, b, 1.0, 1.0, 1e-5, F16, F16)
+    got = c.norm_residual_bwd(dxo, None, xo, y, gate, **par, **kw)
+    assert h is None and set(k for k in got if got[k] is not None) == {"dx", "dy", "gate", "w_post", "b_post"} == set(want)
+    for k in want:
+        R.check(got[k], want[k], k)
+    # no block
+    kw = dict(post=pi.PI_NORM_RMS)
+    xo, h = c.norm_residual(x, None, gate, dtype=F16, **par, **kw)
+    want = R.norm_bwd(dxo, dh, xo, None, None, 0, "rms", "none", w, None, None, 1.0, 1.0, 1e-5, F16, F16)
+    got = c.norm_residual_bwd(dxo, dh, xo, None, gate, **par, **kw)
+    assert set(k for k in got if got[k] is not None) == {"dx", "w_pre", "b_pre"} == set(want)
+    for k in want:
+        R.check(got[k], want[k], k)
+
+
 def test_norm_rows_of_zeros_and_of_nan(c):
     x = torch.zeros(4, 64, device="cuda")
     x[1] = float("nan")
