@@ -39,8 +39,9 @@ struct CtxView {
 
 // Raises a kernel's limit of dynamic shared memory on the current device to all
 // that its static arrays leave, once per device (`ready`: the kernel's own,
-// devices by bit).  The limit belongs to the function, not to a launch: lowered
-// to one call's size, it could make a launch of another thread's context fail.
+// devices by bit).  The limit belongs to the function on a device, not to a
+// launch: set to one call's size, it made launches of another thread's context
+// fail (881 of 5000 norms of 4096 columns beside norms of 64).
 inline cudaError_t raise_limit(const void *kern, std::atomic<uint64_t> &ready)
 {
     int dev = 0, most = 0;

@@ -58,7 +58,9 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
+#include "pi_host.h"
 #include "pi_kernels.h"
 #include "pi_tc.cuh"
 
@@ -621,7 +623,8 @@ cudaError_t launch_up(const MmaParams &p, int grid, cudaStream_t s)
     // ids [256] and the producers' stage counts [kIssuers]
     const int smem = (int)kUpArena + (2 * kUpMaxSt + 1) * 8 + 16 + 256 * 4 + kIssuers * 4;
     auto kern = ffn_up_mma<T, REGLU>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = raise_limit((const void *)kern, ready);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(kMT), smem, s, p);
 }
@@ -639,7 +642,8 @@ cudaError_t launch_up_rows(const MmaParams &p, int grid, int smem_optin, cudaStr
     if (nst > kRowWarps) nst = nst / kRowWarps * kRowWarps; // one consumer warp per slot
     const int smem = fixed + nst * (int)stageB + 2 * nst * 8;
     auto kern = ffn_up_rows<T, REGLU>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = raise_limit((const void *)kern, ready);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(kRowT), smem, s, p, nst, stageB);
 }
@@ -653,7 +657,8 @@ cudaError_t launch_down(const MmaParams &p, int grid, int smem_optin, cudaStream
     const int smem = dn_smem_bytes(p.Npad, st);
     if (smem > smem_optin) return cudaErrorInvalidValue;
     auto kern = ffn_down_mma<T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = raise_limit((const void *)kern, ready);
     if (e != cudaSuccess) return e;
     // as many shares of the list per 256-column block as keep every SM busy with one unit
     const int ncb = (p.d + 255) / 256;

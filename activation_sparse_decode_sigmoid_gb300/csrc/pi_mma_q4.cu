@@ -47,7 +47,9 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
+#include "pi_host.h"
 #include "pi_kernels.h"
 #include "pi_tc.cuh"
 
@@ -671,7 +673,8 @@ cudaError_t launch_up_q4(const MmaParams &p, int grid, int smem_optin, cudaStrea
     const int smem = (int)C::T * 2 * p.Npad * 128 + (int)(C::R * C::raw_slot) + (2 * (int)C::T + 1) * 8 + 16 + 128 * 4;
     if (smem > smem_budget(C::per_sm, smem_optin)) return cudaErrorInvalidValue;
     auto kern = ffn_up_q4<REGLU>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = raise_limit((const void *)kern, ready);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid * C::per_sm), dim3(kUpT), smem, s, p);
 }
@@ -682,7 +685,8 @@ cudaError_t launch_down_q4(const MmaParams &p, int grid, int smem_optin, cudaStr
     while (T > 2 && q4dn_smem(p.Npad, T) > smem_optin) --T;
     const int smem = q4dn_smem(p.Npad, T);
     if (smem > smem_optin) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(ffn_down_q4, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = raise_limit((const void *)ffn_down_q4, ready);
     if (e != cudaSuccess) return e;
     // as many shares of the list per 256-column block as keep every SM busy with one unit
     const int ncb = (p.d + 255) / 256;

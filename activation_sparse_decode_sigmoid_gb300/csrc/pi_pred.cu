@@ -35,8 +35,10 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pi_device.cuh"
+#include "pi_host.h"
 
 namespace pi {
 namespace {
@@ -535,7 +537,8 @@ cudaError_t launch_hidden(const PredParams &p, int sms, cudaStream_t s)
 {
     const int smem = TT * p.L.d * 2, ntb = (p.B + TT - 1) / TT;
     auto kern = pred_hidden<T, R, PD, TT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = raise_limit((const void *)kern, ready);
     if (e != cudaSuccess) return e;
     int per_sm = 1;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kPT, smem);
@@ -551,7 +554,8 @@ cudaError_t launch_out(const PredParams &p, int sms, cudaStream_t s)
 {
     const int smem = out_smem(R, WS, TT, p.L.r);
     auto kern = pred_out<T, R, WS, TT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = raise_limit((const void *)kern, ready);
     if (e != cudaSuccess) return e;
     const int nrt = (p.L.n + 8 * R - 1) / (8 * R) - std::min(p.L.hot, p.L.n) / (8 * R);
     return launch_pdl(kern, dim3(std::max(1, std::min(nrt, sms))), dim3(kPT), smem, s, p);
