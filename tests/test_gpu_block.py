@@ -173,6 +173,27 @@ def test_linear_activations_at_their_ends(c, fn):
     assert bool((y == (0.0 if fn != "none" else float("-inf"))).all()), y
 
 
+@pytest.mark.parametrize("fn", R.FNS)
+@pytest.mark.parametrize("T", [1, 18, 300])
+def test_activations_of_infinities(c, fn, T):
+    """f and f' at z = inf and -inf are their limits, on every path (few
+    tokens, tiles); sums that overflow hand the infinities over."""
+    inf = float("inf")
+    top = {"none": (inf, -inf), "relu": (inf, 0), "sqrelu": (inf, 0), "sigmoid": (1, 0)}.get(fn, (inf, 0))
+    slope = {"none": (1, 1), "relu": (1, 0), "sqrelu": (inf, 0), "sigmoid": (0, 0)}.get(fn, (1, 0))
+    w = torch.ones(8, 16, dtype=BF16, device="cuda")
+    x = torch.full((T, 16), 3e38, dtype=BF16, device="cuda")
+    for k, sign in enumerate((1, -1)):
+        assert bool((c.linear(sign * x, w, fn=FN(fn)) == top[k]).all())
+        z = torch.full((T, 8), sign * inf, dtype=BF16, device="cuda")
+        dy = torch.zeros(T, 8, dtype=BF16, device="cuda")
+        dy[0] = 1
+        db = torch.empty(8, device="cuda")
+        if slope[k] < inf:  # (0 times an infinite slope in the other rows)
+            c.linear_bwd(dy, x, w, z, fn=FN(fn), need=(False, False, True), db=db)
+            assert bool(((db - slope[k]).abs() < 1e-30).all()), db
+
+
 def test_sigmoid_derivative_on_both_sides(c):
     """p (1 - p) to within its rounding, however near p is to 0 or 1.  The
     exponential is off by at most 2 + 1.173 |z| steps of 2^-23, 1 / (1 + e) by
