@@ -111,11 +111,11 @@ __global__ void __launch_bounds__(256) pack_set(const __grid_constant__ CopySet 
 
 // Column sums in two launches: a CTA sums some rows of 256 columns (8 per
 // thread, 8 row lanes), then the row blocks' partials are added in order.
-// Rows per CTA: enough CTAs for four on every SM (152), at least 8 rows; a
+// Rows per CTA: enough CTAs for four on every SM, at least 8 rows; a
 // 4096 x 1024 dz took 52 us with 256 rows each (64 CTAs).
-int sum_rows(int T, int N)
+int sum_rows(int T, int N, int sms)
 {
-    const int64_t ncb = (N + 255) / 256, want = (T * ncb + 607) / 608;
+    const int64_t ncb = (N + 255) / 256, want = (T * ncb + 4 * sms - 1) / (4 * sms);
     return (int)std::min<int64_t>(256, std::max<int64_t>(8, (want + 7) / 8 * 8));
 }
 
@@ -216,7 +216,7 @@ struct SumSet {
         int N, rpb, nparts, vec;
         unsigned block0, join0; // its first block of either launch
     } m[3];
-    int n, T, out32, accumulate;
+    int n, T, out32, accumulate, sms;
 };
 
 template <typename T> __global__ void __launch_bounds__(256) col_sums(const __grid_constant__ SumSet s)
@@ -241,9 +241,10 @@ bool aligned16(const void *p, int64_t ld, int elem) { return ((uintptr_t)p & 15)
 
 template <typename T>
 cudaError_t dact_t(const void *dy, int dy32, int64_t ldy, const void *z, int64_t ldz, int fn, float scale, void *dz,
-                   int64_t lddz, int Trows, int N, void *db, int db32, int accumulate, float *part, cudaStream_t s)
+                   int64_t lddz, int Trows, int N, void *db, int db32, int accumulate, float *part, const CtxView &v)
 {
-    const int rpb = sum_rows(Trows, N), nrb = (Trows + rpb - 1) / rpb;
+    const cudaStream_t s = v.stream;
+    const int rpb = sum_rows(Trows, N, v.sms), nrb = (Trows + rpb - 1) / rpb;
     const int64_t blocks = (int64_t)nrb * ((N + 255) / 256);
     const int vec = (aligned16(dy, ldy, dy32 ? 4 : 2) ? 1 : 0) | (z && aligned16(z, ldz, 2) ? 2 : 0) |
                     (dz && aligned16(dz, lddz, 2) ? 4 : 0);
@@ -459,7 +460,7 @@ LinearBwd plan_linear_bwd(const pi_linear_desc &d, const CtxView &v, const void 
     }
     if (dw) f.x = stage(a, x, d.ldx, d.T, d.K, 1);
     if (dx) f.w = stage(a, w, d.ldw, d.N, d.K, 1);
-    f.part = db ? a.take(colsum_bytes(d.T, d.N)) : nullptr;
+    f.part = db ? a.take(colsum_bytes(d.T, d.N, v.sms)) : nullptr;
     if (dx) {
         Gemm &g = f.p.add();
         g.mode = EPI_LINEAR;
@@ -574,7 +575,7 @@ FfnFwd plan_ffn(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated_ffn
 }
 
 struct FfnBwd {
-    Staged x, wg, wu, wd, dy, a, dyT;
+    Staged x, wg, wu, wd, dy, a;
     void *dg, *du;
     int64_t ldd;
     void *part;
@@ -602,8 +603,8 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
     }
     if (gr.w_up || gr.w_gate) f.x = stage(ar, x, d.ldx, d.T, d.d, 1);
     if (gr.w_down) f.a = stage(ar, s.a, d.lda, d.T, d.n, 1);
-    const size_t part = (gr.b_gate ? colsum_bytes(d.T, d.n) : 0) + (gr.b_up ? colsum_bytes(d.T, d.n) : 0) +
-                        (gr.b_down ? colsum_bytes(d.T, d.d) : 0);
+    const size_t part = (gr.b_gate ? colsum_bytes(d.T, d.n, v.sms) : 0) + (gr.b_up ? colsum_bytes(d.T, d.n, v.sms) : 0) +
+                        (gr.b_down ? colsum_bytes(d.T, d.d, v.sms) : 0);
     f.part = part ? ar.take(part) : nullptr;
     const int g32 = d.grad_dtype == PI_F32;
     if (want_d) {
@@ -657,20 +658,20 @@ FfnBwd plan_ffn_bwd(const pi_gated_ffn_desc &d, const CtxView &v, const pi_gated
 
 } // namespace
 
-size_t colsum_bytes(int T, int N)
+size_t colsum_bytes(int T, int N, int sms)
 {
-    const int rpb = sum_rows(T, N);
+    const int rpb = sum_rows(T, N, sms);
     return (size_t)((T + rpb - 1) / rpb) * N * sizeof(float);
 }
 
 cudaError_t launch_dact(const void *dy, int dy32, int64_t ldy, const void *z, int64_t ldz, int fn, float scale,
                         void *dz, int64_t lddz, int T, int N, void *db, int db32, int accumulate, bool bf16,
-                        void *part, cudaStream_t s)
+                        void *part, const CtxView &v)
 {
     return bf16 ? dact_t<__nv_bfloat16>(dy, dy32, ldy, z, ldz, fn, scale, dz, lddz, T, N, db, db32, accumulate,
-                                        (float *)part, s)
+                                        (float *)part, v)
                 : dact_t<__half>(dy, dy32, ldy, z, ldz, fn, scale, dz, lddz, T, N, db, db32, accumulate, (float *)part,
-                                 s);
+                                 v);
 }
 
 // One more matrix whose column sums are wanted (out NULL: not wanted).  part: its partials.
@@ -678,13 +679,13 @@ void add_sum(SumSet &s, const void *src, int64_t ld, int N, void *out, void *&pa
 {
     if (!out) return;
     SumSet::One &m = s.m[s.n];
-    const int rpb = sum_rows(s.T, N), nparts = (s.T + rpb - 1) / rpb;
+    const int rpb = sum_rows(s.T, N, s.sms), nparts = (s.T + rpb - 1) / rpb;
     m = {(const uint16_t *)src, out, (float *)part, ld, N, rpb, nparts, aligned16(src, ld, 2) ? 1 : 0, 0, 0};
     if (s.n) {
         const SumSet::One &l = s.m[s.n - 1];
         m.block0 = l.block0 + (unsigned)l.nparts * ((l.N + 255) / 256), m.join0 = l.join0 + (l.N + 31) / 32;
     }
-    part = (uint8_t *)part + colsum_bytes(s.T, N);
+    part = (uint8_t *)part + colsum_bytes(s.T, N, s.sms);
     ++s.n;
 }
 
@@ -776,9 +777,9 @@ pi_status pi_linear_bwd(pi_ctx *c, const pi_linear_desc *desc, const void *dy, c
     CUB(run_copies({&f.dz, &f.x, &f.w}, v.stream));
     if (!f.direct) {
         CUB(launch_dact(dy, dy32, d.ldy, z, d.ldz, d.fn, d.scale, f.dzbuf, f.lddz, d.T, d.N, db, g32, accumulate, bf,
-                        f.part, v.stream));
+                        f.part, v));
     } else {
-        SumSet sums = {{}, 0, d.T, g32, accumulate};
+        SumSet sums = {{}, 0, d.T, g32, accumulate, v.sms};
         void *part = f.part;
         add_sum(sums, dy, d.ldy, d.N, db, part);
         CUB(launch_sums(sums, bf, v.stream));
@@ -873,7 +874,7 @@ pi_status pi_gated_ffn_bwd(pi_ctx *c, const pi_gated_ffn_desc *desc, const pi_ga
     CUB(run_copies({&f.dy, &f.wd, &f.wg, &f.wu, &f.x, &f.a}, v.stream));
     if (f.da) CUB(launch_gemm(f.p.g[0], bf, v, f.gws));
     if (f.p.n > f.da) CUB(launch_gemms(f.p.g + f.da, f.p.n - f.da, bf, v, f.gws));
-    SumSet sums = {{}, 0, d.T, g32, accumulate};
+    SumSet sums = {{}, 0, d.T, g32, accumulate, v.sms};
     void *part = f.part;
     add_sum(sums, f.dg, f.ldd, d.n, gr.b_gate, part);
     add_sum(sums, f.du, f.ldd, d.n, gr.b_up, part);

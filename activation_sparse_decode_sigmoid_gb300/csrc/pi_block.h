@@ -76,12 +76,12 @@ size_t skinny_workspace(const Gemm &g, const CtxView &v);
 cudaError_t launch_skinny(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
 // Bytes of the partial column sums of a matrix [T][N].
-size_t colsum_bytes(int T, int N);
+size_t colsum_bytes(int T, int N, int sms);
 
 // dz = scale * dy * fn'(z) [T][N], 16-bit, and its column sums into db (NULL:
 // none; the fp32 values before their rounding are summed)
 cudaError_t launch_dact(const void *dy, int dy32, int64_t ldy, const void *z, int64_t ldz, int fn, float scale,
                         void *dz, int64_t lddz, int T, int N, void *db, int db32, int accumulate, bool bf16,
-                        void *part, cudaStream_t s);
+                        void *part, const CtxView &v);
 
 } // namespace pi

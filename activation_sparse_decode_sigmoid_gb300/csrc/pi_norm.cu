@@ -33,9 +33,9 @@ constexpr int kMaxT = 1 << 22, kMaxNormD = 16384;
 
 // Tokens whose column sums one unit of norm_bwd_cols adds up: enough units for
 // eight CTAs of 1024 columns on every SM, 4 to 64 tokens each.
-int unit_rows(int T, int d)
+int unit_rows(int T, int d, int sms)
 {
-    const int64_t want = (int64_t)T * ((d + 1023) / 1024) / 1216;
+    const int64_t want = (int64_t)T * ((d + 1023) / 1024) / (8 * sms);
     return (int)std::min<int64_t>(64, std::max<int64_t>(4, want));
 }
 
@@ -79,7 +79,7 @@ template <typename T> __device__ __forceinline__ void storex8(void *p, int x32, 
 }
 
 // Sums of two values over the CTA, in a fixed order; every thread gets them.
-// buf: 64 floats of shared memory, a different half on alternating calls.
+// buf: 128 floats of shared memory, one half of 64 on every other call.
 __device__ __forceinline__ float2 cta_sum2(float a, float b, float *buf, int &flip)
 {
 #pragma unroll
@@ -1346,7 +1346,7 @@ Units plan_units(const pi_norm_residual_desc &d, bool gate, int sms)
     Units u;
     const int gr = gate && d.gate_rows ? d.gate_rows : std::max(1, d.T);
     u.per_token = gate && gr == 1 && d.T > 1;
-    u.unit = unit_rows(d.T, d.d);
+    u.unit = unit_rows(d.T, d.d, sms);
     u.per_group = ((u.per_token ? d.T : std::min(gr, std::max(1, d.T))) + u.unit - 1) / u.unit;
     const int64_t groups = u.per_token ? 1 : (d.T + (int64_t)gr - 1) / gr;
     // the last gate row may have fewer tokens, and units without any add zeros
