@@ -874,6 +874,10 @@ pi_status pi_gated_ffn_bwd(pi_ctx *c, const pi_gated_ffn_desc *desc, const pi_ga
     CUB(run_copies({&f.dy, &f.wd, &f.wg, &f.wu, &f.x, &f.a}, v.stream));
     if (f.da) CUB(launch_gemm(f.p.g[0], bf, v, f.gws));
     if (f.p.n > f.da) CUB(launch_gemms(f.p.g + f.da, f.p.n - f.da, bf, v, f.gws));
+    // (the sums of dg and du as they are stored, rounded: the epilogue that holds
+    // them unrounded has a row in each thread, so that sums over rows would cost it
+    // a pass through shared memory per tile; each rounding is off by at most half a
+    // step either way, and T of them add up to about the sum's own rounding)
     SumSet sums = {{}, 0, d.T, g32, accumulate, v.sms};
     void *part = f.part;
     add_sum(sums, f.dg, f.ldd, d.n, gr.b_gate, part);

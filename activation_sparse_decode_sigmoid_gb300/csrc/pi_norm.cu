@@ -10,8 +10,10 @@
 //     P1 = sum dh xh, P0 = sum dh  over tokens: dw_pre, db_pre
 //     S1 = sum D yh, S0 = sum D    over the tokens of one gate row:
 //         dgate = bs (w_post S1 + b_post S0),  dw_post += bs gate S1,  db_post += bs gate S0
-// The forward pass is bound by HBM (a few operations per element), the
-// backward pass, about 50 instructions per element of six arrays, by their issue.
+// The forward pass is bound by HBM (a few operations per element).  The backward
+// pass, about 50 instructions per element of six arrays, fills neither: HBM is
+// half busy and 0.58 instructions issue per cycle, because all warps of an SM
+// work on one row and stand at its barriers and results together.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -815,7 +817,10 @@ enum { ST_SX, ST_SY, ST_MX, ST_SQX, ST_MY, ST_SQ, ST_N = 9 }; // (9: no bank con
 // tensor memory, where each thread adds to its own columns' values: in
 // registers they took half of what 512 threads have (8000 x 8192 layer norms:
 // 345 us with 512 threads and spills, 271 us with 256 threads of 32 columns).
-// Bound by instruction issue: what one gate row's tokens share, bs gate
+// Bound by the latency of one row at a time (4 warps a scheduler, 0.58 issues per
+// cycle, HBM 50 %; of a warp's time 21 % waits for shared memory and shuffles, 7 %
+// at the barriers, 21 % for warps that are ready at the same moment), so fewer
+// instructions still count: what one gate row's tokens share, bs gate
 // w_post, is multiplied once, each element's value is kept in the form that its
 // next use wants (209 -> 196 us), and sums share shuffles (178 us; 172 with the
 // join below; 4.6 TB/s).  (The next row's statistics computed ahead of the same

@@ -413,11 +413,16 @@ pi_status pi_layerwise_min_batch(pi_ctx *ctx, int32_t layer, int32_t *min_batch)
  *   - The calls launch kernels on the context's stream only and can be
  *     captured into a CUDA graph.
  *   - Products are accumulated in fp32; bias, activation, residual and
- *     normalisation are computed in fp32 and rounded once.  What a backward
- *     pass multiplies by a weight or an input (dz, dg, du) is first rounded
- *     to `dtype`: a 16-bit tensor-core product takes both operands in it.
- *   - Sums run in a fixed order: the same call on the same data gives the
- *     same bits.
+ *     normalisation are computed in fp32 and rounded once.  What goes on into
+ *     another product (a between the FFN's products; dz, dg, du in the
+ *     backward passes) is first rounded to `dtype`: a 16-bit tensor-core
+ *     product takes both operands in it.  With PI_F16 such a value beyond
+ *     65504 becomes an infinity, which squared ReLU and gated products can
+ *     reach; PI_BF16 has fp32's range.  pi_linear_bwd's db sums dz before that
+ *     rounding, the FFN's bias gradients sum dg and du after it.
+ *   - Sums run in an order that the device and the call fix (sizes, strides,
+ *     alignment of the buffers, which outputs are wanted): the same call on
+ *     the same data gives the same bits.
  */
 typedef enum {
     PI_FN_NONE = 0,     /* z */
@@ -528,6 +533,8 @@ pi_status pi_gated_ffn_bwd(pi_ctx *ctx, const pi_gated_ffn_desc *desc, const pi_
  * token t uses row t / gate_rows; gate_rows 0 = one row for every token.
  * Without a block before it (y NULL; gate and post then unused) x' =
  * res_scale * x and x_out may be NULL; with pre PI_NORM_NONE h must be NULL.
+ * Parameters of a norm that is PI_NORM_NONE are ignored; wanting their
+ * gradients, or a gradient that needs a y or a gate that is NULL, is PI_ERR_ARG.
  * T in [0, 2^22], d in [1, 16384]. */
 typedef enum { PI_NORM_NONE = 0, PI_NORM_RMS = 1, PI_NORM_LAYER = 2 } pi_norm;
 
