@@ -32,7 +32,7 @@ template <> struct C16<__nv_bfloat16> {
 };
 
 // Clamp that keeps NaN (fminf and fmaxf would drop it): beyond +-lim the
-// smooth functions below equal their limits in fp32, and inf * 0 is avoided.
+// smooth functions below are within 2e-33 of their limits, and inf * 0 is avoided.
 __device__ __forceinline__ float clampn(float z, float lim) { return z < -lim ? -lim : (z > lim ? lim : z); }
 
 // 1 - Phi(x) for x >= 0 as exp(-x^2 / 2) t P(t), t = 1 / (1 + 0.35 x), with ex =
@@ -60,7 +60,8 @@ __device__ __forceinline__ float upper_tail(float x, float &ex)
 // off by up to 2 + 1.173 |a| steps of 2^-23, __fdividef by 2: below 2^-13 of the
 // value where it is smallest, below 2^-16 where f16 has normal numbers, so far
 // below the half step of a 16-bit output (2^-8, 2^-11).  fp32 outputs
-// (pi_linear's out_dtype) have these errors as they are.
+// (pi_linear's out_dtype) have these errors as they are.  (Where a derivative
+// crosses 0 they are relative to its terms, not to their sum.)
 template <int FN> __device__ __forceinline__ float act_one(float z)
 {
     if (FN == PI_FN_RELU) return z < 0.f ? 0.f : z;

@@ -548,6 +548,16 @@ def test_norm_bwd_of_a_stream_and_a_gradient_with_their_own_strides(c, T, d, wid
         R.check(got[k], want[k], k)
 
 
+def test_norm_bwd_refuses_a_stride_below_the_row(c):
+    t = torch.zeros(64, dtype=F16, device="cuda")
+    lib, p = pi.load_library(), t.data_ptr()
+    par, g = pi.pi_norm_residual_params(), pi.pi_norm_residual_grads(p)
+    for ld in (7, -8):
+        d = pi.pi_norm_residual_desc(2, 8, 0, 0, 0, 1, 0, 0, 1.0, 1.0, 1e-5, 0, 0, 0, 0, 0, ld)
+        assert lib.pi_norm_residual_bwd(c.handle, pi._ref(d), pi._ref(par), p, p, p, None, None, pi._ref(g), 0, None, 0) == pi.PI_ERR_SHAPE
+    c.check()
+
+
 def test_norm_parameters_that_nothing_uses_have_no_gradient(c):
     """The forward pass ignores the parameters of a norm that is not there, and
     the gate and the norm of a block that is not there; so does the backward pass."""
