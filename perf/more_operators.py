@@ -132,7 +132,7 @@ def _e2m1(v):
     c += a > 2.5
     c += a >= 3.5
     c += a > 5.0
-    return c + 8 * torch.signbit(v)
+    return c + (torch.signbit(v).to(torch.uint8) << 3)
 
 
 def _power(c):
