@@ -34,6 +34,10 @@ struct Epi {
     uint16_t *out2, *out3;        // or NULL
     const uint16_t *in1, *in2;
     int64_t ldr, ldo, ld2, ld3, ldi1, ldi2;
+    // EPI_LINEAR without residual and EPI_GATED, microscaled output: its kind
+    // (PI_MX8, PI_MX4; 0: none); out are its codes, ldo the bytes of a row
+    int mx, mx_tiles;
+    uint8_t *mx_scales;
 };
 
 // One operand: element (row r, reduction index k) is p[r * ld + k] (mn = 0)
@@ -43,6 +47,9 @@ struct Mat {
     int64_t ld;
     int mn;
 };
+
+// The operands' types: 16 bits, or microscaled (A's, then B's elements).
+enum : int { OPS_16 = 0, OPS_MX88 = 1, OPS_MX84 = 2, OPS_MX44 = 3 };
 
 // D[M][N] = sum over segments of A_s[M][K_s] B_s[N][K_s]^T, then the
 // epilogue; dual (EPI_GATED): one segment, B_0 and B_1 give two accumulators.
@@ -57,6 +64,9 @@ struct Gemm {
     // predecessor before they let their successor start)
     int early;
     Epi e;
+    // microscaled operands: one segment, rows along k, ld in bytes, their scales
+    int ops;
+    const uint8_t *sa, *sb[2];
 };
 
 // Workspace of a launch (bytes), and the launch.

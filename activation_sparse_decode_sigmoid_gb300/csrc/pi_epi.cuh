@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "pi_block.h"
+#include "pi_mx.cuh"
 
 namespace pi {
 namespace {
@@ -292,6 +293,33 @@ __device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int 
             store8<T>(static_cast<uint16_t *>(e.out) + row * e.ldo + col, n, e.vec & V_OUT, v);
         }
     }
+}
+
+// The same with a microscaled output (EPI_LINEAR without residual, EPI_GATED):
+// called by all lanes of a warp, four of which, XOR and 2 XOR apart, hold the 32
+// columns of a block.  on: the row exists, and col lies inside the padded row.
+template <typename T, int MODE, int XOR>
+__device__ __forceinline__ void epilogue8_mx(const Epi &e, int N, int64_t row, int col, bool on, float (&v)[8], float (&v2)[8])
+{
+    const int n = on ? N - col : 0;
+    float b[8];
+    if (e.bias) {
+        load8<T>(e.bias + col, n, e.vec & V_BIAS, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+    if (MODE == EPI_GATED && e.bias2) {
+        load8<T>(e.bias2 + col, n, e.vec & V_BIAS2, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v2[i] += b[i];
+    }
+    acts(e.fn, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] *= MODE == EPI_GATED ? v2[i] : e.scale;
+        if (i >= n) v[i] = 0.f; // (what pads a row is 0)
+    }
+    mx_store8<XOR>(e.mx, static_cast<uint8_t *>(e.out), e.ldo, e.mx_scales, e.mx_tiles, row, col, on, v);
 }
 
 // The epilogue of one element (EPI_LINEAR, EPI_GATED).

@@ -1,0 +1,474 @@
+// Microscaled matrices: quantisation, the values back, and the C entry points
+// of the products of such matrices (a linear layer, a gated FFN).
+//
+// Both conversions are bound by HBM: T K (e + b) bytes for e bytes an element
+// and b = 33 / 32 or 17 / 32 a code with its share of the scale.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "pi.h"
+#include "pi_block.h"
+#include "pi_epi.cuh"
+#include "pi_kernels.h"
+#include "pi_mx.cuh"
+
+namespace pi {
+namespace {
+
+constexpr int kMaxT = 1 << 22, kMaxDim = 1 << 20;
+
+struct MxP {
+    const void *x;   // or the output of the way back
+    int64_t ldx;
+    int vec;         // 16-byte accesses to x
+    int T, K, tiles;
+    uint8_t *codes, *scales;
+    int64_t ld;
+};
+
+// T: __half, __nv_bfloat16 or float
+template <typename T> __device__ __forceinline__ void load_any(const void *p, int64_t at, int n, bool vec, float (&v)[8])
+{
+    load8<T>(static_cast<const uint16_t *>(p) + at, n, vec, v);
+}
+template <> __device__ __forceinline__ void load_any<float>(const void *p, int64_t at, int n, bool vec, float (&v)[8])
+{
+    load8f(static_cast<const float *>(p) + at, n, vec, v);
+}
+template <typename T> __device__ __forceinline__ void store_any(void *p, int64_t at, int n, bool vec, const float (&v)[8])
+{
+    store8<T>(static_cast<uint16_t *>(p) + at, n, vec, v);
+}
+template <> __device__ __forceinline__ void store_any<float>(void *p, int64_t at, int n, bool vec, const float (&v)[8])
+{
+    store8f(static_cast<float *>(p) + at, n, vec, v);
+}
+
+// A warp takes 256 columns of kRows rows, its loads in flight together: a lane
+// holds 8 columns of each, four lanes a block.
+constexpr int kRows = 4, kWarps = 8;
+
+template <typename T, int KIND> __global__ void __launch_bounds__(32 * kWarps) mx_quantize_rows(const __grid_constant__ MxP p)
+{
+    pdl_enter();
+    const int ncb = (p.tiles + 1) / 2, lane = threadIdx.x & 31;
+    const int c = (int)(blockIdx.x % ncb) * 256 + lane * 8, n = p.K - c;
+    const int64_t r0 = ((int64_t)(blockIdx.x / ncb) * kWarps + (threadIdx.x >> 5)) * kRows;
+    const bool in = c < p.tiles * 128;
+    float v[kRows][8];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + i;
+        load_any<T>(p.x, r * p.ldx + c, r < p.T ? n : 0, p.vec, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + i;
+        uint32_t a = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = max(a, mag(v[i][j]));
+        const uint32_t code = mx_scale<KIND>(mx_amax4<1>(a));
+        // the four scales of a tile's row: one word
+        uint32_t word = code << (lane & 12) * 2;
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        if (!in) continue;
+        if (r < p.T) {
+            const uint2 q = mx_pack8<KIND>(v[i], code);
+            if (KIND == PI_MX8) *reinterpret_cast<uint2 *>(p.codes + r * p.ld + c) = q;
+            else *reinterpret_cast<uint32_t *>(p.codes + r * p.ld + (c >> 1)) = q.x;
+        }
+        // (rows behind the last: zeros up to the tile's end)
+        if (!(lane & 15) && r < (int64_t)mx_tiles(p.T) * 128)
+            *reinterpret_cast<uint32_t *>(p.scales + mx_scale_at(r, c >> 7, p.tiles)) = word;
+    }
+}
+
+template <typename T, int KIND> __global__ void __launch_bounds__(32 * kWarps) mx_dequantize_rows(const __grid_constant__ MxP p)
+{
+    pdl_enter();
+    const int ncb = (p.tiles + 1) / 2, lane = threadIdx.x & 31;
+    const int c = (int)(blockIdx.x % ncb) * 256 + lane * 8, n = p.K - c;
+    const int64_t r0 = ((int64_t)(blockIdx.x / ncb) * kWarps + (threadIdx.x >> 5)) * kRows;
+    if (n <= 0) return;
+    uint2 q[kRows];
+    uint32_t s[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t r = r0 + i;
+        if (r >= p.T) continue;
+        if (KIND == PI_MX8) q[i] = *reinterpret_cast<const uint2 *>(p.codes + r * p.ld + c);
+        else q[i] = make_uint2(*reinterpret_cast<const uint32_t *>(p.codes + r * p.ld + (c >> 1)), 0);
+        s[i] = p.scales[mx_scale_at(r, c >> 7, p.tiles) + ((c >> 5) & 3)];
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (r0 + i >= p.T) continue;
+        float v[8];
+        mx_unpack8<KIND>(q[i], v);
+        const float m = mx_power(s[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= m;
+        store_any<T>(const_cast<void *>(p.x), (r0 + i) * p.ldx + c, n, p.vec, v);
+    }
+}
+
+// ------------------------------------------------------------------ products
+// 64 x 64 outputs a CTA, 32 of k at a time through shared memory as fp32; a
+// thread has 8 columns of two rows.
+struct MxGemmP {
+    Gemm g;
+};
+
+template <int KIND> __device__ __forceinline__ void stage32(float (*s)[33], const uint8_t *codes, int64_t ld, const uint8_t *scales, int tiles,
+                                                            int r0, int rows, int k)
+{
+    const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;
+    float v[8] = {};
+    if (r0 + r < rows) {
+        uint2 q;
+        const uint8_t *row = codes + (int64_t)(r0 + r) * ld;
+        if (KIND == PI_MX8) q = *reinterpret_cast<const uint2 *>(row + k + c);
+        else q = make_uint2(*reinterpret_cast<const uint32_t *>(row + ((k + c) >> 1)), 0);
+        mx_unpack8<KIND>(q, v);
+        const float m = mx_power(scales[mx_scale_at(r0 + r, k >> 7, tiles) + ((k >> 5) & 3)]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= m;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[r][c + i] = v[i];
+}
+
+template <typename T, int MODE, int AK, int BK> __global__ void __launch_bounds__(256) mx_product(const __grid_constant__ MxGemmP p)
+{
+    constexpr int NB = MODE == EPI_GATED ? 2 : 1;
+    __shared__ float sa[64][33], sb[NB][64][33];
+    pdl_enter();
+    const Gemm &g = p.g;
+    const int tn = ((g.N + 127) / 128 * 128) / 64, m0 = (int)(blockIdx.x / tn) * 64, n0 = (int)(blockIdx.x % tn) * 64;
+    const int tiles = mx_tiles(g.K[0]), cg = (threadIdx.x & 7) * 8, rp = (threadIdx.x >> 3) * 2;
+    float acc[NB][2][8] = {};
+    for (int k = 0; k < g.K[0]; k += 32) {
+        stage32<AK>(sa, static_cast<const uint8_t *>(g.a[0].p), g.a[0].ld, g.sa, tiles, m0, g.M, k);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) stage32<BK>(sb[b], static_cast<const uint8_t *>(g.b[b].p), g.b[b].ld, g.sb[b], tiles, n0, g.N, k);
+        __syncthreads();
+#pragma unroll 4
+        for (int j = 0; j < 32; ++j)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float w = sb[b][cg + i][j];
+                    acc[b][0][i] = fmaf(sa[rp][j], w, acc[b][0][i]), acc[b][1][i] = fmaf(sa[rp + 1][j], w, acc[b][1][i]);
+                }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = m0 + rp + i, col = n0 + cg;
+        if (g.e.mx) epilogue8_mx<T, MODE, 1>(g.e, g.N, row, col, row < g.M, acc[0][i], acc[NB - 1][i]);
+        else if (row < g.M && col < g.N) epilogue8<T, MODE>(g.e, g.N, row, col, acc[0][i], acc[NB - 1][i]);
+    }
+}
+
+template <typename T, int MODE> cudaError_t product_mode(const Gemm &g, const CtxView &v)
+{
+    const dim3 grid((unsigned)((g.M + 63) / 64) * (mx_tiles(g.N) * 2));
+    const MxGemmP p = {g};
+    return g.ops == OPS_MX88   ? launch_pdl(mx_product<T, MODE, PI_MX8, PI_MX8>, grid, dim3(256), 0, v.stream, p)
+           : g.ops == OPS_MX84 ? launch_pdl(mx_product<T, MODE, PI_MX8, PI_MX4>, grid, dim3(256), 0, v.stream, p)
+                               : launch_pdl(mx_product<T, MODE, PI_MX4, PI_MX4>, grid, dim3(256), 0, v.stream, p);
+}
+
+cudaError_t launch_product(const Gemm &g, bool bf16, const CtxView &v, void *)
+{
+    if (g.mode == EPI_GATED) return bf16 ? product_mode<__nv_bfloat16, EPI_GATED>(g, v) : product_mode<__half, EPI_GATED>(g, v);
+    return bf16 ? product_mode<__nv_bfloat16, EPI_LINEAR>(g, v) : product_mode<__half, EPI_LINEAR>(g, v);
+}
+size_t product_workspace(const Gemm &, const CtxView &) { return 0; }
+
+// ------------------------------------------------------------------ checks
+bool is16(int dt) { return dt == PI_F16 || dt == PI_BF16; }
+bool is_float(int dt) { return is16(dt) || dt == PI_F32; }
+bool is_mx(int k) { return k == PI_MX8 || k == PI_MX4; }
+bool aligned16(const void *p, int64_t ld, int elem) { return ((uintptr_t)p & 15) == 0 && (ld * elem) % 16 == 0; }
+
+#define CUX(call)                                                                                          \
+    do {                                                                                                   \
+        cudaError_t e_ = (call);                                                                           \
+        if (e_ != cudaSuccess) return ctx_fail(c, PI_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_));   \
+    } while (0)
+
+pi_status check_sizes(pi_ctx *c, int rows, int cols, int kind)
+{
+    if (!is_mx(kind)) return ctx_fail(c, PI_ERR_ARG, "kind %d is not PI_MX8 or PI_MX4", kind);
+    if (rows < 0 || rows > kMaxT) return ctx_fail(c, PI_ERR_SHAPE, "%d rows, outside [0, %d]", rows, kMaxT);
+    if (cols < 1 || cols > kMaxDim) return ctx_fail(c, PI_ERR_SHAPE, "%d columns, outside [1, %d]", cols, kMaxDim);
+    return PI_OK;
+}
+
+// A microscaled matrix's buffers and row stride (0: packed).
+pi_status check_mx(pi_ctx *c, const char *what, const pi_mx *m, int rows, int cols, int kind, int64_t &ld)
+{
+    const int64_t row = mx_row_bytes(kind, cols);
+    if (!ld) ld = row;
+    if (ld < row) return ctx_fail(c, PI_ERR_SHAPE, "%s: row stride %lld below the row's %lld bytes", what, (long long)ld, (long long)row);
+    if (ld % 32) return ctx_fail(c, PI_ERR_ARG, "%s: row stride %lld is not a multiple of 32 bytes", what, (long long)ld);
+    if (!rows) return PI_OK;
+    if (!m || !m->codes || !m->scales) return ctx_fail(c, PI_ERR_ARG, "%s: codes or scales are NULL", what);
+    if ((uintptr_t)m->codes % 32 || (uintptr_t)m->scales % 16)
+        return ctx_fail(c, PI_ERR_ARG, "%s: codes have to start at a multiple of 32 bytes, scales at one of 16", what);
+    return PI_OK;
+}
+
+template <int KIND> cudaError_t run_quantize(const MxP &p, int dt, cudaStream_t s, unsigned grid)
+{
+    return dt == PI_F32   ? launch_pdl(mx_quantize_rows<float, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p)
+           : dt == PI_F16 ? launch_pdl(mx_quantize_rows<__half, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p)
+                          : launch_pdl(mx_quantize_rows<__nv_bfloat16, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p);
+}
+template <int KIND> cudaError_t run_dequantize(const MxP &p, int dt, cudaStream_t s, unsigned grid)
+{
+    return dt == PI_F32   ? launch_pdl(mx_dequantize_rows<float, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p)
+           : dt == PI_F16 ? launch_pdl(mx_dequantize_rows<__half, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p)
+                          : launch_pdl(mx_dequantize_rows<__nv_bfloat16, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p);
+}
+
+pi_status convert(pi_ctx *c, const pi_mx_desc *desc, const void *x, const pi_mx *q, bool back)
+{
+    if (!desc) return ctx_fail(c, PI_ERR_ARG, "desc is NULL");
+    const pi_mx_desc d = *desc;
+    if (pi_status st = check_sizes(c, d.rows, d.cols, d.kind)) return st;
+    if (!is_float(d.dtype)) return ctx_fail(c, PI_ERR_ARG, "dtype %d is not PI_F16, PI_BF16 or PI_F32", d.dtype);
+    const int elem = d.dtype == PI_F32 ? 4 : 2;
+    MxP p = {};
+    p.ldx = d.ldx ? d.ldx : d.cols;
+    if (p.ldx < d.cols) return ctx_fail(c, PI_ERR_SHAPE, "row stride %lld below the row's %d elements", (long long)d.ldx, d.cols);
+    p.ld = d.ldq;
+    if (pi_status st = check_mx(c, "q", q, d.rows, d.cols, d.kind, p.ld)) return st;
+    if (!d.rows) return PI_OK;
+    if (!x) return ctx_fail(c, PI_ERR_ARG, "%s is NULL", back ? "y" : "x");
+    if (pi_status st = check_elements(c, elem, {x})) return st;
+    p.x = x, p.T = d.rows, p.K = d.cols, p.tiles = mx_tiles(d.cols);
+    p.vec = ((uintptr_t)x & 15) == 0 && (d.rows == 1 || p.ldx * elem % 16 == 0);
+    p.codes = static_cast<uint8_t *>(q->codes), p.scales = static_cast<uint8_t *>(q->scales);
+    const CtxView v = ctx_view(c);
+    DeviceGuard g(v.device);
+    const int64_t rows = back ? d.rows : (int64_t)mx_tiles(d.rows) * 128;
+    const unsigned grid = (unsigned)((rows + kRows * kWarps - 1) / (kRows * kWarps) * ((p.tiles + 1) / 2));
+    if (back) CUX(d.kind == PI_MX8 ? run_dequantize<PI_MX8>(p, d.dtype, v.stream, grid) : run_dequantize<PI_MX4>(p, d.dtype, v.stream, grid));
+    else CUX(d.kind == PI_MX8 ? run_quantize<PI_MX8>(p, d.dtype, v.stream, grid) : run_quantize<PI_MX4>(p, d.dtype, v.stream, grid));
+    return PI_OK;
+}
+
+pi_status check_kinds(pi_ctx *c, int xk, int wk, int &ops)
+{
+    if (!is_mx(xk) || !is_mx(wk)) return ctx_fail(c, PI_ERR_ARG, "x_kind %d or w_kind %d is not PI_MX8 or PI_MX4", xk, wk);
+    if (xk == PI_MX4 && wk == PI_MX8) return ctx_fail(c, PI_ERR_UNSUPPORTED, "4-bit x with 8-bit weights");
+    ops = wk == PI_MX8 ? OPS_MX88 : xk == PI_MX8 ? OPS_MX84 : OPS_MX44;
+    return PI_OK;
+}
+
+pi_status check_ws(pi_ctx *c, const void *ws, size_t have, size_t need)
+{
+    if (need && (!ws || have < need))
+        return ctx_fail(c, PI_ERR_ARG, "workspace of %zu bytes needed, %zu given", need, ws ? have : (size_t)0);
+    if (((uintptr_t)ws & 15) != 0) return ctx_fail(c, PI_ERR_ARG, "workspace not 16-byte aligned");
+    return PI_OK;
+}
+
+// The product x W^T of a linear layer, without its buffers.
+pi_status check_linear(pi_ctx *c, const pi_mx_linear_desc *desc, pi_mx_linear_desc &d, Gemm &g)
+{
+    if (!desc) return ctx_fail(c, PI_ERR_ARG, "desc is NULL");
+    d = *desc;
+    g = Gemm{};
+    if (!is16(d.dtype)) return ctx_fail(c, PI_ERR_ARG, "dtype %d is not PI_F16 or PI_BF16", d.dtype);
+    if (d.out_dtype != d.dtype && d.out_dtype != PI_F32)
+        return ctx_fail(c, PI_ERR_ARG, "out_dtype %d is neither dtype nor PI_F32", d.out_dtype);
+    if (d.fn < PI_FN_NONE || d.fn > PI_FN_GELU_TANH) return ctx_fail(c, PI_ERR_ARG, "fn %d invalid", d.fn);
+    if (!std::isfinite(d.scale)) return ctx_fail(c, PI_ERR_ARG, "scale is not finite");
+    if (pi_status st = check_kinds(c, d.x_kind, d.w_kind, g.ops)) return st;
+    if (pi_status st = check_sizes(c, d.T, d.K, d.x_kind)) return st;
+    if (d.N < 1 || d.N > kMaxDim) return ctx_fail(c, PI_ERR_SHAPE, "N %d outside [1, %d]", d.N, kMaxDim);
+    for (int64_t *l : {&d.ldr, &d.ldy}) {
+        if (!*l) *l = d.N;
+        if (*l < d.N) return ctx_fail(c, PI_ERR_SHAPE, "row stride %lld below the row's %d elements", (long long)*l, d.N);
+    }
+    g.mode = EPI_LINEAR, g.segs = 1;
+    g.M = d.T, g.N = d.N, g.K[0] = d.K;
+    g.e.fn = d.fn, g.e.scale = d.scale, g.e.out32 = d.out_dtype == PI_F32;
+    g.e.ldr = d.ldr, g.e.ldo = d.ldy;
+    return PI_OK;
+}
+
+void set_mx(Mat &m, const uint8_t *&scales, const pi_mx &q, int64_t ld)
+{
+    m = {q.codes, ld, 0};
+    scales = static_cast<const uint8_t *>(q.scales);
+}
+
+// The two products of an FFN, without the caller's buffers; a lies in the workspace.
+struct Ffn {
+    pi_mx_gated_ffn_desc d;
+    Gemm up, down;
+    size_t codes, scales, gemm; // bytes of the workspace's parts
+    size_t bytes() const { return codes ? 32 + codes + scales + gemm : 0; } // (32: a starts on such a boundary)
+};
+
+pi_status check_ffn(pi_ctx *c, const pi_mx_gated_ffn_desc *desc, const CtxView &v, Ffn &f)
+{
+    if (!desc) return ctx_fail(c, PI_ERR_ARG, "desc is NULL");
+    f = Ffn{};
+    f.d = *desc;
+    pi_mx_gated_ffn_desc &d = f.d;
+    if (!is16(d.dtype)) return ctx_fail(c, PI_ERR_ARG, "dtype %d is not PI_F16 or PI_BF16", d.dtype);
+    if (d.fn < PI_FN_NONE || d.fn > PI_FN_GELU_TANH) return ctx_fail(c, PI_ERR_ARG, "fn %d invalid", d.fn);
+    if (d.gated != 0 && d.gated != 1) return ctx_fail(c, PI_ERR_ARG, "gated %d is not 0 or 1", d.gated);
+    int ops = 0;
+    if (pi_status st = check_kinds(c, d.x_kind, d.w_kind, ops)) return st;
+    if (pi_status st = check_sizes(c, d.T, d.d, d.x_kind)) return st;
+    if (d.n < 1 || d.n > kMaxDim) return ctx_fail(c, PI_ERR_SHAPE, "n %d outside [1, %d]", d.n, kMaxDim);
+    if (!d.ldy) d.ldy = d.d;
+    if (d.ldy < d.d) return ctx_fail(c, PI_ERR_SHAPE, "row stride %lld below the row's %d elements", (long long)d.ldy, d.d);
+    const int64_t lda = mx_row_bytes(d.x_kind, d.n);
+    Gemm &u = f.up, &w = f.down;
+    u.mode = d.gated ? EPI_GATED : EPI_LINEAR, w.mode = EPI_LINEAR;
+    u.segs = w.segs = 1, u.ops = w.ops = ops, u.M = w.M = d.T, u.N = d.n, u.K[0] = d.d, w.N = d.d, w.K[0] = d.n;
+    u.e.fn = d.fn, u.e.scale = w.e.scale = 1.f;
+    u.e.mx = d.x_kind, u.e.mx_tiles = mx_tiles(d.n), u.e.ldo = lda;
+    w.a[0].ld = lda, w.e.ldo = d.ldy;
+    w.early = 1; // the weights are older than the product before
+    if (!d.T) return PI_OK;
+    f.codes = ((size_t)d.T * lda + 255) / 256 * 256;
+    f.scales = (size_t)mx_scale_bytes(d.T, d.n);
+    f.gemm = std::max(product_workspace(u, v), product_workspace(w, v));
+    return PI_OK;
+}
+
+} // namespace
+} // namespace pi
+
+using namespace pi;
+
+extern "C" {
+
+pi_status pi_mx_bytes(int32_t rows, int32_t cols, int32_t kind, size_t *codes, size_t *scales)
+{
+    if (!codes || !scales || !is_mx(kind)) return PI_ERR_ARG;
+    if (rows < 0 || rows > kMaxT || cols < 1 || cols > kMaxDim) return PI_ERR_SHAPE;
+    *codes = (size_t)rows * mx_row_bytes(kind, cols);
+    *scales = (size_t)mx_scale_bytes(rows, cols);
+    return PI_OK;
+}
+
+pi_status pi_mx_quantize(pi_ctx *c, const pi_mx_desc *desc, const void *x, const pi_mx *q)
+{
+    return c ? convert(c, desc, x, q, false) : PI_ERR_ARG;
+}
+
+pi_status pi_mx_dequantize(pi_ctx *c, const pi_mx_desc *desc, const pi_mx *q, void *y)
+{
+    return c ? convert(c, desc, y, q, true) : PI_ERR_ARG;
+}
+
+pi_status pi_mx_linear_workspace(pi_ctx *c, const pi_mx_linear_desc *desc, size_t *bytes)
+{
+    if (!c) return PI_ERR_ARG;
+    if (!bytes) return ctx_fail(c, PI_ERR_ARG, "bytes is NULL");
+    pi_mx_linear_desc d;
+    Gemm g;
+    if (pi_status st = check_linear(c, desc, d, g)) return st;
+    *bytes = d.T ? product_workspace(g, ctx_view(c)) : 0;
+    return PI_OK;
+}
+
+pi_status pi_mx_linear(pi_ctx *c, const pi_mx_linear_desc *desc, const pi_mx *x, const pi_mx *w, const void *b,
+                       const void *residual, void *y, void *ws, size_t ws_bytes)
+{
+    if (!c) return PI_ERR_ARG;
+    pi_mx_linear_desc d;
+    Gemm g;
+    if (pi_status st = check_linear(c, desc, d, g)) return st;
+    if (pi_status st = check_mx(c, "x", x, d.T, d.K, d.x_kind, d.ldx)) return st;
+    if (!d.T) return PI_OK;
+    if (pi_status st = check_mx(c, "w", w, d.N, d.K, d.w_kind, d.ldw)) return st;
+    if (!y) return ctx_fail(c, PI_ERR_ARG, "y is NULL");
+    const int oe = g.e.out32 ? 4 : 2;
+    if (pi_status st = check_elements(c, 2, {b})) return st;
+    if (pi_status st = check_elements(c, oe, {residual, y})) return st;
+    const CtxView v = ctx_view(c);
+    if (pi_status st = check_ws(c, ws, ws_bytes, product_workspace(g, v))) return st;
+    set_mx(g.a[0], g.sa, *x, d.ldx);
+    set_mx(g.b[0], g.sb[0], *w, d.ldw);
+    Epi &e = g.e;
+    e.bias = static_cast<const uint16_t *>(b), e.res = residual, e.out = y;
+    e.vec = (residual && aligned16(residual, d.ldr, oe) ? V_RES : 0u) | (aligned16(y, d.ldy, oe) ? V_OUT : 0u) |
+            (b && aligned16(b, 0, 2) ? V_BIAS : 0u);
+    DeviceGuard guard(v.device);
+    CUX(launch_product(g, d.dtype == PI_BF16, v, ws));
+    return PI_OK;
+}
+
+pi_status pi_mx_gated_ffn_workspace(pi_ctx *c, const pi_mx_gated_ffn_desc *desc, size_t *bytes)
+{
+    if (!c) return PI_ERR_ARG;
+    if (!bytes) return ctx_fail(c, PI_ERR_ARG, "bytes is NULL");
+    Ffn f;
+    if (pi_status st = check_ffn(c, desc, ctx_view(c), f)) return st;
+    *bytes = f.bytes();
+    return PI_OK;
+}
+
+pi_status pi_mx_gated_ffn(pi_ctx *c, const pi_mx_gated_ffn_desc *desc, const pi_mx_gated_ffn_weights *w, const pi_mx *x,
+                          void *y, void *ws, size_t ws_bytes)
+{
+    if (!c) return PI_ERR_ARG;
+    const CtxView v = ctx_view(c);
+    Ffn f;
+    if (pi_status st = check_ffn(c, desc, v, f)) return st;
+    pi_mx_gated_ffn_desc &d = f.d;
+    if (!w) return ctx_fail(c, PI_ERR_ARG, "weights are NULL");
+    if (!d.gated && (w->gate.codes || w->gate.scales || w->b_gate))
+        return ctx_fail(c, PI_ERR_ARG, "gate weights given, but gated is 0");
+    if (pi_status st = check_mx(c, "x", x, d.T, d.d, d.x_kind, d.ldx)) return st;
+    if (!d.T) return PI_OK;
+    if (d.gated)
+        if (pi_status st = check_mx(c, "w_gate", &w->gate, d.n, d.d, d.w_kind, d.ld_gate)) return st;
+    if (pi_status st = check_mx(c, "w_up", &w->up, d.n, d.d, d.w_kind, d.ld_up)) return st;
+    if (pi_status st = check_mx(c, "w_down", &w->down, d.d, d.n, d.w_kind, d.ld_down)) return st;
+    if (!y) return ctx_fail(c, PI_ERR_ARG, "y is NULL");
+    if (pi_status st = check_elements(c, 2, {w->b_gate, w->b_up, w->b_down, y})) return st;
+    if (pi_status st = check_ws(c, ws, ws_bytes, f.bytes())) return st;
+    uint8_t *const base = reinterpret_cast<uint8_t *>(((uintptr_t)ws + 31) / 32 * 32);
+    const pi_mx a = {base, base + f.codes};
+    Gemm &u = f.up, &o = f.down;
+    set_mx(u.a[0], u.sa, *x, d.ldx);
+    const void *first = w->b_up, *second = nullptr;
+    if (d.gated) {
+        set_mx(u.b[0], u.sb[0], w->gate, d.ld_gate);
+        set_mx(u.b[1], u.sb[1], w->up, d.ld_up);
+        first = w->b_gate, second = w->b_up;
+    } else
+        set_mx(u.b[0], u.sb[0], w->up, d.ld_up);
+    u.e.bias = static_cast<const uint16_t *>(first), u.e.bias2 = static_cast<const uint16_t *>(second);
+    u.e.out = a.codes, u.e.mx_scales = static_cast<uint8_t *>(a.scales);
+    u.e.vec = (first && aligned16(first, 0, 2) ? V_BIAS : 0u) | (second && aligned16(second, 0, 2) ? V_BIAS2 : 0u);
+    set_mx(o.a[0], o.sa, a, o.a[0].ld);
+    set_mx(o.b[0], o.sb[0], w->down, d.ld_down);
+    o.e.bias = static_cast<const uint16_t *>(w->b_down), o.e.out = y;
+    o.e.vec = (aligned16(y, d.ldy, 2) ? V_OUT : 0u) | (w->b_down && aligned16(w->b_down, 0, 2) ? V_BIAS : 0u);
+    void *gws = base + f.codes + f.scales;
+    DeviceGuard guard(v.device);
+    CUX(launch_product(u, d.dtype == PI_BF16, v, gws));
+    CUX(launch_product(o, d.dtype == PI_BF16, v, gws));
+    return PI_OK;
+}
+
+} // extern "C"

@@ -26,6 +26,7 @@
 #include "pi_block.h"
 #include "pi_epi.cuh"
 #include "pi_kernels.h"
+#include "pi_mx.cuh"
 #include "pi_tc.cuh"
 
 namespace pi {
@@ -64,6 +65,9 @@ struct NormP {
     int per_token;              // a gate row per token: S1, S0 carry the gate, dgate is written by the row kernel
     void *dgate, *dw_pre, *db_pre, *dw_post, *db_post;
     int g32, acc;
+    // h microscaled: its kind (0: 16 bits), ldh its bytes a row
+    int mx, mx_tiles;
+    uint8_t *mx_scales;
 };
 
 enum : unsigned { NV_X = 1, NV_XO = 2, NV_Y = 4, NV_H = 8, NV_GATE = 16, NV_PAR = 32, NV_DX = 64, NV_DY = 128, NV_DXO = 256, NV_DGATE = 512 };
@@ -162,6 +166,15 @@ __device__ __forceinline__ void apply_norm(const NormP &p, float (&v)[V][8], con
     }
 }
 
+// 8 columns of a microscaled h: four neighbouring lanes hold a block.
+__device__ __forceinline__ void norm_store_mx(const NormP &p, int64_t t, int c, float (&v)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (c + j >= p.d) v[j] = 0.f;
+    mx_store8<1>(p.mx, reinterpret_cast<uint8_t *>(p.h), p.ldh, p.mx_scales, p.mx_tiles, t, c, c < p.mx_tiles * 128, v);
+}
+
 // Forward: one CTA per token, the row in registers.
 template <typename T, int V> __global__ void __launch_bounds__(1024) norm_fwd(const __grid_constant__ NormP p)
 {
@@ -169,6 +182,10 @@ template <typename T, int V> __global__ void __launch_bounds__(1024) norm_fwd(co
     int flip = 0;
     pdl_enter();
     const int64_t t = blockIdx.x;
+    if (t >= p.Tn) { // (microscaled h: CTAs behind the rows)
+        mx_pad_scales(p.mx_scales, p.Tn, p.mx_tiles, (t - p.Tn) * blockDim.x + threadIdx.x, (int64_t)(gridDim.x - p.Tn) * blockDim.x);
+        return;
+    }
     float x[V][8], y[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -205,7 +222,8 @@ template <typename T, int V> __global__ void __launch_bounds__(1024) norm_fwd(co
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8, n = p.d - c;
-        if (n > 0) store8<T>(p.h + t * p.ldh + c, n, p.vec & NV_H, x[i]);
+        if (p.mx) norm_store_mx(p, t, c, x[i]);
+        else if (n > 0) store8<T>(p.h + t * p.ldh + c, n, p.vec & NV_H, x[i]);
     }
 }
 
@@ -725,6 +743,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_co
         rx = lane_of(r, 0), rz = lane_of(r, 16);
         cx = (wmx - lane_of(mean, 0)) * rx, cz = (wmz - lane_of(mean, 16)) * rz;
     };
+    if (p.mx) mx_pad_scales(p.mx_scales, p.Tn, p.mx_tiles, (int64_t)blockIdx.x * blockDim.x + tid, (int64_t)gridDim.x * blockDim.x);
     bool ok = true;
     if (r0 < r1) {
         ok = mbar_wait_bounded(full, 0, q);
@@ -773,7 +792,8 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_co
                 unpack8<T>(wp[i], w8), unpack8<T>(bp[i], b8);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[i][j] = fmaf(fmaf(x[i][j], rx, cx), w8[j], b8[j]);
-                if (on[i]) store8<T>(p.h + (int64_t)t * p.ldh + c[i], 8, true, x[i]);
+                if (p.mx) norm_store_mx(p, t, c[i], x[i]);
+                else if (on[i]) store8<T>(p.h + (int64_t)t * p.ldh + c[i], 8, true, x[i]);
             }
         }
         flip ^= 1;
@@ -1175,7 +1195,9 @@ __global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_co
 template <typename T, int V> cudaError_t launch_fwd(const NormP &p, cudaStream_t s)
 {
     const int nt = ((p.d + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
-    return launch_pdl(norm_fwd<T, V>, dim3(p.Tn), dim3(nt), 0, s, p);
+    // (16 rows of a tile's scales a CTA more, where a microscaled h leaves some)
+    const int pad = p.mx ? (((128 - (p.Tn & 127)) & 127) + 15) / 16 : 0;
+    return launch_pdl(norm_fwd<T, V>, dim3(p.Tn + pad), dim3(nt), 0, s, p);
 }
 
 // The ring of a pipelined launch: rows of up to kPipeMaxD elements, all 16-byte
@@ -1370,6 +1392,23 @@ Units plan_units(const pi_norm_residual_desc &d, bool gate, int sms)
         if (e_ != cudaSuccess) return ctx_fail(c, PI_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_));   \
     } while (0)
 
+// A forward call whose h is in place.
+pi_status forward(pi_ctx *c, const pi_norm_residual_desc &d, NormP &p, const void *x, const void *y, const void *gate, void *x_out)
+{
+    if (!x) return ctx_fail(c, PI_ERR_ARG, "x is NULL");
+    if (y && !x_out) return ctx_fail(c, PI_ERR_ARG, "x_out is NULL");
+    if (!p.h && !x_out) return PI_OK;
+    const CtxView v = ctx_view(c);
+    const int xe = p.x32 ? 4 : 2;
+    if (pi_status st = check_elements(c, xe, {x, x_out})) return st;
+    if (pi_status st = check_elements(c, 2, {y, gate, p.w_pre, p.b_pre, p.w_post, p.b_post})) return st;
+    p.x = x, p.y = (const uint16_t *)y, p.gate = y ? (const uint16_t *)gate : nullptr, p.xo = x_out;
+    p.vec |= vb(x, p.ldx, xe, NV_X) | vb(x_out, p.ldxo, xe, NV_XO) | vb(y, p.ldy, 2, NV_Y) | vb(gate, p.ldgate, 2, NV_GATE);
+    DeviceGuard g(v.device);
+    CUN(d.dtype == PI_BF16 ? fwd<__nv_bfloat16>(p, v) : fwd<__half>(p, v));
+    return PI_OK;
+}
+
 } // namespace
 } // namespace pi
 
@@ -1384,21 +1423,36 @@ pi_status pi_norm_residual(pi_ctx *c, const pi_norm_residual_desc *desc, const p
     pi_norm_residual_desc d;
     if (pi_status st = check(c, desc, d)) return st;
     if (d.T == 0) return PI_OK;
-    if (!x) return ctx_fail(c, PI_ERR_ARG, "x is NULL");
-    if (y && !x_out) return ctx_fail(c, PI_ERR_ARG, "x_out is NULL");
     if ((h != nullptr) != (d.pre != PI_NORM_NONE)) return ctx_fail(c, PI_ERR_ARG, "h goes with a pre norm, and only with it");
-    if (!h && !x_out) return PI_OK;
-    const CtxView v = ctx_view(c);
+    if (pi_status st = check_elements(c, 2, {h})) return st;
     NormP p = params(d, q);
-    if (pi_status st = check_elements(c, p.x32 ? 4 : 2, {x, x_out})) return st;
-    if (pi_status st = check_elements(c, 2, {y, gate, h, p.w_pre, p.b_pre, p.w_post, p.b_post})) return st;
-    p.x = x, p.y = (const uint16_t *)y, p.gate = y ? (const uint16_t *)gate : nullptr, p.xo = x_out, p.h = (uint16_t *)h;
-    const int xe = p.x32 ? 4 : 2;
-    p.vec |= vb(x, p.ldx, xe, NV_X) | vb(x_out, p.ldxo, xe, NV_XO) | vb(y, p.ldy, 2, NV_Y) | vb(h, p.ldh, 2, NV_H) |
-             vb(gate, p.ldgate, 2, NV_GATE);
-    DeviceGuard g(v.device);
-    CUN(d.dtype == PI_BF16 ? fwd<__nv_bfloat16>(p, v) : fwd<__half>(p, v));
-    return PI_OK;
+    p.h = static_cast<uint16_t *>(h);
+    p.vec |= vb(h, p.ldh, 2, NV_H);
+    return forward(c, d, p, x, y, gate, x_out);
+}
+
+pi_status pi_norm_residual_mx(pi_ctx *c, const pi_norm_residual_desc *desc, int32_t kind, const pi_norm_residual_params *q,
+                              const void *x, const void *y, const void *gate, void *x_out, const pi_mx *h)
+{
+    if (!c) return PI_ERR_ARG;
+    if (!desc) return ctx_fail(c, PI_ERR_ARG, "desc is NULL");
+    if (kind != PI_MX8 && kind != PI_MX4) return ctx_fail(c, PI_ERR_ARG, "kind %d is not PI_MX8 or PI_MX4", kind);
+    pi_norm_residual_desc d = *desc;
+    d.ldh = 0; // (bytes, not elements)
+    if (pi_status st = check(c, &d, d)) return st;
+    if (d.pre == PI_NORM_NONE) return ctx_fail(c, PI_ERR_ARG, "h goes with a pre norm");
+    const int64_t row = mx_row_bytes(kind, d.d), ldh = desc->ldh ? desc->ldh : row;
+    if (ldh < row) return ctx_fail(c, PI_ERR_SHAPE, "h: row stride %lld below the row's %lld bytes", (long long)ldh, (long long)row);
+    if (ldh % 32) return ctx_fail(c, PI_ERR_ARG, "h: row stride %lld is not a multiple of 32 bytes", (long long)ldh);
+    if (d.T == 0) return PI_OK;
+    if (!h || !h->codes || !h->scales) return ctx_fail(c, PI_ERR_ARG, "h: codes or scales are NULL");
+    if ((uintptr_t)h->codes % 32 || (uintptr_t)h->scales % 16)
+        return ctx_fail(c, PI_ERR_ARG, "h: codes have to start at a multiple of 32 bytes, scales at one of 16");
+    NormP p = params(d, q);
+    p.h = static_cast<uint16_t *>(h->codes), p.ldh = ldh;
+    p.mx = kind, p.mx_tiles = mx_tiles(d.d), p.mx_scales = static_cast<uint8_t *>(h->scales);
+    p.vec |= NV_H;
+    return forward(c, d, p, x, y, gate, x_out);
 }
 
 pi_status pi_norm_residual_bwd_workspace(pi_ctx *c, const pi_norm_residual_desc *desc, size_t *bytes)

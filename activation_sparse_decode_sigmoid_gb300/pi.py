@@ -24,7 +24,7 @@ PI_OK = 0
 PI_ERR_ARG, PI_ERR_SHAPE, PI_ERR_CUDA, PI_ERR_OOM = -1, -2, -3, -4
 PI_ERR_NOT_LOADED, PI_ERR_TIMEOUT, PI_ERR_DEVICE_FLAG, PI_ERR_UNSUPPORTED = -5, -6, -7, -8
 PI_RELU, PI_REGLU, PI_SQRELU = 0, 1, 2
-PI_F16, PI_BF16, PI_Q4_0, PI_F32 = 0, 1, 2, 3
+PI_F16, PI_BF16, PI_Q4_0, PI_F32, PI_MX8, PI_MX4 = range(6)
 PI_FN_NONE, PI_FN_RELU, PI_FN_SQRELU, PI_FN_SIGMOID, PI_FN_SILU, PI_FN_GELU, PI_FN_GELU_TANH = range(7)
 PI_NORM_NONE, PI_NORM_RMS, PI_NORM_LAYER = 0, 1, 2
 
@@ -39,7 +39,8 @@ EXPORTS = ("pi_create", "pi_destroy", "pi_set_stream", "pi_load_layer", "pi_laye
            "pi_layerwise_min_batch", "pi_load_layer_shard", "pi_layer_shard", "pi_layer_partial",
            "pi_residual_add", "pi_linear_workspace", "pi_linear", "pi_linear_bwd", "pi_gated_ffn_workspace",
            "pi_gated_ffn", "pi_gated_ffn_bwd", "pi_norm_residual", "pi_norm_residual_bwd_workspace",
-           "pi_norm_residual_bwd")
+           "pi_norm_residual_bwd", "pi_mx_bytes", "pi_mx_quantize", "pi_mx_dequantize", "pi_mx_linear_workspace",
+           "pi_mx_linear", "pi_mx_gated_ffn_workspace", "pi_mx_gated_ffn", "pi_norm_residual_mx")
 
 
 class PiError(RuntimeError):
@@ -91,6 +92,17 @@ pi_norm_residual_grads = _struct("pi_norm_residual_grads",
 
 
 _lib = None
+
+pi_mx = _struct("pi_mx", ptr=("codes", "scales"))
+pi_mx_desc = _struct("pi_mx_desc", ("rows", "cols", "kind", "dtype"), (), ("ldx", "ldq"))
+pi_mx_linear_desc = _struct("pi_mx_linear_desc", ("T", "K", "N", "x_kind", "w_kind", "dtype", "out_dtype", "fn", "scale"),
+                            ("scale",), ("ldx", "ldw", "ldr", "ldy"))
+pi_mx_gated_ffn_desc = _struct("pi_mx_gated_ffn_desc", ("T", "d", "n", "x_kind", "w_kind", "dtype", "fn", "gated"), (),
+                               ("ldx", "ld_gate", "ld_up", "ld_down", "ldy"))
+# (the three matrices' pointers one after the other)
+pi_mx_gated_ffn_weights = _struct("pi_mx_gated_ffn_weights",
+                                  ptr=("gate_codes", "gate_scales", "up_codes", "up_scales", "down_codes", "down_scales",
+                                       "b_gate", "b_up", "b_down"))
 
 
 def load_library(path: str = LIB_PATH):
@@ -144,6 +156,14 @@ def load_library(path: str = LIB_PATH):
         "pi_norm_residual": (st, [P] * 8),
         "pi_norm_residual_bwd_workspace": (st, [P, P, P]),
         "pi_norm_residual_bwd": (st, [P] * 9 + [I32, P, ctypes.c_size_t]),
+        "pi_mx_bytes": (st, [I32, I32, I32, P, P]),
+        "pi_mx_quantize": (st, [P] * 4),
+        "pi_mx_dequantize": (st, [P] * 4),
+        "pi_mx_linear_workspace": (st, [P] * 3),
+        "pi_mx_linear": (st, [P] * 8 + [ctypes.c_size_t]),
+        "pi_mx_gated_ffn_workspace": (st, [P] * 3),
+        "pi_mx_gated_ffn": (st, [P] * 6 + [ctypes.c_size_t]),
+        "pi_norm_residual_mx": (st, [P, P, I32] + [P] * 6),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -429,6 +449,72 @@ def pi_norm_residual_bwd(ctx: int, desc, params, dx_out, dh, x_out, y, gate, gra
     rc = load_library().pi_norm_residual_bwd(ctx, _ref(desc), _ref(params), _ptr(dx_out), _ptr(dh), _ptr(x_out), _ptr(y),
                                              _ptr(gate), _ref(grads), int(accumulate), _ptr(ws), ws_bytes)
     _check(ctx, rc, "pi_norm_residual_bwd")
+
+
+def pi_mx_bytes(rows: int, cols: int, kind: int) -> tuple[int, int]:
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    rc = load_library().pi_mx_bytes(rows, cols, kind, ctypes.addressof(a), ctypes.addressof(b))
+    if rc:
+        raise PiError(rc, f"pi_mx_bytes: {rows} rows, {cols} columns, kind {kind}")
+    return a.value, b.value
+
+
+def pi_mx_quantize(ctx: int, desc, x, q) -> None:
+    _check(ctx, load_library().pi_mx_quantize(ctx, _ref(desc), _ptr(x), _ref(q)), "pi_mx_quantize")
+
+
+def pi_mx_dequantize(ctx: int, desc, q, y) -> None:
+    _check(ctx, load_library().pi_mx_dequantize(ctx, _ref(desc), _ref(q), _ptr(y)), "pi_mx_dequantize")
+
+
+def pi_mx_linear_workspace(ctx: int, desc) -> int:
+    n = ctypes.c_size_t()
+    _check(ctx, load_library().pi_mx_linear_workspace(ctx, _ref(desc), ctypes.addressof(n)), "pi_mx_linear_workspace")
+    return n.value
+
+
+def pi_mx_linear(ctx: int, desc, x, w, b, residual, y, ws, ws_bytes: int) -> None:
+    rc = load_library().pi_mx_linear(ctx, _ref(desc), _ref(x), _ref(w), _ptr(b), _ptr(residual), _ptr(y), _ptr(ws), ws_bytes)
+    _check(ctx, rc, "pi_mx_linear")
+
+
+def pi_mx_gated_ffn_workspace(ctx: int, desc) -> int:
+    n = ctypes.c_size_t()
+    _check(ctx, load_library().pi_mx_gated_ffn_workspace(ctx, _ref(desc), ctypes.addressof(n)), "pi_mx_gated_ffn_workspace")
+    return n.value
+
+
+def pi_mx_gated_ffn(ctx: int, desc, weights, x, y, ws, ws_bytes: int) -> None:
+    rc = load_library().pi_mx_gated_ffn(ctx, _ref(desc), _ref(weights), _ref(x), _ptr(y), _ptr(ws), ws_bytes)
+    _check(ctx, rc, "pi_mx_gated_ffn")
+
+
+def pi_norm_residual_mx(ctx: int, desc, kind: int, params, x, y, gate, x_out, h) -> None:
+    rc = load_library().pi_norm_residual_mx(ctx, _ref(desc), kind, _ref(params), _ptr(x), _ptr(y), _ptr(gate), _ptr(x_out),
+                                            _ref(h))
+    _check(ctx, rc, "pi_norm_residual_mx")
+
+
+class MxMatrix:
+    """A microscaled matrix [rows][cols] of kind PI_MX8 or PI_MX4: `codes`
+    uint8 [rows][bytes of a padded row], `scales` uint8 [row tiles][column
+    tiles][32][4][4] (include/pi.h has the layout).  ``Context.mx_quantize``
+    and ``Context.mx_empty`` make them; another program's are wrapped as they are."""
+
+    __slots__ = ("codes", "scales", "cols", "kind")
+
+    def __init__(self, codes, scales, cols: int, kind: int):
+        if kind != PI_MX8 and kind != PI_MX4:
+            raise PiError(PI_ERR_ARG, f"kind {kind} is not PI_MX8 or PI_MX4")
+        self.codes, self.scales, self.cols, self.kind = codes, scales, cols, kind
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def shape(self) -> tuple[int, int]:
+        return self.codes.shape[0], self.cols
 
 
 # ---------------------------------------------------------------- convenience wrapper
@@ -917,6 +1003,168 @@ class Context:
         if rc:
             _check(self.handle, rc, "pi_norm_residual_bwd")
         return {"dx": dx, "dy": dy, **out}
+
+    # -- microscaled matrices: the same block's forward side in 8 and 4 bits
+    def _mx(self, name, q, rows, cols, kind=None):
+        """(address of the codes, of the scales, row stride in bytes: 0 packed)"""
+        if q is None:
+            return 0, 0, 0
+        if not isinstance(q, MxMatrix):
+            self._mx_dims(name, q)
+        if kind is not None and q.kind != kind:
+            raise PiError(PI_ERR_ARG, f"{name} is of kind {q.kind}, expected {kind}")
+        if q.cols != cols:
+            raise PiError(PI_ERR_SHAPE, f"{name} has {q.cols} columns, expected {cols}")
+        u8 = (_torch or _import_torch()).uint8
+        B = (cols + 127) // 128
+        codes, ld = self._at(name + ".codes", q.codes, (rows, B * (128 if q.kind == PI_MX8 else 64)), u8)
+        s, want = q.scales, ((rows + 127) // 128, B, 32, 4, 4)
+        if s.dtype != u8 or s.device != self.torch_device or s.shape != want:
+            self._refuse(name + ".scales", s, want, u8)
+        if not s.is_contiguous():
+            raise PiError(PI_ERR_ARG, f"{name}.scales are not packed")
+        return codes, s.data_ptr(), ld
+
+    @staticmethod
+    def _mx_dims(name, q):
+        if not isinstance(q, MxMatrix):
+            raise PiError(PI_ERR_ARG, f"{name} is not an MxMatrix")
+        return q.shape
+
+    def mx_empty(self, rows: int, cols: int, kind: int) -> MxMatrix:
+        """A matrix for a call to write."""
+        if kind != PI_MX8 and kind != PI_MX4:
+            raise PiError(PI_ERR_ARG, f"kind {kind} is not PI_MX8 or PI_MX4")
+        u8 = (_torch or _import_torch()).uint8
+        B = (cols + 127) // 128
+        return MxMatrix(self._new((rows, B * (128 if kind == PI_MX8 else 64)), u8),
+                        self._new(((rows + 127) // 128, B, 32, 4, 4), u8), cols, kind)
+
+    def mx_quantize(self, x, kind: int = PI_MX8, out: MxMatrix | None = None) -> MxMatrix:
+        """x (float16, bfloat16 or float32 rows) in blocks of 32 columns that
+        share a scale; elements of 8 (PI_MX8) or 4 bits (PI_MX4)."""
+        code = self._code(x.dtype)
+        T, K = self._dims("x", x)
+        if out is None:
+            out = self.mx_empty(T, K, kind)
+        px, ldx = self._at("x", x, (T, K), x.dtype)
+        pc, ps, ldq = self._mx("out", out, T, K, kind)
+        desc, _ = self._plan(pi_mx_desc, (T, K, kind, code, ldx, ldq), None)
+        q = pi_mx(pc, ps)
+        self._s()
+        rc = _lib.pi_mx_quantize(self.handle, ctypes.addressof(desc), px, ctypes.addressof(q))
+        if rc:
+            _check(self.handle, rc, "pi_mx_quantize")
+        return out
+
+    def mx_dequantize(self, q: MxMatrix, dtype=None, out=None):
+        """The values of q in `dtype` (bfloat16 unless given, or out's)."""
+        T, K = self._mx_dims("q", q)
+        if out is None:
+            out = self._new((T, K), dtype or (_torch or _import_torch()).bfloat16)
+        code = self._code(out.dtype)
+        py, ldy = self._at("out", out, (T, K), dtype or out.dtype)
+        pc, ps, ldq = self._mx("q", q, T, K)
+        desc, _ = self._plan(pi_mx_desc, (T, K, q.kind, code, ldy, ldq), None)
+        m = pi_mx(pc, ps)
+        self._s()
+        rc = _lib.pi_mx_dequantize(self.handle, ctypes.addressof(desc), ctypes.addressof(m), py)
+        if rc:
+            _check(self.handle, rc, "pi_mx_dequantize")
+        return out
+
+    def mx_linear(self, x: MxMatrix, w: MxMatrix, b=None, *, fn=PI_FN_NONE, scale=1.0, residual=None, dtype=None, y=None):
+        """y = residual + scale * fn(x W^T + b) of microscaled x and W (kinds
+        8 and 4, 8 and 8, or 4 and 4 bits).  dtype: of b, and of y unless
+        a residual or y says otherwise (float32 residual stream); bfloat16
+        unless given."""
+        T, K = self._mx_dims("x", x)
+        N = self._mx_dims("w", w)[0]
+        if dtype is None:
+            t = b if b is not None else residual if residual is not None else y
+            torch = _torch or _import_torch()
+            dtype = torch.bfloat16 if t is None or t.dtype == torch.float32 else t.dtype
+        code = self._code16(dtype)
+        if y is None:
+            y = self._new((T, N), dtype if residual is None else residual.dtype)
+        out = self._code(y.dtype)
+        pxc, pxs, ldx = self._mx("x", x, T, K)
+        pwc, pws, ldw = self._mx("w", w, N, K)
+        pb, _ = self._at("b", b, (N,), dtype)
+        pr, ldr = self._at("residual", residual, (T, N), y.dtype)
+        py, ldy = self._at("y", y, (T, N), y.dtype)
+        desc, n = self._plan(pi_mx_linear_desc, (T, K, N, x.kind, w.kind, code, out, fn, scale, ldx, ldw, ldr, ldy),
+                             pi_mx_linear_workspace)
+        mx, mw = pi_mx(pxc, pxs), pi_mx(pwc, pws)
+        ws, pw = self._ws(n)
+        self._s()
+        rc = _lib.pi_mx_linear(self.handle, ctypes.addressof(desc), ctypes.addressof(mx), ctypes.addressof(mw), pb, pr, py, pw, n)
+        if rc:
+            _check(self.handle, rc, "pi_mx_linear")
+        return y
+
+    def mx_gated_ffn(self, x: MxMatrix, w_gate, w_up: MxMatrix, w_down: MxMatrix, b_gate=None, b_up=None, b_down=None, *,
+                     fn=PI_FN_RELU, dtype=None, y=None):
+        """y = Q(fn(x Wg^T + bg) * (x Wu^T + bu)) Wd^T + bd of microscaled x
+        and weights; Q quantises to x's kind.  w_gate None: fn(x Wu^T + bu)."""
+        T, d = self._mx_dims("x", x)
+        n = self._mx_dims("w_up", w_up)[0]
+        if dtype is None:
+            t = next((v for v in (b_gate, b_up, b_down, y) if v is not None), None)
+            dtype = (_torch or _import_torch()).bfloat16 if t is None else t.dtype
+        code = self._code16(dtype)
+        if y is None:
+            y = self._new((T, d), dtype)
+        pxc, pxs, ldx = self._mx("x", x, T, d)
+        gc, gs, ldg = self._mx("w_gate", w_gate, n, d, w_up.kind)
+        uc, us, ldu = self._mx("w_up", w_up, n, d)
+        dc, ds, ldd = self._mx("w_down", w_down, d, n, w_up.kind)
+        py, ldy = self._at("y", y, (T, d), dtype)
+        pbg, pbu = self._at("b_gate", b_gate, (n,), dtype)[0], self._at("b_up", b_up, (n,), dtype)[0]
+        pbd = self._at("b_down", b_down, (d,), dtype)[0]
+        desc, nb = self._plan(pi_mx_gated_ffn_desc, (T, d, n, x.kind, w_up.kind, code, fn, w_gate is not None, ldx, ldg, ldu,
+                                                     ldd, ldy), pi_mx_gated_ffn_workspace)
+        wts, mx = pi_mx_gated_ffn_weights(gc, gs, uc, us, dc, ds, pbg, pbu, pbd), pi_mx(pxc, pxs)
+        ws, pws = self._ws(nb)
+        self._s()
+        rc = _lib.pi_mx_gated_ffn(self.handle, ctypes.addressof(desc), ctypes.addressof(wts), ctypes.addressof(mx), py, pws, nb)
+        if rc:
+            _check(self.handle, rc, "pi_mx_gated_ffn")
+        return y
+
+    def norm_residual_mx(self, x, y=None, gate=None, *, kind: int = PI_MX8, pre=PI_NORM_RMS, post=PI_NORM_NONE, w_pre=None,
+                         b_pre=None, w_post=None, b_post=None, res_scale=1.0, branch_scale=1.0, gate_rows=0, eps=1e-5,
+                         dtype=None, x_out=None, h: MxMatrix | None = None):
+        """``norm_residual`` with h quantised to `kind`: (x', h)."""
+        xdt = x.dtype
+        xcode = self._code(xdt)
+        if y is not None:
+            dtype = y.dtype
+        elif dtype is None:
+            dtype = next((v.dtype for v in (w_pre, b_pre) if v is not None),
+                         (_torch or _import_torch()).bfloat16 if xcode == PI_F32 else xdt)
+        code = self._code16(dtype)
+        T, d = self._dims("x", x)
+        if x_out is None:
+            x_out = self._new((T, d), xdt)
+        if h is None:
+            h = self.mx_empty(T, d, kind)
+        px, ldx = self._at("x", x, (T, d), dtype if xcode != PI_F32 else xdt)
+        py, ldy = self._at("y", y, (T, d), dtype)
+        pg, ldg = self._at("gate", gate, (1 if gate_rows == 0 else -(-T // max(gate_rows, 1)), d), dtype)
+        po, ldo = self._at("x_out", x_out, (T, d), xdt)
+        hc, hs, ldh = self._mx("h", h, T, d, kind)
+        par = pi_norm_residual_params(self._at("w_pre", w_pre, (d,), dtype)[0], self._at("b_pre", b_pre, (d,), dtype)[0],
+                                      self._at("w_post", w_post, (d,), dtype)[0], self._at("b_post", b_post, (d,), dtype)[0])
+        desc, _ = self._plan(pi_norm_residual_desc, (T, d, xcode, code, code, pre, post, gate_rows, res_scale, branch_scale,
+                                                     eps, ldx, ldo, ldy, ldh, ldg), None)
+        mh = pi_mx(hc, hs)
+        self._s()
+        rc = _lib.pi_norm_residual_mx(self.handle, ctypes.addressof(desc), kind, ctypes.addressof(par), px, py, pg, po,
+                                      ctypes.addressof(mh))
+        if rc:
+            _check(self.handle, rc, "pi_norm_residual_mx")
+        return x_out, h
 
     def set_trace(self, x_trace=None, xhat_trace=None, idx_trace=None, count_trace=None) -> None:
         pi_set_trace(self.handle, x_trace, xhat_trace, idx_trace, count_trace)

@@ -69,8 +69,9 @@ typedef int32_t pi_status;
  *   PI_SQRELU  a_i = max(W_up[i].x_hat + b_i, 0)^2
  * A neuron is active (its activation nonzero) exactly when its ReLU is. */
 typedef enum { PI_RELU = 0, PI_REGLU = 1, PI_SQRELU = 2 } pi_act;
-typedef enum { PI_F16 = 0, PI_BF16 = 1, PI_Q4_0 = 2, PI_F32 = 3 } pi_dtype;
-/* (PI_F32: the residual stream and gradients of the block operators below; no layer type) */
+typedef enum { PI_F16 = 0, PI_BF16 = 1, PI_Q4_0 = 2, PI_F32 = 3, PI_MX8 = 4, PI_MX4 = 5 } pi_dtype;
+/* (PI_F32: the residual stream and gradients of the block operators below; PI_MX8, PI_MX4: the
+ * microscaled matrices at the end; no layer types) */
 
 /* Shape and types of one FFN layer and its predictor.
  *   d_model in [8, 8192], multiple of 8 (of 32 for Q4_0 weights)
@@ -578,6 +579,112 @@ pi_status pi_norm_residual_bwd_workspace(pi_ctx *ctx, const pi_norm_residual_des
 pi_status pi_norm_residual_bwd(pi_ctx *ctx, const pi_norm_residual_desc *desc, const pi_norm_residual_params *p,
                                const void *dx_out, const void *dh, const void *x_out, const void *y, const void *gate,
                                const pi_norm_residual_grads *grads, int32_t accumulate, void *ws, size_t ws_bytes);
+
+/* ---------------------------------------------------------------- microscaled matrices
+ * The block operators' forward side with weights of 4 or 8 bits and
+ * activations of 8 or 4: a layer's weights are read once per token, so 4 bits
+ * cut that time by 3.8, and a prompt's products run at two (one operand of 8
+ * bits) or four times (both of 4) the 16-bit tensor rate.  The format is the
+ * OCP microscaling one (MXFP8 E4M3, MXFP4 E2M1).  Training keeps the 16-bit
+ * operators above.
+ *
+ * A matrix [rows][cols]: blocks of 32 columns of a row share a scale
+ * 2^(c - 127), c one byte (255: every value of the block is NaN).
+ *   PI_MX8  elements e4m3 (largest 448), a byte each
+ *   PI_MX4  elements e2m1 (0 0.5 1 1.5 2 3 4 6 and their negatives), two to a
+ *           byte, the even column in the low half
+ *   codes   rows of cols rounded up to 128 elements (128 or 64 bytes per 128),
+ *           starting on 32-byte boundaries
+ *   scales  tiles of 128 rows x 4 blocks, 512 bytes each, the tiles of 128
+ *           rows one after the other (starting on a 16-byte boundary): with
+ *           B = cols rounded up to 128, divided by 128, row r's block b is at
+ *           ((r / 128) B + b / 4) 512 + (r % 32) 16 + (r % 128 / 32) 4 + b % 4
+ * Codes and scales of what pads rows and columns are 0, as the calls that
+ * write a matrix leave them; another program's matrix has to be laid out
+ * so too (a code of NaN in a padded column would reach the products).
+ *
+ * Quantisation: a block's scale is the least power of two s (from 2^-127) with
+ * amax / s at most the type's largest value; elements are v / s rounded to
+ * nearest, ties to even.  So no element is cut off, and a block's rounding is at
+ * most half a step of its largest element's.  A block with an infinity or a
+ * NaN is NaN as a whole; one of zeros has scale 2^-127 (c 0).
+ *
+ * The common rules of the block operators hold here too (T may be 0; outputs
+ * do not overlap inputs; workspaces; one stream; fixed order of sums), with these
+ * differences: matrices of these kinds are used in place, and rows of 16- or
+ * 32-bit values may start at any element. */
+typedef struct {
+    void *codes, *scales;
+} pi_mx;
+
+/* Bytes of a packed matrix's codes and scales.  rows in [0, 2^22], cols in [1, 2^20]. */
+pi_status pi_mx_bytes(int32_t rows, int32_t cols, int32_t kind, size_t *codes, size_t *scales);
+
+typedef struct {
+    int32_t rows, cols;
+    int32_t kind;  /* PI_MX8 or PI_MX4 */
+    int32_t dtype; /* of x or y: PI_F16, PI_BF16 or PI_F32 */
+    int64_t ldx;   /* row stride of x or y, elements; 0 = packed */
+    int64_t ldq;   /* row stride of q's codes, bytes, a multiple of 32; 0 = packed */
+} pi_mx_desc;
+
+/* q = x quantised. */
+pi_status pi_mx_quantize(pi_ctx *ctx, const pi_mx_desc *desc, const void *x, const pi_mx *q);
+
+/* y = the values of q, rounded to dtype (PI_F32 and, but for values past its
+ * range, PI_BF16 hold them exactly; PI_F16 lacks scales far from 1). */
+pi_status pi_mx_dequantize(pi_ctx *ctx, const pi_mx_desc *desc, const pi_mx *q, void *y);
+
+/* pi_linear of microscaled x [T][K] and W [N][K]:
+ *     y = r + scale * fn(x W^T + b)
+ * Kinds of (x, W): (PI_MX8, PI_MX4), (PI_MX8, PI_MX8), (PI_MX4, PI_MX4);
+ * (PI_MX4, PI_MX8) is PI_ERR_UNSUPPORTED.  Products are accumulated in fp32;
+ * bias, activation and residual are computed in fp32 and rounded once.  b and
+ * residual may be NULL; y may be the residual itself (same stride). */
+typedef struct {
+    int32_t T, K, N;
+    int32_t x_kind, w_kind;
+    int32_t dtype;      /* of b: PI_F16 or PI_BF16 */
+    int32_t out_dtype;  /* of y and r: dtype or PI_F32 */
+    int32_t fn;         /* pi_fn */
+    float scale;        /* finite */
+    int64_t ldx, ldw;   /* bytes */
+    int64_t ldr, ldy;   /* elements */
+} pi_mx_linear_desc;
+
+pi_status pi_mx_linear_workspace(pi_ctx *ctx, const pi_mx_linear_desc *desc, size_t *bytes);
+pi_status pi_mx_linear(pi_ctx *ctx, const pi_mx_linear_desc *desc, const pi_mx *x, const pi_mx *w, const void *b,
+                       const void *residual, void *y, void *ws, size_t ws_bytes);
+
+/* pi_gated_ffn of microscaled x [T][d], Wg and Wu [n][d], Wd [d][n]:
+ *     gated:  a = fn(x Wg^T + bg) * (x Wu^T + bu),  else  a = fn(x Wu^T + bu)
+ *     y = Q(a) Wd^T + bd
+ * Q quantises a, from fp32, to x's kind: what goes on into another product is
+ * rounded, as in pi_gated_ffn, where the products take 16 bits.  Kinds as for
+ * pi_mx_linear, the three weight matrices alike. */
+typedef struct {
+    int32_t T, d, n;
+    int32_t x_kind, w_kind;
+    int32_t dtype;      /* of y and the biases: PI_F16 or PI_BF16 */
+    int32_t fn;         /* pi_fn */
+    int32_t gated;      /* 0 or 1 */
+    int64_t ldx, ld_gate, ld_up, ld_down; /* bytes */
+    int64_t ldy;        /* elements */
+} pi_mx_gated_ffn_desc;
+
+typedef struct {
+    pi_mx gate, up, down; /* gate NULL if not gated */
+    const void *b_gate, *b_up, *b_down; /* NULL = 0 */
+} pi_mx_gated_ffn_weights;
+
+pi_status pi_mx_gated_ffn_workspace(pi_ctx *ctx, const pi_mx_gated_ffn_desc *desc, size_t *bytes);
+pi_status pi_mx_gated_ffn(pi_ctx *ctx, const pi_mx_gated_ffn_desc *desc, const pi_mx_gated_ffn_weights *w, const pi_mx *x,
+                          void *y, void *ws, size_t ws_bytes);
+
+/* pi_norm_residual with h quantised, from fp32, to `kind`; pre is a norm, and
+ * h is given.  desc's ldh counts h's bytes (a multiple of 32; 0 = packed). */
+pi_status pi_norm_residual_mx(pi_ctx *ctx, const pi_norm_residual_desc *desc, int32_t kind, const pi_norm_residual_params *p,
+                              const void *x, const void *y, const void *gate, void *x_out, const pi_mx *h);
 
 #ifdef __cplusplus
 }
