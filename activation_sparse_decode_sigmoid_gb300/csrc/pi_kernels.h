@@ -266,6 +266,13 @@ cudaError_t launch_list_all(const PredParams &p, cudaStream_t s);
 // a 2D TMA map over a row-major 16-bit matrix: box = 64 columns x box_rows rows, 128-byte swizzle
 cudaError_t encode_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
                        uint32_t box_rows);
+// microscaled matrices: 128 bytes of a row's codes; 128 codes of 4 bits, each 16 of them spread over 16 bytes of
+// shared memory (the first 8 bytes hold them), as the MMA of mixed types takes them (base and rows on 32-byte
+// boundaries, cols a multiple of 128); tiles of scales, 512 bytes each
+cudaError_t encode_map_bytes(CUtensorMap *map, const void *base, uint64_t row, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
+cudaError_t encode_map_nibbles(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
+cudaError_t encode_map_scales(CUtensorMap *map, const void *base, uint64_t tiles, uint64_t row_tiles, uint32_t box_tiles,
+                              uint32_t box_row_tiles);
 
 cudaError_t launch_permute_rows(const void *src, void *dst, const int32_t *perm, int rows, size_t rowBytes,
                                 cudaStream_t s, size_t dstStride = 0);

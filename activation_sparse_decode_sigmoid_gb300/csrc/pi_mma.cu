@@ -675,8 +675,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 
 } // namespace
 
-cudaError_t encode_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
-                       uint32_t box_rows)
+static cudaError_t encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols, uint64_t rows,
+                          uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle)
 {
     static EncodeTiledFn fn = nullptr;
     if (!fn) {
@@ -688,12 +688,34 @@ cudaError_t encode_map(CUtensorMap *map, const void *base, uint64_t cols, uint64
     }
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t es[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = fn(map, type, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_map(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
+                       uint32_t box_rows)
+{
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, base, cols, rows, row_bytes, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t encode_map_bytes(CUtensorMap *map, const void *base, uint64_t row, uint64_t rows, uint64_t row_bytes, uint32_t box_rows)
+{
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, row, rows, row_bytes, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t encode_map_nibbles(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes, uint32_t box_rows)
+{
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, base, cols, rows, row_bytes, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t encode_map_scales(CUtensorMap *map, const void *base, uint64_t tiles, uint64_t row_tiles, uint32_t box_tiles,
+                              uint32_t box_row_tiles)
+{
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, base, tiles * 128, row_tiles, tiles * 512, box_tiles * 128, box_row_tiles,
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 cudaError_t launch_ffn_merge(const MmaParams &p, bool bf16, int nks, int grid, cudaStream_t s)

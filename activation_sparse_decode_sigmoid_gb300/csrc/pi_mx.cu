@@ -186,12 +186,13 @@ template <typename T, int MODE> cudaError_t product_mode(const Gemm &g, const Ct
                                : launch_pdl(mx_product<T, MODE, PI_MX4, PI_MX4>, grid, dim3(256), 0, v.stream, p);
 }
 
-cudaError_t launch_product(const Gemm &g, bool bf16, const CtxView &v, void *)
+cudaError_t launch_product(const Gemm &g, bool bf16, const CtxView &v, void *ws)
 {
+    if (skinny_takes(g)) return launch_skinny(g, bf16, v, ws);
     if (g.mode == EPI_GATED) return bf16 ? product_mode<__nv_bfloat16, EPI_GATED>(g, v) : product_mode<__half, EPI_GATED>(g, v);
     return bf16 ? product_mode<__nv_bfloat16, EPI_LINEAR>(g, v) : product_mode<__half, EPI_LINEAR>(g, v);
 }
-size_t product_workspace(const Gemm &, const CtxView &) { return 0; }
+size_t product_workspace(const Gemm &g, const CtxView &v) { return skinny_takes(g) ? skinny_workspace(g, v) : 0; }
 
 // ------------------------------------------------------------------ checks
 bool is16(int dt) { return dt == PI_F16 || dt == PI_BF16; }
