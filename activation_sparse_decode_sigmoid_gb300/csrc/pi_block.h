@@ -73,6 +73,11 @@ struct Gemm {
 size_t gemm_workspace(const Gemm &g, const CtxView &v);
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
+// Products of microscaled operands that skinny_tc does not take, by their types.
+cudaError_t launch_gemm_mx88(const Gemm &g, bool bf16, const CtxView &v, void *ws);
+cudaError_t launch_gemm_mx84(const Gemm &g, bool bf16, const CtxView &v, void *ws);
+cudaError_t launch_gemm_mx44(const Gemm &g, bool bf16, const CtxView &v, void *ws);
+
 // The same for up to four products that are independent of one another, in one
 // launch; their epilogues are EPI_LINEAR without bias, activation, scale or z.
 size_t gemms_workspace(const Gemm *g, int n, const CtxView &v);

@@ -118,82 +118,6 @@ template <typename T, int KIND> __global__ void __launch_bounds__(32 * kWarps) m
     }
 }
 
-// ------------------------------------------------------------------ products
-// 64 x 64 outputs a CTA, 32 of k at a time through shared memory as fp32; a
-// thread has 8 columns of two rows.
-struct MxGemmP {
-    Gemm g;
-};
-
-template <int KIND> __device__ __forceinline__ void stage32(float (*s)[33], const uint8_t *codes, int64_t ld, const uint8_t *scales, int tiles,
-                                                            int r0, int rows, int k)
-{
-    const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;
-    float v[8] = {};
-    if (r0 + r < rows) {
-        uint2 q;
-        const uint8_t *row = codes + (int64_t)(r0 + r) * ld;
-        if (KIND == PI_MX8) q = *reinterpret_cast<const uint2 *>(row + k + c);
-        else q = make_uint2(*reinterpret_cast<const uint32_t *>(row + ((k + c) >> 1)), 0);
-        mx_unpack8<KIND>(q, v);
-        const float m = mx_power(scales[mx_scale_at(r0 + r, k >> 7, tiles) + ((k >> 5) & 3)]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= m;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[r][c + i] = v[i];
-}
-
-template <typename T, int MODE, int AK, int BK> __global__ void __launch_bounds__(256) mx_product(const __grid_constant__ MxGemmP p)
-{
-    constexpr int NB = MODE == EPI_GATED ? 2 : 1;
-    __shared__ float sa[64][33], sb[NB][64][33];
-    pdl_enter();
-    const Gemm &g = p.g;
-    const int tn = ((g.N + 127) / 128 * 128) / 64, m0 = (int)(blockIdx.x / tn) * 64, n0 = (int)(blockIdx.x % tn) * 64;
-    const int tiles = mx_tiles(g.K[0]), cg = (threadIdx.x & 7) * 8, rp = (threadIdx.x >> 3) * 2;
-    float acc[NB][2][8] = {};
-    for (int k = 0; k < g.K[0]; k += 32) {
-        stage32<AK>(sa, static_cast<const uint8_t *>(g.a[0].p), g.a[0].ld, g.sa, tiles, m0, g.M, k);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) stage32<BK>(sb[b], static_cast<const uint8_t *>(g.b[b].p), g.b[b].ld, g.sb[b], tiles, n0, g.N, k);
-        __syncthreads();
-#pragma unroll 4
-        for (int j = 0; j < 32; ++j)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float w = sb[b][cg + i][j];
-                    acc[b][0][i] = fmaf(sa[rp][j], w, acc[b][0][i]), acc[b][1][i] = fmaf(sa[rp + 1][j], w, acc[b][1][i]);
-                }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = m0 + rp + i, col = n0 + cg;
-        if (g.e.mx) epilogue8_mx<T, MODE, 1>(g.e, g.N, row, col, row < g.M, acc[0][i], acc[NB - 1][i]);
-        else if (row < g.M && col < g.N) epilogue8<T, MODE>(g.e, g.N, row, col, acc[0][i], acc[NB - 1][i]);
-    }
-}
-
-template <typename T, int MODE> cudaError_t product_mode(const Gemm &g, const CtxView &v)
-{
-    const dim3 grid((unsigned)((g.M + 63) / 64) * (mx_tiles(g.N) * 2));
-    const MxGemmP p = {g};
-    return g.ops == OPS_MX88   ? launch_pdl(mx_product<T, MODE, PI_MX8, PI_MX8>, grid, dim3(256), 0, v.stream, p)
-           : g.ops == OPS_MX84 ? launch_pdl(mx_product<T, MODE, PI_MX8, PI_MX4>, grid, dim3(256), 0, v.stream, p)
-                               : launch_pdl(mx_product<T, MODE, PI_MX4, PI_MX4>, grid, dim3(256), 0, v.stream, p);
-}
-
-cudaError_t launch_product(const Gemm &g, bool bf16, const CtxView &v, void *ws)
-{
-    if (skinny_takes(g)) return launch_skinny(g, bf16, v, ws);
-    if (g.mode == EPI_GATED) return bf16 ? product_mode<__nv_bfloat16, EPI_GATED>(g, v) : product_mode<__half, EPI_GATED>(g, v);
-    return bf16 ? product_mode<__nv_bfloat16, EPI_LINEAR>(g, v) : product_mode<__half, EPI_LINEAR>(g, v);
-}
-size_t product_workspace(const Gemm &g, const CtxView &v) { return skinny_takes(g) ? skinny_workspace(g, v) : 0; }
-
 // ------------------------------------------------------------------ checks
 bool is16(int dt) { return dt == PI_F16 || dt == PI_BF16; }
 bool is_float(int dt) { return is16(dt) || dt == PI_F32; }
@@ -349,7 +273,7 @@ pi_status check_ffn(pi_ctx *c, const pi_mx_gated_ffn_desc *desc, const CtxView &
     if (!d.T) return PI_OK;
     f.codes = ((size_t)d.T * lda + 255) / 256 * 256;
     f.scales = (size_t)mx_scale_bytes(d.T, d.n);
-    f.gemm = std::max(product_workspace(u, v), product_workspace(w, v));
+    f.gemm = std::max(gemm_workspace(u, v), gemm_workspace(w, v));
     return PI_OK;
 }
 
@@ -386,7 +310,7 @@ pi_status pi_mx_linear_workspace(pi_ctx *c, const pi_mx_linear_desc *desc, size_
     pi_mx_linear_desc d;
     Gemm g;
     if (pi_status st = check_linear(c, desc, d, g)) return st;
-    *bytes = d.T ? product_workspace(g, ctx_view(c)) : 0;
+    *bytes = d.T ? gemm_workspace(g, ctx_view(c)) : 0;
     return PI_OK;
 }
 
@@ -405,7 +329,7 @@ pi_status pi_mx_linear(pi_ctx *c, const pi_mx_linear_desc *desc, const pi_mx *x,
     if (pi_status st = check_elements(c, 2, {b})) return st;
     if (pi_status st = check_elements(c, oe, {residual, y})) return st;
     const CtxView v = ctx_view(c);
-    if (pi_status st = check_ws(c, ws, ws_bytes, product_workspace(g, v))) return st;
+    if (pi_status st = check_ws(c, ws, ws_bytes, gemm_workspace(g, v))) return st;
     set_mx(g.a[0], g.sa, *x, d.ldx);
     set_mx(g.b[0], g.sb[0], *w, d.ldw);
     Epi &e = g.e;
@@ -413,7 +337,7 @@ pi_status pi_mx_linear(pi_ctx *c, const pi_mx_linear_desc *desc, const pi_mx *x,
     e.vec = (residual && aligned16(residual, d.ldr, oe) ? V_RES : 0u) | (aligned16(y, d.ldy, oe) ? V_OUT : 0u) |
             (b && aligned16(b, 0, 2) ? V_BIAS : 0u);
     DeviceGuard guard(v.device);
-    CUX(launch_product(g, d.dtype == PI_BF16, v, ws));
+    CUX(launch_gemm(g, d.dtype == PI_BF16, v, ws));
     return PI_OK;
 }
 
@@ -467,8 +391,8 @@ pi_status pi_mx_gated_ffn(pi_ctx *c, const pi_mx_gated_ffn_desc *desc, const pi_
     o.e.vec = (aligned16(y, d.ldy, 2) ? V_OUT : 0u) | (w->b_down && aligned16(w->b_down, 0, 2) ? V_BIAS : 0u);
     void *gws = base + f.codes + f.scales;
     DeviceGuard guard(v.device);
-    CUX(launch_product(u, d.dtype == PI_BF16, v, gws));
-    CUX(launch_product(o, d.dtype == PI_BF16, v, gws));
+    CUX(launch_gemm(u, d.dtype == PI_BF16, v, gws));
+    CUX(launch_gemm(o, d.dtype == PI_BF16, v, gws));
     return PI_OK;
 }
 

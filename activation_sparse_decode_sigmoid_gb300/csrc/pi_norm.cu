@@ -176,13 +176,14 @@ __device__ __forceinline__ void norm_store_mx(const NormP &p, int64_t t, int c, 
 }
 
 // Forward: one CTA per token, the row in registers.
-template <typename T, int V> __global__ void __launch_bounds__(1024) norm_fwd(const __grid_constant__ NormP p)
+// MX: h is microscaled.
+template <typename T, int V, bool MX> __global__ void __launch_bounds__(1024) norm_fwd(const __grid_constant__ NormP p)
 {
     __shared__ float buf[128];
     int flip = 0;
     pdl_enter();
     const int64_t t = blockIdx.x;
-    if (t >= p.Tn) { // (microscaled h: CTAs behind the rows)
+    if (MX && t >= p.Tn) { // CTAs behind the rows
         mx_pad_scales(p.mx_scales, p.Tn, p.mx_tiles, (t - p.Tn) * blockDim.x + threadIdx.x, (int64_t)(gridDim.x - p.Tn) * blockDim.x);
         return;
     }
@@ -222,7 +223,7 @@ template <typename T, int V> __global__ void __launch_bounds__(1024) norm_fwd(co
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8, n = p.d - c;
-        if (p.mx) norm_store_mx(p, t, c, x[i]);
+        if (MX) norm_store_mx(p, t, c, x[i]);
         else if (n > 0) store8<T>(p.h + t * p.ldh + c, n, p.vec & NV_H, x[i]);
     }
 }
@@ -652,7 +653,7 @@ __device__ __forceinline__ void pipe_settle()
 // One barrier a row: behind it lie all warps' shares of the statistics of x'
 // and, computed ahead about each warp's own mean, of the next row's y (4096 x
 // 7168 with both norms: 72 us, 84 % of the copy rate; with three barriers 75).
-template <typename T, bool X32, int V>
+template <typename T, bool X32, int V, bool MX>
 __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_constant__ NormP p, const __grid_constant__ PipeP q)
 {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_co
         rx = lane_of(r, 0), rz = lane_of(r, 16);
         cx = (wmx - lane_of(mean, 0)) * rx, cz = (wmz - lane_of(mean, 16)) * rz;
     };
-    if (p.mx) mx_pad_scales(p.mx_scales, p.Tn, p.mx_tiles, (int64_t)blockIdx.x * blockDim.x + tid, (int64_t)gridDim.x * blockDim.x);
+    if (MX) mx_pad_scales(p.mx_scales, p.Tn, p.mx_tiles, (int64_t)blockIdx.x * blockDim.x + tid, (int64_t)gridDim.x * blockDim.x);
     bool ok = true;
     if (r0 < r1) {
         ok = mbar_wait_bounded(full, 0, q);
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) norm_fwd_pipe(const __grid_co
                 unpack8<T>(wp[i], w8), unpack8<T>(bp[i], b8);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[i][j] = fmaf(fmaf(x[i][j], rx, cx), w8[j], b8[j]);
-                if (p.mx) norm_store_mx(p, t, c[i], x[i]);
+                if (MX) norm_store_mx(p, t, c[i], x[i]);
                 else if (on[i]) store8<T>(p.h + (int64_t)t * p.ldh + c[i], 8, true, x[i]);
             }
         }
@@ -1192,12 +1193,12 @@ __global__ void __launch_bounds__(32 * kJoinLanes) norm_bwd_join(const __grid_co
     if (p.dgate && groups == 1 && !p.per_token) put<T>(p, p.dgate, c, p.bs * fmaf(w, v[4], b * v[5]));
 }
 
-template <typename T, int V> cudaError_t launch_fwd(const NormP &p, cudaStream_t s)
+template <typename T, int V, bool MX> cudaError_t launch_fwd(const NormP &p, cudaStream_t s)
 {
     const int nt = ((p.d + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
     // (16 rows of a tile's scales a CTA more, where a microscaled h leaves some)
-    const int pad = p.mx ? (((128 - (p.Tn & 127)) & 127) + 15) / 16 : 0;
-    return launch_pdl(norm_fwd<T, V>, dim3(p.Tn + pad), dim3(nt), 0, s, p);
+    const int pad = MX ? (((128 - (p.Tn & 127)) & 127) + 15) / 16 : 0;
+    return launch_pdl(norm_fwd<T, V, MX>, dim3(p.Tn + pad), dim3(nt), 0, s, p);
 }
 
 // The ring of a pipelined launch: rows of up to kPipeMaxD elements, all 16-byte
@@ -1259,19 +1260,20 @@ template <auto KERN> cudaError_t run_pipe(const NormP &p, const Pipe &o, cudaStr
 // flight at once answers sooner.
 constexpr int kPipeRows = 2;
 
-template <typename T> cudaError_t fwd(const NormP &p, const CtxView &c)
+template <typename T, bool MX> cudaError_t fwd_as(const NormP &p, const CtxView &c)
 {
     Pipe o;
     const bool row_gate = p.gate && p.gate_rows == 1;
     if (p.Tn >= kPipeRows * c.sms && plan_pipe(p, false, row_gate, c, o)) {
         if (p.x32)
-            return o.v == 1 ? run_pipe<norm_fwd_pipe<T, true, 1>>(p, o, c.stream)
-                            : run_pipe<norm_fwd_pipe<T, true, 2>>(p, o, c.stream);
-        return o.v == 1 ? run_pipe<norm_fwd_pipe<T, false, 1>>(p, o, c.stream)
-                        : run_pipe<norm_fwd_pipe<T, false, 2>>(p, o, c.stream);
+            return o.v == 1 ? run_pipe<norm_fwd_pipe<T, true, 1, MX>>(p, o, c.stream)
+                            : run_pipe<norm_fwd_pipe<T, true, 2, MX>>(p, o, c.stream);
+        return o.v == 1 ? run_pipe<norm_fwd_pipe<T, false, 1, MX>>(p, o, c.stream)
+                        : run_pipe<norm_fwd_pipe<T, false, 2, MX>>(p, o, c.stream);
     }
-    return p.d <= 8192 ? launch_fwd<T, 1>(p, c.stream) : launch_fwd<T, 2>(p, c.stream);
+    return p.d <= 8192 ? launch_fwd<T, 1, MX>(p, c.stream) : launch_fwd<T, 2, MX>(p, c.stream);
 }
+template <typename T> cudaError_t fwd(const NormP &p, const CtxView &c) { return p.mx ? fwd_as<T, true>(p, c) : fwd_as<T, false>(p, c); }
 
 template <typename T, bool X32, bool FULL> cudaError_t bwd_pipe(const NormP &p, const Pipe &o, cudaStream_t s)
 {
