@@ -73,7 +73,8 @@ struct Gemm {
 size_t gemm_workspace(const Gemm &g, const CtxView &v);
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
-// Products of microscaled operands that skinny_tc does not take, by their types.
+// Products of microscaled operands: of up to kSkinnyRows rows of A, without a workspace (pi_mx_skinny.cu); others by their types.
+cudaError_t launch_mx_skinny(const Gemm &g, bool bf16, const CtxView &v);
 cudaError_t launch_gemm_mx88(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 cudaError_t launch_gemm_mx84(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 cudaError_t launch_gemm_mx44(const Gemm &g, bool bf16, const CtxView &v, void *ws);

@@ -24,16 +24,18 @@ template <typename T> cudaError_t run_mode(const Gemm *g, int n, const CtxView &
 
 size_t gemm_workspace(const Gemm &g, const CtxView &v)
 {
+    if (g.ops != OPS_16 && g.M <= kSkinnyRows) return 0;
     return skinny_takes(g) ? skinny_workspace(g, v) : plan_group(&g, 1, v.sms).bytes;
 }
 
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws)
 {
-    if (skinny_takes(g)) return launch_skinny(g, bf16, v, ws);
     if (g.ops != OPS_16)
-        return g.ops == OPS_MX88   ? launch_gemm_mx88(g, bf16, v, ws)
+        return g.M <= kSkinnyRows    ? launch_mx_skinny(g, bf16, v)
+               : g.ops == OPS_MX88   ? launch_gemm_mx88(g, bf16, v, ws)
                : g.ops == OPS_MX84 ? launch_gemm_mx84(g, bf16, v, ws)
                                    : launch_gemm_mx44(g, bf16, v, ws);
+    if (skinny_takes(g)) return launch_skinny(g, bf16, v, ws);
     return bf16 ? run_mode<__nv_bfloat16>(&g, 1, v, ws) : run_mode<__half>(&g, 1, v, ws);
 }
 

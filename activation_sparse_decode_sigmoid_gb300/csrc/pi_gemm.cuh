@@ -65,6 +65,7 @@
 #include "pi_epi.cuh"
 #include "pi_kernels.h"
 #include "pi_mx_tc.cuh"
+#include "pi_pair.cuh"
 #include "pi_tc.cuh"
 
 namespace pi {
@@ -187,32 +188,6 @@ template <int NP, bool MX> struct Walk {
 };
 
 // ------------------------------------------------------------------ pair helpers
-__device__ __forceinline__ uint32_t cta_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// address of the first CTA's copy of a shared-memory object
-__device__ __forceinline__ uint32_t in_first(uint32_t addr)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-    return r;
-}
-
-__device__ __forceinline__ void arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // a box of 64 columns into this CTA's shared memory; the bytes count on `bar`, which may be the first CTA's
 __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *tm, int col, int row, uint32_t bar)
 {
@@ -277,15 +252,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32])
                  :
                  : "memory");
     asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-
-// After a failure: copies and MMAs in flight finish within microseconds; the
-// CTA stays for a bounded time that covers them.
-__device__ __forceinline__ void linger()
-{
-    const uint64_t t0 = gtimer();
-    while (gtimer() - t0 < 5000000ull) {
-    }
 }
 
 // ------------------------------------------------------------------ boxes of the epilogue

@@ -23,12 +23,10 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "pi_block.h"
 #include "pi_epi.cuh"
 #include "pi_kernels.h"
-#include "pi_mx_tc.cuh"
 #include "pi_tc.cuh"
 
 namespace pi {
@@ -40,7 +38,6 @@ constexpr int kMaxRing = 12;
 
 struct SkParams {
     CUtensorMap mw[2], mx;
-    CUtensorMap msw[2], msx; // microscaled operands' scales
     int T, Tp, N;         // tokens, rounded up to 16; features of one weight matrix
     int tn, tiles, KT;    // tiles of one matrix, of all; k steps
     int parts, smax;
@@ -59,12 +56,8 @@ __host__ __device__ inline int sk_part_of(int64_t units, int64_t u, int parts)
     return (int)(((u + 1) * parts + units - 1) / units - 1);
 }
 
-// Tensor memory: two accumulators of up to 128 columns; four sets of scales, of W in the first 16 columns of a set
-constexpr uint32_t kSkScales = 256, kSkSet = 32, kSkSetX = 16;
-
-template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc(const __grid_constant__ SkParams p)
+template <typename T> __global__ void __launch_bounds__(kSkThreads, 1) skinny_tc(const __grid_constant__ SkParams p)
 {
-    using O = Ops<OPS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     using H = H16<T>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -79,8 +72,7 @@ template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) 
         for (int s = 0; s < 2; ++s) mbar_init1(acc_full + s), mbar_init(acc_empty + s, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    constexpr uint32_t kCols = O::mx ? 512 : 256;
-    const uint32_t tmem = tmem_alloc(tslot, kCols);
+    const uint32_t tmem = tmem_alloc(tslot, 256); // two accumulators of up to 128 columns
     if (!(p.early && warp == 4)) pdl_enter();
     const int64_t units = (int64_t)p.tiles * p.KT;
     int64_t u = sk_range(units, (int)blockIdx.x, p.parts);
@@ -90,21 +82,12 @@ template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) 
     if (warp == 4) {
         Cur cur(0, S);
         uint32_t round = 0;
-        constexpr uint32_t sfB = O::mx ? 512u * O::words : 0u; // scales of W, and of x, to a step
-        const uint32_t bytes = 128u * mx_row_tx(O::nibbles) + (uint32_t)p.Tp * 128u + 2 * sfB, sf = kWTile + (uint32_t)p.Tp * 128u;
+        const uint32_t bytes = kWTile + (uint32_t)p.Tp * 128u;
         int tile = (int)(u / p.KT), k = (int)(u - (int64_t)tile * p.KT);
         auto load_w = [&](uint32_t s) {
             const int m = tile >= p.tn ? 1 : 0;
             mbar_expect(full + s, bytes);
-            const uint32_t at = base + s * p.slotB;
-            // (a step's column: in codes where those are spread, else in bytes, or in 16-bit elements)
-            tile_load(at, &p.mw[m], k * (O::mx ? 128 : kBK), (tile - m * p.tn) * 128, full + s);
-            if (O::mx) tile_load(at + sf, &p.msw[m], k * 128 * O::words, tile - m * p.tn, full + s);
-        };
-        auto load_x = [&](uint32_t s, int kx) {
-            const uint32_t at = base + s * p.slotB;
-            tile_load(at + kWTile, &p.mx, kx * (O::mx ? 128 : kBK), 0, full + s);
-            if (O::mx) tile_load(at + sf + sfB, &p.msx, kx * 128 * O::words, 0, full + s);
+            tile_load(base + s * p.slotB, &p.mw[m], k * kBK, (tile - m * p.tn) * 128, full + s);
         };
         if (p.early) {
             // fill the ring's weights while the launch before finishes, then their tokens
@@ -116,7 +99,7 @@ template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) 
             }
             pdl_enter();
             for (uint32_t s = 0; s < round; ++s) {
-                if (elect_one()) load_x(s, kx);
+                if (elect_one()) tile_load(base + s * p.slotB + kWTile, &p.mx, kx * kBK, 0, full + s);
                 __syncwarp();
                 if (++kx == p.KT) kx = 0;
             }
@@ -129,7 +112,7 @@ template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) 
             }
             if (elect_one()) {
                 load_w(cur.s);
-                load_x(cur.s, k);
+                tile_load(base + cur.s * p.slotB + kWTile, &p.mx, k * kBK, 0, full + cur.s);
             }
             __syncwarp();
             cur.next(S);
@@ -141,9 +124,7 @@ template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) 
             ok = mbar_wait_all(empty + last.s, last.ph, p);
         }
     } else if (warp == 5) {
-        const uint32_t id = O::mx ? idesc_mx(O::wfmt, O::xfmt, 128, (uint32_t)p.Tp) : idesc(H::fmt, 0, 0, 128, (uint32_t)p.Tp);
-        const uint32_t sf = base + kWTile + (uint32_t)p.Tp * 128u;
-        uint32_t set = 0;
+        const uint32_t id = idesc(H::fmt, 0, 0, 128, (uint32_t)p.Tp);
         const uint64_t d0 = sdesc(base, 16, 1024);
         Cur cur(0, S);
         for (uint32_t it = 0; ok && u < u1; ++it) {
@@ -159,24 +140,10 @@ template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) 
                 tc_after();
                 if (elect_one()) {
                     const uint64_t a = d0 + ((cur.s * p.slotB) >> 4), b = a + (kWTile >> 4);
-                    if constexpr (O::mx) {
-                        const uint32_t ts = tmem + kSkScales + set * kSkSet;
 #pragma unroll
-                        for (int w = 0; w < O::words; ++w) {
-                            cp_scales(ts + 4 * w, sf + cur.s * p.slotB + 512 * w);
-                            cp_scales(ts + kSkSetX + 4 * w, sf + cur.s * p.slotB + 512 * (O::words + w));
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_mx<OPS>(tmem + buf * 128u, a + 2 * j, b + 2 * j, id | sf_id<OPS>(j), ts + 4 * sf_word<OPS>(j),
-                                        ts + kSkSetX + 4 * sf_word<OPS>(j), (!first || j > 0) ? 1u : 0u);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kBK / 16; ++j) mma(tmem + buf * 128u, a + 2 * j, b + 2 * j, id, (!first || j > 0) ? 1u : 0u);
-                    }
+                    for (int j = 0; j < kBK / 16; ++j) mma(tmem + buf * 128u, a + 2 * j, b + 2 * j, id, (!first || j > 0) ? 1u : 0u);
                     mma_commit(empty + cur.s);
                 }
-                set = (set + 1) & 3;
                 __syncwarp();
                 cur.next(S);
             }
@@ -212,23 +179,20 @@ template <typename T, int OPS> __global__ void __launch_bounds__(kSkThreads, 1) 
         while (gtimer() - t0 < 5000000ull) {
         }
     }
-    tmem_free(tmem, kCols);
+    tmem_free(tmem, 256);
 }
 
-// MXO: a microscaled output (four neighbouring lanes hold a block)
-template <typename T, int MODE, bool MXO> __global__ void __launch_bounds__(128) skinny_join(const __grid_constant__ SkParams p)
+template <typename T, int MODE> __global__ void __launch_bounds__(128) skinny_join(const __grid_constant__ SkParams p)
 {
     pdl_enter();
     const int per = p.tn * 16; // groups of 8 features of a token
     const int i = blockIdx.x * 128 + threadIdx.x;
     const int t = i / per, f = (i - t * per) * 8;
-    const bool on = t < p.T && (MXO || f < p.N);
-    if (!MXO && !on) return;
+    if (t >= p.T || f >= p.N) return;
     const int64_t units = (int64_t)p.tiles * p.KT;
     float v[2][8] = {};
 #pragma unroll
     for (int m = 0; m < (MODE == EPI_GATED ? 2 : 1); ++m) {
-        if (MXO && !on) break;
         const int tile = f / 128 + m * p.tn;
         const int cnt = sk_part_of(units, (int64_t)(tile + 1) * p.KT - 1, p.parts) - sk_part_of(units, (int64_t)tile * p.KT, p.parts) + 1;
         const float *src = p.part + ((size_t)tile * p.smax * p.T + t) * 128 + (f & 127);
@@ -240,8 +204,7 @@ template <typename T, int MODE, bool MXO> __global__ void __launch_bounds__(128)
             for (int j = 0; j < 8; ++j) v[m][j] += w[j];
         }
     }
-    if constexpr (MXO) epilogue8_mx<T, MODE, 1>(p.e, p.N, t, f, on, v[0], v[1]);
-    else epilogue8<T, MODE>(p.e, p.N, t, f, v[0], v[1]);
+    epilogue8<T, MODE>(p.e, p.N, t, f, v[0], v[1]);
 }
 
 // ------------------------------------------------------------------ one token, or few and a smaller matrix
@@ -376,12 +339,11 @@ SkParams plan(const Gemm &g, const CtxView &v)
     p.T = g.M, p.Tp = (g.M + 15) / 16 * 16, p.N = g.N;
     p.tn = (g.N + 127) / 128;
     p.tiles = p.tn * (g.mode == EPI_GATED ? 2 : 1);
-    const int step = g.ops == OPS_16 ? kBK : g.ops == OPS_MX44 ? 256 : 128;
-    p.KT = (g.K[0] + step - 1) / step;
+    p.KT = (g.K[0] + kBK - 1) / kBK;
     const int64_t units = (int64_t)p.tiles * p.KT;
     p.parts = (int)std::min<int64_t>(v.sms, std::max<int64_t>(1, units / 6)); // at least six k steps each
     p.smax = (int)std::min<int64_t>(p.parts, p.KT / (units / p.parts) + 2);
-    p.slotB = kWTile + (uint32_t)p.Tp * 128u + (g.ops == OPS_16 ? 0u : g.ops == OPS_MX44 ? 2048u : 1024u);
+    p.slotB = kWTile + (uint32_t)p.Tp * 128u;
     p.slots = std::min(kMaxRing, (v.smem_optin - 1024) / (int)p.slotB);
     p.status = v.status, p.abort_flag = v.abort_flag, p.wait_ns = v.wait_ns;
     p.early = g.early;
@@ -389,68 +351,43 @@ SkParams plan(const Gemm &g, const CtxView &v)
     return p;
 }
 
-template <typename T, int MODE, int OPS, bool MXO> cudaError_t run(const SkParams &p, cudaStream_t s)
+template <typename T, int MODE> cudaError_t run(const SkParams &p, cudaStream_t s)
 {
-    // (microscaled products: one kernel for both 16-bit types, which only the outputs have)
-    using In = std::conditional_t<OPS == OPS_16, T, __nv_bfloat16>;
-    auto kern = skinny_tc<In, OPS>;
+    auto kern = skinny_tc<T>;
     const int smem = p.slots * (int)p.slotB + (2 * kMaxRing + 4) * 8 + 16;
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = raise_limit((const void *)kern, ready);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(p.parts), dim3(kSkThreads), smem, s, p);
     if (e != cudaSuccess) return e;
     const int64_t threads = (int64_t)p.T * p.tn * 16;
-    return launch_pdl(skinny_join<T, MODE, MXO>, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, p);
+    return launch_pdl(skinny_join<T, MODE>, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, p);
 }
 
 template <typename T> cudaError_t run_mode(const Gemm &g, const SkParams &p, cudaStream_t s)
 {
-    return g.mode == EPI_GATED ? run<T, EPI_GATED, OPS_16, false>(p, s) : run<T, EPI_LINEAR, OPS_16, false>(p, s);
-}
-
-template <typename T, int OPS> cudaError_t run_mx(const Gemm &g, const SkParams &p, cudaStream_t s)
-{
-    return g.mode == EPI_GATED ? run<T, EPI_GATED, OPS, true>(p, s)
-           : g.e.mx            ? run<T, EPI_LINEAR, OPS, true>(p, s)
-                               : run<T, EPI_LINEAR, OPS, false>(p, s);
+    return g.mode == EPI_GATED ? run<T, EPI_GATED>(p, s) : run<T, EPI_LINEAR>(p, s);
 }
 
 } // namespace
 
 bool skinny_takes(const Gemm &g)
 {
-    if (g.ops != OPS_16) return g.M <= kSkinnyRows;
     return g.M <= kSkinnyRows && g.segs == 1 && g.mode != EPI_DACT && !g.a[0].mn && !g.b[0].mn;
 }
 
 size_t skinny_workspace(const Gemm &g, const CtxView &v)
 {
-    if (g.ops == OPS_16 && gemv_takes(g)) return 0;
+    if (gemv_takes(g)) return 0;
     const SkParams p = plan(g, v);
     return (size_t)p.tiles * p.smax * p.T * 128 * sizeof(float);
 }
 
 cudaError_t launch_skinny(const Gemm &g, bool bf16, const CtxView &v, void *ws)
 {
-    if (g.ops == OPS_16 && gemv_takes(g)) return bf16 ? gemv<__nv_bfloat16>(g, v) : gemv<__half>(g, v);
+    if (gemv_takes(g)) return bf16 ? gemv<__nv_bfloat16>(g, v) : gemv<__half>(g, v);
     SkParams p = plan(g, v);
     p.part = static_cast<float *>(ws);
     const int nm = g.mode == EPI_GATED ? 2 : 1;
-    if (g.ops != OPS_16) {
-        const int xk = g.ops == OPS_MX44 ? PI_MX4 : PI_MX8, wk = g.ops == OPS_MX88 ? PI_MX8 : PI_MX4;
-        const int tiles = mx_tiles(g.K[0]), words = g.ops == OPS_MX44 ? 2 : 1;
-        cudaError_t e = encode_map_bytes(&p.mx, g.a[0].p, (uint64_t)mx_row_bytes(xk, g.K[0]), (uint64_t)g.M, (uint64_t)g.a[0].ld, (uint32_t)p.Tp);
-        if (e == cudaSuccess) e = encode_map_scales(&p.msx, g.sa, tiles, 1, words, 1);
-        for (int i = 0; i < nm && e == cudaSuccess; ++i) {
-            e = g.ops == OPS_MX84 ? encode_map_nibbles(&p.mw[i], g.b[i].p, (uint64_t)tiles * 128, (uint64_t)g.N, (uint64_t)g.b[i].ld, 128)
-                                  : encode_map_bytes(&p.mw[i], g.b[i].p, (uint64_t)mx_row_bytes(wk, g.K[0]), (uint64_t)g.N, (uint64_t)g.b[i].ld, 128);
-            if (e == cudaSuccess) e = encode_map_scales(&p.msw[i], g.sb[i], tiles, mx_tiles(g.N), words, 1);
-        }
-        if (e != cudaSuccess) return e;
-        return g.ops == OPS_MX84   ? (bf16 ? run_mx<__nv_bfloat16, OPS_MX84>(g, p, v.stream) : run_mx<__half, OPS_MX84>(g, p, v.stream))
-               : g.ops == OPS_MX88 ? (bf16 ? run_mx<__nv_bfloat16, OPS_MX88>(g, p, v.stream) : run_mx<__half, OPS_MX88>(g, p, v.stream))
-                                   : (bf16 ? run_mx<__nv_bfloat16, OPS_MX44>(g, p, v.stream) : run_mx<__half, OPS_MX44>(g, p, v.stream));
-    }
     cudaError_t e = encode_map(&p.mx, g.a[0].p, (uint64_t)g.K[0], (uint64_t)g.M, (uint64_t)g.a[0].ld * 2, (uint32_t)p.Tp);
     for (int i = 0; i < nm && e == cudaSuccess; ++i)
         e = encode_map(&p.mw[i], g.b[i].p, (uint64_t)g.K[0], (uint64_t)g.N, (uint64_t)g.b[i].ld * 2, 128);

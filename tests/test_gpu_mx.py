@@ -128,7 +128,8 @@ def test_quantize_of_nothing(c):
 # ------------------------------------------------------------------ linear
 # one token to several row tiles; features below, at and past tile borders; odd
 # sizes; few tiles of a long k; many tiles; thin outputs
-LINEAR = [(1, 8, 1), (1, 1024, 4096), (2, 64, 128), (3, 257, 31), (8, 512, 129), (16, 640, 384), (17, 1000, 515), (33, 72, 1000),
+LINEAR = [(1, 8, 1), (1, 1024, 4096), (2, 64, 128), (3, 257, 31), (4, 3000, 70), (5, 300, 33), (6, 1024, 200), (7, 90, 4000), (8, 512, 129),
+          (9, 512, 129), (16, 640, 384), (17, 1000, 515), (33, 72, 1000),
           (64, 2048, 256), (65, 128, 264), (128, 130, 256), (129, 33, 128), (130, 320, 520), (257, 1, 3), (300, 1001, 257),
           (513, 192, 777), (1100, 96, 640), (200, 12296, 520), (2600, 136, 2056), (3000, 264, 100), (40, 4104, 2500)]
 
@@ -166,7 +167,7 @@ def test_linear_adds_into_an_fp32_stream(c, T, K, N, xk, wk):
     assert r.equal(y)
 
 
-@pytest.mark.parametrize("T", [1, 20, 128, 300])
+@pytest.mark.parametrize("T", [1, 3, 8, 20, 128, 300])
 @pytest.mark.parametrize("xk,wk", KINDS)
 def test_each_scale_meets_its_block(c, T, xk, wk):
     """One block of x and of W at a time is not zero, with a scale of its own:
@@ -181,7 +182,7 @@ def test_each_scale_meets_its_block(c, T, xk, wk):
         assert torch.equal(y, x @ w.t()), k
 
 
-@pytest.mark.parametrize("T", [1, 20, 128, 300])
+@pytest.mark.parametrize("T", [1, 3, 8, 20, 128, 300])
 @pytest.mark.parametrize("xk,wk", KINDS)
 def test_scales_of_the_whole_range(c, T, xk, wk):
     """Values of 2^-60 times ones of 2^60; a product past fp32's range is not finite."""
@@ -194,7 +195,7 @@ def test_scales_of_the_whole_range(c, T, xk, wk):
     assert not bool(y.isfinite().any())
 
 
-@pytest.mark.parametrize("T", [1, 20, 128, 300])
+@pytest.mark.parametrize("T", [1, 3, 8, 20, 128, 300])
 @pytest.mark.parametrize("xk,wk", KINDS)
 def test_a_nan_block_stays_in_its_row(c, T, xk, wk):
     m = Maker(4)
@@ -208,7 +209,7 @@ def test_a_nan_block_stays_in_its_row(c, T, xk, wk):
 
 
 # ------------------------------------------------------------------ gated FFN
-FFN = [(1, 64, 200), (1, 1024, 2736), (3, 100, 257), (20, 264, 777), (64, 512, 1000), (65, 130, 384), (128, 192, 96), (200, 192, 515),
+FFN = [(1, 64, 200), (1, 1024, 2736), (2, 264, 777), (3, 100, 257), (4, 520, 130), (7, 264, 1000), (8, 100, 257), (20, 264, 777), (64, 512, 1000), (65, 130, 384), (128, 192, 96), (200, 192, 515),
        (300, 520, 1025), (700, 1000, 2600)]
 
 
