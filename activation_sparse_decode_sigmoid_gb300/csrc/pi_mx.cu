@@ -32,14 +32,6 @@ struct MxP {
 };
 
 // T: __half, __nv_bfloat16 or float
-template <typename T> __device__ __forceinline__ void load_any(const void *p, int64_t at, int n, bool vec, float (&v)[8])
-{
-    load8<T>(static_cast<const uint16_t *>(p) + at, n, vec, v);
-}
-template <> __device__ __forceinline__ void load_any<float>(const void *p, int64_t at, int n, bool vec, float (&v)[8])
-{
-    load8f(static_cast<const float *>(p) + at, n, vec, v);
-}
 template <typename T> __device__ __forceinline__ void store_any(void *p, int64_t at, int n, bool vec, const float (&v)[8])
 {
     store8<T>(static_cast<uint16_t *>(p) + at, n, vec, v);
@@ -49,46 +41,124 @@ template <> __device__ __forceinline__ void store_any<float>(void *p, int64_t at
     store8f(static_cast<float *>(p) + at, n, vec, v);
 }
 
-// A warp takes 256 columns of kRows rows, its loads in flight together: a lane
-// holds 8 columns of each, four lanes a block.
-constexpr int kRows = 4, kWarps = 8;
+// A block as a thread loads it: 32 elements of 16 or 32 bits.
+template <typename T> struct Raw {
+    uint32_t w[16];
+    __device__ __forceinline__ void load(const void *p, int64_t at, int n, bool vec)
+    {
+        const uint16_t *s = static_cast<const uint16_t *>(p) + at;
+        if (vec && n >= 32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(s) + i);
+                w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            w[i] = 2 * i < n ? s[2 * i] : 0u;
+            if (2 * i + 1 < n) w[i] |= (uint32_t)s[2 * i + 1] << 16;
+        }
+    }
+    // the largest magnitude, as a float's bits (two halves at a time: as integers they order alike, NaN above all)
+    __device__ __forceinline__ uint32_t amax() const
+    {
+        uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return mag(C16<T>::one((uint16_t)max(m & 0xffffu, m >> 16)));
+    }
+    // elements 8 j to 8 j + 7 times a power of two
+    __device__ __forceinline__ void scaled(int j, float m, float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scale2(w[4 * j + i], m, v[2 * i], v[2 * i + 1]);
+    }
+    static __device__ __forceinline__ void scale2(uint32_t w, float m, float &a, float &b);
+};
+template <> __device__ __forceinline__ void Raw<__half>::scale2(uint32_t w, float m, float &a, float &b)
+{
+    a = C16<__half>::one((uint16_t)w) * m, b = C16<__half>::one((uint16_t)(w >> 16)) * m;
+}
+// (bf16 holds every power of two that a scale can be: one instruction an element; -0 added keeps the zeros' signs)
+template <> __device__ __forceinline__ void Raw<__nv_bfloat16>::scale2(uint32_t w, float m, float &a, float &b)
+{
+    asm("{ .reg .b16 l, h, x; .reg .b32 z; mov.b32 {l, h}, %2; mov.b32 {x, _}, %3; fma.rn.f32.bf16 %0, l, x, %4; fma.rn.f32.bf16 %1, h, x, %4; }"
+        : "=f"(a), "=f"(b)
+        : "r"(w), "r"(__float_as_uint(m) >> 16), "f"(-0.f));
+}
+template <> struct Raw<float> {
+    float f[32];
+    __device__ __forceinline__ void load(const void *p, int64_t at, int n, bool vec)
+    {
+        const float *s = static_cast<const float *>(p) + at;
+        if (vec && n >= 32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 q = __ldg(reinterpret_cast<const float4 *>(s) + i);
+                f[4 * i] = q.x, f[4 * i + 1] = q.y, f[4 * i + 2] = q.z, f[4 * i + 3] = q.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = i < n ? s[i] : 0.f;
+    }
+    __device__ __forceinline__ uint32_t amax() const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = max(m, mag(f[i]));
+        return m;
+    }
+    __device__ __forceinline__ void scaled(int j, float m, float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f[8 * j + i] * m;
+    }
+};
 
-template <typename T, int KIND> __global__ void __launch_bounds__(32 * kWarps) mx_quantize_rows(const __grid_constant__ MxP p)
+// A thread has a block: neither its largest magnitude nor its scale is shared.
+// (8 elements a thread and the rest by shuffles took 166 us for 28672 x 8192 from bf16 to
+// 4 bits, twice what memory needs.)
+constexpr int kQThreads = 128;
+__host__ __device__ inline int quantize_rows(int nb) { return nb < kQThreads ? kQThreads / nb : 1; }
+
+template <typename T, int KIND> __global__ void __launch_bounds__(kQThreads) mx_quantize_rows(const __grid_constant__ MxP p)
 {
     pdl_enter();
-    const int ncb = (p.tiles + 1) / 2, lane = threadIdx.x & 31;
-    const int c = (int)(blockIdx.x % ncb) * 256 + lane * 8, n = p.K - c;
-    const int64_t r0 = ((int64_t)(blockIdx.x / ncb) * kWarps + (threadIdx.x >> 5)) * kRows;
-    const bool in = c < p.tiles * 128;
-    float v[kRows][8];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t r = r0 + i;
-        load_any<T>(p.x, r * p.ldx + c, r < p.T ? n : 0, p.vec, v[i]);
+    // blocks of a row; CTAs to a row, or rows to a CTA
+    const int nb = p.tiles * 4, per = (nb + kQThreads - 1) / kQThreads, rows = quantize_rows(nb);
+    const int64_t r = (int64_t)(blockIdx.x / per) * rows + (rows > 1 ? threadIdx.x / nb : 0);
+    const int b = rows > 1 ? threadIdx.x % nb : (int)(blockIdx.x % per) * kQThreads + threadIdx.x;
+    if (b >= nb || (rows > 1 && threadIdx.x >= rows * nb) || r >= (int64_t)mx_tiles(p.T) * 128) return;
+    uint8_t *scale = p.scales + mx_scale_at(r, b >> 2, p.tiles) + (b & 3);
+    if (r >= p.T) { // (rows behind the last: zeros up to the tile's end)
+        *scale = 0;
+        return;
     }
+    Raw<T> x;
+    x.load(p.x, r * p.ldx + b * 32, p.K - b * 32, p.vec);
+    const uint32_t code = mx_scale<KIND>(x.amax());
+    const float m = mx_inverse(code);
+    uint2 q[4];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t r = r0 + i;
-        uint32_t a = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a = max(a, mag(v[i][j]));
-        const uint32_t code = mx_scale<KIND>(mx_amax4<1>(a));
-        // the four scales of a tile's row: one word
-        uint32_t word = code << (lane & 12) * 2;
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if (!in) continue;
-        if (r < p.T) {
-            const uint2 q = mx_pack8<KIND>(v[i], code);
-            if (KIND == PI_MX8) *reinterpret_cast<uint2 *>(p.codes + r * p.ld + c) = q;
-            else *reinterpret_cast<uint32_t *>(p.codes + r * p.ld + (c >> 1)) = q.x;
-        }
-        // (rows behind the last: zeros up to the tile's end)
-        if (!(lane & 15) && r < (int64_t)mx_tiles(p.T) * 128)
-            *reinterpret_cast<uint32_t *>(p.scales + mx_scale_at(r, c >> 7, p.tiles)) = word;
+    for (int j = 0; j < 4; ++j) {
+        float v[8];
+        x.scaled(j, m, v);
+        q[j] = mx_pack8<KIND>(v);
     }
+    *scale = (uint8_t)code;
+    uint4 *o = reinterpret_cast<uint4 *>(p.codes + r * p.ld + b * (KIND == PI_MX8 ? 32 : 16));
+    if (KIND == PI_MX8) {
+        o[0] = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+        o[1] = make_uint4(q[2].x, q[2].y, q[3].x, q[3].y);
+    } else // (4 bits have no NaN: the scale says it)
+        o[0] = code == 255u ? make_uint4(0, 0, 0, 0) : make_uint4(q[0].x, q[1].x, q[2].x, q[3].x);
 }
 
+// The way back: a warp takes 256 columns of kRows rows, its loads in flight together.
+constexpr int kRows = 4, kWarps = 8;
 template <typename T, int KIND> __global__ void __launch_bounds__(32 * kWarps) mx_dequantize_rows(const __grid_constant__ MxP p)
 {
     pdl_enter();
@@ -154,9 +224,9 @@ pi_status check_mx(pi_ctx *c, const char *what, const pi_mx *m, int rows, int co
 
 template <int KIND> cudaError_t run_quantize(const MxP &p, int dt, cudaStream_t s, unsigned grid)
 {
-    return dt == PI_F32   ? launch_pdl(mx_quantize_rows<float, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p)
-           : dt == PI_F16 ? launch_pdl(mx_quantize_rows<__half, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p)
-                          : launch_pdl(mx_quantize_rows<__nv_bfloat16, KIND>, dim3(grid), dim3(32 * kWarps), 0, s, p);
+    return dt == PI_F32   ? launch_pdl(mx_quantize_rows<float, KIND>, dim3(grid), dim3(kQThreads), 0, s, p)
+           : dt == PI_F16 ? launch_pdl(mx_quantize_rows<__half, KIND>, dim3(grid), dim3(kQThreads), 0, s, p)
+                          : launch_pdl(mx_quantize_rows<__nv_bfloat16, KIND>, dim3(grid), dim3(kQThreads), 0, s, p);
 }
 template <int KIND> cudaError_t run_dequantize(const MxP &p, int dt, cudaStream_t s, unsigned grid)
 {
@@ -185,8 +255,9 @@ pi_status convert(pi_ctx *c, const pi_mx_desc *desc, const void *x, const pi_mx 
     p.codes = static_cast<uint8_t *>(q->codes), p.scales = static_cast<uint8_t *>(q->scales);
     const CtxView v = ctx_view(c);
     DeviceGuard g(v.device);
-    const int64_t rows = back ? d.rows : (int64_t)mx_tiles(d.rows) * 128;
-    const unsigned grid = (unsigned)((rows + kRows * kWarps - 1) / (kRows * kWarps) * ((p.tiles + 1) / 2));
+    const unsigned grid = back ? (unsigned)((d.rows + kRows * kWarps - 1) / (kRows * kWarps) * ((p.tiles + 1) / 2))
+                               : (unsigned)(((int64_t)mx_tiles(d.rows) * 128 + quantize_rows(p.tiles * 4) - 1) / quantize_rows(p.tiles * 4) *
+                                            ((p.tiles * 4 + kQThreads - 1) / kQThreads));
     if (back) CUX(d.kind == PI_MX8 ? run_dequantize<PI_MX8>(p, d.dtype, v.stream, grid) : run_dequantize<PI_MX4>(p, d.dtype, v.stream, grid));
     else CUX(d.kind == PI_MX8 ? run_quantize<PI_MX8>(p, d.dtype, v.stream, grid) : run_quantize<PI_MX4>(p, d.dtype, v.stream, grid));
     return PI_OK;

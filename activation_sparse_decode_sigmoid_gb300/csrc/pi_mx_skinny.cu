@@ -352,8 +352,9 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
 
 // ------------------------------------------------------------------ host
 // CTAs to a cluster: the number that leaves the fewest steps to the busiest CTA,
-// a tile's exchange counted as kExchange steps; of numbers as good, the smallest.
-constexpr int kExchange = 4;
+// the last tile's exchange (2 to 3 us; the others' lie behind the next tile's
+// products) counted as kExchange steps; of numbers as good, the smallest.
+constexpr int kExchange = 12;
 
 MsParams plan(const Gemm &g, const CtxView &v, int &grid)
 {
@@ -364,7 +365,7 @@ MsParams plan(const Gemm &g, const CtxView &v, int &grid)
     int64_t best = INT64_MAX;
     for (int cs = 1; cs <= kMsMaxCluster && cs <= p.KT; cs *= 2) {
         const int n = v.sms / cs;
-        const int64_t cost = (int64_t)((p.tn + n - 1) / n) * (nm * ((p.KT + cs - 1) / cs) + (cs > 1 ? kExchange : 0));
+        const int64_t cost = (int64_t)((p.tn + n - 1) / n) * (nm * ((p.KT + cs - 1) / cs)) + (cs > 1 ? kExchange : 0);
         if (cost < best) best = cost, p.cs = cs;
     }
     p.own = ((p.T + p.cs - 1) / p.cs + 15) / 16 * 16;

@@ -1035,20 +1035,32 @@ class Context:
         """A matrix for a call to write."""
         if kind != PI_MX8 and kind != PI_MX4:
             raise PiError(PI_ERR_ARG, f"kind {kind} is not PI_MX8 or PI_MX4")
-        u8 = (_torch or _import_torch()).uint8
-        B = (cols + 127) // 128
-        return MxMatrix(self._new((rows, B * (128 if kind == PI_MX8 else 64)), u8),
-                        self._new(((rows + 127) // 128, B, 32, 4, 4), u8), cols, kind)
+        torch = _torch or _import_torch()
+        B, dev = (cols + 127) // 128, self.torch_device
+        return MxMatrix(torch.empty((rows, B * (128 if kind == PI_MX8 else 64)), dtype=torch.uint8, device=dev),
+                        torch.empty(((rows + 127) // 128, B, 32, 4, 4), dtype=torch.uint8, device=dev), cols, kind)
+
+    def _mx_out(self, name, q, rows, cols, kind):
+        """(q or a new matrix, and what _mx says of it)"""
+        if q is not None:
+            return q, *self._mx(name, q, rows, cols, kind)
+        q = self.mx_empty(rows, cols, kind)
+        return q, q.codes.data_ptr(), q.scales.data_ptr(), 0
+
+    def _out(self, name, t, shape, dtype):
+        """(t or a new tensor, and what _at says of it)"""
+        if t is not None:
+            return t, *self._at(name, t, shape, dtype)
+        t = (_torch or _import_torch()).empty(shape, dtype=dtype, device=self.torch_device)
+        return t, t.data_ptr(), 0
 
     def mx_quantize(self, x, kind: int = PI_MX8, out: MxMatrix | None = None) -> MxMatrix:
         """x (float16, bfloat16 or float32 rows) in blocks of 32 columns that
         share a scale; elements of 8 (PI_MX8) or 4 bits (PI_MX4)."""
         code = self._code(x.dtype)
         T, K = self._dims("x", x)
-        if out is None:
-            out = self.mx_empty(T, K, kind)
         px, ldx = self._at("x", x, (T, K), x.dtype)
-        pc, ps, ldq = self._mx("out", out, T, K, kind)
+        out, pc, ps, ldq = self._mx_out("out", out, T, K, kind)
         desc, _ = self._plan(pi_mx_desc, (T, K, kind, code, ldx, ldq), None)
         q = pi_mx(pc, ps)
         self._s()
@@ -1060,11 +1072,11 @@ class Context:
     def mx_dequantize(self, q: MxMatrix, dtype=None, out=None):
         """The values of q in `dtype` (bfloat16 unless given, or out's)."""
         T, K = self._mx_dims("q", q)
-        if out is None:
-            out = self._new((T, K), dtype or (_torch or _import_torch()).bfloat16)
-        code = self._code(out.dtype)
-        py, ldy = self._at("out", out, (T, K), dtype or out.dtype)
+        if dtype is None:
+            dtype = (_torch or _import_torch()).bfloat16 if out is None else out.dtype
+        code = self._code(dtype)
         pc, ps, ldq = self._mx("q", q, T, K)
+        out, py, ldy = self._out("out", out, (T, K), dtype)
         desc, _ = self._plan(pi_mx_desc, (T, K, q.kind, code, ldy, ldq), None)
         m = pi_mx(pc, ps)
         self._s()
@@ -1085,14 +1097,13 @@ class Context:
             torch = _torch or _import_torch()
             dtype = torch.bfloat16 if t is None or t.dtype == torch.float32 else t.dtype
         code = self._code16(dtype)
-        if y is None:
-            y = self._new((T, N), dtype if residual is None else residual.dtype)
-        out = self._code(y.dtype)
+        ydt = y.dtype if y is not None else dtype if residual is None else residual.dtype
+        out = self._code(ydt)
         pxc, pxs, ldx = self._mx("x", x, T, K)
         pwc, pws, ldw = self._mx("w", w, N, K)
-        pb, _ = self._at("b", b, (N,), dtype)
-        pr, ldr = self._at("residual", residual, (T, N), y.dtype)
-        py, ldy = self._at("y", y, (T, N), y.dtype)
+        pb = 0 if b is None else self._at("b", b, (N,), dtype)[0]
+        pr, ldr = (0, 0) if residual is None else self._at("residual", residual, (T, N), ydt)
+        y, py, ldy = self._out("y", y, (T, N), ydt)
         desc, n = self._plan(pi_mx_linear_desc, (T, K, N, x.kind, w.kind, code, out, fn, scale, ldx, ldw, ldr, ldy),
                              pi_mx_linear_workspace)
         mx, mw = pi_mx(pxc, pxs), pi_mx(pwc, pws)
@@ -1113,13 +1124,11 @@ class Context:
             t = next((v for v in (b_gate, b_up, b_down, y) if v is not None), None)
             dtype = (_torch or _import_torch()).bfloat16 if t is None else t.dtype
         code = self._code16(dtype)
-        if y is None:
-            y = self._new((T, d), dtype)
         pxc, pxs, ldx = self._mx("x", x, T, d)
         gc, gs, ldg = self._mx("w_gate", w_gate, n, d, w_up.kind)
         uc, us, ldu = self._mx("w_up", w_up, n, d)
         dc, ds, ldd = self._mx("w_down", w_down, d, n, w_up.kind)
-        py, ldy = self._at("y", y, (T, d), dtype)
+        y, py, ldy = self._out("y", y, (T, d), dtype)
         pbg, pbu = self._at("b_gate", b_gate, (n,), dtype)[0], self._at("b_up", b_up, (n,), dtype)[0]
         pbd = self._at("b_down", b_down, (d,), dtype)[0]
         desc, nb = self._plan(pi_mx_gated_ffn_desc, (T, d, n, x.kind, w_up.kind, code, fn, w_gate is not None, ldx, ldg, ldu,
@@ -1145,15 +1154,11 @@ class Context:
                          (_torch or _import_torch()).bfloat16 if xcode == PI_F32 else xdt)
         code = self._code16(dtype)
         T, d = self._dims("x", x)
-        if x_out is None:
-            x_out = self._new((T, d), xdt)
-        if h is None:
-            h = self.mx_empty(T, d, kind)
         px, ldx = self._at("x", x, (T, d), dtype if xcode != PI_F32 else xdt)
         py, ldy = self._at("y", y, (T, d), dtype)
         pg, ldg = self._at("gate", gate, (1 if gate_rows == 0 else -(-T // max(gate_rows, 1)), d), dtype)
-        po, ldo = self._at("x_out", x_out, (T, d), xdt)
-        hc, hs, ldh = self._mx("h", h, T, d, kind)
+        x_out, po, ldo = self._out("x_out", x_out, (T, d), xdt)
+        h, hc, hs, ldh = self._mx_out("h", h, T, d, kind)
         par = pi_norm_residual_params(self._at("w_pre", w_pre, (d,), dtype)[0], self._at("b_pre", b_pre, (d,), dtype)[0],
                                       self._at("w_post", w_post, (d,), dtype)[0], self._at("b_post", b_post, (d,), dtype)[0])
         desc, _ = self._plan(pi_norm_residual_desc, (T, d, xcode, code, code, pre, post, gate_rows, res_scale, branch_scale,
