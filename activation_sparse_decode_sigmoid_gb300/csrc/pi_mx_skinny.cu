@@ -26,6 +26,7 @@
 #include "pi_block.h"
 #include "pi_epi.cuh"
 #include "pi_kernels.h"
+#include "pi_mx_cluster.cuh"
 #include "pi_mx_tc.cuh"
 #include "pi_pair.cuh"
 #include "pi_tc.cuh"
@@ -36,7 +37,6 @@ namespace {
 constexpr int kMsThreads = 192;    // warps 0-3: epilogue; 4: TMA; 5: MMA
 constexpr uint32_t kMsW = 16384;   // 128 features of a step
 constexpr int kMsRing = 12;
-constexpr int kMsMaxCluster = 8;
 // Tensor memory: four sets of scales, of W in the first 8 columns of a set; then the accumulators
 constexpr uint32_t kMsSet = 16, kMsSetX = 8, kMsAcc = 64;
 
@@ -55,54 +55,10 @@ struct MsParams {
     Epi e;
 };
 
-// address of a shared-memory object in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 __device__ __forceinline__ void st_cluster(uint32_t at, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-
-// a warp's wait for arrivals from other CTAs, after which it sees what they wrote before them
-__device__ __forceinline__ bool mbar_try_cluster(uint64_t *b, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{ .reg .pred q; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2; "
-                 "selp.u32 %0, 1, 0, q; }"
-                 : "=r"(ok)
-                 : "r"(smem_addr(b)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-template <typename P> __device__ __forceinline__ bool warp_wait_cluster(uint64_t *b, uint32_t parity, const P &p, int lane)
-{
-    bool ok = true;
-    if (lane == 0) ok = mbar_wait_bounded(b, parity, p) && mbar_try_cluster(b, parity); // (the second returns at once)
-    return __shfl_sync(0xffffffffu, ok, 0);
-}
-
-// The steps of a CTA in order: tiles, the matrices of each, this CTA's part of k.
-struct MsWalk {
-    int tile, m, k, k0, k1, nm, step, tn;
-    __device__ __forceinline__ MsWalk(const MsParams &p, int nm_, int cluster, int clusters, int rank)
-        : tile(cluster), m(0), nm(nm_), step(clusters), tn(p.tn)
-    {
-        k0 = (int)((int64_t)p.KT * rank / p.cs), k1 = (int)((int64_t)p.KT * (rank + 1) / p.cs);
-        k = k0;
-    }
-    __device__ __forceinline__ bool more() const { return tile < tn; }
-    __device__ __forceinline__ void next()
-    {
-        if (++k < k1) return;
-        k = k0;
-        if (++m < nm) return;
-        m = 0, tile += step;
-    }
-};
 
 // The outputs of tokens t0 .. t0 + n - 1 (n <= 16) in a warp's 32 features, one a lane.
 template <int KIND> __device__ __forceinline__ void put_mx(const Epi &e, int t0, int n, int f, int N, const float (&v)[16])
@@ -160,7 +116,7 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
     uint64_t *acc_full = empty + kMsRing, *acc_empty = acc_full + 2;
     uint64_t *part_full = acc_empty + 2, *part_free = part_full + 1;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(part_free + 1);
-    MsWalk w(p, NM, cluster, clusters, rank);
+    MxWalk w(p.tn, NM, p.KT, p.cs, cluster, clusters, rank);
     if (tid == 128) prefetch_map(&p.mw[0]), prefetch_map(&p.mx), prefetch_map(&p.msw[0]), prefetch_map(&p.msx);
     if (tid == 0) {
         for (uint32_t s = 0; s < S; ++s) mbar_init1(full + s), mbar_init1(empty + s);
@@ -192,7 +148,7 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
         };
         if (p.early) {
             // fill the ring's weights while the launch before finishes, then their tokens
-            MsWalk x = w;
+            MxWalk x = w;
             for (; w.more() && round < S; w.next(), ++round) {
                 if (elect_one()) load_w(round);
                 __syncwarp();
@@ -351,23 +307,16 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
 }
 
 // ------------------------------------------------------------------ host
-// CTAs to a cluster: the number that leaves the fewest steps to the busiest CTA,
-// the last tile's exchange (2 to 3 us; the others' lie behind the next tile's
-// products) counted as kExchange steps; of numbers as good, the smallest.
-constexpr int kExchange = 12;
+constexpr int kMsExchange = 12; // steps
 
-MsParams plan(const Gemm &g, const CtxView &v, int &grid)
+MsParams plan(const Gemm &g, const CtxView &v, const int (&n)[4], int &grid)
 {
     MsParams p = {};
     const int words = g.ops == OPS_MX44 ? 2 : 1, nm = g.mode == EPI_GATED ? 2 : 1;
     p.T = g.M, p.Tp = (g.M + 15) / 16 * 16, p.N = g.N;
     p.tn = mx_tiles(g.N), p.KT = (mx_tiles(g.K[0]) + words - 1) / words;
-    int64_t best = INT64_MAX;
-    for (int cs = 1; cs <= kMsMaxCluster && cs <= p.KT; cs *= 2) {
-        const int n = v.sms / cs;
-        const int64_t cost = (int64_t)((p.tn + n - 1) / n) * (nm * ((p.KT + cs - 1) / cs)) + (cs > 1 ? kExchange : 0);
-        if (cost < best) best = cost, p.cs = cs;
-    }
+    int clusters = 1;
+    p.cs = mx_cluster(p.tn, nm, p.KT, n, 8, kMsExchange, clusters);
     p.own = ((p.T + p.cs - 1) / p.cs + 15) / 16 * 16;
     p.owners = (p.T + p.own - 1) / p.own;
     // half of an SM's shared and tensor memory where that gives a ring of four
@@ -384,40 +333,13 @@ MsParams plan(const Gemm &g, const CtxView &v, int &grid)
     p.status = v.status, p.abort_flag = v.abort_flag, p.wait_ns = v.wait_ns;
     p.early = g.early;
     p.e = g.e;
-    grid = std::min(p.tn, v.sms / p.cs) * p.cs;
+    grid = clusters * p.cs;
     return p;
 }
 
-template <typename T, int MODE, int OPS> cudaError_t run(const MsParams &p, int grid, cudaStream_t s)
+// The operands' maps.
+cudaError_t maps(const Gemm &g, MsParams &p)
 {
-    auto kern = mx_skinny<T, MODE, OPS>;
-    static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = raise_limit((const void *)kern, ready);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kMsThreads), cfg.stream = s;
-    cfg.dynamicSmemBytes = (size_t)p.slots * p.slotB + p.partB + (2 * kMsRing + 6) * 8 + 16;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)p.cs, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
-    cfg.attrs = at, cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-template <int OPS> cudaError_t run_ops(const Gemm &g, bool bf16, const MsParams &p, int grid, cudaStream_t s)
-{
-    if (g.mode == EPI_GATED) return bf16 ? run<__nv_bfloat16, EPI_GATED, OPS>(p, grid, s) : run<__half, EPI_GATED, OPS>(p, grid, s);
-    return bf16 ? run<__nv_bfloat16, EPI_LINEAR, OPS>(p, grid, s) : run<__half, EPI_LINEAR, OPS>(p, grid, s);
-}
-
-} // namespace
-
-cudaError_t launch_mx_skinny(const Gemm &g, bool bf16, const CtxView &v)
-{
-    int grid;
-    MsParams p = plan(g, v, grid);
     const int xk = g.ops == OPS_MX44 ? PI_MX4 : PI_MX8, wk = g.ops == OPS_MX88 ? PI_MX8 : PI_MX4;
     const int tiles = mx_tiles(g.K[0]), words = g.ops == OPS_MX44 ? 2 : 1;
     cudaError_t e = encode_map_bytes(&p.mx, g.a[0].p, (uint64_t)mx_row_bytes(xk, g.K[0]), (uint64_t)g.M, (uint64_t)g.a[0].ld, (uint32_t)p.Tp);
@@ -427,10 +349,37 @@ cudaError_t launch_mx_skinny(const Gemm &g, bool bf16, const CtxView &v)
                               : encode_map_bytes(&p.mw[i], g.b[i].p, (uint64_t)mx_row_bytes(wk, g.K[0]), (uint64_t)g.N, (uint64_t)g.b[i].ld, 128);
         if (e == cudaSuccess) e = encode_map_scales(&p.msw[i], g.sb[i], tiles, p.tn, words, 1);
     }
+    return e;
+}
+
+template <typename T, int MODE, int OPS> cudaError_t run(const Gemm &g, const CtxView &v)
+{
+    static std::atomic<uint64_t> ready{0};
+    static ClusterCounts known;
+    auto kern = mx_skinny<T, MODE, OPS>;
+    int n[4], grid = 0;
+    cudaError_t e = raise_limit((const void *)kern, ready);
+    if (e == cudaSuccess) e = cluster_counts(kern, known, kMsThreads, v, n);
     if (e != cudaSuccess) return e;
-    return g.ops == OPS_MX84   ? run_ops<OPS_MX84>(g, bf16, p, grid, v.stream)
-           : g.ops == OPS_MX88 ? run_ops<OPS_MX88>(g, bf16, p, grid, v.stream)
-                               : run_ops<OPS_MX44>(g, bf16, p, grid, v.stream);
+    MsParams p = plan(g, v, n, grid);
+    e = maps(g, p);
+    if (e != cudaSuccess) return e;
+    return launch_cluster(kern, grid, p.cs, kMsThreads, (size_t)p.slots * p.slotB + p.partB + (2 * kMsRing + 6) * 8 + 16, v.stream, p);
+}
+
+template <int OPS> cudaError_t run_ops(const Gemm &g, bool bf16, const CtxView &v)
+{
+    if (g.mode == EPI_GATED) return bf16 ? run<__nv_bfloat16, EPI_GATED, OPS>(g, v) : run<__half, EPI_GATED, OPS>(g, v);
+    return bf16 ? run<__nv_bfloat16, EPI_LINEAR, OPS>(g, v) : run<__half, EPI_LINEAR, OPS>(g, v);
+}
+
+} // namespace
+
+cudaError_t launch_mx_skinny(const Gemm &g, bool bf16, const CtxView &v)
+{
+    return g.ops == OPS_MX84   ? run_ops<OPS_MX84>(g, bf16, v)
+           : g.ops == OPS_MX88 ? run_ops<OPS_MX88>(g, bf16, v)
+                               : run_ops<OPS_MX44>(g, bf16, v);
 }
 
 } // namespace pi
