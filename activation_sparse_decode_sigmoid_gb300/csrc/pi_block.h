@@ -75,8 +75,8 @@ cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 
 // Products of microscaled operands: of up to kSkinnyRows rows of A, without a workspace (pi_mx_skinny.cu); others by their types.
 cudaError_t launch_mx_skinny(const Gemm &g, bool bf16, const CtxView &v);
-// the same for 8-bit x of up to kMxRows rows and 4-bit W (pi_mx_rows.cu)
-constexpr int kMxRows = 32;
+// the same for 8-bit x of very few rows and a large 4-bit W (pi_mx_rows.cu)
+bool mx_rows_takes(const Gemm &g);
 cudaError_t launch_mx_rows(const Gemm &g, bool bf16, const CtxView &v);
 cudaError_t launch_gemm_mx88(const Gemm &g, bool bf16, const CtxView &v, void *ws);
 cudaError_t launch_gemm_mx84(const Gemm &g, bool bf16, const CtxView &v, void *ws);

@@ -31,8 +31,8 @@ size_t gemm_workspace(const Gemm &g, const CtxView &v)
 cudaError_t launch_gemm(const Gemm &g, bool bf16, const CtxView &v, void *ws)
 {
     if (g.ops != OPS_16)
-        return g.ops == OPS_MX84 && g.M <= kMxRows ? launch_mx_rows(g, bf16, v)
-               : g.M <= kSkinnyRows  ? launch_mx_skinny(g, bf16, v)
+        return mx_rows_takes(g)     ? launch_mx_rows(g, bf16, v)
+               : g.M <= kSkinnyRows ? launch_mx_skinny(g, bf16, v)
                : g.ops == OPS_MX88   ? launch_gemm_mx88(g, bf16, v, ws)
                : g.ops == OPS_MX84 ? launch_gemm_mx84(g, bf16, v, ws)
                                    : launch_gemm_mx44(g, bf16, v, ws);

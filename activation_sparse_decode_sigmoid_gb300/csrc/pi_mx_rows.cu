@@ -1,5 +1,5 @@
-// The product of 8-bit x and 4-bit W, both microscaled, for a few tokens (M <= 32
-// rows of A), with its epilogue:
+// The product of 8-bit x and 4-bit W, both microscaled, for very few tokens and
+// large matrices (mx_rows_takes), with its epilogue:
 //     D[t][f] = sum_k X[t][k] W[f][k]
 //
 // Bound by HBM: every weight is read once.  Here the tokens are the MMA's 128
@@ -7,7 +7,8 @@
 // their sums are not read) and 256 features its columns.  An MMA of mixed types
 // takes 32 of k and about 130 cycles, with 256 columns as with 16: as in
 // pi_mx_skinny.cu, with the weights as rows, 8192 x 28672 takes 377 of them an
-// SM, 27 us, where reading it takes 18; so, it takes half as many.
+// SM, 27 us, where reading it takes 18; so, it takes half as many, and streams at
+// 6.2 TB/s instead of 4.8.  (One token 28.2 us, there 30.9; 28672 x 8192 28.6 and 34.0.)
 //
 // A cluster of CTAs shares a tile of 256 features (gated: of 128 in both
 // matrices), each CTA a part of k.  At a tile's end one warp takes the sums out
@@ -363,6 +364,17 @@ template <typename T, int MODE> cudaError_t run(const Gemm &g, const CtxView &v)
 }
 
 } // namespace
+
+// The sums' way from lanes to columns, and a whole SM for a CTA, so that no launch
+// waits beside the one before it, cost about 3 us at one token and 0.3 more for
+// each further one: worth it from about 48 MB of weights on, to 8 tokens (28672 x 1024, 15.6
+// MB: 9.6 us at one token, in pi_mx_skinny.cu 8.5; 8192 x 28672, 125 MB, at 8, 12 and 16 tokens 30.6,
+// 31.6 and 32.7, there 31.2, 31.5 and 31.7).
+bool mx_rows_takes(const Gemm &g)
+{
+    const int64_t bytes = (int64_t)g.N * mx_tiles(g.K[0]) * 68 * (g.mode == EPI_GATED ? 2 : 1);
+    return g.ops == kMrOps && g.M <= 8 && bytes >= 48 << 20;
+}
 
 cudaError_t launch_mx_rows(const Gemm &g, bool bf16, const CtxView &v)
 {

@@ -155,6 +155,54 @@ def test_linear(c, T, K, N, xk, wk):
     assert r.equal(want)
 
 
+# matrices of 50 MB and more, whose few tokens are the rows of the products
+LARGE = [(1, 16400, 6200), (2, 8192, 12288), (5, 8200, 12500), (8, 28672, 4100), (9, 8200, 12500)]
+
+
+@pytest.mark.parametrize("T,K,N", LARGE)
+def test_linear_of_a_large_matrix(c, T, K, N):
+    m = Maker(T)
+    x, w = m.mx(c, T, K, MX8), m.mx(c, N, K, MX4, K ** -0.5)
+    b, r = m(N, dt=BF16), m(T, N, dt=BF16, pad=3)
+    for fn in R.FNS:
+        y = c.mx_linear(x, w, b, fn=FN(fn), residual=r, scale=0.5)
+        R.check(y, X.linear(x, w, b, fn, 0.5, r, BF16), fn)
+        assert c.mx_linear(x, w, b, fn=FN(fn), residual=r, scale=0.5).equal(y)
+    buf = torch.full((T + 1, N + 5), 7.0, dtype=F16, device="cuda")
+    c.mx_linear(x, w, dtype=F16, y=buf[:T, :N])
+    R.check(buf[:T, :N], X.linear(x, w, None, "none", 1.0, None, F16), "plain")
+    assert bool((buf[T] == 7).all()) and bool((buf[:, N:] == 7).all())
+    r32 = m(T, N, dt=F32)
+    want = X.linear(x, w, b, "silu", 2.0, r32, F32)
+    c.mx_linear(x, w, b, fn=pi.PI_FN_SILU, scale=2.0, residual=r32, y=r32)
+    R.check(r32, want, "fp32, in place")
+    # a block's scale meets its block; a NaN stays in its row
+    for k in (0, 33, (K - 1) // 32):
+        xs, ws = torch.zeros(T, K, device="cuda"), torch.zeros(N, K, device="cuda")
+        xs[:, 32 * k] = 2.0 ** (torch.arange(T, device="cuda") * 5 % 23 - 11)
+        ws[:, 32 * k] = 2.0 ** (torch.arange(N, device="cuda") * 3 % 19 - 9)
+        y = c.mx_linear(c.mx_quantize(xs, MX8), c.mx_quantize(ws, MX4), y=torch.empty(T, N, device="cuda"))
+        assert torch.equal(y, xs @ ws.t()), k
+    ws[N // 2, K - 1] = math.nan
+    xs[T // 2, 5] = math.inf
+    y = c.mx_linear(c.mx_quantize(xs, MX8), c.mx_quantize(ws, MX4))
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[T // 2], bad[:, N // 2] = True, True
+    assert torch.equal(y.isnan(), bad)
+
+
+@pytest.mark.parametrize("T,d,n", [(1, 8192, 6400), (3, 4100, 12500), (8, 8200, 6300)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_gated_ffn_of_large_matrices(c, T, d, n, gated):
+    m = Maker(T)
+    n = n if gated else 2 * n
+    x = m.mx(c, T, d, MX8)
+    w = ffn_weights(m, c, d, n, MX4, BF16, gated, T != 3)
+    for fn in ("relu", "silu", "gelu"):
+        y = c.mx_gated_ffn(x, *w, fn=FN(fn), dtype=BF16)
+        R.check(y, X.ffn(x, *w, fn, BF16), fn)
+
+
 @pytest.mark.parametrize("T,K,N", [(1, 256, 512), (40, 1000, 130), (300, 512, 384)])
 @pytest.mark.parametrize("xk,wk", KINDS)
 def test_linear_adds_into_an_fp32_stream(c, T, K, N, xk, wk):
