@@ -47,9 +47,9 @@
 //
 // Microscaled operands (OPS): a step of k is 128 bytes of a row as before, with
 // its scales beside it; each MMA takes a quarter of it.  The scales pass through
-// tensor memory, which two accumulators would fill: there is one, and the
-// epilogue takes all of it into registers before it computes, so that the next
-// tile's products wait for that only.
+// tensor memory, which two accumulators of 256 columns would fill: they overlap
+// by 64 columns, which the epilogue takes into registers before all else, so that the
+// next tile's products wait for those only.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -419,9 +419,10 @@ __device__ __forceinline__ void mx_block_out(const Epi &e, int64_t row, int col,
 // Shared memory: stages, their scales (of A, then of B's one or two tiles of 128 rows), the epilogue's boxes and biases, barriers
 template <int OPS> constexpr uint32_t kScalesA = Ops<OPS>::mx ? 512u * Ops<OPS>::words : 0u;
 template <int OPS> constexpr uint32_t kBoxesAt = kStagesOf<OPS> * (kStageBytes + 3 * kScalesA<OPS>);
-template <int OPS> constexpr uint32_t kSmemOf = kBoxesAt<OPS> + kBoxes + kEpiWarps * kBiasB + (2 * kStagesOf<OPS> + 4) * 8 + 16;
-// Tensor memory behind a microscaled product's accumulator: four sets of scales, of B from its column 8
-constexpr uint32_t kScalesAt = 256, kScaleSet = 32, kScaleSetB = 8;
+template <int OPS> constexpr uint32_t kSmemOf = kBoxesAt<OPS> + kBoxes + kEpiWarps * kBiasB + (2 * kStagesOf<OPS> + 5) * 8 + 16;
+// Tensor memory of a microscaled product: the second accumulator from column 192
+// on, and behind it two sets of scales, of B from a set's column 8.
+constexpr uint32_t kSecond = 192, kScalesAt = 448, kScaleSet = 32, kScaleSetB = 8;
 
 // WIDE: columns of a tile's accumulator, 256 or 128.
 template <typename T, int MODE, int NP, int WIDE, int OPS>
@@ -432,7 +433,8 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
     using H = H16<T>;
     using O = Ops<OPS>;
     constexpr int kStages = kStagesOf<OPS>;
-    constexpr uint32_t kAccs = O::mx ? 1 : 2;
+    constexpr bool kOverlap = O::mx && WIDE == kTile;
+    constexpr uint32_t kAcc1 = O::mx ? kSecond : 256; // the second accumulator
     constexpr uint32_t kSfA = kScalesA<OPS>, kSfB = kSfA * (WIDE / 128), kSf = 3 * kSfA;
     constexpr int kOutN = MODE == EPI_GATED ? 128 : WIDE; // output columns of a tile
     constexpr bool kPlain = NP > 1; // a backward pass's products: no bias, activation, scale or z
@@ -442,7 +444,8 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
     uint64_t *empty = full + kStages;
     uint64_t *acc_full = empty + kStages;  // [2]
     uint64_t *acc_empty = acc_full + 2;    // [2], used in the first CTA
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *common = acc_empty + 2;      // the columns of both accumulators, used in the first CTA
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(common + 1);
     if (warp == kEpiWarps && lane == 0) {
         // the maps are on their way while the rest is set up
         const Prob &pr = p.prob[NP == 1 ? 0 : p.s.ndeal ? p.s.deal[0].prob : p.s.sprob];
@@ -452,6 +455,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init1(full + s), mbar_init1(empty + s);
         for (int s = 0; s < 2; ++s) mbar_init1(acc_full + s), mbar_init(acc_empty + s, 2 * kEpiWarps);
+        if (kOverlap) mbar_init(common, kEpiWarps); // half of the warps of either CTA
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -533,13 +537,14 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                 const uint64_t da = pr.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
                 const uint64_t db = pr.b_mn ? sdesc(base + kOpBytes, kAtom, 1024) : sdesc(base + kOpBytes, 16, 1024);
                 const uint32_t ka = pr.a_mn ? 128 : 2, kb = pr.b_mn ? 128 : 2; // 16 elements of k
-                const uint32_t buf = it % kAccs, ph = (it / kAccs) & 1;
-                if (it >= kAccs && !mbar_wait_all(acc_empty + buf, ph ^ 1u, p)) {
+                const uint32_t buf = it & 1, ph = (it >> 1) & 1;
+                if ((it >= 2 && !mbar_wait_all(acc_empty + buf, ph ^ 1u, p)) ||
+                    (kOverlap && it >= 1 && !mbar_wait_all(common, (it - 1) & 1, p))) {
                     ok = false;
                     break;
                 }
                 tc_after();
-                const uint32_t d = tmem + buf * 256u;
+                const uint32_t d = tmem + buf * kAcc1;
                 for (int k = w.k0; k < w.k1; ++k) {
                     if (!mbar_wait_all(full + cur.s, cur.ph, p)) {
                         ok = false;
@@ -568,7 +573,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                         }
                         commit2(empty + cur.s);
                     }
-                    set = (set + 1) & 3;
+                    set ^= 1;
                     __syncwarp();
                     cur.next(kStages);
                 }
@@ -597,17 +602,21 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
             const bool biased = !kPlain && MODE != EPI_DACT && (e.bias || e.bias2);
             const bool simple = !O::mx && MODE == EPI_LINEAR && !has_in && !out32 && out.vec &&
                                 (kPlain || (!biased && !e.out2 && e.fn == PI_FN_NONE && e.scale == 1.f));
-            const uint32_t buf = it % kAccs, ph = (it / kAccs) & 1;
+            const uint32_t buf = it & 1, ph = (it >> 1) & 1;
             const bool mxo = O::mx && (MODE == EPI_GATED || e.mx); // a microscaled output
             const int Nend = mxo ? e.mx_tiles * 128 : N;           // (whose padding is written too)
             int mi, ni;
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
             const int row0 = mi * kTile + (int)rank * 128 + q * 32, col0 = ni * kOutN + half * kCols;
             const bool whole = w.slot < 0;
+            // the first accumulator's last 64 columns are the second one's first:
+            // the half that reads them does so early (but in tiles at the edge), and in their turn
+            const bool keeps = kOverlap && half == (buf ? 0 : 1), early = keeps && whole && row0 < M && col0 + kCols <= Nend;
+            const int turn = MODE != EPI_GATED && early && !buf ? 64 : 0;
             uint4 q1[4], q2[4]; // the next chunk's inputs
             if (whole && has_in) { // in flight while the products finish
-                strip_load(in1, lane, row0, col0, M, N, q1);
-                if (two) strip_load(in2, lane, row0, col0, M, N, q2);
+                strip_load(in1, lane, row0, col0 + turn, M, N, q1);
+                if (two) strip_load(in2, lane, row0, col0 + turn, M, N, q2);
             }
             if (whole && biased) { // 4 values a lane
                 const int h = MODE == EPI_GATED ? lane >> 4 : 0, k = (MODE == EPI_GATED ? lane & 15 : lane) * 4;
@@ -625,7 +634,14 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
             ok = warp_wait(acc_full + buf, ph, p, lane);
             if (!ok) break;
             tc_after();
-            const uint32_t ta = lane_addr + buf * 256u;
+            const uint32_t ta = lane_addr + buf * kAcc1;
+            bool kept = !keeps;
+            auto keep = [&]() { // the common columns are in registers, or not needed
+                tc_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_first(smem_addr(common)));
+                kept = true;
+            };
             bool released = false;
             if (!whole) {
                 const int r = (int)rank * 128 + q * 32 + lane; // row within the tile
@@ -649,46 +665,36 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                 released = true;
             } else if (row0 < M) {
                 if (MODE == EPI_LINEAR) box_settle(lane);
-                // microscaled products: the accumulator's columns of this warp, all in registers
-                constexpr int kHeld = O::mx ? kCols / 32 : 1;
-                uint32_t hv[kHeld][32], hu[MODE == EPI_GATED ? kHeld : 1][32];
-                if constexpr (O::mx) {
-#pragma unroll
-                    for (int i = 0; i < kHeld; ++i) {
-                        tmem_ld32_async(ta + half * kCols + 32 * i, hv[i]);
-                        if (MODE == EPI_GATED) tmem_ld32_async(ta + 128 + half * kCols + 32 * i, hu[i]);
+                // the common columns, into registers: with one matrix two chunks of
+                // this warp's, else both of g's or of u's
+                uint32_t hold[kOverlap ? 2 : 1][32];
+                if constexpr (kOverlap)
+                    if (early) {
+                        tmem_ld32_async(ta + (buf ? 0 : 192), hold[0]);
+                        tmem_ld32_async(ta + (buf ? 32 : 224), hold[1]);
+                        tmem_wait32(hold[0]);
+                        tmem_wait32(hold[1]);
+                        keep();
                     }
-#pragma unroll
-                    for (int i = 0; i < kHeld; ++i) {
-                        tmem_wait32(hv[i]);
-                        if (MODE == EPI_GATED) tmem_wait32(hu[i]);
-                    }
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
-                    released = true;
-                }
 #pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
-                    const int col = col0 + c;
+                for (int k = 0; k < kCols; k += 32) {
+                    const int c = k ^ turn, col = col0 + c;
                     if (col >= Nend) break;
-                    const bool inside = row0 + 32 <= M && col + 32 <= N, final = c + 32 >= kCols || col + 32 >= Nend;
+                    const bool inside = row0 + 32 <= M && col + 32 <= N, final = k + 32 >= kCols || (!turn && col + 32 >= Nend);
                     float v[32], u[MODE == EPI_GATED ? 32 : 1];
-                    if constexpr (O::mx) { // (the others move up: one copy of the code below)
+                    const bool held_v = kOverlap && early && (MODE == EPI_GATED ? buf == 1 : k < 64);
+                    const bool held_u = kOverlap && MODE == EPI_GATED && early && buf == 0;
+                    if (!held_v) tmem_ld32(ta + half * kCols + c, v);
+                    if (MODE == EPI_GATED && !held_u) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
+                    if constexpr (kOverlap)
+                        if (held_v || held_u) { // (the second moves up: one copy of the code below)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            v[i] = __uint_as_float(hv[0][i]);
-                            if (MODE == EPI_GATED) u[i % (MODE == EPI_GATED ? 32 : 1)] = __uint_as_float(hu[0][i]);
-#pragma unroll
-                            for (int j = 1; j < kHeld; ++j) {
-                                hv[j - 1][i] = hv[j][i];
-                                if (MODE == EPI_GATED) hu[j - 1][i] = hu[j][i];
+                            for (int i = 0; i < 32; ++i) {
+                                if (held_v) v[i] = __uint_as_float(hold[0][i]);
+                                else u[i % (MODE == EPI_GATED ? 32 : 1)] = __uint_as_float(hold[0][i]);
+                                hold[0][i] = hold[1][i];
                             }
                         }
-                    } else {
-                        tmem_ld32(ta + half * kCols + c, v);
-                        if (MODE == EPI_GATED) tmem_ld32(ta + 128 + half * kCols + c, *reinterpret_cast<float(*)[32]>(u));
-                    }
                     if (!released && final) {
                         // the accumulator is in registers: the next tile's products may begin
                         tc_before();
@@ -700,8 +706,9 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                         strip_to_box(box0, lane, q1);
                         if (two) strip_to_box(box1, lane, q2);
                         if (!final) {
-                            strip_load(in1, lane, row0, col + 32, M, N, q1);
-                            if (two) strip_load(in2, lane, row0, col + 32, M, N, q2);
+                            const int next = col0 + ((k + 32) ^ turn);
+                            strip_load(in1, lane, row0, next, M, N, q1);
+                            if (two) strip_load(in2, lane, row0, next, M, N, q2);
                         }
                         __syncwarp();
                     }
@@ -796,6 +803,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                 __syncwarp();
                 if (lane == 0) arrive_cluster(in_first(smem_addr(acc_empty + buf)));
             }
+            if (!kept) keep();
         }
         if (MODE == EPI_LINEAR && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // written
     }
