@@ -393,6 +393,119 @@ def test_calls_on_two_streams_at_once(c):
     assert not bad
 
 
+def wider(q, extra=64, off=32):
+    """The same matrix as rows of wider ones."""
+    rows, n = q.codes.shape
+    buf = torch.full((rows + 1, off + n + extra - off), 0x7f, dtype=torch.uint8, device="cuda")
+    buf[:rows, off: off + n] = q.codes
+    return pi.MxMatrix(buf[:rows, off: off + n], q.scales, q.cols, q.kind)
+
+
+@pytest.mark.parametrize("T", [1, 8, 40, 300])
+@pytest.mark.parametrize("xk,wk", KINDS)
+def test_rows_of_wider_buffers(c, T, xk, wk):
+    m = Maker(12)
+    d, n = 300, 520
+    x, w = m.mx(c, T, d, xk), ffn_weights(m, c, d, n, wk, BF16, True, True)
+    assert c.mx_linear(wider(x), wider(w[0])).equal(c.mx_linear(x, w[0]))
+    assert c.mx_gated_ffn(wider(x), *map(wider, w[:3]), *w[3:]).equal(c.mx_gated_ffn(x, *w))
+
+
+@pytest.mark.parametrize("T", [1, 8])
+def test_rows_of_wider_large_matrices(c, T):
+    m = Maker(13)
+    x, w = m.mx(c, T, 8200, MX8), m.mx(c, 12500, 8200, MX4)
+    assert c.mx_linear(wider(x), wider(w)).equal(c.mx_linear(x, w))
+
+
+def test_tokens_from_a_row_tile_on(c):
+    """Rows from a multiple of 128 on are a matrix of their own."""
+    m = Maker(14)
+    x, w = m.mx(c, 400, 300, MX8), m.mx(c, 200, 300, MX4)
+    y = c.mx_linear(x, w)
+    for a in (128, 256, 384):
+        part = pi.MxMatrix(x.codes[a:], x.scales[a // 128:], 300, MX8)
+        want = X.linear(part, w, None, "none", 1.0, None, BF16)
+        R.check(c.mx_linear(part, w), want)
+        R.check(y[a:], want)
+
+
+@pytest.mark.parametrize("kind", [MX8, MX4])
+def test_more_than_2_31_elements(c, kind):
+    """Offsets past 32 bits: the last rows as they are by themselves."""
+    T, K = 270000, 8000
+    x = torch.zeros(T, K, dtype=BF16, device="cuda")
+    x[-300:] = Maker(15)(300, K, dt=BF16)
+    q = c.mx_quantize(x, kind)
+    y = c.mx_dequantize(q)
+    same(c.mx_quantize(x[-300:], kind), X.quantize(kind, x[-300:].double()))
+    assert torch.equal(y[-300:].double(), X.quantize(kind, x[-300:].double())[2])
+    assert not bool(y[:-300].any())
+    w = Maker(16).mx(c, 16, K, kind)
+    out = c.mx_linear(q, w)
+    R.check(out[-300:], X.linear(c.mx_quantize(x[-300:], kind), w, None, "none", 1.0, None, BF16))
+    assert not bool(out[:-300].any())
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("xk,wk", KINDS)
+def test_weights_written_right_before_their_use(c, T, xk, wk):
+    """Launches may begin before those in front of them end: no load is ahead of what writes its data."""
+    m = Maker(17)
+    d, n = 1000, 2700
+    raw = [[m(*s, dt=BF16, std=s[1] ** -0.5) for s in ((n, d), (n, d), (d, n))] for _ in range(3)]
+    xs = [m(T, d, dt=F32) for _ in range(3)]
+    want = []
+    for r, x in zip(raw, xs):
+        q = [c.mx_quantize(w, wk) for w in r]
+        h = c.norm_residual_mx(x, kind=xk)[1]
+        torch.cuda.synchronize()
+        want.append(c.mx_gated_ffn(h, *q))
+        torch.cuda.synchronize()
+    q = [c.mx_empty(*w.shape, wk) for w in raw[0]]
+    h, xo = c.mx_empty(T, d, xk), torch.empty(T, d, device="cuda")
+    got = []
+    for i in range(30):
+        for w, o in zip(raw[i % 3], q):
+            c.mx_quantize(w, wk, out=o)
+        c.norm_residual_mx(xs[i % 3], kind=xk, h=h, x_out=xo)
+        got.append(c.mx_gated_ffn(h, *q))
+    assert all(y.equal(want[i % 3]) for i, y in enumerate(got))
+
+
+def test_norm_in_place(c):
+    m = Maker(18)
+    for T in (3, 400):
+        x, y = m(T, 520, dt=F32), m(T, 520, dt=BF16)
+        want, h = c.norm_residual_mx(x, y)
+        xo, h2 = c.norm_residual_mx(x, y, x_out=x)
+        assert xo is x and x.equal(want) and h2.codes.equal(h.codes) and h2.scales.equal(h.scales)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 2048, 512), (100, 2048, 512), (300, 2048, 512), (4, 8200, 12500)])
+@pytest.mark.parametrize("xk,wk", KINDS)
+def test_a_wait_that_runs_out_is_reported(T, K, N, xk, wk):
+    """With a wait limit of a nanosecond the products' waits run out: the
+    kernels return, the status says so, and the context goes on working."""
+    ctx = G.ctx()
+    try:
+        m = Maker(21)
+        x, w = m.mx(ctx, T, K, xk), m.mx(ctx, N, K, wk, 0.02)
+        want = ctx.mx_linear(x, w)
+        ctx.check()
+        pi.pi_debug_set_wait_limit(ctx.handle, 1)
+        status = 0
+        for _ in range(5):  # (a wait may be over before the clock is read)
+            ctx.mx_linear(x, w)
+            status = ctx.sync_status() or status  # (which also clears it)
+        assert status == pi.PI_ERR_TIMEOUT
+        pi.pi_debug_set_wait_limit(ctx.handle, 2_000_000_000)
+        assert ctx.mx_linear(x, w).equal(want)
+        ctx.check()
+    finally:
+        ctx.close()
+
+
 def test_refusals(c):
     lib = pi.load_library()
     dev = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
