@@ -6,7 +6,7 @@ The compute lives in ``libpi.so`` (hand-written CUDA, C ABI declared in
 ctypes binding with the same entry-point names; ``workload`` draws the seeded
 synthetic layers.  The dense side of the same models (long prompts, training)
 has its own calls: a linear layer, a gated FFN block and the norms around it,
-forward and backward.  Nothing here falls back to a CPU path: if the extension is
+forward and backward, and forward with microscaled matrices of 8 and 4 bits.  Nothing here falls back to a CPU path: if the extension is
 missing, loading the binding raises.
 """
 import importlib

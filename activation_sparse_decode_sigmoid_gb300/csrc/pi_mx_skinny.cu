@@ -4,15 +4,19 @@
 //
 // Bound by HBM: every weight is read once.  The weights are the MMA's 128-row
 // operand and the tokens its columns (M rounded up to 16); a CTA per SM streams
-// its share of W through a ring of boxes that fills shared memory.
+// its share of W through a ring of boxes in half of the SM's shared memory (more
+// in flight gained nothing), so that the next launch's CTAs can start beside
+// them.  8192 -> 28672, one token: both of 4 bits 24.0 us (5.2 TB/s of weights), of 8
+// 42.6 (5.7 TB/s; a copy reaches 6.8), 4-bit weights under 8-bit x 30.9 (4.0 TB/s: bound by the
+// MMAs' number, see pi_mx_rows.cu).
 //
 // A cluster of CTAs takes a tile of 128 features at a time, each CTA a part of
 // k: as many CTAs to a cluster as deal the tiles' steps most evenly.  At a
 // tile's end every CTA sends the sums of a token to the CTA of the cluster that
 // owns the token (distributed shared memory), which adds them in a fixed
-// order and runs the epilogue: one launch, no workspace.  (Work cut by bytes over all CTAs,
-// partial sums through memory and a second launch that joins them, as in
-// pi_skinny.cu, cost 5 us more.)
+// order and runs the epilogue: one launch, no workspace.  (Work cut by bytes
+// over all CTAs, partial sums through memory and a second launch that joins
+// them, as in pi_skinny.cu: both of 4 bits 26.3 us at 8192 -> 28672.)
 //
 // Every wait is bounded, as in pi_tc.cuh.
 #include <cuda_bf16.h>
@@ -307,7 +311,7 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
 }
 
 // ------------------------------------------------------------------ host
-constexpr int kMsExchange = 12; // steps
+constexpr int kMsExchange = 12; // steps: 2 to 3 us at about 0.2 us a step of 16 KB
 
 MsParams plan(const Gemm &g, const CtxView &v, const int (&n)[4], int &grid)
 {
@@ -321,7 +325,7 @@ MsParams plan(const Gemm &g, const CtxView &v, const int (&n)[4], int &grid)
     p.owners = (p.T + p.own - 1) / p.own;
     // half of an SM's shared and tensor memory where that gives a ring of four
     // steps: the next launch's CTAs then wait beside these for their end, their
-    // barriers set up and their first weights on the way into L2
+    // barriers set up (and, with `early`, their first weights loaded)
     const int acc = nm * p.Tp;
     p.slotB = kMsW + (uint32_t)p.Tp * 128u + 1024u * words;
     p.partB = (uint32_t)(p.cs - 1) * nm * p.own * 512u;
