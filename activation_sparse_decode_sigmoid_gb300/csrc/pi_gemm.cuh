@@ -50,9 +50,11 @@
 // tensor memory, which two accumulators of 256 columns would fill: they overlap
 // by 64 columns, which the epilogue takes into registers before all else, so that the
 // next tile's products wait for those only (one accumulator: 2048 x 28672 -> 8192 in
-// 4 bits 165 us, so 157).  That product runs at 6.1 PFLOP/s, 2048 x 8192 -> 2 x 28672 in
-// 8 and 4 bits at 3.2, 1.6 to 3.2 times the 16-bit peak; the tensor cores are
-// busy 80 % of the time (16 bits: 93 %), the rest being the scales' copies.
+// 4 bits 165 us, so 157).  Long runs are bound by the power limit: 2048 x 7168 -> 28672
+// in 8 and 4 bits takes 217 us on matrices of ones (3.9 PFLOP/s, twice the 16-bit peak),
+// 238 on normal values in a short run and 259 in a long one; 2048 x 28672 -> 8192 in
+// 4 bits 138, 145 and 150 (7.0, 6.6, 6.4 PFLOP/s).  Five stages: with four 277 and 170 us
+// where five take 268 and 157; six, with the epilogue's boxes halved, 267 and 158.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -10,9 +10,10 @@
 // instruction descriptor says which of a word's bytes an MMA takes.
 //
 // Each step's copies are issued right before its MMAs, into the next of a few
-// sets of columns, by the same warp.  Copies for up to four steps at a time
-// (2048 x 28672 -> 8192 in 4 bits 157 -> 166 us), in the middle of the step before's MMAs
-// (173) and from a warp of their own (184) were all slower.
+// sets of columns, by the same warp.  There they cost nothing (left out but for a tile's
+// first two steps, 2048 x 28672 -> 8192 in 4 bits took the same time); for two or up to four
+// steps at a time (157 -> 160, 166 us), in the middle of the step before's MMAs (173) and from
+// a warp of their own (184) they did.
 #pragma once
 
 #include <stdint.h>
