@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "pi_block.h"
 #include "pi_epi.cuh"
@@ -38,7 +39,7 @@ namespace pi {
 namespace {
 
 constexpr int kMrOps = OPS_MX84;
-constexpr int kMrThreads = 256;              // warp 0: sums out of tensor memory; 1: TMA; 2: MMA; 4-7: epilogue
+constexpr int kMrThreads = 288;              // warps 0, 8: sums out of tensor memory; 1: TMA; 2: MMA; 4-7: epilogue
 constexpr uint32_t kMrX = 4096, kMrW = 32768; // a step's tokens, its 256 features
 constexpr uint32_t kMrSlot = kMrX + kMrW + 2048;
 constexpr int kMrRing = 5;
@@ -101,14 +102,20 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
     if (tid == 32) prefetch_map(&p.mw[0]), prefetch_map(&p.mx), prefetch_map(&p.msw[0]), prefetch_map(&p.msx);
     if (tid == 0) {
         for (uint32_t s = 0; s < S; ++s) mbar_init1(full + s), mbar_init1(empty + s);
-        mbar_init1(acc_full), mbar_init1(acc_empty), mbar_init1(sums_full), mbar_init(sums_free, 4);
+        mbar_init1(acc_full), mbar_init(acc_empty, 2), mbar_init(sums_full, 2), mbar_init(sums_free, 4);
         const uint32_t others = 4u * (uint32_t)max(1, p.cs - 1); // four warps of each other CTA
         mbar_init(part_full, others), mbar_init(part_free, others); // have sent, have read
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const uint32_t tmem = tmem_alloc(tslot, 512);
-    if (p.cs > 1) cluster_sync(); // all barriers are set up
-    if (!(p.early && warp == 1)) pdl_enter();
+    // The code behind the products runs once or a few times a launch, and the first
+    // time it comes from memory: the weights have passed through L2 since the
+    // launch before.  Its warps go through it once ahead, with nothing to wait for,
+    // send to another CTA or store (8192 x 28672 at one token 29.6 -> 27.4 us, 28672 x 8192
+    // at eight 30.1 -> 28.2).  Others send sums only when that is over.
+    const bool rehearses = (warp & 7) == 0 || warp >= 4;
+    if (p.cs > 1 && !rehearses) cluster_arrive(); // all barriers are set up
+    if (!rehearses && !(p.early && warp == 1)) pdl_enter();
     const uint32_t base = smem_addr(smem);
     MxWalk w(p.tn, 1, p.KT, p.cs, cluster, clusters, rank);
     // this CTA's sums, [token][256 and a pad: rows start in different banks], and the
@@ -203,42 +210,68 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
             if (ok && elect_one()) mma_commit(acc_full);
             __syncwarp();
         }
-    } else if (warp == 0) { // the tokens lie in its lanes of tensor memory
+    } else if ((warp & 7) == 0) { // the tokens lie in these warps' lanes of tensor memory; half of the columns each
+        const int half = warp >> 3;
+        bool dry = true;
         uint32_t it = 0;
-        for (int tile = cluster; tile < p.tn; tile += clusters, ++it) {
-            ok = warp_wait(acc_full, it & 1, p, lane);
-            if (ok && it > 0) ok = warp_wait(sums_free, (it - 1) & 1, p, lane);
-            if (!ok) break;
-            tc_after();
+        for (int tile = cluster; tile < p.tn;) {
+            if (!dry) {
+                ok = warp_wait(acc_full, it & 1, p, lane);
+                if (ok && it > 0) ok = warp_wait(sums_free, (it - 1) & 1, p, lane);
+                if (!ok) break;
+                tc_after();
+            }
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
-                float v[32];
-                tmem_ld32(tmem + (uint32_t)c, v);
+            for (int c = 128 * half; c < 128 * half + 128; c += 64) {
+                uint32_t v[2][32];
+                tmem_ld32_async(tmem + (uint32_t)c, v[0]);
+                tmem_ld32_async(tmem + (uint32_t)c + 32, v[1]);
+                tmem_wait32(v[0]);
+                tmem_wait32(v[1]);
                 const uint32_t at = sums + (uint32_t)lane * kSumRow + (uint32_t)c * 4u;
                 if (lane < p.T) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 4 * i), "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]) : "memory");
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 128 * h + 4 * i), "r"(v[h][i]), "r"(v[h][i + 1]), "r"(v[h][i + 2]), "r"(v[h][i + 3]) : "memory");
                 }
             }
             tc_before();
             __syncwarp();
+            if (dry) {
+                if (p.cs > 1) cluster_arrive();
+                pdl_enter();
+                dry = false;
+                continue;
+            }
             if (lane == 0) {
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(acc_empty)) : "memory");
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(sums_full)) : "memory");
             }
+            tile += clusters, ++it;
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4) { // (4 to 7)
         // A feature to a thread (two, where a CTA owns all 256); where a slice has
         // fewer than 128, the other warps take other tokens.  The code of the call's
         // own activation and output type only: it runs once or a few times a launch, so that every
         // line of it comes from memory (all of them, unrolled over 8 tokens, took 5 to 7 us instead of 1).
         const int e = tid - 128, shift = 31 - __clz(p.slice), i0 = e & (p.slice - 1), tg = e >> shift, ng = max(1, 128 >> shift);
+        bool dry = true;
         uint32_t it = 0;
-        for (int tile = cluster; tile < p.tn; tile += clusters, ++it) {
+        for (int tile = cluster; tile < p.tn;) {
             const int fs = tile * kTileN + rank * p.slice; // the slice's first feature
-            // the residual, on its way while the products run; a thread reads back what it put
-            if (MODE == EPI_LINEAR && p.e.res) {
+            // biases and the residual, on their way while the products run; a thread reads back what it put
+            float bias[2][2] = {}; // [matrix][i0, i0 + 128]
+            if (!dry)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int f = fs + i0 + 128 * h;
+                    if (128 * h >= p.slice || f >= p.N) continue;
+                    if (p.e.bias) bias[0][h] = C16<T>::one(p.e.bias[f]);
+                    if (NM == 2 && p.e.bias2) bias[1][h] = C16<T>::one(p.e.bias2[f]);
+                }
+            if (MODE == EPI_LINEAR && p.e.res && !dry) {
 #pragma unroll 1
                 for (int i = i0; i < p.slice; i += 128) {
                     const int f = fs + i;
@@ -251,16 +284,18 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
                     }
                 }
             }
-            ok = warp_wait(sums_full, it & 1, p, lane);
-            if (ok && p.cs > 1) {
-                if (it > 0) ok = warp_wait_cluster(part_free, (it - 1) & 1, p, lane);
+            if (!dry) {
+                ok = warp_wait(sums_full, it & 1, p, lane);
+                if (ok && p.cs > 1 && it > 0) ok = warp_wait_cluster(part_free, (it - 1) & 1, p, lane);
                 if (!ok) break;
+            }
+            if (p.cs > 1) {
                 // 16 bytes a thread; at the owner [matrix][token][slice]
                 const int qs = shift - 2, c4 = e & ((1 << qs) - 1);
 #pragma unroll 1
                 for (int r = 1; r < p.cs; ++r) {
                     const int q = (rank + r) & (p.cs - 1);
-                    const uint32_t dst = in_cta(part, (uint32_t)q) + (uint32_t)(rank - (rank > q ? 1 : 0)) * srcB + 16u * (uint32_t)c4;
+                    const uint32_t dst = (dry ? part : in_cta(part, (uint32_t)q) + (uint32_t)(rank - (rank > q ? 1 : 0)) * srcB) + 16u * (uint32_t)c4;
                     const uint32_t src = sums + (uint32_t)(q * p.slice + 4 * c4) * 4u;
 #pragma unroll 2
                     for (int row = e >> qs; row < NM * p.T; row += 128 >> qs) {
@@ -272,17 +307,17 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
                     }
                 }
                 __syncwarp(); // (the arrivals release what the whole warp wrote)
-                if (lane < p.cs && lane != rank) arrive_cluster(in_cta(smem_addr(part_full), (uint32_t)lane));
-                ok = warp_wait_cluster(part_full, it & 1, p, lane);
+                if (!dry) {
+                    if (lane < p.cs && lane != rank) arrive_cluster(in_cta(smem_addr(part_full), (uint32_t)lane));
+                    ok = warp_wait_cluster(part_full, it & 1, p, lane);
+                    if (!ok) break;
+                }
             }
-            if (!ok) break;
             finish<T, MODE>(p, [&](auto fn, auto out) {
 #pragma unroll 1
                 for (int i = i0; i < p.slice; i += 128) {
-                    const int f = fs + i;
-                    float b[2] = {};
-                    if (p.e.bias && f < p.N) b[0] = C16<T>::one(p.e.bias[f]);
-                    if (NM == 2 && p.e.bias2 && f < p.N) b[1] = C16<T>::one(p.e.bias2[f]);
+                    const int f = dry ? INT_MAX : fs + i;
+                    const float b[2] = {i < 128 ? bias[0][0] : bias[0][1], i < 128 ? bias[1][0] : bias[1][1]};
 #pragma unroll 4
                     for (int t = tg; t < p.T; t += ng) {
                         float v[2], r = 0.f;
@@ -307,13 +342,22 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
                 }
             });
             __syncwarp();
+            if (dry) {
+                if (p.cs > 1) cluster_arrive();
+                pdl_enter();
+                if (p.cs > 1) cluster_wait();
+                dry = false;
+                continue;
+            }
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(sums_free)) : "memory");
             if (lane < p.cs && lane != rank) arrive_cluster(in_cta(smem_addr(part_free), (uint32_t)lane));
+            tile += clusters, ++it;
         }
     }
     __syncwarp();
     if (*(volatile int *)p.abort_flag) linger(); // copies and MMAs in flight finish before the CTA leaves
     if (p.cs > 1) {
+        if (warp < 4 || warp == 8) cluster_wait(); // (of the first arrival)
         __syncthreads();
         cluster_sync(); // no CTA leaves while another still writes to it
     }
