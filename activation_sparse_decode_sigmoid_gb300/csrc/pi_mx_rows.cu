@@ -8,10 +8,10 @@
 // takes 32 of k and about 130 cycles, with 256 columns as with 16: as in
 // pi_mx_skinny.cu, with the weights as rows, 8192 x 28672 takes 377 of them an
 // SM, 27 us, where reading it takes 18; so, it takes half as many, and streams at
-// 6.2 TB/s instead of 4.8.  (One token 28.2 us, there 30.9; 28672 x 8192 28.6 and 34.0.)
+// 6.3 TB/s instead of 5.5.  (One token 27.3 us, there 30.9; 28672 x 8192 27.2 and 34.1.)
 //
 // A cluster of CTAs shares a tile of 256 features (gated: of 128 in both
-// matrices), each CTA a part of k.  At a tile's end one warp takes the sums out
+// matrices), each CTA a part of k.  At a tile's end two warps take the sums out
 // of tensor memory, a token to a lane, into shared memory; four others send
 // them on, slice by slice of the features, whole lines at a time, to the CTA that owns the slice
 // (distributed shared memory; straight from the lanes, a row to each, took 10 us),
@@ -410,14 +410,18 @@ template <typename T, int MODE> cudaError_t run(const Gemm &g, const CtxView &v)
 } // namespace
 
 // The sums' way from lanes to columns, and a whole SM for a CTA, so that no launch
-// waits beside the one before it, cost about 3 us at one token and 0.3 more for
-// each further one: worth it from about 48 MB of weights on, to 8 tokens (28672 x 1024, 15.6
-// MB: 9.6 us at one token, in pi_mx_skinny.cu 8.5; 8192 x 28672, 125 MB, at 8, 12 and 16 tokens 30.6,
-// 31.6 and 32.7, there 31.2, 31.5 and 31.7).
+// waits beside the one before it, cost about a microsecond at one token and 0.15 more for
+// each further one, and again at each tile where k is too short to hide them: worth it
+// from 20 MB of weights on (2 more a token) and 2048 values of k, to 16 tokens.  us, here and in pi_mx_skinny.cu:
+//   28672 x 1024, 16 MB:    8.7,  8.4 at one token,  9.6,  8.5 at 8, 10.6,  8.5 at 16
+//   28672 x 2048, 31 MB:   11.3, 12.5               12.4, 12.5       13.4, 12.5
+//   28672 x 4096, 62 MB:   17.4, 19.8               18.2, 19.9       19.4, 20.1
+//   28672 x 8192, 125 MB:  27.3, 30.9               28.5, 31.3       29.7, 31.6
+//   128256 x 1024, 70 MB:  21.2, 19.6               22.3, 19.7       24.5, 19.9
 bool mx_rows_takes(const Gemm &g)
 {
     const int64_t bytes = (int64_t)g.N * mx_tiles(g.K[0]) * 68 * (g.mode == EPI_GATED ? 2 : 1);
-    return g.ops == kMrOps && g.M <= 8 && bytes >= 48 << 20;
+    return g.ops == kMrOps && g.M <= 16 && g.K[0] >= 2048 && bytes >= (int64_t)(18 + 2 * g.M) << 20;
 }
 
 cudaError_t launch_mx_rows(const Gemm &g, bool bf16, const CtxView &v)

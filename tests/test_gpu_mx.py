@@ -155,8 +155,9 @@ def test_linear(c, T, K, N, xk, wk):
     assert r.equal(want)
 
 
-# matrices of 50 MB and more, whose few tokens are the rows of the products
-LARGE = [(1, 16400, 6200), (2, 8192, 12288), (5, 8200, 12500), (8, 28672, 4100), (9, 8200, 12500)]
+# matrices of 20 MB and more, whose few tokens are the rows of the products, and just below
+LARGE = [(1, 16400, 6200), (2, 8192, 12288), (5, 8200, 12500), (8, 28672, 4100), (9, 8200, 12500), (1, 2048, 19300), (16, 8200, 12500),
+         (16, 2050, 50000), (13, 30000, 2900), (17, 8200, 12500), (4, 1920, 40000)]
 
 
 @pytest.mark.parametrize("T,K,N", LARGE)
@@ -191,7 +192,7 @@ def test_linear_of_a_large_matrix(c, T, K, N):
     assert torch.equal(y.isnan(), bad)
 
 
-@pytest.mark.parametrize("T,d,n", [(1, 8192, 6400), (3, 4100, 12500), (8, 8200, 6300)])
+@pytest.mark.parametrize("T,d,n", [(1, 8192, 6400), (3, 4100, 12500), (8, 8200, 6300), (16, 8200, 6300), (11, 2060, 20500)])
 @pytest.mark.parametrize("gated", [True, False])
 def test_gated_ffn_of_large_matrices(c, T, d, n, gated):
     m = Maker(T)
