@@ -787,8 +787,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
         }
         if (MODE == EPI_LINEAR && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); // written
     }
-    __syncwarp();
-    if (*(volatile int *)p.abort_flag) linger();
+    settle(p);
     tc_before();
     __syncthreads();
     cluster_sync(); // neither CTA leaves while the other still reads its shared or tensor memory

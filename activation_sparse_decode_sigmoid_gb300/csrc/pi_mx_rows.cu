@@ -354,8 +354,7 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
             tile += clusters, ++it;
         }
     }
-    __syncwarp();
-    if (*(volatile int *)p.abort_flag) linger(); // copies and MMAs in flight finish before the CTA leaves
+    settle(p); // copies and MMAs in flight finish before the CTA leaves
     if (p.cs > 1) {
         if (warp < 4 || warp == 8) cluster_wait(); // (of the first arrival)
         __syncthreads();

@@ -301,8 +301,7 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
             buf.next((uint32_t)p.nbuf);
         }
     }
-    __syncwarp();
-    if (*(volatile int *)p.abort_flag) linger(); // copies and MMAs in flight finish before the CTA leaves
+    settle(p); // copies and MMAs in flight finish before the CTA leaves
     if (p.cs > 1) {
         __syncthreads();
         cluster_sync(); // no CTA leaves while another still writes to it

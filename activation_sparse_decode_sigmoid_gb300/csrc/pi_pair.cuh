@@ -78,13 +78,19 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32])
     asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// After a failure: copies and MMAs in flight finish within microseconds; the
-// CTA stays for a bounded time that covers them.
-__device__ __forceinline__ void linger()
+// A warp's end of its work.  After a failure: copies and MMAs in flight finish
+// within microseconds; the CTA stays for a bounded time that covers them.  Each
+// lane reads the clock for itself, so lanes may leave that loop in different turns: they
+// meet again before the barriers behind it, which take whole warps.
+template <typename P> __device__ __forceinline__ void settle(const P &p)
 {
-    const uint64_t t0 = gtimer();
-    while (gtimer() - t0 < 5000000ull) {
+    __syncwarp();
+    if (*(volatile int *)p.abort_flag) {
+        const uint64_t t0 = gtimer();
+        while (gtimer() - t0 < 5000000ull) {
+        }
     }
+    __syncwarp();
 }
 
 } // namespace

@@ -507,6 +507,32 @@ def test_a_wait_that_runs_out_is_reported(T, K, N, xk, wk):
         ctx.close()
 
 
+@pytest.mark.parametrize("T,d,n", [(3, 8192, 6400), (40, 520, 2600), (300, 520, 2600)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_waits_that_run_out_in_a_block(T, d, n, gated):
+    """The same in both products of a block, the second of which loads ahead of
+    the first one's end: every warp comes to the end of its launch, clusters too."""
+    ctx = G.ctx()
+    try:
+        m = Maker(22)
+        n = n if gated else 2 * n
+        x, w = m.mx(ctx, T, d, MX8), ffn_weights(m, ctx, d, n, MX4, F16, gated, True)
+        run = lambda: ctx.mx_gated_ffn(x, *w, fn=pi.PI_FN_SILU, dtype=F16)
+        want = run()
+        ctx.check()
+        pi.pi_debug_set_wait_limit(ctx.handle, 1)
+        status = 0
+        for _ in range(5):
+            run()
+            status = ctx.sync_status() or status
+        assert status == pi.PI_ERR_TIMEOUT
+        pi.pi_debug_set_wait_limit(ctx.handle, 2_000_000_000)
+        assert run().equal(want)
+        ctx.check()
+    finally:
+        ctx.close()
+
+
 def test_refusals(c):
     lib = pi.load_library()
     dev = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
