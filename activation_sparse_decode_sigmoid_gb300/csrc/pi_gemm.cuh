@@ -629,6 +629,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
 #pragma unroll 1
                 for (int c = half * (WIDE / 2); c < (half + 1) * (WIDE / 2); c += 32) {
                     float v[32];
+                    __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
                     tmem_ld32(ta + c, v);
                     if (row0 + lane < M) {
 #pragma unroll
@@ -662,6 +663,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                     if (col >= Nend) break;
                     const bool inside = row0 + 32 <= M && col + 32 <= N, final = k + 32 >= kCols || (!turn && col + 32 >= Nend);
                     float v[32], u[MODE == EPI_GATED ? 32 : 1];
+                    __syncwarp(); // (as above)
                     const bool held_v = kOverlap && early && (MODE == EPI_GATED ? buf == 1 : k < 64);
                     const bool held_u = kOverlap && MODE == EPI_GATED && early && buf == 0;
                     if (!held_v) tmem_ld32(ta + half * kCols + c, v);

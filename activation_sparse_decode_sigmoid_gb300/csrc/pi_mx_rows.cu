@@ -224,6 +224,7 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
 #pragma unroll 1
             for (int c = 128 * half; c < 128 * half + 128; c += 64) {
                 uint32_t v[2][32];
+                __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
                 tmem_ld32_async(tmem + (uint32_t)c, v[0]);
                 tmem_ld32_async(tmem + (uint32_t)c + 32, v[1]);
                 tmem_wait32(v[0]);

@@ -224,6 +224,7 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
         Cur buf(0, (uint32_t)p.nbuf);
         // this lane's sums of 16 tokens from t0 on
         auto sums = [&](uint32_t b, int m, int t0, float(&v)[16]) {
+            __syncwarp(); // (lanes may have left the outputs before: these loads take whole warps)
             tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + kMsAcc + (uint32_t)((b * NM + m) * p.Tp + t0), v);
         };
         // where CTA q keeps what CTA s sends of matrix m, token t (q's own): [s, q left out][m][token][128]

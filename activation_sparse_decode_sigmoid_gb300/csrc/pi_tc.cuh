@@ -227,6 +227,7 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ uint32_t tmem_alloc(uint32_t *slot, uint32_t ncols)
 {
     if (threadIdx.x < 32) {
+        __syncwarp(); // (its first lane may come from the barriers' setup)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)),
                      "r"(ncols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
