@@ -620,6 +620,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                 tc_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(in_first(smem_addr(common)));
+                __syncwarp();
                 kept = true;
             };
             bool released = false;
@@ -629,13 +630,13 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
 #pragma unroll 1
                 for (int c = half * (WIDE / 2); c < (half + 1) * (WIDE / 2); c += 32) {
                     float v[32];
-                    __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
                     tmem_ld32(ta + c, v);
                     if (row0 + lane < M) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             dst[(c + i) / 4 * kTile] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
+                    __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
                 }
             } else if (simple && row0 + 32 <= M && col0 + kCols <= N) {
                 plain_strip<T, kCols>(ta + half * kCols, box0, &pr.mo, lane, row0, col0, [&]() {
@@ -663,7 +664,6 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                     if (col >= Nend) break;
                     const bool inside = row0 + 32 <= M && col + 32 <= N, final = k + 32 >= kCols || (!turn && col + 32 >= Nend);
                     float v[32], u[MODE == EPI_GATED ? 32 : 1];
-                    __syncwarp(); // (as above)
                     const bool held_v = kOverlap && early && (MODE == EPI_GATED ? buf == 1 : k < 64);
                     const bool held_u = kOverlap && MODE == EPI_GATED && early && buf == 0;
                     if (!held_v) tmem_ld32(ta + half * kCols + c, v);
@@ -759,6 +759,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                                         }
                                         store8f(static_cast<float *>(e.out) + (int64_t)(row0 + lane) * e.ldo + cj, N - cj, e.vec & V_OUT, x);
                                     }
+                                __syncwarp();
                                 continue;
                             }
                             if (has_in) {
@@ -774,6 +775,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                     }
                     if (O::mx && mxo) {
                         if (row0 + lane < M) mx_block_out(e, row0 + lane, col, N, v);
+                        __syncwarp();
                         continue;
                     }
                     box_put<T>(box0, lane, v);

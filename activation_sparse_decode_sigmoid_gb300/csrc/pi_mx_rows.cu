@@ -224,7 +224,6 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
 #pragma unroll 1
             for (int c = 128 * half; c < 128 * half + 128; c += 64) {
                 uint32_t v[2][32];
-                __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
                 tmem_ld32_async(tmem + (uint32_t)c, v[0]);
                 tmem_ld32_async(tmem + (uint32_t)c + 32, v[1]);
                 tmem_wait32(v[0]);
@@ -237,6 +236,7 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
                         for (int i = 0; i < 32; i += 4)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 128 * h + 4 * i), "r"(v[h][i]), "r"(v[h][i + 1]), "r"(v[h][i + 2]), "r"(v[h][i + 3]) : "memory");
                 }
+                __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
             }
             tc_before();
             __syncwarp();

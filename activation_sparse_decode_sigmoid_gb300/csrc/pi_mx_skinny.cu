@@ -224,7 +224,6 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
         Cur buf(0, (uint32_t)p.nbuf);
         // this lane's sums of 16 tokens from t0 on
         auto sums = [&](uint32_t b, int m, int t0, float(&v)[16]) {
-            __syncwarp(); // (lanes may have left the outputs before: these loads take whole warps)
             tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + kMsAcc + (uint32_t)((b * NM + m) * p.Tp + t0), v);
         };
         // where CTA q keeps what CTA s sends of matrix m, token t (q's own): [s, q left out][m][token][128]
@@ -294,6 +293,7 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
                     for (int i = 0; i < 16; ++i) v[0][i] *= v[NM - 1][i] + bias2;
                 }
                 put16<T>(p.e, t0, min(16, t1 - t0), f, p.N, v[0]);
+                __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
             }
             tc_before();
             __syncwarp();
