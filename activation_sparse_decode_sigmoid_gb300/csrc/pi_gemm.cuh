@@ -687,7 +687,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                     if (has_in) {
                         strip_to_box(box0, lane, q1);
                         if (two) strip_to_box(box1, lane, q2);
-                        if (!final) {
+                        if (!released) {
                             const int next = col0 + ((k + 32) ^ turn);
                             strip_load(in1, lane, row0, next, M, N, q1);
                             if (two) strip_load(in2, lane, row0, next, M, N, q2);
