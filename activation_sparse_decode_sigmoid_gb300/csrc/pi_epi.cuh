@@ -298,7 +298,7 @@ __device__ __forceinline__ void epilogue8(const Epi &e, int N, int64_t row, int 
 // The same with a microscaled output (EPI_LINEAR without residual, EPI_GATED):
 // called by all lanes of a warp, four of which, XOR and 2 XOR apart, hold the 32
 // columns of a block.  on: the row exists, and col lies inside the padded row.
-template <typename T, int MODE, int XOR>
+template <typename T, int MODE, int XOR, int KIND>
 __device__ __forceinline__ void epilogue8_mx(const Epi &e, int N, int64_t row, int col, bool on, float (&v)[8], float (&v2)[8])
 {
     const int n = on ? N - col : 0;
@@ -319,7 +319,7 @@ __device__ __forceinline__ void epilogue8_mx(const Epi &e, int N, int64_t row, i
         v[i] *= MODE == EPI_GATED ? v2[i] : e.scale;
         if (i >= n) v[i] = 0.f; // (what pads a row is 0)
     }
-    mx_store8<XOR>(e.mx, static_cast<uint8_t *>(e.out), e.ldo, e.mx_scales, e.mx_tiles, row, col, on, v);
+    mx_store8<XOR>(KIND, static_cast<uint8_t *>(e.out), e.ldo, e.mx_scales, e.mx_tiles, row, col, on, v);
 }
 
 // The epilogue of one element (EPI_LINEAR, EPI_GATED).

@@ -368,8 +368,12 @@ __device__ __forceinline__ void plain_strip(uint32_t ta, uint32_t box, const CUt
 }
 
 // A block of a microscaled output: this thread's row, columns [col, col + 32).
-template <int KIND> __device__ __forceinline__ void mx_block_of(const Epi &e, int64_t row, int col, const float (&v)[32])
+template <int KIND> __device__ __forceinline__ void mx_block_out(const Epi &e, int64_t row, int col, int N, float (&v)[32])
 {
+    if (col + 32 > N) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = col + i < N ? v[i] : 0.f; // (what pads a row is 0)
+    }
     uint32_t a = 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) a = max(a, mag(v[i]));
@@ -384,15 +388,6 @@ template <int KIND> __device__ __forceinline__ void mx_block_of(const Epi &e, in
     } else
         *reinterpret_cast<uint4 *>(o) = make_uint4(q[0].x, q[1].x, q[2].x, q[3].x);
     e.mx_scales[mx_scale_at(row, col >> 7, e.mx_tiles) + ((col >> 5) & 3)] = (uint8_t)code;
-}
-__device__ __forceinline__ void mx_block_out(const Epi &e, int64_t row, int col, int N, float (&v)[32])
-{
-    if (col + 32 > N) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = col + i < N ? v[i] : 0.f; // (what pads a row is 0)
-    }
-    if (e.mx == PI_MX8) mx_block_of<PI_MX8>(e, row, col, v);
-    else mx_block_of<PI_MX4>(e, row, col, v);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -418,6 +413,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
     constexpr uint32_t kSfA = kScalesA<OPS>, kSfB = kSfA * (WIDE / 128), kSf = 3 * kSfA;
     constexpr int kOutN = MODE == EPI_GATED ? 128 : WIDE; // output columns of a tile
     constexpr bool kPlain = NP > 1; // a backward pass's products: no bias, activation, scale or z
+    constexpr bool kQuantised = O::mx && MODE == EPI_GATED; // a microscaled output always (else where e.mx says so)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kBoxesAt<OPS> + kBoxes + kEpiWarps * kBiasB); // used in the first CTA
@@ -483,12 +479,12 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                             pair_load(sf + kSfA, &p.msb[0], ks, MODE == EPI_GATED ? ni : ni * (WIDE / 128), bar);
                             if (MODE == EPI_GATED) pair_load(sf + 2 * kSfA, &p.msb[1], ks, ni, bar);
                         }
-                        if (pr.a_mn) {
+                        if (!O::mx && pr.a_mn) {
                             pair_load(sa, ma, m0, kc, bar);
                             pair_load(sa + kAtom, ma, m0 + 64, kc, bar);
                         } else
                             pair_load(sa, ma, kc, m0, bar);
-                        if (pr.b_mn) {
+                        if (!O::mx && pr.b_mn) {
                             pair_load(sb, mb, n0, kc, bar);
                             if (WIDE == kTile) pair_load(sb + kAtom, mb, n0 + 64, kc, bar);
                         } else
@@ -514,8 +510,8 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                 const uint32_t id = O::mx ? idesc_mx(O::xfmt, O::wfmt, 256, WIDE)
                                           : idesc(H::fmt, (uint32_t)pr.a_mn, (uint32_t)pr.b_mn, 256, WIDE);
                 // descriptors of stage 0; a byte offset o adds o / 16 (the start address field)
-                const uint64_t da = pr.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
-                const uint64_t db = pr.b_mn ? sdesc(base + kOpBytes, kAtom, 1024) : sdesc(base + kOpBytes, 16, 1024);
+                const uint64_t da = !O::mx && pr.a_mn ? sdesc(base, kAtom, 1024) : sdesc(base, 16, 1024);
+                const uint64_t db = !O::mx && pr.b_mn ? sdesc(base + kOpBytes, kAtom, 1024) : sdesc(base + kOpBytes, 16, 1024);
                 const uint32_t ka = pr.a_mn ? 128 : 2, kb = pr.b_mn ? 128 : 2; // 16 elements of k
                 const uint32_t buf = it & 1, ph = (it >> 1) & 1;
                 if ((it >= 2 && !mbar_wait_all(acc_empty + buf, ph ^ 1u, p)) ||
@@ -583,7 +579,7 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
             const bool simple = !O::mx && MODE == EPI_LINEAR && !has_in && !out32 && out.vec &&
                                 (kPlain || (!biased && !e.out2 && e.fn == PI_FN_NONE && e.scale == 1.f));
             const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-            const bool mxo = O::mx && (MODE == EPI_GATED || e.mx); // a microscaled output
+            const bool mxo = kQuantised || (O::mx && e.mx); // a microscaled output
             const int Nend = mxo ? e.mx_tiles * 128 : N;           // (whose padding is written too)
             int mi, ni;
             tile_at(w.tile, pr.tm, pr.tn, mi, ni);
@@ -708,11 +704,11 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                             }
                         }
                     }
-                    if (!kPlain && MODE != EPI_DACT && e.out2) {
+                    if (!kPlain && !O::mx && MODE != EPI_DACT && e.out2) { // (microscaled products save nothing)
                         box_put<T>(box1, lane, v);
                         box_send(box1, out2, lane, row0, col, M, N, inside);
                     }
-                    if (MODE == EPI_GATED && e.out3) {
+                    if (!O::mx && MODE == EPI_GATED && e.out3) {
                         box_put<T>(box1, lane, *reinterpret_cast<float(*)[32]>(u));
                         box_send(box1, out3, lane, row0, col, M, N, inside);
                     }
@@ -773,13 +769,16 @@ gemm_tc(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p)
                             }
                         }
                     }
-                    if (O::mx && mxo) {
-                        if (row0 + lane < M) mx_block_out(e, row0 + lane, col, N, v);
-                        __syncwarp();
-                        continue;
+                    if constexpr (O::mx)
+                        if (mxo) {
+                            if (row0 + lane < M) mx_block_out<O::xkind>(e, row0 + lane, col, N, v);
+                            __syncwarp();
+                            continue;
+                        }
+                    if constexpr (!kQuantised) {
+                        box_put<T>(box0, lane, v);
+                        box_send(box0, out, lane, row0, col, M, N, inside);
                     }
-                    box_put<T>(box0, lane, v);
-                    box_send(box0, out, lane, row0, col, M, N, inside);
                 }
             }
             if (!released) {
@@ -809,8 +808,9 @@ __device__ __forceinline__ void load4x2(const float4 *a, const float4 *b, float 
 // The split tiles: partials added in the order of k, then the epilogue.
 // 256 threads take 8 columns each of 8 (gated: 16) rows; a warp's 8 rows x 32
 // columns are 128 bytes in a row of the partials, 64 of the output.
-template <typename T, int MODE, int NP, bool MX, bool MXO>
-__global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcParams<NP, MX> p, int wide)
+// MXO: the output is microscaled.
+template <typename T, int MODE, int NP, int OPS, bool MXO>
+__global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcParams<NP, Ops<OPS>::mx> p, int wide)
 {
     pdl_enter();
     const Prob &pr = p.prob[NP == 1 ? 0 : p.s.sprob];
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(256) gemm_fixup(const __grid_constant__ TcPara
             for (int i = 0; i < 8; ++i) u[i] += t[i];
         }
     }
-    if constexpr (MXO) epilogue8_mx<T, MODE, 8>(pr.e, pr.N, grow, gcol, on, v, u);
+    if constexpr (MXO) epilogue8_mx<T, MODE, 8, Ops<OPS>::xkind>(pr.e, pr.N, grow, gcol, on, v, u);
     else epilogue8<T, MODE>(pr.e, pr.N, grow, gcol, v, u);
 }
 
@@ -959,14 +959,14 @@ inline cudaError_t map_of(CUtensorMap *m, const Mat &a, int rows, int K, int box
 template <int MODE, int WIDE, int OPS> cudaError_t mx_maps(const Gemm &g, TcParams<1, true> &p)
 {
     using O = Ops<OPS>;
-    constexpr int xk = OPS == OPS_MX44 ? PI_MX4 : PI_MX8, wk = OPS == OPS_MX88 ? PI_MX8 : PI_MX4, box = MODE == EPI_GATED ? 128 : WIDE / 2;
+    constexpr int box = MODE == EPI_GATED ? 128 : WIDE / 2;
     const int tiles = mx_tiles(g.K[0]);
     Prob &pr = p.prob[0];
-    cudaError_t e = encode_map_bytes(&pr.ma[0], g.a[0].p, (uint64_t)mx_row_bytes(xk, g.K[0]), (uint64_t)g.M, (uint64_t)g.a[0].ld, 128);
+    cudaError_t e = encode_map_bytes(&pr.ma[0], g.a[0].p, (uint64_t)mx_row_bytes(O::xkind, g.K[0]), (uint64_t)g.M, (uint64_t)g.a[0].ld, 128);
     if (e == cudaSuccess) e = encode_map_scales(&p.msa, g.sa, tiles, mx_tiles(g.M), O::words, 1);
     for (int i = 0; i < (MODE == EPI_GATED ? 2 : 1) && e == cudaSuccess; ++i) {
         e = O::nibbles ? encode_map_nibbles(&pr.mb[i], g.b[i].p, (uint64_t)tiles * 128, (uint64_t)g.N, (uint64_t)g.b[i].ld, box)
-                       : encode_map_bytes(&pr.mb[i], g.b[i].p, (uint64_t)mx_row_bytes(wk, g.K[0]), (uint64_t)g.N, (uint64_t)g.b[i].ld, box);
+                       : encode_map_bytes(&pr.mb[i], g.b[i].p, (uint64_t)mx_row_bytes(O::wkind, g.K[0]), (uint64_t)g.N, (uint64_t)g.b[i].ld, box);
         if (e == cudaSuccess) e = encode_map_scales(&p.msb[i], g.sb[i], tiles, mx_tiles(g.N), O::words, MODE == EPI_GATED ? 1 : WIDE / 128);
     }
     return e;
@@ -985,15 +985,14 @@ cudaError_t run_plan(const Gemm *g, int n, const Plan &q, const CtxView &v, void
         pr.M = x.M, pr.N = x.N, pr.tm = q.tm[j], pr.tn = q.tn[j], pr.kt0 = q.kt0[j], pr.KT = q.KT[j];
         pr.a_mn = x.a[0].mn, pr.b_mn = x.b[0].mn;
         pr.e = x.e;
-        if constexpr (kMx) {
-            e = mx_maps<MODE, WIDE, OPS>(x, p);
-            continue;
+        if constexpr (kMx) e = mx_maps<MODE, WIDE, OPS>(x, p);
+        else {
+            for (int i = 0; i < x.segs && e == cudaSuccess; ++i) e = map_of(&pr.ma[i], x.a[i], x.M, x.K[i], 128);
+            const int nb = MODE == EPI_GATED ? 2 : x.segs;
+            if (MODE == EPI_LINEAR && !x.e.out32 && (x.e.vec & V_OUT) && e == cudaSuccess)
+                e = encode_map(&pr.mo, x.e.out, (uint64_t)x.N, (uint64_t)x.M, (uint64_t)x.e.ldo * 2, 32);
+            for (int i = 0; i < nb && e == cudaSuccess; ++i) e = map_of(&pr.mb[i], x.b[i], x.N, x.K[MODE == EPI_GATED ? 0 : i], MODE == EPI_GATED ? 128 : WIDE / 2);
         }
-        for (int i = 0; i < x.segs && e == cudaSuccess; ++i) e = map_of(&pr.ma[i], x.a[i], x.M, x.K[i], 128);
-        const int nb = MODE == EPI_GATED ? 2 : x.segs;
-        if (MODE == EPI_LINEAR && !x.e.out32 && (x.e.vec & V_OUT) && e == cudaSuccess)
-            e = encode_map(&pr.mo, x.e.out, (uint64_t)x.N, (uint64_t)x.M, (uint64_t)x.e.ldo * 2, 32);
-        for (int i = 0; i < nb && e == cudaSuccess; ++i) e = map_of(&pr.mb[i], x.b[i], x.N, x.K[MODE == EPI_GATED ? 0 : i], MODE == EPI_GATED ? 128 : WIDE / 2);
     }
     if (e != cudaSuccess) return e;
     p.part = static_cast<float *>(ws);
@@ -1012,9 +1011,13 @@ cudaError_t run_plan(const Gemm *g, int n, const Plan &q, const CtxView &v, void
     if (e != cudaSuccess || !p.s.nsplit) return e;
     constexpr int kCols = (MODE == EPI_GATED ? 128 : kTile) / 8;
     const dim3 grid(p.s.nsplit * kTile / (256 / kCols));
-    if constexpr (kMx)
-        if (g->e.mx) return launch_pdl(gemm_fixup<T, MODE, NP, true, true>, grid, dim3(256), 0, v.stream, p, WIDE);
-    return launch_pdl(gemm_fixup<T, MODE, NP, kMx, false>, grid, dim3(256), 0, v.stream, p, WIDE);
+    auto join = [&](auto fixup) { return launch_pdl(fixup, grid, dim3(256), 0, v.stream, p, WIDE); };
+    if constexpr (kMx && MODE == EPI_GATED) return join(gemm_fixup<T, MODE, NP, OPS, true>);
+    else {
+        if constexpr (kMx)
+            if (g->e.mx) return join(gemm_fixup<T, MODE, NP, OPS, true>);
+        return join(gemm_fixup<T, MODE, NP, OPS, false>);
+    }
 }
 
 } // namespace

@@ -33,11 +33,9 @@ namespace {
 template <int KIND> struct Mx; // KIND: PI_MX8, PI_MX4
 template <> struct Mx<PI_MX8> {
     static constexpr uint32_t emax = 8, mant = 0x600000u; // 448's exponent and mantissa bits
-    static constexpr int bits = 8;
 };
 template <> struct Mx<PI_MX4> {
     static constexpr uint32_t emax = 2, mant = 0x400000u; // 6's
-    static constexpr int bits = 4;
 };
 
 // largest magnitude so far, as the bits of a non-negative float: NaN and

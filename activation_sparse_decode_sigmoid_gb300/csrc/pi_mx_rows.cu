@@ -63,15 +63,15 @@ __device__ __forceinline__ void st_cluster4(uint32_t at, float a, float b, float
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
-// Calls f with the call's activation and output type as types.
+// Calls f with the call's activation and output type as types (a microscaled output has x's kind).
 template <int V> struct Const {
     static constexpr int value = V;
 };
 template <typename T, int MODE, typename F> __device__ __forceinline__ void finish(const MrParams &p, F f)
 {
     auto by_out = [&](auto fn) {
-        if (p.e.mx == PI_MX8) f(fn, Const<PI_MX8>{});
-        else if (MODE == EPI_GATED || p.e.mx) f(fn, Const<PI_MX4>{});
+        if constexpr (MODE == EPI_GATED) f(fn, Const<Ops<kMrOps>::xkind>{});
+        else if (p.e.mx) f(fn, Const<Ops<kMrOps>::xkind>{});
         else if (p.e.out32) f(fn, Const<PI_F32>{});
         else f(fn, Const<PI_F16>{}); // (either 16-bit type)
     };

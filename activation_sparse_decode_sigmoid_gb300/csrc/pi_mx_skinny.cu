@@ -98,13 +98,16 @@ template <typename U, typename F> __device__ __forceinline__ void put_rows(const
             if (i < n) *o = conv(v[i] * e.scale, (const U *)nullptr);
     }
 }
-template <typename T> __device__ __forceinline__ void put16(const Epi &e, int t0, int n, int f, int N, const float (&v)[16])
+// (gated: a, which has x's kind; so has what an ungated block's first product leaves)
+template <typename T, int MODE, int OPS> __device__ __forceinline__ void put16(const Epi &e, int t0, int n, int f, int N, const float (&v)[16])
 {
-    if (e.mx == PI_MX8) return put_mx<PI_MX8>(e, t0, n, f, N, v);
-    if (e.mx == PI_MX4) return put_mx<PI_MX4>(e, t0, n, f, N, v);
-    if (f >= N) return;
-    if (e.out32) put_rows<float>(e, t0, n, f, v, [](float a, const float *r) { return r ? a + *r : a; });
-    else put_rows<uint16_t>(e, t0, n, f, v, [](float a, const uint16_t *r) { return C16<T>::round(r ? a + C16<T>::one(*r) : a); });
+    if constexpr (MODE == EPI_GATED) put_mx<Ops<OPS>::xkind>(e, t0, n, f, N, v);
+    else {
+        if (e.mx) return put_mx<Ops<OPS>::xkind>(e, t0, n, f, N, v);
+        if (f >= N) return;
+        if (e.out32) put_rows<float>(e, t0, n, f, v, [](float a, const float *r) { return r ? a + *r : a; });
+        else put_rows<uint16_t>(e, t0, n, f, v, [](float a, const uint16_t *r) { return C16<T>::round(r ? a + C16<T>::one(*r) : a); });
+    }
 }
 
 template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsThreads, 2) mx_skinny(const __grid_constant__ MsParams p)
@@ -292,7 +295,7 @@ template <typename T, int MODE, int OPS> __global__ void __launch_bounds__(kMsTh
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[0][i] *= v[NM - 1][i] + bias2;
                 }
-                put16<T>(p.e, t0, min(16, t1 - t0), f, p.N, v[0]);
+                put16<T, MODE, OPS>(p.e, t0, min(16, t1 - t0), f, p.N, v[0]);
                 __syncwarp(); // (some lanes stored: loads from tensor memory take whole warps)
             }
             tc_before();

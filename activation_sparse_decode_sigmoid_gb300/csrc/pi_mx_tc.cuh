@@ -33,7 +33,8 @@ namespace {
 template <int OPS> struct Ops {
     static constexpr bool mx = OPS != OPS_16;
     static constexpr int words = OPS == OPS_MX44 ? 2 : 1;
-    static constexpr int step = mx ? 128 * words : kBK;       // elements of k to a step
+    static constexpr int xkind = OPS == OPS_MX44 ? PI_MX4 : PI_MX8; // also a microscaled output's
+    static constexpr int wkind = OPS == OPS_MX88 ? PI_MX8 : PI_MX4;
     static constexpr bool nibbles = OPS == OPS_MX84;          // W's codes are spread to bytes
     static constexpr uint32_t xfmt = OPS == OPS_MX44 ? 1 : 0; // operand formats: e4m3 0; e2m1 5, or 1 where both have 4 bits
     static constexpr uint32_t wfmt = OPS == OPS_MX44 ? 1 : OPS == OPS_MX84 ? 5 : 0;
