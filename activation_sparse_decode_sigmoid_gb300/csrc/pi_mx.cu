@@ -1,8 +1,13 @@
 // Microscaled matrices: quantisation, the values back, and the C entry points
 // of the products of such matrices (a linear layer, a gated FFN).
 //
-// Both conversions are bound by HBM: T K (e + b) bytes for e bytes an element
-// and b = 33 / 32 or 17 / 32 a code with its share of the scale.
+// Both conversions move T K (e + b) bytes, for e bytes an element and b = 33 / 32
+// or 17 / 32 a code with its share of the scale.  28672 x 8192, there and back: rows
+// of 16 bits that start on 16-byte boundaries are bound by HBM (from and to bf16 84
+// and 87 us in 4 bits, 101 and 102 in 8: 6.8 to 7.1 TB/s), rows of 32 bits come to
+// 5.2 to 5.5 TB/s (205 to 217 us).  Rows on other boundaries are read and written
+// element by element, neighbouring threads 32 elements apart (writing: 8), and take 3 to 7 times as
+// long: bf16 395 to 412 us there, 493 to 600 back, fp32 767 to 778 and 601 to 738.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

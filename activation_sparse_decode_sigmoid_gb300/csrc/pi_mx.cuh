@@ -52,7 +52,7 @@ template <int KIND> __device__ __forceinline__ uint32_t mx_scale(uint32_t amax)
 // what elements are multiplied with (a byte of 255: with NaN)
 __device__ __forceinline__ float mx_inverse(uint32_t code)
 {
-    return code == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - code) << 23); // (code <= 247)
+    return code == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - code) << 23); // (code <= 253: a normal power)
 }
 __device__ __forceinline__ float mx_power(uint32_t code)
 {

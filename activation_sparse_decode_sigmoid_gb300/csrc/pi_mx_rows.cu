@@ -6,9 +6,9 @@
 // rows (those behind the last are whatever lies behind them in shared memory;
 // their sums are not read) and 256 features its columns.  An MMA of mixed types
 // takes 32 of k and about 130 cycles, with 256 columns as with 16: as in
-// pi_mx_skinny.cu, with the weights as rows, 8192 x 28672 takes 377 of them an
+// pi_mx_skinny.cu, with the weights as rows, 8192 -> 28672 takes 377 of them an
 // SM, 27 us, where reading it takes 18; so, it takes half as many, and streams at
-// 6.3 TB/s instead of 5.5.  (One token 27.3 us, there 30.9; 28672 x 8192 27.2 and 34.1.)
+// 6.3 TB/s instead of 5.5.  (One token 27.3 us, there 30.9; 28672 -> 8192 27.2 and 34.1.)
 //
 // A cluster of CTAs shares a tile of 256 features (gated: of 128 in both
 // matrices), each CTA a part of k.  At a tile's end two warps take the sums out
@@ -111,8 +111,8 @@ template <typename T, int MODE> __global__ void __launch_bounds__(kMrThreads, 1)
     // The code behind the products runs once or a few times a launch, and the first
     // time it comes from memory: the weights have passed through L2 since the
     // launch before.  Its warps go through it once ahead, with nothing to wait for,
-    // send to another CTA or store (8192 x 28672 at one token 29.6 -> 27.4 us, 28672 x 8192
-    // at eight 30.1 -> 28.2).  Others send sums only when that is over.
+    // send to another CTA or store (8192 -> 28672 at one token 29.6, so 27.4 us, 28672 -> 8192
+    // at eight 30.1, so 28.2).  Others send sums only when that is over.
     const bool rehearses = (warp & 7) == 0 || warp >= 4;
     if (p.cs > 1 && !rehearses) cluster_arrive(); // all barriers are set up
     if (!rehearses && !(p.early && warp == 1)) pdl_enter();
@@ -413,11 +413,11 @@ template <typename T, int MODE> cudaError_t run(const Gemm &g, const CtxView &v)
 // waits beside the one before it, cost about a microsecond at one token and 0.15 more for
 // each further one, and again at each tile where k is too short to hide them: worth it
 // from 20 MB of weights on (2 more a token) and 2048 values of k, to 16 tokens.  us, here and in pi_mx_skinny.cu:
-//   28672 x 1024, 16 MB:    8.7,  8.4 at one token,  9.6,  8.5 at 8, 10.6,  8.5 at 16
-//   28672 x 2048, 31 MB:   11.3, 12.5               12.4, 12.5       13.4, 12.5
-//   28672 x 4096, 62 MB:   17.4, 19.8               18.2, 19.9       19.4, 20.1
-//   28672 x 8192, 125 MB:  27.3, 30.9               28.5, 31.3       29.7, 31.6
-//   128256 x 1024, 70 MB:  21.2, 19.6               22.3, 19.7       24.5, 19.9
+//   1024 -> 28672, 16 MB:    8.7,  8.4 at one token,  9.6,  8.5 at 8, 10.6,  8.5 at 16
+//   2048 -> 28672, 31 MB:   11.3, 12.5               12.4, 12.5       13.4, 12.5
+//   4096 -> 28672, 62 MB:   17.4, 19.8               18.2, 19.9       19.4, 20.1
+//   8192 -> 28672, 125 MB:  27.3, 30.9               28.5, 31.3       29.7, 31.6
+//   1024 -> 128256, 70 MB:  21.2, 19.6               22.3, 19.7       24.5, 19.9
 bool mx_rows_takes(const Gemm &g)
 {
     const int64_t bytes = (int64_t)g.N * mx_tiles(g.K[0]) * 68 * (g.mode == EPI_GATED ? 2 : 1);

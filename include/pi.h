@@ -600,8 +600,9 @@ pi_status pi_norm_residual_bwd(pi_ctx *ctx, const pi_norm_residual_desc *desc, c
  *           B = cols rounded up to 128, divided by 128, row r's block b is at
  *           ((r / 128) B + b / 4) 512 + (r % 32) 16 + (r % 128 / 32) 4 + b % 4
  * Codes and scales of what pads rows and columns are 0, as the calls that
- * write a matrix leave them; another program's matrix has to be laid out
- * so too (a code of NaN in a padded column would reach the products).
+ * write a matrix leave them (but in a block that is NaN what pads it is NaN
+ * too); another program's matrix has to be laid out so too (a code of NaN in a
+ * padded column would reach the products).
  *
  * Quantisation: a block's scale is the least power of two s (from 2^-127) with
  * amax / s at most the type's largest value; elements are v / s rounded to
@@ -631,8 +632,9 @@ typedef struct {
 /* q = x quantised. */
 pi_status pi_mx_quantize(pi_ctx *ctx, const pi_mx_desc *desc, const void *x, const pi_mx *q);
 
-/* y = the values of q, rounded to dtype (PI_F32 and, but for values past its
- * range, PI_BF16 hold them exactly; PI_F16 lacks scales far from 1). */
+/* y = the values of q, rounded to dtype.  PI_F32 holds them exactly, but for 2^128
+ * and more, to which the values next to its own largest may round up; PI_BF16
+ * also lacks what lies below 2^-133, PI_F16 whatever has a scale far from 1. */
 pi_status pi_mx_dequantize(pi_ctx *ctx, const pi_mx_desc *desc, const pi_mx *q, void *y);
 
 /* pi_linear of microscaled x [T][K] and W [N][K]:

@@ -210,3 +210,29 @@ def test_linear_of_a_large_matrix_in_f16(c, T, K, N):
     assert r.equal(want)
     r32 = m(T, N, dt=F32)
     R.check(c.mx_linear(x, w, b, residual=r32, dtype=F16), X.linear(x, w, b, "none", 1.0, r32, F32), "fp32")
+
+
+# ------------------------------------------------------------------ ends of the range
+@pytest.mark.parametrize("kind", [MX8, MX4])
+def test_values_at_the_ends_of_the_range(c, kind):
+    """Values next to fp32's largest may round up to 2^128, which fp32 and bf16
+    hold as infinity; the least ones are below bf16's subnormals.  What a NaN block
+    holds behind the row's end is NaN, and nothing else that pads is."""
+    g = torch.Generator(device="cuda").manual_seed(80)
+    u = torch.rand(64, 70, generator=g, device="cuda") * 2 - 1
+    for s in (torch.finfo(F32).max, 2.0 ** -118, 2.0 ** -126, 2.0 ** -140):
+        x = u * s
+        x[:, 3] = s
+        q = c.mx_quantize(x, kind)
+        codes, scales, want = X.quantize(kind, x.double())
+        got = X.unpack(q)
+        assert torch.equal(got[0], codes) and torch.equal(got[1], scales) and got[2]
+        for dt in (F32, BF16):
+            assert torch.equal(c.mx_dequantize(q, dt), want.float().to(dt)), (s, dt)
+    x = u.clone()
+    x[5, 69] = float("nan")
+    codes, scales, pad = X.unpack(c.mx_quantize(x, kind))
+    assert pad and int(scales[5, 2]) == 255 and not bool(scales[:, 3].any())
+    assert bool((codes[5, 64:96] == (0x7f if kind == MX8 else 0)).all()) and not bool(codes[:, 96:].any())
+    codes[5] = 0
+    assert not bool(codes[:, 70:].any())
